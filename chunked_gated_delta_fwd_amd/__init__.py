@@ -29,7 +29,19 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_checkpoints", "gdr_chunk_bwd", "gdr_c
            "gdr_prepare_chunks", "gdr_dispatch_order",
            "gdr_chunk_local_cumsum", "gdr_last_error", "gdr_version", "gdr_selftest_mfma",
            "gdr_debug_set", "gdr_device_status", "gdr_free_workspaces", "gdr_chunk_fwd_noalloc",
-           "gdr_chunk_fwd_checkpoints_n")
+           "gdr_chunk_fwd_checkpoints_n", "gdr_short_conv_fwd", "gdr_short_conv_bwd", "gdr_short_conv_step",
+           "gdr_qk_norm_rope_fwd", "gdr_qk_norm_rope_bwd", "gdr_ssm_step")
+
+# the operators around the recurrence (mixer.py), loaded on first use
+_MIXER = ("short_conv_fwd", "short_conv_bwd", "short_conv_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "ssm_step")
+
+
+def __getattr__(name):
+    if name in _MIXER:
+        from . import mixer
+        globals().update({n: getattr(mixer, n) for n in _MIXER})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 # gdr_debug_set options and device status bits (include/gdr.h)
 GDR_DEBUG_CHECK_CU, GDR_DEBUG_FAIL_LAUNCHES, GDR_DEBUG_SPIN_LIMIT = 1, 2, 3
@@ -93,6 +105,16 @@ def library(path: Optional[str] = None):
     lib.gdr_dispatch_order.restype = ctypes.c_int
     lib.gdr_chunk_local_cumsum.argtypes = [TP] * 3 + [ctypes.c_void_p]
     lib.gdr_chunk_local_cumsum.restype = ctypes.c_int
+    P = ctypes.c_void_p   # the operators of mixer.py take packed descriptors by address
+    lib.gdr_short_conv_fwd.argtypes = [P] * 7 + [ctypes.c_int, P]
+    lib.gdr_short_conv_bwd.argtypes = [P] * 11 + [ctypes.c_int, P, P, P]
+    lib.gdr_short_conv_step.argtypes = [P] * 5 + [ctypes.c_int, P]
+    lib.gdr_qk_norm_rope_fwd.argtypes = [P] * 9 + [ctypes.c_int, ctypes.c_float, ctypes.c_int, P]
+    lib.gdr_qk_norm_rope_bwd.argtypes = [P] * 13 + [ctypes.c_int, ctypes.c_float, ctypes.c_int, P, P, P]
+    lib.gdr_ssm_step.argtypes = [P] * 10
+    for name in ("short_conv_fwd", "short_conv_bwd", "short_conv_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
+                 "ssm_step"):
+        getattr(lib, "gdr_" + name).restype = ctypes.c_int
     lib.gdr_last_error.argtypes = []
     lib.gdr_last_error.restype = ctypes.c_char_p
     lib.gdr_version.argtypes = []

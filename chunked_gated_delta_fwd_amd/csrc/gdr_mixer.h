@@ -1,0 +1,76 @@
+// Internal interface between the host API (gdr_mixer_api.cpp) and the kernels
+// of the operators around the recurrence: the short causal convolution
+// (gdr_conv.hip), the query/key norm with rotation (gdr_qknorm.hip) and the
+// state space scan (gdr_ssm.hip).  Not installed; not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdr {
+
+// Blocks are dispatched round-robin over the 8 XCDs; this renumbering gives
+// each XCD one contiguous run of the `count` blocks, so that neighbours share
+// an L2 (a bijection on 0 .. count-1 for any count).
+__device__ __forceinline__ int64_t xcd_run(int64_t block, int64_t count) {
+    const int64_t q = count / 8, r = count % 8, x = block % 8;
+    return x * q + (x < r ? x : r) + block / 8;
+}
+
+// Short causal depthwise convolution; rows of x and dy are ld* elements apart.
+struct ConvArgs {
+    const void *x, *w, *bias;   // bias NULL: none
+    const int32_t *cu;          // NULL: n_seq rows of seq_len tokens
+    const void *s0;             // [N, W-1, ch], NULL: zeros
+    void *y, *st;               // st NULL: not written
+    int64_t ldx, n_seq, seq_len, total;
+    int32_t ch, width, bf16, silu, vec;   // vec: 16-byte pieces of the channels
+    // backward
+    const void *dy, *dst;       // dst NULL: zeros
+    void *dx, *ds0;             // ds0 NULL: not written
+    float *dw, *db;             // db NULL: not written
+    float *part;                // [conv_bwd_rows][ch][W + 1]
+    int64_t lddy;
+};
+hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t stream);
+// Rows of per-block partial sums of dw and db that a backward call stores.
+int64_t conv_bwd_rows(int64_t total, int32_t ch, int32_t bf16, int32_t vec);
+hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t stream);
+// One token for each of n_seq sequences: x rows ldx apart, st read and updated in place.
+hipError_t launch_conv_step(const ConvArgs &a, hipStream_t stream);
+
+// Norm of each head row of q and k, rotated by position.
+struct NormArgs {
+    const void *q, *k, *wq, *wk;          // weights [d], NULL: ones
+    const float *cos, *sin;               // [table, rot/2]
+    const int32_t *pos;                   // [tokens], NULL: the token's index in its row
+    void *oq, *ok;
+    int64_t tokens, seq_len, table, ldq, ldk;
+    int32_t hq, hk, d, rot, bf16, rms, interleaved;
+    float eps;
+    // backward
+    const void *doq, *dok;
+    void *dq, *dk;
+    float *dwq, *dwk;                     // [d], NULL: no weights
+    float *part;                          // [norm_bwd_blocks][2][d]
+    int64_t lddoq, lddok;
+};
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream);
+int64_t norm_bwd_blocks(const NormArgs &a);
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream);
+
+// Selective state space scan.
+struct SsmArgs {
+    const void *x, *dt, *b, *c;
+    const float *A, *D, *dt_bias;         // [H]; D, dt_bias NULL: zeros
+    const int32_t *cu;                    // NULL: n_seq rows of seq_len tokens
+    const float *h0;                      // [N, H, n, p], NULL: zeros
+    void *y;
+    float *ht;                            // NULL: not written (step: the state, in place)
+    int64_t n_seq, seq_len, total;
+    int64_t ldx, lddt, ldb, ldc;
+    int32_t heads, groups, n, p, bf16, gate_bf16;
+};
+hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream);
+
+}  // namespace gdr

@@ -313,6 +313,130 @@ int gdr_decode_step(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *
                     const gdr_tensor *g, const gdr_tensor *beta, const gdr_tensor *h,
                     const gdr_tensor *o, float scale, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the recurrence in a token mixer.
+ *
+ * Inputs whose description says "rows" may be a slice of the columns of a
+ * wider projection: their last dimensions are compact and the rows (all
+ * leading dimensions) evenly spaced, strides[..] >= a row's elements; every
+ * other tensor is compact.  Backward entries need a workspace.  With
+ * workspace and workspace_bytes both NULL it is the library's (the ring of
+ * gdr_chunk_fwd up to 1 MiB, the large buffer of gdr_chunk_bwd above), which
+ * a stream capture cannot use (GDR_EINVAL); with workspace NULL and
+ * workspace_bytes set, the call validates its arguments, stores the size it
+ * needs and enqueues nothing; with both set, `workspace` (device memory,
+ * 16-byte aligned, *workspace_bytes long) is used and must stay untouched
+ * until the call's work is done.  All sums run in a fixed order: repeated
+ * calls give the same bits.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
+typedef enum { GDR_NORM_L2 = 0, GDR_NORM_RMS = 1 } gdr_norm;
+
+/*
+ * gdr_short_conv_fwd - short causal depthwise convolution over tokens:
+ *
+ *     y[t, c] = act(bias[c] + sum_j w[c, j] x[t - (W-1) + j, c])
+ *
+ * within each sequence; positions before its first token are its state.
+ *
+ *   x           [B, T, ch] rows, bf16 or f32 (one dtype with w, bias, s0, y, st)
+ *   w           [ch, W], W = 2, 3 or 4
+ *   bias        [ch] or NULL
+ *   cu_seqlens  [N+1] int32 or NULL, as gdr_chunk_fwd (preconditions too)
+ *   s0          [N, W-1, ch] state before the call, or NULL for zeros
+ *   y           [B, T, ch] out; rows of tokens outside every segment are not written
+ *   st          [N, W-1, ch] out, or NULL: the last W - 1 rows of [s0, x] of
+ *               each sequence (a length-0 sequence hands its s0 on)
+ *   activation  GDR_ACT_NONE or GDR_ACT_SILU (z sigmoid(z))
+ *
+ * fp32 arithmetic, y rounded once; st is a copy.  No workspace.  Any channel
+ * count; multiples of 16 bytes on 16-byte addresses run in 16-byte pieces.
+ * Errors as gdr_chunk_fwd.
+ */
+int gdr_short_conv_fwd(const gdr_tensor *x, const gdr_tensor *w, const gdr_tensor *bias,
+                       const gdr_tensor *cu_seqlens, const gdr_tensor *s0, const gdr_tensor *y,
+                       const gdr_tensor *st, int activation, hipStream_t stream);
+
+/*
+ * gdr_short_conv_bwd - gradients of gdr_short_conv_fwd.
+ *
+ *   dy    [B, T, ch] rows, dtype of x
+ *   dst   [N, W-1, ch] gradient of st, dtype of x, or NULL for zeros
+ *   dx    [B, T, ch] out, dtype of x
+ *   dw    [ch, W] out, f32;   db  [ch] out, f32, or NULL
+ *   ds0   [N, W-1, ch] out, dtype of x, or NULL (written also when s0 is NULL)
+ */
+int gdr_short_conv_bwd(const gdr_tensor *x, const gdr_tensor *w, const gdr_tensor *bias,
+                       const gdr_tensor *cu_seqlens, const gdr_tensor *s0, const gdr_tensor *dy,
+                       const gdr_tensor *dst, const gdr_tensor *dx, const gdr_tensor *dw,
+                       const gdr_tensor *db, const gdr_tensor *ds0, int activation, void *workspace,
+                       int64_t *workspace_bytes, hipStream_t stream);
+
+/*
+ * gdr_short_conv_step - one token for each of B sequences.
+ *   x [B, ch] rows;  state [B, W-1, ch] read and updated in place;  y [B, ch] out.
+ */
+int gdr_short_conv_step(const gdr_tensor *x, const gdr_tensor *state, const gdr_tensor *w,
+                        const gdr_tensor *bias, const gdr_tensor *y, int activation,
+                        hipStream_t stream);
+
+/*
+ * gdr_qk_norm_rope_fwd - norm of every query and key head and, with tables,
+ * the position rotation in the same pass.  Per head row x of d channels:
+ *
+ *     n = x / sqrt(sum x^2 + eps) w  (GDR_NORM_L2), mean x^2 with GDR_NORM_RMS
+ *     (a, b) -> (a cos - b sin, a sin + b cos) on the first rot channels of n
+ *
+ * with a, b channels i, i + rot/2, or 2i, 2i + 1 when interleaved != 0, and
+ * cos, sin entry i of the token's position's row.
+ *
+ *   q, k        [B, T, Hq, d], [B, T, Hk, d] rows, bf16 or f32, d 64, 128 or 256
+ *   wq, wk      [d] dtype of q, or NULL for ones
+ *   cos, sin    [table, rot/2] f32, rot a multiple of 16 up to d; both NULL: no rotation
+ *   positions   [B, T] int32, or NULL for 0 .. T-1 (T <= table).  A position
+ *               outside the table takes its nearest row.
+ *   oq, ok      out, the shapes and dtype of q and k
+ *
+ * fp32 arithmetic, one rounding.  q, k, oq, ok, weights and tables on 16-byte
+ * addresses, rows too.  No workspace.
+ */
+int gdr_qk_norm_rope_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *wq,
+                         const gdr_tensor *wk, const gdr_tensor *cos, const gdr_tensor *sin,
+                         const gdr_tensor *positions, const gdr_tensor *oq, const gdr_tensor *ok,
+                         int norm, float eps, int interleaved, hipStream_t stream);
+
+/*
+ * gdr_qk_norm_rope_bwd - gradients: doq, dok (rows) of oq, ok; dq, dk out in
+ * the dtype of q; dwq, dwk [d] f32 out, each or NULL.  With neither there is
+ * no workspace.
+ */
+int gdr_qk_norm_rope_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *wq,
+                         const gdr_tensor *wk, const gdr_tensor *cos, const gdr_tensor *sin,
+                         const gdr_tensor *positions, const gdr_tensor *doq, const gdr_tensor *dok,
+                         const gdr_tensor *dq, const gdr_tensor *dk, const gdr_tensor *dwq,
+                         const gdr_tensor *dwk, int norm, float eps, int interleaved,
+                         void *workspace, int64_t *workspace_bytes, hipStream_t stream);
+
+/*
+ * gdr_ssm_step - one token of the selective state space scan for each of B
+ * sequences.  Per sequence and head, with the state S as [n][p]:
+ *
+ *     dt = softplus(dt_raw + dt_bias),  S <- exp(dt A) S + dt b x^T,  y = S^T c + D x
+ *
+ *   x        [B, H, p] rows, bf16 or f32 (one dtype with b, c, y); p 64 or 128
+ *   dt       [B, H] rows, bf16 or f32
+ *   A        [H] f32;  D, dt_bias [H] f32 or NULL for zeros
+ *   b, c     [B, G, n] rows, n 64 or 128, H % G == 0; head h reads group h / (H/G)
+ *   h        [B, H, n, p] f32, read and updated in place
+ *   y        [B, H, p] out, rounded once
+ *
+ * fp32 arithmetic.  No workspace.  x, b, c rows, h and y on 16-byte addresses.
+ */
+int gdr_ssm_step(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A, const gdr_tensor *b,
+                 const gdr_tensor *c, const gdr_tensor *D, const gdr_tensor *dt_bias,
+                 const gdr_tensor *h, const gdr_tensor *y, hipStream_t stream);
+
 /*
  * Launch plan of a gdr_chunk_fwd call, computed from shapes only (no device
  * access, no allocation).  gdr_plan validates exactly like gdr_chunk_fwd and
