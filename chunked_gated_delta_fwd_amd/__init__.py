@@ -30,10 +30,11 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_checkpoints", "gdr_chunk_bwd", "gdr_c
            "gdr_chunk_local_cumsum", "gdr_last_error", "gdr_version", "gdr_selftest_mfma",
            "gdr_debug_set", "gdr_device_status", "gdr_free_workspaces", "gdr_chunk_fwd_noalloc",
            "gdr_chunk_fwd_checkpoints_n", "gdr_short_conv_fwd", "gdr_short_conv_bwd", "gdr_short_conv_step",
-           "gdr_qk_norm_rope_fwd", "gdr_qk_norm_rope_bwd", "gdr_ssm_step")
+           "gdr_qk_norm_rope_fwd", "gdr_qk_norm_rope_bwd", "gdr_ssm_scan_fwd", "gdr_ssm_scan_bwd", "gdr_ssm_step")
 
 # the operators around the recurrence (mixer.py), loaded on first use
-_MIXER = ("short_conv_fwd", "short_conv_bwd", "short_conv_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "ssm_step")
+_MIXER = ("short_conv_fwd", "short_conv_bwd", "short_conv_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "ssm_scan_fwd",
+          "ssm_scan_bwd", "ssm_step")
 
 
 def __getattr__(name):
@@ -111,9 +112,10 @@ def library(path: Optional[str] = None):
     lib.gdr_short_conv_step.argtypes = [P] * 5 + [ctypes.c_int, P]
     lib.gdr_qk_norm_rope_fwd.argtypes = [P] * 9 + [ctypes.c_int, ctypes.c_float, ctypes.c_int, P]
     lib.gdr_qk_norm_rope_bwd.argtypes = [P] * 13 + [ctypes.c_int, ctypes.c_float, ctypes.c_int, P, P, P]
+    lib.gdr_ssm_scan_fwd.argtypes = [P] * 14
+    lib.gdr_ssm_scan_bwd.argtypes = [P] * 22
     lib.gdr_ssm_step.argtypes = [P] * 10
-    for name in ("short_conv_fwd", "short_conv_bwd", "short_conv_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
-                 "ssm_step"):
+    for name in _MIXER:
         getattr(lib, "gdr_" + name).restype = ctypes.c_int
     lib.gdr_last_error.argtypes = []
     lib.gdr_last_error.restype = ctypes.c_char_p

@@ -12,7 +12,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdr.so")
 
 SOURCES = ["gdr_kernels.hip", "gdr_bwd.hip", "gdr_kda.hip", "gdr_conv.hip", "gdr_qknorm.hip", "gdr_ssm.hip",
-           "gdr_api.cpp", "gdr_mixer_api.cpp"]
+           "gdr_ssm_bwd.hip", "gdr_api.cpp", "gdr_mixer_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

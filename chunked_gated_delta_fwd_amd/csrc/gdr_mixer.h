@@ -70,7 +70,39 @@ struct SsmArgs {
     int64_t n_seq, seq_len, total;
     int64_t ldx, lddt, ldb, ldc;
     int32_t heads, groups, n, p, bf16, gate_bf16;
+    // Spans of span_len tokens (a multiple of 64) that are walked in parallel;
+    // spans NULL: one per sequence.  {first token, length (< 0: surplus entry),
+    // sequence << 2 | last << 1 | first, chunk row of its first chunk}
+    const int4 *spans;
+    const int32_t *span_first;            // [N + 1] first span of each sequence
+    int64_t n_spans;                      // entries: an upper bound on the spans
+    int64_t span_len;
+    float *span_state;                    // [directions][n_spans][H][n p]; NULL: not split
+    float *span_decay;                    // [directions][n_spans][H]
+    // backward
+    const void *dy;
+    const float *dht;                     // [N, H, n, p], NULL: zeros
+    int64_t lddy;
+    float *chunk_state;                   // [2][n_chunks][H][n p]: states before chunks, gradients after them
+    int64_t n_chunks;                     // entries: an upper bound on the 64-token chunks
+    const int4 *chunks;                   // as spans, span_len 64
+    void *dx, *ddt, *db, *dc;
+    float *dA, *dD, *dbias, *dh0;         // dD, dbias, dh0 NULL: not written
+    int32_t slices, slice_heads;          // the heads of a group in slices, one block each
+    float *bc_part;                       // [slices][db, dc][total][G][n]; not used with one slice
+    float *head_part;                     // [n_chunks][H]{dA, dD, dbias}
 };
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream);
+// Tokens of a span, or 0 where each sequence is walked by one block.
+int64_t ssm_span_len(const SsmArgs &a);
+// Table of spans (or, with span_len 64, of chunks) from the content of
+// cu_seqlens: first [N + 1], table [count].  chunk_first: that of the chunks'
+// table, for the spans' chunk rows (NULL: the entry's own index).
+hipError_t launch_ssm_table(const SsmArgs &a, int64_t span_len, int64_t count, const int32_t *chunk_first,
+                            int32_t *first, int4 *table, hipStream_t stream);
+hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream);
+// Slices of a group's heads in a backward call (a.n_chunks set).
+int ssm_slices(const SsmArgs &a);
+hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream);
 
 }  // namespace gdr

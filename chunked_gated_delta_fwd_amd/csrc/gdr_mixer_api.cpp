@@ -326,6 +326,9 @@ int plan_norm(NormIn &c, gdr::NormArgs &a) {
 
 // --- state space scan ---------------------------------------------------------------
 
+// Chunk tiles are addressed with 32-bit byte offsets over 64 rows.
+constexpr int64_t kMaxRow = 1 << 25;
+
 struct SsmIn {
     const gdr_tensor *x, *dt, *A, *b, *c, *D, *dt_bias, *cu, *h0;
     Span sx, sdt, sA, sb, sc, sD, sbias, scu, sh0;
@@ -387,6 +390,9 @@ int plan_ssm(SsmIn &s, int lead, gdr::SsmArgs &a) {
         (rc = want_shape(s.h0, "h0", {s.N, H, nn, p}, "[N, H, n, p]")))
         return rc;
     if (s.N * H > 0x3FFFFFFFLL) return fail(GDR_ESHAPE, "N * H exceeds the launch grid limit");
+    const int64_t e = static_cast<int64_t>(dtype_size(s.x->dtype));
+    if (a.ldx * e > kMaxRow || a.ldb * e > kMaxRow || a.ldc * e > kMaxRow)
+        return fail(GDR_ESTRIDE, "x, b and c: rows may be at most %lld bytes apart", (long long)kMaxRow);
     a.x = s.x->data;
     a.dt = s.dt->data;
     a.b = s.b->data;
@@ -406,6 +412,83 @@ int plan_ssm(SsmIn &s, int lead, gdr::SsmArgs &a) {
     a.bf16 = s.x->dtype == GDR_BF16;
     a.gate_bf16 = s.dt->dtype == GDR_BF16;
     return GDR_OK;
+}
+
+// Carves a workspace into 256-byte aligned parts: one pass with a NULL base
+// sums the size, a second one hands out the addresses.
+struct Carve {
+    unsigned char *base;
+    size_t used = 0;
+    template <class T>
+    T *take(int64_t count) {
+        T *p = base ? reinterpret_cast<T *>(base + used) : nullptr;
+        used += (static_cast<size_t>(count) * sizeof(T) + 255) & ~static_cast<size_t>(255);
+        return p;
+    }
+};
+
+struct SsmTables {
+    int32_t *span_first, *chunk_first;
+    int4 *spans, *chunks;
+    bool split;
+};
+// Parts of a call's workspace; also sets the counts that the launches need.
+// The entries of a table bound the spans: each sequence has at least one and
+// at most its length / span + 1.
+void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, SsmTables &t) {
+    std::memset(&t, 0, sizeof(t));
+    const int64_t state = static_cast<int64_t>(a.n) * a.p, H = a.heads;
+    auto entries = [&](int64_t span) {
+        if (a.cu) return a.total / span + a.n_seq;
+        const int64_t each = (a.seq_len + span - 1) / span;
+        return a.n_seq * (each < 1 ? 1 : each);
+    };
+    a.span_len = gdr::ssm_span_len(a);
+    t.split = a.span_len > 0;
+    if (!t.split) {
+        const int64_t longest = a.cu ? a.total : a.seq_len;
+        a.span_len = (longest / 64 + 1) * 64;
+    }
+    a.n_spans = t.split ? entries(a.span_len) : a.n_seq;
+    const int64_t ways = bwd ? 2 : 1;
+    if (t.split || bwd) {
+        t.span_first = c.take<int32_t>(a.n_seq + 1);
+        t.spans = c.take<int4>(a.n_spans);
+    }
+    if (t.split) {
+        a.span_state = c.take<float>(ways * a.n_spans * H * state);
+        a.span_decay = c.take<float>(ways * a.n_spans * H);
+    }
+    if (bwd) {
+        a.n_chunks = entries(64);
+        t.chunk_first = c.take<int32_t>(a.n_seq + 1);
+        t.chunks = c.take<int4>(a.n_chunks);
+        a.chunk_state = c.take<float>(2 * a.n_chunks * H * state);
+        a.head_part = c.take<float>(a.n_chunks * H * 3);
+        if (a.n_chunks > 0) {
+            a.slices = gdr::ssm_slices(a);
+            a.slice_heads = (a.heads / a.groups + a.slices - 1) / a.slices;
+        } else {
+            a.slices = 1;
+        }
+        if (a.slices > 1) a.bc_part = c.take<float>(2 * a.slices * a.total * a.groups * a.n);
+    }
+}
+
+// Tables, then the walks.
+hipError_t run_ssm(gdr::SsmArgs &a, const SsmTables &t, bool bwd, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    if (bwd && a.n_seq > 0) {
+        e = gdr::launch_ssm_table(a, 64, a.n_chunks, nullptr, t.chunk_first, t.chunks, stream);
+        a.chunks = t.chunks;
+    }
+    if (e == hipSuccess && t.spans && a.n_seq > 0) {
+        e = gdr::launch_ssm_table(a, a.span_len, a.n_spans, t.chunk_first, t.span_first, t.spans, stream);
+        a.spans = t.spans;
+        a.span_first = t.span_first;
+    }
+    if (e != hipSuccess) return e;
+    return bwd ? gdr::launch_ssm_bwd(a, stream) : gdr::launch_ssm_fwd(a, stream);
 }
 
 }  // namespace
@@ -627,6 +710,129 @@ int gdr_ssm_step(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
         a.ht = static_cast<float *>(h->data);
         a.y = y->data;
         return launch([&] { return gdr::launch_ssm_step(a, stream); }, "state space step kernel");
+    });
+}
+
+int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A, const gdr_tensor *b,
+                     const gdr_tensor *c, const gdr_tensor *D, const gdr_tensor *dt_bias, const gdr_tensor *cu_seqlens,
+                     const gdr_tensor *h0, const gdr_tensor *y, const gdr_tensor *ht, void *workspace,
+                     int64_t *workspace_bytes, hipStream_t stream) {
+    return entry([&]() -> int {
+        SsmIn s{x, dt, A, b, c, D, dt_bias, cu_seqlens, h0};
+        gdr::SsmArgs a;
+        int64_t ny, nht = 0;
+        int rc;
+        if ((rc = plan_ssm(s, 2, a))) return rc;
+        if ((rc = check_tensor(y, "y", 4, &ny, 16))) return rc;
+        if (ht && (rc = check_tensor(ht, "ht", 4, &nht, 16))) return rc;
+        if ((rc = want_dtype(y, "y", x->dtype)) || (rc = want_dtype(ht, "ht", GDR_F32))) return rc;
+        if ((rc = want_shape(y, "y", {s.B, s.T, a.heads, a.p}, "x's shape")) ||
+            (rc = want_shape(ht, "ht", {s.N, a.heads, a.n, a.p}, "[N, H, n, p]")))
+            return rc;
+        if ((rc = check_overlaps({{"x", s.sx}, {"dt", s.sdt}, {"A", s.sA}, {"b", s.sb}, {"c", s.sc}, {"D", s.sD},
+                                  {"dt_bias", s.sbias}, {"cu_seqlens", s.scu}, {"h0", s.sh0}},
+                                 {{"y", span_of(y, ny)}, {"ht", span_of(ht, nht)}})))
+            return rc;
+        a.y = y->data;
+        a.ht = ht ? static_cast<float *>(ht->data) : nullptr;
+        Carve size{nullptr};
+        SsmTables t;
+        carve_ssm(a, false, size, t);
+        if (workspace || !workspace_bytes) {
+            if ((rc = check_device())) return rc;
+            if ((rc = check_cu(cu_seqlens, a.n_seq, a.total, stream))) return rc;
+        }
+        Workspace ws;
+        void *p;
+        if ((rc = ws.get(size.used, workspace, workspace_bytes, stream, &p))) return rc == 1 ? ok() : rc;
+        if (a.n_seq == 0 || (a.total == 0 && !ht)) return ok();
+        Carve parts{static_cast<unsigned char *>(p)};
+        carve_ssm(a, false, parts, t);
+        rc = launch([&] { return run_ssm(a, t, false, stream); }, "state space scan kernels");
+        const int rr = ws.release();
+        return rc ? rc : rr;
+    });
+}
+
+int gdr_ssm_scan_bwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A, const gdr_tensor *b,
+                     const gdr_tensor *c, const gdr_tensor *D, const gdr_tensor *dt_bias, const gdr_tensor *cu_seqlens,
+                     const gdr_tensor *h0, const gdr_tensor *dy, const gdr_tensor *dht, const gdr_tensor *dx,
+                     const gdr_tensor *ddt, const gdr_tensor *dA, const gdr_tensor *db, const gdr_tensor *dc,
+                     const gdr_tensor *dD, const gdr_tensor *ddt_bias, const gdr_tensor *dh0, void *workspace,
+                     int64_t *workspace_bytes, hipStream_t stream) {
+    return entry([&]() -> int {
+        SsmIn s{x, dt, A, b, c, D, dt_bias, cu_seqlens, h0};
+        gdr::SsmArgs a;
+        int64_t ndht = 0;
+        Span sdy;
+        int rc;
+        if ((rc = plan_ssm(s, 2, a))) return rc;
+        if ((rc = check_rows(dy, "dy", 4, 2, 16, &a.lddy, &sdy))) return rc;
+        if (dht && (rc = check_tensor(dht, "dht", 4, &ndht, 16))) return rc;
+        struct Out {
+            const gdr_tensor *t;
+            const char *name;
+            int ndim;
+            size_t align;
+            int32_t dtype;
+            bool needed;
+            int64_t n;
+        } outs[] = {{dx, "dx", 4, 16, x->dtype, true, 0},   {ddt, "ddt", 3, 4, dt->dtype, true, 0},
+                    {dA, "dA", 1, 4, GDR_F32, true, 0},     {db, "db", 4, 16, x->dtype, true, 0},
+                    {dc, "dc", 4, 16, x->dtype, true, 0},   {dD, "dD", 1, 4, GDR_F32, false, 0},
+                    {ddt_bias, "ddt_bias", 1, 4, GDR_F32, false, 0}, {dh0, "dh0", 4, 16, GDR_F32, false, 0}};
+        for (Out &o : outs) {
+            if (!o.t && !o.needed) continue;
+            if ((rc = check_tensor(o.t, o.name, o.ndim, &o.n, o.align))) return rc;
+            if ((rc = want_dtype(o.t, o.name, o.dtype))) return rc;
+        }
+        if ((rc = want_dtype(dy, "dy", x->dtype)) || (rc = want_dtype(dht, "dht", GDR_F32))) return rc;
+        const int64_t H = a.heads, G = a.groups;
+        if ((rc = want_shape(dy, "dy", {s.B, s.T, H, a.p}, "x's shape")) ||
+            (rc = want_shape(dht, "dht", {s.N, H, a.n, a.p}, "[N, H, n, p]")) ||
+            (rc = want_shape(dx, "dx", {s.B, s.T, H, a.p}, "x's shape")) ||
+            (rc = want_shape(ddt, "ddt", {s.B, s.T, H}, "dt's shape")) || (rc = want_shape(dA, "dA", {H}, "[H]")) ||
+            (rc = want_shape(db, "db", {s.B, s.T, G, a.n}, "b's shape")) ||
+            (rc = want_shape(dc, "dc", {s.B, s.T, G, a.n}, "c's shape")) || (rc = want_shape(dD, "dD", {H}, "[H]")) ||
+            (rc = want_shape(ddt_bias, "ddt_bias", {H}, "[H]")) ||
+            (rc = want_shape(dh0, "dh0", {s.N, H, a.n, a.p}, "[N, H, n, p]")))
+            return rc;
+        if (a.lddy * static_cast<int64_t>(dtype_size(x->dtype)) > kMaxRow)
+            return fail(GDR_ESTRIDE, "dy: rows may be at most %lld bytes apart", (long long)kMaxRow);
+        if ((rc = check_overlaps({{"x", s.sx}, {"dt", s.sdt}, {"A", s.sA}, {"b", s.sb}, {"c", s.sc}, {"D", s.sD},
+                                  {"dt_bias", s.sbias}, {"cu_seqlens", s.scu}, {"h0", s.sh0}, {"dy", sdy},
+                                  {"dht", span_of(dht, ndht)}},
+                                 {{"dx", span_of(dx, outs[0].n)}, {"ddt", span_of(ddt, outs[1].n)},
+                                  {"dA", span_of(dA, outs[2].n)}, {"db", span_of(db, outs[3].n)},
+                                  {"dc", span_of(dc, outs[4].n)}, {"dD", span_of(dD, outs[5].n)},
+                                  {"ddt_bias", span_of(ddt_bias, outs[6].n)}, {"dh0", span_of(dh0, outs[7].n)}})))
+            return rc;
+        auto f32 = [](const gdr_tensor *t) { return t ? static_cast<float *>(t->data) : nullptr; };
+        a.dy = dy->data;
+        a.dht = f32(dht);
+        a.dx = dx->data;
+        a.ddt = ddt->data;
+        a.db = db->data;
+        a.dc = dc->data;
+        a.dA = f32(dA);
+        a.dD = f32(dD);
+        a.dbias = f32(ddt_bias);
+        a.dh0 = f32(dh0);
+        Carve size{nullptr};
+        SsmTables t;
+        carve_ssm(a, true, size, t);
+        if (workspace || !workspace_bytes) {
+            if ((rc = check_device())) return rc;
+            if ((rc = check_cu(cu_seqlens, a.n_seq, a.total, stream))) return rc;
+        }
+        Workspace ws;
+        void *p;
+        if ((rc = ws.get(size.used, workspace, workspace_bytes, stream, &p))) return rc == 1 ? ok() : rc;
+        Carve parts{static_cast<unsigned char *>(p)};
+        carve_ssm(a, true, parts, t);
+        rc = launch([&] { return run_ssm(a, t, true, stream); }, "state space scan backward kernels");
+        const int rr = ws.release();
+        return rc ? rc : rr;
     });
 }
 

@@ -5,18 +5,23 @@
 //   S_t = a_t S_{t-1} + dt_t b_t x_t^T,   y_t = S_t^T c_t + D x_t
 //
 // b and c are shared by the H / G heads of a group.
-#include "gdr_device.h"
-#include "gdr_mixer.h"
+//
+// Prompts run in chunks of 64 tokens.  With G the running sum of dt A inside
+// a chunk and S the state before it,
+//
+//   y_i = e^G_i S^T c_i + sum_{j <= i} e^(G_i - G_j) dt_j (c_i . b_j) x_j + D x_i
+//   S'  = e^G_end S + sum_j e^(G_end - G_j) dt_j b_j x_j^T
+//
+// are four matrix products.  The state stays in registers over a walk of
+// chunks; long sequences are cut into spans that are walked at once: first
+// each span's own state from zero, then a pass that joins them along the
+// sequence, then the outputs.
+#include <type_traits>
+
+#include "gdr_ssm_device.h"
 
 namespace gdr {
 namespace {
-
-// log(1 + e^v) without overflow; log1p keeps the small values' bits
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
-
-__device__ __forceinline__ float time_step(const SsmArgs &a, float raw, int h) {
-    return softplus(raw + (a.dt_bias ? a.dt_bias[h] : 0.f));
-}
 
 // --- one token ------------------------------------------------------------------
 // HBM bound: the state is read and written once, 8 n p bytes a head.  A block
@@ -38,8 +43,7 @@ __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
     for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4 *>(hp + (i0 + i) * P + j0);
     if (t < N) s_b[t] = load_scalar<BF16>(a.b, seq * a.ldb + g * N + t);
     else if (t < 2 * N) s_c[t - N] = load_scalar<BF16>(a.c, seq * a.ldc + g * N + t - N);
-    const float raw = a.gate_bf16 ? load_scalar<true>(a.dt, seq * a.lddt + h) : load_scalar<false>(a.dt, seq * a.lddt + h);
-    const float dt = time_step(a, raw, h);
+    const float dt = softplus(dt_raw(a, seq, h) + (a.dt_bias ? a.dt_bias[h] : 0.f));
     const float decay = expf(dt * a.A[h]);
     f32x4 x;
 #pragma unroll
@@ -64,6 +68,79 @@ __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
     }
 }
 
+// --- tables ---------------------------------------------------------------------
+constexpr int kTableThreads = 1024;
+
+// One block: prefix sums of every sequence's number of spans (at least one,
+// so that a length-0 sequence has a walk that hands its state on), then the
+// entries, each of which finds its sequence by bisection.
+__global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a, int64_t span, int64_t count,
+                                                                       const int32_t *chunk_first, int32_t *first,
+                                                                       int4 *table) {
+    __shared__ int32_t s_scan[kTableThreads];
+    const int tid = threadIdx.x;
+    auto range = [&](int64_t n, int64_t &b, int64_t &e) {
+        if (a.cu) {
+            b = a.cu[n];
+            e = a.cu[n + 1];
+            b = b < 0 ? 0 : b > a.total ? a.total : b;
+            e = e < b ? b : e > a.total ? a.total : e;
+        } else {
+            b = n * a.seq_len;
+            e = b + a.seq_len;
+        }
+    };
+    int64_t carry = 0;
+    for (int64_t base = 0; base < a.n_seq; base += kTableThreads) {
+        int32_t mine = 0;
+        if (base + tid < a.n_seq) {
+            int64_t b, e;
+            range(base + tid, b, e);
+            mine = static_cast<int32_t>((e - b + span - 1) / span);
+            if (mine < 1) mine = 1;
+        }
+        s_scan[tid] = mine;
+        __syncthreads();
+        for (int m = 1; m < kTableThreads; m *= 2) {
+            const int32_t o = tid >= m ? s_scan[tid - m] : 0;
+            __syncthreads();
+            s_scan[tid] += o;
+            __syncthreads();
+        }
+        if (base + tid < a.n_seq) {
+            const int64_t v = carry + s_scan[tid] - mine;
+            first[base + tid] = static_cast<int32_t>(v < count ? v : count);
+        }
+        carry += s_scan[kTableThreads - 1];
+        __syncthreads();
+    }
+    if (tid == 0) first[a.n_seq] = static_cast<int32_t>(carry < count ? carry : count);
+    __threadfence_block();
+    __syncthreads();
+    const int64_t used = first[a.n_seq];
+    for (int64_t i = tid; i < count; i += kTableThreads) {
+        int4 v = make_int4(0, -1, 0, 0);
+        if (i < used) {
+            int64_t lo = 0, hi = a.n_seq;
+            while (hi - lo > 1) {
+                const int64_t m = (lo + hi) / 2;
+                if (first[m] <= i) lo = m;
+                else hi = m;
+            }
+            int64_t b, e;
+            range(lo, b, e);
+            const int64_t at = (i - first[lo]) * span;
+            const int64_t left = e - b - at;
+            v.x = static_cast<int32_t>(b + at);
+            v.y = static_cast<int32_t>(left < 0 ? 0 : left < span ? left : span);
+            v.z = static_cast<int32_t>((static_cast<uint32_t>(lo) << 2) | (i + 1 == first[lo + 1] ? 2u : 0u) |
+                                       (i == first[lo] ? 1u : 0u));
+            v.w = static_cast<int32_t>(chunk_first ? chunk_first[lo] + at / 64 : i);
+        }
+        table[i] = v;
+    }
+}
+
 template <class F>
 hipError_t by_ssm(const SsmArgs &a, F f) {
     auto type = [&]<int N, int P>() {
@@ -74,6 +151,39 @@ hipError_t by_ssm(const SsmArgs &a, F f) {
 }
 
 }  // namespace
+
+int64_t ssm_span_len(const SsmArgs &a) {
+    // Enough walks to fill the chip several times; not split when no sequence
+    // can be longer than a span.
+    const int64_t longest = a.cu ? a.total : a.seq_len;
+    int64_t len = (a.total * a.heads / 2048 + 63) / 64 * 64;
+    if (len < 64) len = 64;
+    return longest <= len ? 0 : len;
+}
+
+hipError_t launch_ssm_table(const SsmArgs &a, int64_t span_len, int64_t count, const int32_t *chunk_first,
+                            int32_t *first, int4 *table, hipStream_t stream) {
+    hipLaunchKernelGGL(gdr_ssm_table_kernel, dim3(1), dim3(kTableThreads), 0, stream, a, span_len, count, chunk_first, first,
+                       table);
+    return hipGetLastError();
+}
+
+hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream) {
+    return by_ssm(a, [&]<int N, int P, bool BF16>() {
+        typedef std::conditional_t<BF16, BfT, FpT> T;
+        const dim3 block(kSsmThreads);
+        const int64_t walks = (a.span_state ? a.n_spans : a.n_seq) * a.heads;
+        if (walks > 0x7FFFFFFF || a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF) return hipErrorInvalidValue;
+        const dim3 grid(static_cast<uint32_t>(walks));
+        if (a.span_state) {
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, false>), grid, block, 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_join_kernel<N, P, false>), dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024))),
+                               block, 0, stream, a);
+        }
+        hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kOut, false>), grid, block, 0, stream, a);
+        return hipGetLastError();
+    });
+}
 
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream) {
     return by_ssm(a, [&]<int N, int P, bool BF16>() {

@@ -1,0 +1,471 @@
+// Gradients of the state space scan (gdr_ssm.hip), in chunks of 64 tokens.
+// With S the state before a chunk, E the gradient of the state after it, G
+// the running sum of dt A inside it, and for i >= j
+//
+//   L_ij = e^(G_i - G_j),  K_ij = c_i . b_j,  M_ij = dy_i . x_j,  W = L K M:
+//
+//   dx_j = D dy_j + dt_j (sum_i L_ij K_ij dy_i + e^(G_end - G_j) E^T b_j)
+//   db_j = sum_i L_ij M_ij dt_j c_i + dt_j e^(G_end - G_j) E x_j    (over the group's heads)
+//   dc_i = sum_j L_ij M_ij dt_j b_j + e^G_i S dy_i                  (likewise)
+//   v_j  = sum_i W_ij + e^(G_end - G_j) b_j^T E x_j                 (dt's own part)
+//   l_t  = l_{t+1} + sum_{j<t} W_tj dt_j + e^G_t c_t^T S dy_t
+//          - dt_t (sum_{i>t} W_it + e^(G_end - G_t) b_t^T E x_t),   l_{end+1} = <E, S_end>
+//   ddt  = (v + A l) sigmoid(raw),  dA = sum dt l,  dbias = sum ddt,  dD = sum dy . x
+//
+// l is the gradient of dt A.  Its recursion starts anew in every chunk from
+// the inner product of E and the state after the chunk, so its rounding does
+// not grow with the sequence; the diagonal of W is left out of it because it
+// would cancel.  W's sums use fp32 products of exact bf16 inputs, the states
+// enter c^T S dy and b^T E x as exact sums of bf16 parts, so ddt, dA and dbias
+// are fp32-accurate also for bf16 inputs; operands that only reach bf16
+// outputs (L K, L M, E in dx) are rounded once to bf16.
+//
+// S and E of every chunk come from the walks of gdr_ssm_device.h.
+#include <type_traits>
+
+#include "gdr_ssm_device.h"
+
+namespace gdr {
+namespace {
+
+// sum over the 16 lanes of a row of the wave, in every lane
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int m = 1; m < 16; m *= 2) x += __shfl_xor(x, m);
+    return x;
+}
+// sum over the four rows of 16 lanes
+__device__ __forceinline__ float sum_rows(float x) {
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
+    return x;
+}
+__device__ __forceinline__ float sum64(float x) { return sum_rows(sum16(x)); }
+
+// One block per (chunk, group, slice of the group's heads).  Wave w owns the
+// (i, j) tiles w, w + 4, w + 8 of the lower triangle's ten, the rows n of db
+// and dc's tiles NW w .. and the rows p of dx's tiles CT w ...  db and dc are
+// summed over the slice's heads in registers; their L M parts as one matrix,
+// multiplied once.
+template <class T, int N, int P>
+__global__ void __launch_bounds__(kSsmThreads, T::kBf16 && P == 64 ? 2 : 1) gdr_ssm_grad_kernel(SsmArgs a) {
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    constexpr int PT = P / 16, CT = PT / 4, NW = N / 64;
+    typedef Tile<T, N> TileN;
+    typedef Tile<T, P> TileP;
+    constexpr int PN = TileN::kPitch, PP = TileP::kPitch, PS = 64 + T::kPad;
+    constexpr int kXY = 2 * 64 * PP > 64 * PN ? 2 * 64 * PP : 64 * PN;   // x and dy; c before and after the heads
+    constexpr int kE = T::kBf16 ? (N * PP > 64 * PS ? N * PP : 64 * PS) : 64 * PS;
+    __shared__ __attribute__((aligned(16))) E sB[64 * PN], sXY[kXY], sE[kE], sPd[64 * PS];
+    __shared__ __attribute__((aligned(16))) Gates sg[2];
+    __shared__ float s_row[4][64], s_col[4][64], s_s[4][64], s_e[4][64], s_w[64], s_m[64], s_es[4];
+    E *const sX = sXY, *const sY = sXY + 64 * PP, *const sC = sXY;
+
+    const int per_group = a.heads / a.groups;
+    const int64_t item = blockIdx.x;
+    const int slice = static_cast<int>(item % a.slices);
+    const int g = static_cast<int>(item / a.slices % a.groups);
+    const int64_t row = item / a.slices / a.groups;
+    const int h0 = g * per_group + slice * a.slice_heads;
+    const int h1 = h0 + a.slice_heads < (g + 1) * per_group ? h0 + a.slice_heads : (g + 1) * per_group;
+    const int4 entry = a.chunks[row];
+    const int rows = entry.y;
+    const int64_t t0 = entry.x;
+    const int tid = threadIdx.x, wave = tid / 64, l = tid % 64, l16 = l % 16, lq = l / 16;
+    if (rows <= 0) {
+        for (int i = tid; i < 3 * (h1 - h0); i += kSsmThreads) a.head_part[(row * a.heads + h0) * 3 + i] = 0.f;
+        return;
+    }
+    constexpr int es = sizeof(E);
+    auto tile_rsrc = [&](const void *base, int64_t ld, int64_t col, int cols) {
+        return chunk_rsrc(static_cast<const E *>(base) + t0 * ld + col, static_cast<uint32_t>(((rows - 1) * ld + cols) * es));
+    };
+    TileP tx, ty;
+    auto load_xy = [&](int h) {
+        tx.load(tile_rsrc(a.x, a.ldx, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.ldx * es));
+        ty.load(tile_rsrc(a.dy, a.lddy, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.lddy * es));
+    };
+    auto load_raw = [&](int h) { return l < rows ? dt_raw(a, t0 + l, h) : 0.f; };
+    TileN tn;
+    tn.load(tile_rsrc(a.b, a.ldb, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldb * es));
+    tn.store(sB);
+    tn.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+    tn.store(sC);
+    float raw = 0.f;
+    if (wave == 2) {
+        raw = load_raw(h0);
+        chunk_gates(a, raw, l < rows, h0, sg[0]);
+    }
+    load_xy(h0);
+    __syncthreads();
+
+    // this wave's tiles of the lower triangle
+    int ti[3], tj[3];
+    f32x4 K[3], R[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int idx = wave + 4 * k;
+        ti[k] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
+        tj[k] = idx - ti[k] * (ti[k] + 1) / 2;
+        K[k] = R[k] = zero4();
+        if (idx < 10) {
+#pragma unroll
+            for (int q = 0; q < N / 32; ++q)
+                K[k] = T::mma(T::kfrag(sC + (16 * ti[k] + l16) * PN + 32 * q + 4 * lq),
+                              T::kfrag(sB + (16 * tj[k] + l16) * PN + 32 * q + 4 * lq), K[k]);
+        }
+    }
+    // the values of c and b beside this wave's rows n of dc and db
+    f32x4 cd[NW][4], bd[NW][4];
+#pragma unroll
+    for (int k = 0; k < NW; ++k)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            cd[k][it] = T::load4(sC + (16 * it + l16) * PN + 16 * (NW * wave + k) + 4 * lq);
+            bd[k][it] = T::load4(sB + (16 * it + l16) * PN + 16 * (NW * wave + k) + 4 * lq);
+        }
+    // tiles above the diagonal that pairs of tiles reach
+    if (wave % 2 == 1) T::store4(sPd + (16 * wave + l16) * PS + 16 * (wave - 1) + 4 * lq, zero4());
+    f32x4 dc[NW][4], db[NW][4];
+#pragma unroll
+    for (int k = 0; k < NW; ++k)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) dc[k][it] = db[k][it] = zero4();
+    __syncthreads();
+
+    for (int h = h0; h < h1; ++h) {
+        const Gates &s = sg[(h - h0) & 1];
+        const int64_t slot = (row * a.heads + h) * (N * P);
+        const float *Sp = a.chunk_state + slot;
+        const float *Ep = a.chunk_state + a.n_chunks * a.heads * (N * P) + slot;
+        tx.store(sX);
+        ty.store(sY);
+        f32x4 Sv[NW][PT], Ev[NW][PT];
+#pragma unroll
+        for (int k = 0; k < NW; ++k)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) {
+                const int at = (((NW * wave + k) * PT + pt) * 64 + l) * 4;
+                Sv[k][pt] = *reinterpret_cast<const f32x4 *>(Sp + at);
+                Ev[k][pt] = *reinterpret_cast<const f32x4 *>(Ep + at);
+            }
+        __syncthreads();
+        if (h + 1 < h1) {
+            load_xy(h + 1);
+            if (wave == 2) raw = load_raw(h + 1);
+        }
+        // M, W and what they give
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (wave + 4 * k >= 10) continue;
+            f32x4 m = zero4();
+#pragma unroll
+            for (int q = 0; q < P / 32; ++q)
+                m = T::mma(T::kfrag(sY + (16 * ti[k] + l16) * PP + 32 * q + 4 * lq),
+                           T::kfrag(sX + (16 * tj[k] + l16) * PP + 32 * q + 4 * lq), m);
+            const int i0 = 16 * ti[k] + 4 * lq, j = 16 * tj[k] + l16;
+            const f32x4 gi = *reinterpret_cast<const f32x4 *>(&s.ghi[i0]), gil = *reinterpret_cast<const f32x4 *>(&s.glo[i0]);
+            const float gj = s.ghi[j], gjl = s.glo[j], dtj = s.dt[j];
+            f32x4 pd, rs;
+            float col = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool below = i0 + r > j, on = i0 + r == j;
+                const float e = expf((gi[r] - gj) + (gil[r] - gjl));
+                const float lk = below || on ? e * K[k][r] : 0.f;
+                const float lm = below || on ? e * m[r] : 0.f;
+                const float w = lk * m[r];
+                pd[r] = lk;
+                R[k][r] += lm * dtj;
+                rs[r] = below ? w * dtj : 0.f;
+                col += below ? w : 0.f;
+                if (on) {
+                    s_w[j] = w;
+                    s_m[j] = m[r];
+                }
+            }
+            T::store4(sPd + j * PS + i0, pd);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rs[r] = sum16(rs[r]);
+            if (l16 == 0) *reinterpret_cast<f32x4 *>(&s_row[tj[k]][i0]) = rs;
+            col = sum_rows(col);
+            if (lq == 0) s_col[ti[k]][j] = col;
+        }
+        // S dy^T and E x^T for this wave's rows n
+        float es_sum = 0.f;
+        f32x4 acc[NW][4];
+        float dot[4];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const E *rhs = side ? sX : sY;
+#pragma unroll
+            for (int k = 0; k < NW; ++k)
+#pragma unroll
+                for (int it = 0; it < 4; ++it) acc[k][it] = zero4();
+#pragma unroll
+            for (int q = 0; q < P / 32; ++q) {
+                F8 st[NW][T::kParts];
+#pragma unroll
+                for (int k = 0; k < NW; ++k)
+                    T::split(side ? Ev[k][2 * q] : Sv[k][2 * q], side ? Ev[k][2 * q + 1] : Sv[k][2 * q + 1], st[k]);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const F8 f = T::kfrag(rhs + (16 * it + l16) * PP + 32 * q + 4 * lq);
+#pragma unroll
+                    for (int k = 0; k < NW; ++k)
+#pragma unroll
+                        for (int e = T::kParts - 1; e >= 0; --e) acc[k][it] = T::mma(st[k][e], f, acc[k][it]);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const float f = side ? s.w[16 * it + l16] : s.eg[16 * it + l16];
+                dot[it] = 0.f;
+#pragma unroll
+                for (int k = 0; k < NW; ++k) {
+                    const f32x4 o = side ? bd[k][it] : cd[k][it];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) dot[it] += acc[k][it][r] * o[r];
+                    if (side) db[k][it] = db[k][it] + acc[k][it] * f;
+                    else dc[k][it] = dc[k][it] + acc[k][it] * f;
+                }
+                dot[it] = sum_rows(dot[it]);
+                if (lq == 0) (side ? s_e : s_s)[wave][16 * it + l16] = dot[it];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NW; ++k)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) es_sum += Ev[k][pt][r] * Sv[k][pt][r];
+                if constexpr (T::kBf16) T::store4(sE + (16 * (NW * wave + k) + l16) * PP + 16 * pt + 4 * lq, Ev[k][pt]);
+            }
+        es_sum = sum64(es_sum);
+        if (l == 0) s_es[wave] = es_sum;
+        __syncthreads();
+
+        // dx for this wave's rows p
+        {
+            f32x4 X[4][CT], V[4][CT];
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+                for (int i = 0; i < CT; ++i) X[jt][i] = V[jt][i] = zero4();
+#pragma unroll
+            for (int q = 0; q < N / 32; ++q) {
+                F8 e[CT];
+#pragma unroll
+                for (int i = 0; i < CT; ++i) {
+                    const int pt = CT * wave + i;
+                    if constexpr (T::kBf16) {
+                        e[i] = T::tr(sE, PP, 32 * q, 16 * pt, l16, lq);
+                    } else {
+                        // lane p = l16 of E's tile holds p = 4 (lane / 16) + r: gather the four rows n
+                        f32x4 v[2];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                v[b][r] = Ep[(((2 * q + b) * PT + pt) * 64 + 16 * (l16 / 4) + 4 * lq + r) * 4 + l16 % 4];
+                        e[i] = T::round(v[0], v[1]);
+                    }
+                }
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) {
+                    const F8 f = T::kfrag(sB + (16 * jt + l16) * PN + 32 * q + 4 * lq);
+#pragma unroll
+                    for (int i = 0; i < CT; ++i) V[jt][i] = T::mma(e[i], f, V[jt][i]);
+                }
+            }
+            F8 y[2][CT];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < CT; ++i) y[q][i] = T::tr(sY, PP, 32 * q, 16 * (CT * wave + i), l16, lq);
+            const float dh = a.D ? a.D[h] : 0.f;
+            const uint32_t ldx = static_cast<uint32_t>(a.heads * P * es);
+            const __amdgpu_buffer_rsrc_t rx = chunk_rsrc(static_cast<E *>(a.dx) + (t0 * a.heads + h) * P,
+                                                         static_cast<uint32_t>((rows - 1) * ldx + P * es));
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) {
+#pragma unroll
+                for (int q = jt / 2; q < 2; ++q) {
+                    const F8 f = T::kfrag(sPd + (16 * jt + l16) * PS + 32 * q + 4 * lq);
+#pragma unroll
+                    for (int i = 0; i < CT; ++i) X[jt][i] = T::mma(y[q][i], f, X[jt][i]);
+                }
+                const float ew = s.ew[16 * jt + l16], dt = s.dt[16 * jt + l16];
+#pragma unroll
+                for (int i = 0; i < CT; ++i) {
+                    const int p0 = 16 * (CT * wave + i) + 4 * lq;
+                    const f32x4 v = (X[jt][i] + V[jt][i] * ew) * dt + T::load4(sY + (16 * jt + l16) * PP + p0) * dh;
+                    const uint32_t off = (16 * jt + l16) * ldx + p0 * es;
+                    if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(v)), rx, off, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
+                }
+            }
+        }
+        if (wave == 2 && h + 1 < h1) chunk_gates(a, raw, l < rows, h + 1, sg[(h + 1 - h0) & 1]);
+        if (wave == 3) {   // lane = token
+            const int tile = l / 16;
+            float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k <= tile) rw += s_row[k][l];
+                if (k >= tile) cl += s_col[k][l];
+                st += s_s[k][l];
+                et += s_e[k][l];
+            }
+            const float dt = s.dt[l], far = s.ew[l] * et;
+            const float v = cl + s_w[l] + far;
+            float u = rw + s.eg[l] * st - dt * (cl + far);
+            const float z = s.decay * ((s_es[0] + s_es[1]) + (s_es[2] + s_es[3])) + sum64(s.w[l] * et);
+#pragma unroll
+            for (int m = 1; m < 64; m *= 2) {
+                const float o = __shfl_down(u, m);
+                if (l + m < 64) u += o;
+            }
+            const float dl = z + u;
+            const bool valid = l < rows;
+            float draw = 0.f;
+            if (valid) {
+                const float x = dt_raw(a, t0 + l, h) + (a.dt_bias ? a.dt_bias[h] : 0.f);
+                draw = (v + a.A[h] * dl) / (1.f + expf(-x));
+                const int64_t to = (t0 + l) * a.heads + h;
+                if (a.gate_bf16) static_cast<uint16_t *>(a.ddt)[to] = bf16_bits(draw);
+                else static_cast<float *>(a.ddt)[to] = draw;
+            }
+            const float da = sum64(valid ? dt * dl : 0.f), dd = sum64(valid ? s_m[l] : 0.f), dbias = sum64(draw);
+            if (l == 0) {
+                float *to = a.head_part + (row * a.heads + h) * 3;
+                to[0] = da;
+                to[1] = dd;
+                to[2] = dbias;
+            }
+        }
+        __syncthreads();
+    }
+
+    // the heads' L M dt parts: dc += R B, db += R^T C
+    tn.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        if (wave + 4 * k >= 10) continue;
+        T::store4(sPd + (16 * tj[k] + l16) * PS + 16 * ti[k] + 4 * lq, R[k]);
+        for (int r = 0; r < 4; ++r) {
+            const int at = (16 * ti[k] + 4 * lq + r) * PS + 16 * tj[k] + l16;
+            if constexpr (T::kBf16) sE[at] = bf16_bits(R[k][r]);
+            else sE[at] = R[k][r];
+        }
+    }
+    if (wave % 2 == 0) T::store4(sE + (16 * wave + l16) * PS + 16 * (wave + 1) + 4 * lq, zero4());
+    tn.store(sC);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const int n0 = 16 * (NW * wave + k);
+            const F8 bt = T::tr(sB, PN, 32 * q, n0, l16, lq), ct = T::tr(sC, PN, 32 * q, n0, l16, lq);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                if (q <= it / 2) dc[k][it] = T::mma(bt, T::kfrag(sE + (16 * it + l16) * PS + 32 * q + 4 * lq), dc[k][it]);
+                if (q >= it / 2) db[k][it] = T::mma(ct, T::kfrag(sPd + (16 * it + l16) * PS + 32 * q + 4 * lq), db[k][it]);
+            }
+        }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int i = 16 * it + l16;
+        if (i >= rows) continue;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const int64_t to = ((t0 + i) * a.groups + g) * N + 16 * (NW * wave + k) + 4 * lq;
+            if (a.slices > 1) {
+                const int64_t plane = a.total * a.groups * N;
+                *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice) * plane + to) = db[k][it];
+                *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice + 1) * plane + to) = dc[k][it];
+            } else {
+                T::store4(static_cast<E *>(a.db) + to, db[k][it]);
+                T::store4(static_cast<E *>(a.dc) + to, dc[k][it]);
+            }
+        }
+    }
+}
+
+// db and dc from the slices' parts, added in order
+template <class T>
+__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_bc_kernel(SsmArgs a, int64_t plane) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kSsmThreads + threadIdx.x) * 4;
+    if (i >= plane) return;
+    const int side = blockIdx.y;
+    f32x4 s = zero4();
+    for (int k = 0; k < a.slices; ++k) s = s + *reinterpret_cast<const f32x4 *>(a.bc_part + (2 * k + side) * plane + i);
+    T::store4(static_cast<typename T::E *>(side ? a.dc : a.db) + i, s);
+}
+
+// dA, dD and dbias of a head from its chunks
+__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_heads_kernel(SsmArgs a) {
+    __shared__ float sum[3][4];
+    const int h = blockIdx.x;
+    float s[3] = {};
+    for (int64_t r = threadIdx.x; r < a.n_chunks; r += kSsmThreads)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s[k] += a.head_part[(r * a.heads + h) * 3 + k];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        s[k] = sum64(s[k]);
+        if (threadIdx.x % 64 == 0) sum[k][threadIdx.x / 64] = s[k];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float *const to[3] = {a.dA, a.dD, a.dbias};
+        for (int k = 0; k < 3; ++k)
+            if (to[k]) to[k][h] = (sum[k][0] + sum[k][1]) + (sum[k][2] + sum[k][3]);
+    }
+}
+
+}  // namespace
+
+int ssm_slices(const SsmArgs &a) {
+    // one block sums the heads of a slice: enough slices to fill the chip, as
+    // few as that takes, because db and dc pass through HBM once a slice
+    const int64_t per_group = a.heads / a.groups;
+    int64_t s = (1024 + a.n_chunks * a.groups - 1) / (a.n_chunks * a.groups);
+    s = s < 1 ? 1 : s > per_group ? per_group : s;
+    const int64_t heads = (per_group + s - 1) / s;
+    return static_cast<int>((per_group + heads - 1) / heads);
+}
+
+hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
+    const dim3 block(kSsmThreads);
+    auto run = [&]<class T, int N, int P>() {
+        const int64_t walks = a.n_spans * a.heads, grads = a.n_chunks * a.groups * a.slices;
+        if (walks > 0x7FFFFFFF || grads > 0x7FFFFFFF || a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF)
+            return hipErrorInvalidValue;
+        const dim3 grid(static_cast<uint32_t>(walks), 2);
+        if (walks > 0) {
+            if (a.span_state) {
+                hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, true>), grid, block, 0, stream, a);
+                hipLaunchKernelGGL((gdr_ssm_join_kernel<N, P, true>),
+                                   dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024)), 2), block, 0, stream, a);
+            }
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true>), grid, block, 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(static_cast<uint32_t>(grads)), block, 0, stream, a);
+        }
+        const int64_t plane = a.total * a.groups * N;
+        if (a.slices > 1 && plane > 0)
+            hipLaunchKernelGGL((gdr_ssm_bc_kernel<T>), dim3(static_cast<uint32_t>((plane / 4 + kSsmThreads - 1) / kSsmThreads), 2),
+                               block, 0, stream, a, plane);
+        hipLaunchKernelGGL(gdr_ssm_heads_kernel, dim3(a.heads), block, 0, stream, a);
+        return hipGetLastError();
+    };
+    auto dims = [&]<class T>() {
+        if (a.n == 64) return a.p == 64 ? run.template operator()<T, 64, 64>() : run.template operator()<T, 64, 128>();
+        return a.p == 64 ? run.template operator()<T, 128, 64>() : run.template operator()<T, 128, 128>();
+    };
+    return a.bf16 ? dims.template operator()<BfT>() : dims.template operator()<FpT>();
+}
+
+}  // namespace gdr

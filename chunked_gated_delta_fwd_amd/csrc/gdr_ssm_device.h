@@ -1,0 +1,490 @@
+// Device code shared by the state space scan's kernels (gdr_ssm.hip, gdr_ssm_bwd.hip).
+#pragma once
+
+#include "gdr_device.h"
+#include "gdr_mixer.h"
+
+namespace gdr {
+namespace {
+
+// Matrix operands.  A product runs over 32 contraction indices k at a time,
+// as two blocks of 16: lane (l16, lq) supplies row (or column) l16 with
+// k = 4 lq + r of the first block and 16 + 4 lq + r of the second, r = 0..3,
+// the order in which result tiles hold their rows.  bf16 operands take one
+// 16x16x32 instruction, f32 operands eight 16x16x4 ones (fp32 products, no
+// rounding of the inputs).
+struct BfT {
+    typedef uint16_t E;
+    typedef bf16x8 F8;
+    static constexpr bool kBf16 = true;
+    static constexpr int kPad = 8;     // elements added to an LDS row: 16-byte rows, spread over the banks
+    static constexpr int kParts = 3;   // operands that a split fp32 value takes
+    static __device__ __forceinline__ f32x4 mma(F8 a, F8 b, f32x4 c) { return mfma32(a, b, c); }
+    // k contiguous in memory: row pointer + 32 s + 4 lq
+    static __device__ __forceinline__ F8 kfrag(const E *p) { return cat(ld4(p), ld4(p + 16)); }
+    // k along the rows of an LDS array: rows j0 .. j0 + 31, column x0 + l16
+    static __device__ __forceinline__ F8 tr(const E *m, int pitch, int j0, int x0, int l16, int lq) {
+        const E *p = m + (j0 + 4 * lq + l16 / 4) * pitch + x0 + 4 * (l16 % 4);
+        return cat(ld4_tr(p), ld4_tr(p + 16 * pitch));
+    }
+    static __device__ __forceinline__ F8 round(f32x4 a, f32x4 b) { return cat(cvt4(a), cvt4(b)); }
+    static __device__ __forceinline__ f32x4 lo(F8 a) { return up4(__builtin_shufflevector(a, a, 0, 1, 2, 3)); }
+    static __device__ __forceinline__ f32x4 hi(F8 a) { return up4(__builtin_shufflevector(a, a, 4, 5, 6, 7)); }
+    static __device__ __forceinline__ f32x4 load4(const E *p) { return up4(ld4(p)); }
+    static __device__ __forceinline__ void store4(E *p, f32x4 v) { st4(p, cvt4(v)); }
+    // An fp32 value as a sum of three bf16 ones: each takes the top 8 bits of
+    // what is left, so the sum is the value exactly (a bf16 product keeps all
+    // 16 bits of its operands' product in fp32).  This keeps the states, and
+    // everything a gradient sums from them, at fp32 accuracy at three times
+    // the matrix work; one rounded operand would leave 2^-9.
+    static __device__ __forceinline__ void split(f32x4 a, f32x4 b, F8 (&o)[3]) {
+        typedef unsigned int u8v __attribute__((ext_vector_type(4)));
+        u8v w[3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x = e < 2 ? a[2 * e] : b[2 * e - 4], y = e < 2 ? a[2 * e + 1] : b[2 * e - 3];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
+                w[k][e] = __builtin_amdgcn_perm(yb, xb, 0x07060302u);   // top halves of x (low) and y (high)
+                if (k < 2) {
+                    x -= __uint_as_float(xb & 0xFFFF0000u);
+                    y -= __uint_as_float(yb & 0xFFFF0000u);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) o[k] = __builtin_bit_cast(F8, w[k]);
+    }
+};
+
+struct FpT {
+    typedef float E;
+    struct F8 {
+        f32x4 a, b;
+    };
+    static constexpr bool kBf16 = false;
+    static constexpr int kPad = 4;
+    static constexpr int kParts = 1;
+    static __device__ __forceinline__ f32x4 mma(F8 a, F8 b, f32x4 c) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[r], b.a[r], c, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[r], b.b[r], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ f32x4 load4(const E *p) { return *reinterpret_cast<const f32x4 *>(p); }
+    static __device__ __forceinline__ void store4(E *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
+    static __device__ __forceinline__ F8 kfrag(const E *p) { return {load4(p), load4(p + 16)}; }
+    static __device__ __forceinline__ F8 tr(const E *m, int pitch, int j0, int x0, int l16, int lq) {
+        F8 o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            o.a[r] = m[(j0 + 4 * lq + r) * pitch + x0 + l16];
+            o.b[r] = m[(j0 + 16 + 4 * lq + r) * pitch + x0 + l16];
+        }
+        return o;
+    }
+    static __device__ __forceinline__ F8 round(f32x4 a, f32x4 b) { return {a, b}; }
+    static __device__ __forceinline__ f32x4 lo(F8 a) { return a.a; }
+    static __device__ __forceinline__ f32x4 hi(F8 a) { return a.b; }
+    static __device__ __forceinline__ void split(f32x4 a, f32x4 b, F8 (&o)[1]) { o[0] = {a, b}; }
+};
+
+constexpr int kSsmThreads = 256;
+
+// A 64-row tile of COLS columns on its way from HBM to LDS through registers.
+template <class T, int COLS>
+struct Tile {
+    static constexpr int kPitch = COLS + T::kPad;
+    static constexpr int kPiece = 16 / sizeof(typename T::E);       // elements of 16 bytes
+    static constexpr int kPerRow = COLS / kPiece;
+    static constexpr int kN = 64 * kPerRow / kSsmThreads;
+    v4u32 r[kN];
+    // rows `ld` bytes apart; rows past the resource's end read as zeros
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, uint32_t ld) {
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            const int id = threadIdx.x + k * kSsmThreads;
+            r[k] = __builtin_bit_cast(v4u32, buf_load<16>(rsrc, (id / kPerRow) * ld + (id % kPerRow) * 16));
+        }
+    }
+    __device__ __forceinline__ void store(typename T::E *m) const {
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            const int id = threadIdx.x + k * kSsmThreads;
+            *reinterpret_cast<v4u32 *>(m + (id / kPerRow) * kPitch + (id % kPerRow) * kPiece) = r[k];
+        }
+    }
+};
+
+// log(1 + e^v) without overflow; log1p keeps the small values' bits
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+
+__device__ __forceinline__ float dt_raw(const SsmArgs &a, int64_t token, int h) {
+    return a.gate_bf16 ? load_scalar<true>(a.dt, token * a.lddt + h) : load_scalar<false>(a.dt, token * a.lddt + h);
+}
+
+// Per-token scalars of a 64-token chunk, G the running sum of dt A from the
+// chunk's start.  The sum is taken in fp64 and kept as two floats, because
+// e^(G_i - G_j) of near tokens has to be right where both are large.
+struct Gates {
+    float dt[64], ghi[64], glo[64];
+    float eg[64];      // e^G_i: what the chunk's incoming state has decayed to
+    float ew[64];      // e^(G_end - G_j): what token j's write has decayed to at the end
+    float w[64];       // dt_j times that
+    float decay;       // e^G_end
+};
+
+// One wave, lane = token.  Tokens past the end have dt = 0 and write nothing.
+__device__ __forceinline__ void chunk_gates(const SsmArgs &a, float raw, bool valid, int h, Gates &s) {
+    const int l = threadIdx.x % 64;
+    const float dt = valid ? softplus(raw + (a.dt_bias ? a.dt_bias[h] : 0.f)) : 0.f;
+    double g = static_cast<double>(dt) * static_cast<double>(a.A[h]);
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+        const double o = __shfl_up(g, m);
+        if (l >= m) g += o;
+    }
+    const double end = __shfl(g, 63);
+    const float hi = static_cast<float>(g);
+    const float ew = expf(static_cast<float>(end - g));
+    s.dt[l] = dt;
+    s.ghi[l] = hi;
+    s.glo[l] = static_cast<float>(g - hi);
+    s.eg[l] = expf(hi);
+    s.ew[l] = ew;
+    s.w[l] = dt * ew;
+    if (l == 63) s.decay = expf(static_cast<float>(end));
+}
+
+// A span: consecutive whole chunks of one sequence (its last may be ragged),
+// walked by one block per head.  Without a table each sequence is one span.
+struct Span {
+    int64_t t0;      // first token
+    int64_t len;
+    int64_t seq;
+    int64_t row0;    // the sequence's chunk rows start here, plus the span's place in it
+    bool first, last;
+};
+__device__ __forceinline__ Span span_of_block(const SsmArgs &a, int64_t s) {
+    Span r;
+    if (a.spans) {
+        const int4 v = a.spans[s];
+        r.t0 = v.x;
+        r.len = v.y;
+        r.seq = static_cast<uint32_t>(v.z) >> 2;
+        r.first = v.z & 1;
+        r.last = v.z & 2;
+        r.row0 = v.w;
+    } else {
+        r.seq = s;
+        r.first = r.last = true;
+        r.row0 = 0;
+        if (a.cu) {
+            int64_t b = a.cu[s], e = a.cu[s + 1];
+            b = b < 0 ? 0 : b > a.total ? a.total : b;
+            e = e < b ? b : e > a.total ? a.total : e;
+            r.t0 = b;
+            r.len = e - b;
+        } else {
+            r.t0 = s * a.seq_len;
+            r.len = a.seq_len;
+        }
+    }
+    return r;
+}
+
+// Element of a [n][p] state that a lane's register r of tile (nt, pt) holds:
+// OB false: rows n = 4 lq + r, column p = l16; OB true: row n = l16, p = 4 lq + r.
+// Work buffers keep states as tiles, nt * (P / 16) + pt, of 64 lanes x 4 values.
+template <int P, bool OB>
+__device__ __forceinline__ f32x4 load_state_tile(const float *m, int nt, int pt, int l16, int lq) {
+    if constexpr (OB) {
+        return *reinterpret_cast<const f32x4 *>(m + (16 * nt + l16) * P + 16 * pt + 4 * lq);
+    } else {
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = m[(16 * nt + 4 * lq + r) * P + 16 * pt + l16];
+        return v;
+    }
+}
+template <int P, bool OB>
+__device__ __forceinline__ void store_state_tile(float *m, int nt, int pt, int l16, int lq, f32x4 v) {
+    if constexpr (OB) {
+        *reinterpret_cast<f32x4 *>(m + (16 * nt + l16) * P + 16 * pt + 4 * lq) = v;
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[(16 * nt + 4 * lq + r) * P + 16 * pt + l16] = v[r];
+    }
+}
+
+// Walks of the state over the chunks of a span, one block per (span, head):
+//   kLocal   the state that the span's own tokens make from zero, and its decay
+//   kStates  the state before each chunk, stored for the gradients
+//   kOut     the outputs y, and the final state
+// Backward in time (rev; not kOut) the same walk makes the gradient E of the
+// state: E <- e^G_end E + sum_i e^G_i c_i dy_i^T, stored at each chunk's end.
+enum WalkMode { kLocal, kStates, kOut };
+
+template <class T, int N, int P, int MODE, bool OB>
+__global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_kernel(SsmArgs a) {
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    constexpr int NT = N / 16, PT = P / 16, CT = PT / 4;   // a wave owns CT of the column tiles
+    constexpr bool kY = MODE == kOut;
+    typedef Tile<T, N> TileN;
+    typedef Tile<T, P> TileP;
+    constexpr int PN = TileN::kPitch, PP = TileP::kPitch, PS = 64 + T::kPad;
+    __shared__ __attribute__((aligned(16))) E sU[64 * PN], sV[64 * PP], sC[kY ? 64 * PN : 16], sP[kY ? 64 * PS : 16];
+    __shared__ __attribute__((aligned(16))) Gates sg[2];
+
+    const int64_t item = gqa_xcd_item(blockIdx.x, gridDim.x, a.heads, a.groups);
+    const int64_t si = item / a.heads;
+    const int h = static_cast<int>(item - si * a.heads);
+    const int g = h / (a.heads / a.groups);
+    const bool rev = MODE != kOut && blockIdx.y == 1;
+    const Span sp = span_of_block(a, si);
+    if (a.spans && sp.len < 0) return;                              // surplus entry
+    if (MODE == kLocal && (rev ? sp.first : sp.last)) return;       // nothing follows it
+    const int tid = threadIdx.x, wave = tid / 64, l = tid % 64, l16 = l % 16, lq = l / 16;
+    const int64_t hb = (static_cast<int64_t>(rev ? 1 : 0) * a.n_spans + si) * a.heads + h;   // slot in the span buffers
+
+    f32x4 Z[NT][CT];
+    const float *init = rev ? a.dht : a.h0;
+    const bool split = MODE != kLocal && a.span_state;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            const int pt = CT * wave + c;
+            Z[nt][c] = zero4();
+            if (MODE == kLocal) continue;
+            if (split) Z[nt][c] = *reinterpret_cast<const f32x4 *>(a.span_state + hb * (N * P) + ((nt * PT + pt) * 64 + l) * 4);
+            else if (init) Z[nt][c] = load_state_tile<P, OB>(init + (sp.seq * a.heads + h) * (N * P), nt, pt, l16, lq);
+        }
+
+    const int chunks = static_cast<int>((sp.len + 63) / 64);
+    const int64_t ldu = rev ? a.ldc : a.ldb, ldv = rev ? a.lddy : a.ldx;
+    const E *ub = static_cast<const E *>(rev ? a.c : a.b) + g * N;
+    const E *vb = static_cast<const E *>(rev ? a.dy : a.x) + h * P;
+    const E *cb = static_cast<const E *>(a.c) + g * N;
+    TileN tu, tc;
+    TileP tv;
+    float raw = 0.f;   // wave 0: dt of the chunk after the prefetched one
+    auto chunk_at = [&](int k) { return rev ? chunks - 1 - k : k; };
+    auto rows_of = [&](int c) {
+        const int64_t left = sp.len - 64 * static_cast<int64_t>(c);
+        return static_cast<int>(left < 64 ? left : 64);
+    };
+    auto load_tiles = [&](int k) {
+        const int c = chunk_at(k), rows = rows_of(c);
+        const int64_t t = sp.t0 + 64 * static_cast<int64_t>(c);
+        constexpr int es = sizeof(E);
+        const uint32_t u = static_cast<uint32_t>(((rows - 1) * ldu + N) * es), v = static_cast<uint32_t>(((rows - 1) * ldv + P) * es);
+        tu.load(chunk_rsrc(ub + t * ldu, u), static_cast<uint32_t>(ldu * es));
+        tv.load(chunk_rsrc(vb + t * ldv, v), static_cast<uint32_t>(ldv * es));
+        if constexpr (kY) {
+            const uint32_t w = static_cast<uint32_t>(((rows - 1) * a.ldc + N) * es);
+            tc.load(chunk_rsrc(cb + t * a.ldc, w), static_cast<uint32_t>(a.ldc * es));
+        }
+    };
+    auto load_raw = [&](int k) {
+        const int c = chunk_at(k);
+        return l < rows_of(c) ? dt_raw(a, sp.t0 + 64 * static_cast<int64_t>(c) + l, h) : 0.f;
+    };
+    if (chunks > 0) {
+        load_tiles(0);
+        if (wave == 0) {
+            chunk_gates(a, load_raw(0), l < rows_of(chunk_at(0)), h, sg[0]);
+            if (chunks > 1) raw = load_raw(1);
+        }
+    }
+    float total = 0.f;   // kLocal: log of the span's decay
+    for (int k = 0; k < chunks; ++k) {
+        const int c = chunk_at(k), rows = rows_of(c);
+        const int64_t t = sp.t0 + 64 * static_cast<int64_t>(c);
+        const Gates &s = sg[k & 1];
+        if (MODE == kStates && sp.row0 + c < a.n_chunks) {   // always, unless cu_seqlens breaks its preconditions
+            float *to = a.chunk_state + ((static_cast<int64_t>(rev ? 1 : 0) * a.n_chunks + sp.row0 + c) * a.heads + h) * (N * P);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+                    *reinterpret_cast<f32x4 *>(to + ((nt * PT + CT * wave + i) * 64 + l) * 4) = Z[nt][i];
+        }
+        tu.store(sU);
+        tv.store(sV);
+        if constexpr (kY) tc.store(sC);
+        __syncthreads();
+        if (k + 1 < chunks) load_tiles(k + 1);
+
+        f32x4 Y[4][CT];
+        if constexpr (kY) {
+            // scores, transposed: tile (j, i) of B C^T, wave w the rows i of y's tile w
+            F8 ci[N / 32];
+#pragma unroll
+            for (int q = 0; q < N / 32; ++q) ci[q] = T::kfrag(sC + (16 * wave + l16) * PN + 32 * q + 4 * lq);
+            const float gi = s.ghi[16 * wave + l16], gil = s.glo[16 * wave + l16];
+            for (int jt = 0; jt <= wave; ++jt) {
+                f32x4 acc = zero4();
+#pragma unroll
+                for (int q = 0; q < N / 32; ++q) acc = T::mma(T::kfrag(sU + (16 * jt + l16) * PN + 32 * q + 4 * lq), ci[q], acc);
+                const int j0 = 16 * jt + 4 * lq;
+                const f32x4 gj = *reinterpret_cast<const f32x4 *>(&s.ghi[j0]), gl = *reinterpret_cast<const f32x4 *>(&s.glo[j0]);
+                const f32x4 dj = *reinterpret_cast<const f32x4 *>(&s.dt[j0]);
+                f32x4 p;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = (gi - gj[r]) + (gil - gl[r]);
+                    const float v = acc[r] * (T::kBf16 ? __expf(e) : expf(e)) * dj[r];
+                    p[r] = j0 + r <= 16 * wave + l16 ? v : 0.f;
+                }
+                T::store4(sP + (16 * wave + l16) * PS + j0, p);
+            }
+            if (wave % 2 == 0)   // the upper tile of a K32 pair that the products below read
+                T::store4(sP + (16 * wave + l16) * PS + 16 * (wave + 1) + 4 * lq, zero4());
+            // what the incoming state gives: Y^T = S^T C^T
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int i = 0; i < CT; ++i) Y[it][i] = zero4();
+#pragma unroll
+            for (int q = 0; q < N / 32; ++q) {
+                F8 z[CT];
+#pragma unroll
+                for (int i = 0; i < CT; ++i) z[i] = T::round(Z[2 * q][i], Z[2 * q + 1][i]);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const F8 cf = T::kfrag(sC + (16 * it + l16) * PN + 32 * q + 4 * lq);
+#pragma unroll
+                    for (int i = 0; i < CT; ++i) Y[it][i] = T::mma(z[i], cf, Y[it][i]);
+                }
+            }
+        }
+        if (wave == 0 && k + 1 < chunks) {   // the next chunk's gates (wave 0 has the fewest score tiles)
+            chunk_gates(a, raw, l < rows_of(chunk_at(k + 1)), h, sg[(k + 1) & 1]);
+            if (k + 2 < chunks) raw = load_raw(k + 2);
+        }
+        F8 v[2][CT];   // x (or dy) with tokens as k
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < CT; ++i) v[q][i] = T::tr(sV, PP, 32 * q, 16 * (CT * wave + i), l16, lq);
+        if constexpr (kY) {
+            __syncthreads();
+            const float dh = a.D ? a.D[h] : 0.f;
+            const uint32_t ldy = static_cast<uint32_t>(a.heads * P * sizeof(E));
+            E *yb = static_cast<E *>(a.y) + (t * a.heads + h) * P;
+            const __amdgpu_buffer_rsrc_t ry = chunk_rsrc(yb, static_cast<uint32_t>((rows - 1) * ldy + P * sizeof(E)));
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const float eg = s.eg[16 * it + l16];
+#pragma unroll
+                for (int i = 0; i < CT; ++i) Y[it][i] = Y[it][i] * eg;
+#pragma unroll
+                for (int q = 0; q <= it / 2; ++q) {
+                    const F8 pf = T::kfrag(sP + (16 * it + l16) * PS + 32 * q + 4 * lq);
+#pragma unroll
+                    for (int i = 0; i < CT; ++i) Y[it][i] = T::mma(v[q][i], pf, Y[it][i]);
+                }
+#pragma unroll
+                for (int i = 0; i < CT; ++i) {
+                    const int p0 = 16 * (CT * wave + i) + 4 * lq;
+                    const f32x4 y = Y[it][i] + T::load4(sV + (16 * it + l16) * PP + p0) * dh;
+                    const uint32_t off = (16 * it + l16) * ldy + p0 * sizeof(E);
+                    if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(y)), ry, off, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, y), ry, off, 0, 0);
+                }
+            }
+        }
+        // Z <- decay Z + U^T (w V)
+        const float decay = s.decay;
+        if (MODE == kLocal) total += s.ghi[63] + s.glo[63];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < CT; ++i) Z[nt][i] = Z[nt][i] * decay;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float *w = rev ? s.eg : s.w;
+            const f32x4 wa = *reinterpret_cast<const f32x4 *>(w + 32 * q + 4 * lq);
+            const f32x4 wb = *reinterpret_cast<const f32x4 *>(w + 32 * q + 16 + 4 * lq);
+            F8 vs[CT][T::kParts];
+#pragma unroll
+            for (int i = 0; i < CT; ++i) T::split(T::lo(v[q][i]) * wa, T::hi(v[q][i]) * wb, vs[i]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const F8 u = T::tr(sU, PN, 32 * q, 16 * nt, l16, lq);
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+#pragma unroll
+                    for (int e = T::kParts - 1; e >= 0; --e)
+                        Z[nt][i] = OB ? T::mma(vs[i][e], u, Z[nt][i]) : T::mma(u, vs[i][e], Z[nt][i]);
+            }
+        }
+        __syncthreads();
+    }
+
+    float *out = nullptr;
+    if (MODE == kLocal) out = a.span_state + hb * (N * P);
+    else if (MODE == kOut && sp.last && a.ht) out = a.ht + (sp.seq * a.heads + h) * (N * P);
+    else if (MODE == kStates && rev && sp.first && a.dh0) out = a.dh0 + (sp.seq * a.heads + h) * (N * P);
+    if (out) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                const int pt = CT * wave + i;
+                if (MODE == kLocal) *reinterpret_cast<f32x4 *>(out + ((nt * PT + pt) * 64 + l) * 4) = Z[nt][i];
+                else store_state_tile<P, OB>(out, nt, pt, l16, lq, Z[nt][i]);
+            }
+    }
+    if (MODE == kLocal && tid == 0) a.span_decay[hb] = expf(total);
+}
+
+// States at the spans' starts (rev: their gradients at the spans' ends) from
+// the spans' own: s <- decay s + local along each sequence, in place, 4 values
+// a thread.  grid.x: (sequence, head, 1024 values), grid.y: direction.
+template <int N, int P, bool OB>
+__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_join_kernel(SsmArgs a) {
+    constexpr int kParts = N * P / (4 * kSsmThreads);
+    const int64_t item = blockIdx.x / kParts;
+    const int piece = static_cast<int>(blockIdx.x % kParts) * kSsmThreads + threadIdx.x;   // (tile, lane)
+    const int64_t seq = item / a.heads;
+    const int h = static_cast<int>(item % a.heads);
+    const bool rev = blockIdx.y == 1;
+    const int64_t first = a.span_first[seq], count = a.span_first[seq + 1] - first;
+    const int tile = piece / 64, l16 = piece % 16, lq = (piece % 64) / 16;
+    const float *init = rev ? a.dht : a.h0;
+    f32x4 s = zero4();
+    if (init) s = load_state_tile<P, OB>(init + (seq * a.heads + h) * (N * P), tile / (P / 16), tile % (P / 16), l16, lq);
+    const int64_t base = rev ? a.n_spans : 0;
+    constexpr int U = 4;   // spans in flight
+    for (int64_t k0 = 0; k0 < count; k0 += U) {
+        f32x4 v[U];
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u;
+            v[u] = zero4();
+            d[u] = 0.f;
+            if (k + 1 < count) {   // the last one's own state leads nowhere
+                const int64_t slot = (base + first + (rev ? count - 1 - k : k)) * a.heads + h;
+                v[u] = *reinterpret_cast<const f32x4 *>(a.span_state + slot * (N * P) + piece * 4);
+                d[u] = a.span_decay[slot];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u;
+            if (k >= count) break;
+            const int64_t slot = (base + first + (rev ? count - 1 - k : k)) * a.heads + h;
+            *reinterpret_cast<f32x4 *>(a.span_state + slot * (N * P) + piece * 4) = s;
+            s = s * d[u] + v[u];
+        }
+    }
+}
+
+}  // namespace
+}  // namespace gdr

@@ -168,6 +168,47 @@ def qk_norm_rope_bwd(q, k, doq, dok, wq=None, wk=None, cos=None, sin=None, posit
     return dq, dk, dwq, dwk
 
 
+def ssm_scan_fwd(x, dt, A, b, c, D=None, dt_bias=None, cu_seqlens=None, h0=None, output_final_state=True, y=None, ht=None):
+    """Selective state space scan: x ``[B, T, H, p]``, raw dt ``[B, T, H]``, A
+    ``[H]``, b and c ``[B, T, G, n]``, D and dt_bias ``[H]`` or None,
+    ``cu_seqlens`` int32 ``[N+1]`` (B == 1), h0 fp32 ``[N, H, n, p]`` or None.
+    Returns ``(y, ht)``; ht is None unless ``output_final_state``, and a
+    length-0 sequence hands its h0 on."""
+    if y is None:
+        y = x.new_empty(x.shape)
+    if ht is None and output_final_state:
+        ht = x.new_empty((_n_seq(x, cu_seqlens), x.shape[2], b.shape[3], x.shape[3]), dtype=torch.float32)
+    _call_ws(library().gdr_ssm_scan_fwd, (x, dt, A, b, c, D, dt_bias, cu_seqlens, h0, y, ht))
+    return y, ht
+
+
+def ssm_scan_bwd(x, dt, A, b, c, dy, D=None, dt_bias=None, cu_seqlens=None, h0=None, dht=None, want_dh0=True,
+                 dx=None, ddt=None, dA=None, db=None, dc=None, dD=None, ddt_bias=None, dh0=None):
+    """Gradients of ``ssm_scan_fwd`` given dy ``[B, T, H, p]`` and dht (gradient
+    of ht, or None): ``(dx, ddt, dA, db, dc, dD, ddt_bias, dh0)`` in the dtypes
+    of their inputs (dD and ddt_bias None without the input, dh0 None when
+    ``want_dh0`` is False)."""
+    if dx is None:
+        dx = x.new_empty(x.shape)
+    if ddt is None:
+        ddt = dt.new_empty(dt.shape)
+    if dA is None:
+        dA = A.new_empty(A.shape)
+    if db is None:
+        db = b.new_empty(b.shape)
+    if dc is None:
+        dc = c.new_empty(c.shape)
+    if dD is None and D is not None:
+        dD = A.new_empty(A.shape)
+    if ddt_bias is None and dt_bias is not None:
+        ddt_bias = A.new_empty(A.shape)
+    if dh0 is None and want_dh0:
+        dh0 = x.new_empty((_n_seq(x, cu_seqlens), x.shape[2], b.shape[3], x.shape[3]), dtype=torch.float32)
+    _call_ws(library().gdr_ssm_scan_bwd,
+             (x, dt, A, b, c, D, dt_bias, cu_seqlens, h0, dy, dht, dx, ddt, dA, db, dc, dD, ddt_bias, dh0))
+    return dx, ddt, dA, db, dc, dD, ddt_bias, dh0
+
+
 def ssm_step(x, dt, A, b, c, h, D=None, dt_bias=None, y=None):
     """One token of the state space scan per sequence: x ``[B, H, p]``, dt
     ``[B, H]``, A ``[H]``, b and c ``[B, G, n]``, state h fp32 ``[B, H, n, p]``

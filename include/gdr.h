@@ -419,6 +419,59 @@ int gdr_qk_norm_rope_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_ten
                          void *workspace, int64_t *workspace_bytes, hipStream_t stream);
 
 /*
+ * gdr_ssm_scan_fwd - selective state space scan with one decay per head.  Per
+ * sequence and head, with the state S as [n][p]:
+ *
+ *     dt_t = softplus(dt_raw_t + dt_bias)
+ *     S_t = exp(dt_t A) S_{t-1} + dt_t b_t x_t^T,   y_t = S_t^T c_t + D x_t
+ *
+ *   x           [B, T, H, p] rows, bf16 or f32 (one dtype with b, c, y); p 64 or 128
+ *   dt          [B, T, H] rows, bf16 or f32: raw, before softplus
+ *   A           [H] f32 (negative in use; the decay is exp(dt A))
+ *   b, c        [B, T, G, n] rows, n 64 or 128, H % G == 0; head h reads group h / (H/G)
+ *   D, dt_bias  [H] f32, or NULL for zeros
+ *   cu_seqlens  [N+1] int32 or NULL, as gdr_chunk_fwd (preconditions too)
+ *   h0          [N, H, n, p] f32, or NULL for zeros
+ *   y           [B, T, H, p] out; rows of tokens outside every segment are not written
+ *   ht          [N, H, n, p] f32 out, or NULL (a length-0 sequence hands its h0 on)
+ *
+ * x, b, c rows, y, h0 and ht on 16-byte addresses.  Rows at most 32 MiB apart.
+ * bf16 inputs: bf16 matrix operands with fp32 sums for y (rounded once), and a
+ * state of fp32 accuracy (its products take exact bf16 parts).  f32 inputs:
+ * fp32 products throughout.  A non-finite x can reach the y of earlier tokens
+ * of its 64-token chunk.  Workspace: none when no sequence is longer than a
+ * span, else 4 H n p bytes a span and tables; spans have about
+ * T H / 2048 tokens.
+ */
+int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
+                     const gdr_tensor *b, const gdr_tensor *c, const gdr_tensor *D,
+                     const gdr_tensor *dt_bias, const gdr_tensor *cu_seqlens, const gdr_tensor *h0,
+                     const gdr_tensor *y, const gdr_tensor *ht, void *workspace,
+                     int64_t *workspace_bytes, hipStream_t stream);
+
+/*
+ * gdr_ssm_scan_bwd - gradients of gdr_ssm_scan_fwd.
+ *
+ *   dy    [B, T, H, p] rows, dtype of x;  dht [N, H, n, p] f32 or NULL for zeros
+ *   dx    [B, T, H, p] out, dtype of x
+ *   ddt   [B, T, H] out, dtype of dt: gradient of the raw dt
+ *   db, dc  [B, T, G, n] out, dtype of x, summed over each group's heads
+ *   dA    [H] out, f32;  dD, ddt_bias [H] out, f32, each or NULL
+ *   dh0   [N, H, n, p] out, f32, or NULL (written also when h0 is NULL)
+ *
+ * ddt, dA, dD, ddt_bias and dh0 are fp32-accurate for bf16 inputs too.
+ * Workspace: about 8 n p bytes a (64-token chunk, head).
+ */
+int gdr_ssm_scan_bwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
+                     const gdr_tensor *b, const gdr_tensor *c, const gdr_tensor *D,
+                     const gdr_tensor *dt_bias, const gdr_tensor *cu_seqlens, const gdr_tensor *h0,
+                     const gdr_tensor *dy, const gdr_tensor *dht, const gdr_tensor *dx,
+                     const gdr_tensor *ddt, const gdr_tensor *dA, const gdr_tensor *db,
+                     const gdr_tensor *dc, const gdr_tensor *dD, const gdr_tensor *ddt_bias,
+                     const gdr_tensor *dh0, void *workspace, int64_t *workspace_bytes,
+                     hipStream_t stream);
+
+/*
  * gdr_ssm_step - one token of the selective state space scan for each of B
  * sequences.  Per sequence and head, with the state S as [n][p]:
  *

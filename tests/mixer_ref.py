@@ -62,26 +62,35 @@ def norm_rope(x, weight, cos, sin, pos, rms, eps, interleaved):
     return torch.cat([turned, y[..., 2 * half:]], -1)
 
 
-def ssm(x, dt, A, b, c, D, dt_bias, cu, h0):
-    """x [B, T, H, p], dt [B, T, H], b and c [B, T, G, n], all double; returns
-    (y, ht, steps): the literal recurrence, one token at a time."""
+def softplus(raw):
+    return torch.clamp(raw, min=0) + torch.log1p(torch.exp(-raw.abs()))
+
+
+def ssm_walk(x, step, decay, b, c, D, cu, h0):
+    """The literal recurrence, one token at a time, from the steps and decays
+    [B, T, H]: (y, ht)."""
     B, T, H, p = x.shape
     G, n = b.shape[2:]
-    X, DT = x.reshape(-1, H, p), dt.reshape(-1, H)
+    X, st, dec = x.reshape(-1, H, p), step.reshape(-1, H), decay.reshape(-1, H)
     Bh = b.reshape(-1, G, n).repeat_interleave(H // G, 1)
     Ch = c.reshape(-1, G, n).repeat_interleave(H // G, 1)
-    raw = DT if dt_bias is None else DT + dt_bias
-    step = torch.clamp(raw, min=0) + torch.log1p(torch.exp(-raw.abs()))
     ys, hts = [], []
     for i, (s, e) in enumerate(bounds(cu, B, T)):
         S = x.new_zeros(H, n, p) if h0 is None else h0[i]
         for t in range(s, e):
-            S = torch.exp(step[t] * A)[:, None, None] * S + (step[t][:, None] * Bh[t])[:, :, None] * X[t][:, None]
+            S = dec[t][:, None, None] * S + (st[t][:, None] * Bh[t])[:, :, None] * X[t][:, None]
             y = (Ch[t][:, :, None] * S).sum(1)
             ys.append(y if D is None else y + D[:, None] * X[t])
         hts.append(S)
     y = torch.stack(ys) if ys else x.new_zeros(0, H, p)
-    return y.reshape(B, T, H, p), torch.stack(hts), step
+    return y.reshape(B, T, H, p), torch.stack(hts)
+
+
+def ssm(x, dt, A, b, c, D, dt_bias, cu, h0):
+    """x [B, T, H, p], raw dt [B, T, H], b and c [B, T, G, n], all double; returns (y, ht, steps)."""
+    step = softplus(dt if dt_bias is None else dt + dt_bias)
+    y, ht = ssm_walk(x, step, torch.exp(step * A), b, c, D, cu, h0)
+    return y, ht, step
 
 
 def check(what, got, ref, tol):

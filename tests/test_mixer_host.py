@@ -260,3 +260,63 @@ def test_python_choices():
         gdr.short_conv_fwd(x, w)
     with pytest.raises(AttributeError):
         gdr.no_such_operator
+
+
+def scan_descs(T=100, H=4, G=2, n=128, p=64, N=3):
+    A = Alloc()
+    return dict(x=A(GDR_BF16, [1, T, H, p]), dt=A(GDR_F32, [1, T, H]), A=A(GDR_F32, [H]), b=A(GDR_BF16, [1, T, G, n]),
+                c=A(GDR_BF16, [1, T, G, n]), D=A(GDR_F32, [H]), bias=A(GDR_F32, [H]), cu=A(GDR_I32, [N + 1]),
+                h0=A(GDR_F32, [N, H, n, p]), y=A(GDR_BF16, [1, T, H, p]), ht=A(GDR_F32, [N, H, n, p]))
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (lambda d, A: d.update(x=None), EINVAL, "x: descriptor is NULL"),
+    (lambda d, A: d.update(dt=None), EINVAL, "dt: descriptor is NULL"),
+    (lambda d, A: d.update(c=None), EINVAL, "c: descriptor is NULL"),
+    (lambda d, A: d.update(y=None), EINVAL, "y: descriptor is NULL"),
+    (lambda d, A: d.update(x=A(GDR_BF16, [1, 100, 4, 32])), ESHAPE, "p must be"),
+    (lambda d, A: d.update(b=A(GDR_BF16, [1, 100, 2, 256])), ESHAPE, "n must be"),
+    (lambda d, A: d.update(b=A(GDR_BF16, [1, 100, 3, 128]), c=A(GDR_BF16, [1, 100, 3, 128])), ESHAPE, "multiple of G"),
+    (lambda d, A: d.update(b=A(GDR_BF16, [1, 99, 2, 128])), ESHAPE, "b: shape"),
+    (lambda d, A: d.update(dt=A(GDR_F32, [1, 100, 3])), ESHAPE, "dt: shape"),
+    (lambda d, A: d.update(h0=A(GDR_F32, [2, 4, 128, 64])), ESHAPE, "h0: shape"),
+    (lambda d, A: d.update(ht=A(GDR_BF16, [3, 4, 128, 64])), EDTYPE, "ht: dtype"),
+    (lambda d, A: d.update(y=A(GDR_F32, [1, 100, 4, 64])), EDTYPE, "y: dtype"),
+    (lambda d, A: d.update(ht=d["h0"]), EALIAS, "ht overlaps h0"),
+    (lambda d, A: d.update(cu=A(GDR_BF16, [4])), EDTYPE, "cu_seqlens"),
+    (lambda d, A: d.update(x=A(GDR_BF16, [1, 100, 4, 64], [1 << 26, 1 << 25, 64, 1])), ESTRIDE, "bytes apart"),
+    (lambda d, A: d.update(b=A(GDR_BF16, [1, 100, 2, 128], [0, 1001, 128, 1])), ESTRIDE, "16 bytes"),
+    (lambda d, A: None, 0, ""),
+])
+def test_scan_refusals(lib, change, status, text):  # noqa: F811
+    d = scan_descs()
+    change(d, Alloc2())
+    size = ctypes.c_int64(-1)
+    got = call(lib, "ssm_scan_fwd", list(d.values()), None, ctypes.addressof(size))
+    assert got[0] == status and text in got[1], got
+    assert (size.value >= 0) == (status == 0)
+
+
+@pytest.mark.parametrize("change,status,text", [
+    (lambda d, A: d.update(dx=None), EINVAL, "dx: descriptor is NULL"),
+    (lambda d, A: d.update(dA=None), EINVAL, "dA: descriptor is NULL"),
+    (lambda d, A: d.update(ddt=A(GDR_BF16, [1, 100, 4])), EDTYPE, "ddt: dtype"),
+    (lambda d, A: d.update(db=A(GDR_BF16, [1, 100, 4, 128])), ESHAPE, "db: shape"),
+    (lambda d, A: d.update(dht=A(GDR_F32, [3, 4, 64, 128])), ESHAPE, "dht: shape"),
+    (lambda d, A: d.update(dh0=d["dht"]), EALIAS, "dh0 overlaps dht"),
+    (lambda d, A: d.update(db=d["dc"]), EALIAS, "dc overlaps db"),
+    (lambda d, A: None, 0, ""),
+])
+def test_scan_backward_refusals(lib, change, status, text):  # noqa: F811
+    f = scan_descs()
+    A = Alloc2()
+    A.next = 1 << 45
+    d = {k: f[k] for k in ("x", "dt", "A", "b", "c", "D", "bias", "cu", "h0")}
+    d.update(dy=A(GDR_BF16, [1, 100, 4, 64]), dht=A(GDR_F32, [3, 4, 128, 64]), dx=A(GDR_BF16, [1, 100, 4, 64]),
+             ddt=A(GDR_F32, [1, 100, 4]), dA=A(GDR_F32, [4]), db=A(GDR_BF16, [1, 100, 2, 128]), dc=A(GDR_BF16, [1, 100, 2, 128]),
+             dD=A(GDR_F32, [4]), dbias=A(GDR_F32, [4]), dh0=A(GDR_F32, [3, 4, 128, 64]))
+    change(d, Alloc2())
+    size = ctypes.c_int64(-1)
+    got = call(lib, "ssm_scan_bwd", list(d.values()), None, ctypes.addressof(size))
+    assert got[0] == status and text in got[1], got
+    assert (size.value > 0) == (status == 0)
