@@ -60,6 +60,7 @@ int64_t norm_bwd_blocks(const NormArgs &a);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream);
 
 // Selective state space scan.
+constexpr int kTokenPart = 6 * 64 + 4;   // floats of a (chunk, head) in token_part
 struct SsmArgs {
     const void *x, *dt, *b, *c;
     const float *A, *D, *dt_bias;         // [H]; D, dt_bias NULL: zeros
@@ -90,6 +91,7 @@ struct SsmArgs {
     float *dA, *dD, *dbias, *dh0;         // dD, dbias, dh0 NULL: not written
     int32_t slices, slice_heads;          // the heads of a group in slices, one block each
     float *bc_part;                       // [slices][db, dc][total][G][n]; not used with one slice
+    float *token_part;                    // [n_chunks][H][kTokenPart]: per-token sums
     float *head_part;                     // [n_chunks][H]{dA, dD, dbias}
 };
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream);

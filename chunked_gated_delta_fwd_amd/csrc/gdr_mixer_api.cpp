@@ -464,6 +464,7 @@ void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, SsmTables &t) {
         t.chunk_first = c.take<int32_t>(a.n_seq + 1);
         t.chunks = c.take<int4>(a.n_chunks);
         a.chunk_state = c.take<float>(2 * a.n_chunks * H * state);
+        a.token_part = c.take<float>(a.n_chunks * H * gdr::kTokenPart);
         a.head_part = c.take<float>(a.n_chunks * H * 3);
         if (a.n_chunks > 0) {
             a.slices = gdr::ssm_slices(a);

@@ -28,38 +28,27 @@
 namespace gdr {
 namespace {
 
-// sum over the 16 lanes of a row of the wave, in every lane
-__device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-    for (int m = 1; m < 16; m *= 2) x += __shfl_xor(x, m);
-    return x;
-}
-// sum over the four rows of 16 lanes
-__device__ __forceinline__ float sum_rows(float x) {
-    x += __shfl_xor(x, 16);
-    x += __shfl_xor(x, 32);
-    return x;
-}
-__device__ __forceinline__ float sum64(float x) { return sum_rows(sum16(x)); }
+// One block of 8 waves per (chunk, group, slice of the group's heads); a wave
+// owns one or two of the (i, j) tiles of the lower triangle, one tile of rows
+// n of db and dc (of half the tokens when n is 64) and one tile of rows p of
+// dx (likewise).  db and dc are summed over the slice's heads in registers;
+// their L M parts as one matrix, multiplied once.  8 waves, because with 4 the
+// sums and states of a wave take over 256 registers and spill.
+constexpr int kGradThreads = 512;
 
-// One block per (chunk, group, slice of the group's heads).  Wave w owns the
-// (i, j) tiles w, w + 4, w + 8 of the lower triangle's ten, the rows n of db
-// and dc's tiles NW w .. and the rows p of dx's tiles CT w ...  db and dc are
-// summed over the slice's heads in registers; their L M parts as one matrix,
-// multiplied once.
 template <class T, int N, int P>
-__global__ void __launch_bounds__(kSsmThreads, T::kBf16 && P == 64 ? 2 : 1) gdr_ssm_grad_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     typedef typename T::E E;
     typedef typename T::F8 F8;
-    constexpr int PT = P / 16, CT = PT / 4, NW = N / 64;
-    typedef Tile<T, N> TileN;
-    typedef Tile<T, P> TileP;
+    constexpr int NT = N / 16, PT = P / 16, IW = NT / 2, JW = PT / 2;   // i tiles of db, dc and j tiles of dx per wave
+    typedef Tile<T, N, kGradThreads> TileN;
+    typedef Tile<T, P, kGradThreads> TileP;
     constexpr int PN = TileN::kPitch, PP = TileP::kPitch, PS = 64 + T::kPad;
     constexpr int kXY = 2 * 64 * PP > 64 * PN ? 2 * 64 * PP : 64 * PN;   // x and dy; c before and after the heads
     constexpr int kE = T::kBf16 ? (N * PP > 64 * PS ? N * PP : 64 * PS) : 64 * PS;
     __shared__ __attribute__((aligned(16))) E sB[64 * PN], sXY[kXY], sE[kE], sPd[64 * PS];
     __shared__ __attribute__((aligned(16))) Gates sg[2];
-    __shared__ float s_row[4][64], s_col[4][64], s_s[4][64], s_e[4][64], s_w[64], s_m[64], s_es[4];
+    __shared__ __attribute__((aligned(16))) float s_row[4][64], s_col[4][64], s_s[NT][64], s_e[NT][64], s_w[64], s_m[64], s_es[8];
     E *const sX = sXY, *const sY = sXY + 64 * PP, *const sC = sXY;
 
     const int per_group = a.heads / a.groups;
@@ -72,11 +61,12 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 && P == 64 ? 2 : 1) gdr_
     const int4 entry = a.chunks[row];
     const int rows = entry.y;
     const int64_t t0 = entry.x;
-    const int tid = threadIdx.x, wave = tid / 64, l = tid % 64, l16 = l % 16, lq = l / 16;
-    if (rows <= 0) {
-        for (int i = tid; i < 3 * (h1 - h0); i += kSsmThreads) a.head_part[(row * a.heads + h0) * 3 + i] = 0.f;
-        return;
-    }
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64);   // the same in every lane
+    const int l = tid % 64, l16 = l % 16, lq = l / 16;
+    if (rows <= 0) return;   // a length-0 sequence's row, or a surplus one
+    const int nt = wave % NT, it0 = wave / NT * IW;     // db, dc: rows 16 nt .., tokens 16 it0 ..
+    const int pt = wave % PT, jt0 = wave / PT * JW;     // dx: rows 16 pt .., tokens 16 jt0 ..
+    const bool first_n = wave < NT;
     constexpr int es = sizeof(E);
     auto tile_rsrc = [&](const void *base, int64_t ld, int64_t col, int cols) {
         return chunk_rsrc(static_cast<const E *>(base) + t0 * ld + col, static_cast<uint32_t>(((rows - 1) * ld + cols) * es));
@@ -86,26 +76,39 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 && P == 64 ? 2 : 1) gdr_
         tx.load(tile_rsrc(a.x, a.ldx, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.ldx * es));
         ty.load(tile_rsrc(a.dy, a.lddy, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.lddy * es));
     };
+    const float *const Sbase = a.chunk_state, *const Ebase = a.chunk_state + a.n_chunks * a.heads * (N * P);
+    f32x4 Sv[PT], Ev[PT];   // this wave's rows n of S and E
+    auto load_states = [&](int h) {
+        const int64_t at = (row * a.heads + h) * (N * P) + (nt * PT * 64 + l) * 4;
+#pragma unroll
+        for (int k = 0; k < PT; ++k) {
+            Sv[k] = *reinterpret_cast<const f32x4 *>(Sbase + at + k * 256);
+            Ev[k] = *reinterpret_cast<const f32x4 *>(Ebase + at + k * 256);
+        }
+    };
     auto load_raw = [&](int h) { return l < rows ? dt_raw(a, t0 + l, h) : 0.f; };
-    TileN tn;
-    tn.load(tile_rsrc(a.b, a.ldb, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldb * es));
-    tn.store(sB);
-    tn.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
-    tn.store(sC);
+    {
+        TileN tb, tc;
+        tb.load(tile_rsrc(a.b, a.ldb, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldb * es));
+        tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+        tb.store(sB);
+        tc.store(sC);
+    }
     float raw = 0.f;
-    if (wave == 2) {
+    if (wave == 5) {
         raw = load_raw(h0);
         chunk_gates(a, raw, l < rows, h0, sg[0]);
     }
     load_xy(h0);
+    load_states(h0);
     __syncthreads();
 
-    // this wave's tiles of the lower triangle
-    int ti[3], tj[3];
-    f32x4 K[3], R[3];
+    // this wave's tiles of the lower triangle's ten: number wave, and wave + 8
+    int ti[2], tj[2];
+    f32x4 K[2], R[2];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const int idx = wave + 4 * k;
+    for (int k = 0; k < 2; ++k) {
+        const int idx = wave + 8 * k;
         ti[k] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
         tj[k] = idx - ti[k] * (ti[k] + 1) / 2;
         K[k] = R[k] = zero4();
@@ -116,49 +119,30 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 && P == 64 ? 2 : 1) gdr_
                               T::kfrag(sB + (16 * tj[k] + l16) * PN + 32 * q + 4 * lq), K[k]);
         }
     }
-    // the values of c and b beside this wave's rows n of dc and db
-    f32x4 cd[NW][4], bd[NW][4];
+    // the values of c beside this wave's rows n of dc (c leaves LDS for x and dy)
+    typename T::F4 cd[IW];
 #pragma unroll
-    for (int k = 0; k < NW; ++k)
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            cd[k][it] = T::load4(sC + (16 * it + l16) * PN + 16 * (NW * wave + k) + 4 * lq);
-            bd[k][it] = T::load4(sB + (16 * it + l16) * PN + 16 * (NW * wave + k) + 4 * lq);
-        }
+    for (int i = 0; i < IW; ++i) cd[i] = T::raw4(sC + (16 * (it0 + i) + l16) * PN + 16 * nt + 4 * lq);
     // tiles above the diagonal that pairs of tiles reach
-    if (wave % 2 == 1) T::store4(sPd + (16 * wave + l16) * PS + 16 * (wave - 1) + 4 * lq, zero4());
-    f32x4 dc[NW][4], db[NW][4];
+    if (wave == 1 || wave == 3) T::store4(sPd + (16 * wave + l16) * PS + 16 * (wave - 1) + 4 * lq, zero4());
+    f32x4 dc[IW], db[IW];
 #pragma unroll
-    for (int k = 0; k < NW; ++k)
-#pragma unroll
-        for (int it = 0; it < 4; ++it) dc[k][it] = db[k][it] = zero4();
+    for (int i = 0; i < IW; ++i) dc[i] = db[i] = zero4();
     __syncthreads();
 
     for (int h = h0; h < h1; ++h) {
         const Gates &s = sg[(h - h0) & 1];
-        const int64_t slot = (row * a.heads + h) * (N * P);
-        const float *Sp = a.chunk_state + slot;
-        const float *Ep = a.chunk_state + a.n_chunks * a.heads * (N * P) + slot;
         tx.store(sX);
         ty.store(sY);
-        f32x4 Sv[NW][PT], Ev[NW][PT];
-#pragma unroll
-        for (int k = 0; k < NW; ++k)
-#pragma unroll
-            for (int pt = 0; pt < PT; ++pt) {
-                const int at = (((NW * wave + k) * PT + pt) * 64 + l) * 4;
-                Sv[k][pt] = *reinterpret_cast<const f32x4 *>(Sp + at);
-                Ev[k][pt] = *reinterpret_cast<const f32x4 *>(Ep + at);
-            }
         __syncthreads();
         if (h + 1 < h1) {
             load_xy(h + 1);
-            if (wave == 2) raw = load_raw(h + 1);
+            if (wave == 5) raw = load_raw(h + 1);
         }
         // M, W and what they give
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            if (wave + 4 * k >= 10) continue;
+        for (int k = 0; k < 2; ++k) {
+            if (wave + 8 * k >= 10) continue;
             f32x4 m = zero4();
 #pragma unroll
             for (int q = 0; q < P / 32; ++q)
@@ -172,7 +156,7 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 && P == 64 ? 2 : 1) gdr_
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool below = i0 + r > j, on = i0 + r == j;
-                const float e = expf((gi[r] - gj) + (gil[r] - gjl));
+                const float e = __expf((gi[r] - gj) + (gil[r] - gjl));
                 const float lk = below || on ? e * K[k][r] : 0.f;
                 const float lm = below || on ? e * m[r] : 0.f;
                 const float w = lk * m[r];
@@ -193,204 +177,215 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 && P == 64 ? 2 : 1) gdr_
             if (lq == 0) s_col[ti[k]][j] = col;
         }
         // S dy^T and E x^T for this wave's rows n
-        float es_sum = 0.f;
-        f32x4 acc[NW][4];
-        float dot[4];
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            const E *rhs = side ? sX : sY;
+            f32x4 acc[IW];
 #pragma unroll
-            for (int k = 0; k < NW; ++k)
-#pragma unroll
-                for (int it = 0; it < 4; ++it) acc[k][it] = zero4();
+            for (int i = 0; i < IW; ++i) acc[i] = zero4();
 #pragma unroll
             for (int q = 0; q < P / 32; ++q) {
-                F8 st[NW][T::kParts];
+                F8 st[T::kParts];
+                T::split(side ? Ev[2 * q] : Sv[2 * q], side ? Ev[2 * q + 1] : Sv[2 * q + 1], st);
 #pragma unroll
-                for (int k = 0; k < NW; ++k)
-                    T::split(side ? Ev[k][2 * q] : Sv[k][2 * q], side ? Ev[k][2 * q + 1] : Sv[k][2 * q + 1], st[k]);
+                for (int i = 0; i < IW; ++i) {
+                    const F8 f = T::kfrag((side ? sX : sY) + (16 * (it0 + i) + l16) * PP + 32 * q + 4 * lq);
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const F8 f = T::kfrag(rhs + (16 * it + l16) * PP + 32 * q + 4 * lq);
-#pragma unroll
-                    for (int k = 0; k < NW; ++k)
-#pragma unroll
-                        for (int e = T::kParts - 1; e >= 0; --e) acc[k][it] = T::mma(st[k][e], f, acc[k][it]);
+                    for (int e = T::kParts - 1; e >= 0; --e) acc[i] = T::mma(st[e], f, acc[i]);
                 }
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const float f = side ? s.w[16 * it + l16] : s.eg[16 * it + l16];
-                dot[it] = 0.f;
+            for (int i = 0; i < IW; ++i) {
+                const int at = 16 * (it0 + i) + l16;
+                const float f = side ? s.w[at] : s.eg[at];
+                const f32x4 o = side ? T::load4(sB + at * PN + 16 * nt + 4 * lq) : T::up(cd[i]);
+                float d = 0.f;
 #pragma unroll
-                for (int k = 0; k < NW; ++k) {
-                    const f32x4 o = side ? bd[k][it] : cd[k][it];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) dot[it] += acc[k][it][r] * o[r];
-                    if (side) db[k][it] = db[k][it] + acc[k][it] * f;
-                    else dc[k][it] = dc[k][it] + acc[k][it] * f;
-                }
-                dot[it] = sum_rows(dot[it]);
-                if (lq == 0) (side ? s_e : s_s)[wave][16 * it + l16] = dot[it];
+                for (int r = 0; r < 4; ++r) d += acc[i][r] * o[r];
+                if (side) db[i] = db[i] + acc[i] * f;
+                else dc[i] = dc[i] + acc[i] * f;
+                d = sum_rows(d);
+                if (lq == 0) (side ? s_e : s_s)[nt][at] = d;
             }
         }
+        if (first_n) {
+            float es_sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < NW; ++k)
+            for (int k = 0; k < PT; ++k) {
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) es_sum += Ev[k][pt][r] * Sv[k][pt][r];
-                if constexpr (T::kBf16) T::store4(sE + (16 * (NW * wave + k) + l16) * PP + 16 * pt + 4 * lq, Ev[k][pt]);
+                for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
+                if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PP + 16 * k + 4 * lq, Ev[k]);
             }
-        es_sum = sum64(es_sum);
-        if (l == 0) s_es[wave] = es_sum;
+            es_sum = sum64(es_sum);
+            if (l == 0) s_es[wave] = es_sum;
+        }
         __syncthreads();
+        if (h + 1 < h1) load_states(h + 1);
 
         // dx for this wave's rows p
         {
-            f32x4 X[4][CT], V[4][CT];
+            f32x4 X[JW], V[JW];
 #pragma unroll
-            for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-                for (int i = 0; i < CT; ++i) X[jt][i] = V[jt][i] = zero4();
+            for (int j = 0; j < JW; ++j) X[j] = V[j] = zero4();
+            const float *Ep = Ebase + (row * a.heads + h) * (N * P);
 #pragma unroll
             for (int q = 0; q < N / 32; ++q) {
-                F8 e[CT];
+                F8 e;
+                if constexpr (T::kBf16) {
+                    e = T::tr(sE, PP, 32 * q, 16 * pt, l16, lq);
+                } else {
+                    // lane p = l16 of E's tile holds p = 4 (lane / 16) + r: gather the four rows n
+                    f32x4 v[2];
 #pragma unroll
-                for (int i = 0; i < CT; ++i) {
-                    const int pt = CT * wave + i;
-                    if constexpr (T::kBf16) {
-                        e[i] = T::tr(sE, PP, 32 * q, 16 * pt, l16, lq);
-                    } else {
-                        // lane p = l16 of E's tile holds p = 4 (lane / 16) + r: gather the four rows n
-                        f32x4 v[2];
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                v[b][r] = Ep[(((2 * q + b) * PT + pt) * 64 + 16 * (l16 / 4) + 4 * lq + r) * 4 + l16 % 4];
-                        e[i] = T::round(v[0], v[1]);
-                    }
+                        for (int r = 0; r < 4; ++r)
+                            v[b][r] = Ep[(((2 * q + b) * PT + pt) * 64 + 16 * (l16 / 4) + 4 * lq + r) * 4 + l16 % 4];
+                    e = T::round(v[0], v[1]);
                 }
 #pragma unroll
-                for (int jt = 0; jt < 4; ++jt) {
-                    const F8 f = T::kfrag(sB + (16 * jt + l16) * PN + 32 * q + 4 * lq);
-#pragma unroll
-                    for (int i = 0; i < CT; ++i) V[jt][i] = T::mma(e[i], f, V[jt][i]);
-                }
+                for (int j = 0; j < JW; ++j)
+                    V[j] = T::mma(e, T::kfrag(sB + (16 * (jt0 + j) + l16) * PN + 32 * q + 4 * lq), V[j]);
             }
-            F8 y[2][CT];
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int i = 0; i < CT; ++i) y[q][i] = T::tr(sY, PP, 32 * q, 16 * (CT * wave + i), l16, lq);
             const float dh = a.D ? a.D[h] : 0.f;
             const uint32_t ldx = static_cast<uint32_t>(a.heads * P * es);
             const __amdgpu_buffer_rsrc_t rx = chunk_rsrc(static_cast<E *>(a.dx) + (t0 * a.heads + h) * P,
                                                          static_cast<uint32_t>((rows - 1) * ldx + P * es));
 #pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
+            for (int q = 0; q < 2; ++q) {
+                const F8 y = T::tr(sY, PP, 32 * q, 16 * pt, l16, lq);
 #pragma unroll
-                for (int q = jt / 2; q < 2; ++q) {
-                    const F8 f = T::kfrag(sPd + (16 * jt + l16) * PS + 32 * q + 4 * lq);
+                for (int j = 0; j < JW; ++j)
+                    if (q >= (jt0 + j) / 2) X[j] = T::mma(y, T::kfrag(sPd + (16 * (jt0 + j) + l16) * PS + 32 * q + 4 * lq), X[j]);
+            }
 #pragma unroll
-                    for (int i = 0; i < CT; ++i) X[jt][i] = T::mma(y[q][i], f, X[jt][i]);
-                }
-                const float ew = s.ew[16 * jt + l16], dt = s.dt[16 * jt + l16];
-#pragma unroll
-                for (int i = 0; i < CT; ++i) {
-                    const int p0 = 16 * (CT * wave + i) + 4 * lq;
-                    const f32x4 v = (X[jt][i] + V[jt][i] * ew) * dt + T::load4(sY + (16 * jt + l16) * PP + p0) * dh;
-                    const uint32_t off = (16 * jt + l16) * ldx + p0 * es;
-                    if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(v)), rx, off, 0, 0);
-                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
-                }
+            for (int j = 0; j < JW; ++j) {
+                const int at = 16 * (jt0 + j) + l16, p0 = 16 * pt + 4 * lq;
+                const f32x4 v = (X[j] + V[j] * s.ew[at]) * s.dt[at] + T::load4(sY + at * PP + p0) * dh;
+                const uint32_t off = at * ldx + p0 * es;
+                if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(v)), rx, off, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
             }
         }
-        if (wave == 2 && h + 1 < h1) chunk_gates(a, raw, l < rows, h + 1, sg[(h + 1 - h0) & 1]);
-        if (wave == 3) {   // lane = token
+        if (wave == 5 && h + 1 < h1) chunk_gates(a, raw, l < rows, h + 1, sg[(h + 1 - h0) & 1]);
+        if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_dt_kernel
             const int tile = l / 16;
-            float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f;
+            float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f, es_sum = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (k <= tile) rw += s_row[k][l];
                 if (k >= tile) cl += s_col[k][l];
+            }
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
                 st += s_s[k][l];
                 et += s_e[k][l];
+                es_sum += s_es[k];
             }
-            const float dt = s.dt[l], far = s.ew[l] * et;
-            const float v = cl + s_w[l] + far;
-            float u = rw + s.eg[l] * st - dt * (cl + far);
-            const float z = s.decay * ((s_es[0] + s_es[1]) + (s_es[2] + s_es[3])) + sum64(s.w[l] * et);
-#pragma unroll
-            for (int m = 1; m < 64; m *= 2) {
-                const float o = __shfl_down(u, m);
-                if (l + m < 64) u += o;
-            }
-            const float dl = z + u;
-            const bool valid = l < rows;
-            float draw = 0.f;
-            if (valid) {
-                const float x = dt_raw(a, t0 + l, h) + (a.dt_bias ? a.dt_bias[h] : 0.f);
-                draw = (v + a.A[h] * dl) / (1.f + expf(-x));
-                const int64_t to = (t0 + l) * a.heads + h;
-                if (a.gate_bf16) static_cast<uint16_t *>(a.ddt)[to] = bf16_bits(draw);
-                else static_cast<float *>(a.ddt)[to] = draw;
-            }
-            const float da = sum64(valid ? dt * dl : 0.f), dd = sum64(valid ? s_m[l] : 0.f), dbias = sum64(draw);
-            if (l == 0) {
-                float *to = a.head_part + (row * a.heads + h) * 3;
-                to[0] = da;
-                to[1] = dd;
-                to[2] = dbias;
-            }
+            float *to = a.token_part + (row * a.heads + h) * kTokenPart + l;
+            to[0] = rw;
+            to[64] = cl;
+            to[128] = s_w[l];
+            to[192] = s_m[l];
+            to[256] = st;
+            to[320] = et;
+            if (l == 0) to[384] = es_sum;
         }
         __syncthreads();
     }
 
     // the heads' L M dt parts: dc += R B, db += R^T C
-    tn.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+    {
+        TileN tc;
+        tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        if (wave + 4 * k >= 10) continue;
-        T::store4(sPd + (16 * tj[k] + l16) * PS + 16 * ti[k] + 4 * lq, R[k]);
-        for (int r = 0; r < 4; ++r) {
-            const int at = (16 * ti[k] + 4 * lq + r) * PS + 16 * tj[k] + l16;
-            if constexpr (T::kBf16) sE[at] = bf16_bits(R[k][r]);
-            else sE[at] = R[k][r];
+        for (int k = 0; k < 2; ++k) {
+            if (wave + 8 * k >= 10) continue;
+            T::store4(sPd + (16 * tj[k] + l16) * PS + 16 * ti[k] + 4 * lq, R[k]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int at = (16 * ti[k] + 4 * lq + r) * PS + 16 * tj[k] + l16;
+                if constexpr (T::kBf16) sE[at] = bf16_bits(R[k][r]);
+                else sE[at] = R[k][r];
+            }
         }
+        if (wave == 0 || wave == 2) T::store4(sE + (16 * wave + l16) * PS + 16 * (wave + 1) + 4 * lq, zero4());
+        tc.store(sC);
     }
-    if (wave % 2 == 0) T::store4(sE + (16 * wave + l16) * PS + 16 * (wave + 1) + 4 * lq, zero4());
-    tn.store(sC);
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 2; ++q) {
+        const F8 bt = T::tr(sB, PN, 32 * q, 16 * nt, l16, lq), ct = T::tr(sC, PN, 32 * q, 16 * nt, l16, lq);
 #pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            const int n0 = 16 * (NW * wave + k);
-            const F8 bt = T::tr(sB, PN, 32 * q, n0, l16, lq), ct = T::tr(sC, PN, 32 * q, n0, l16, lq);
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                if (q <= it / 2) dc[k][it] = T::mma(bt, T::kfrag(sE + (16 * it + l16) * PS + 32 * q + 4 * lq), dc[k][it]);
-                if (q >= it / 2) db[k][it] = T::mma(ct, T::kfrag(sPd + (16 * it + l16) * PS + 32 * q + 4 * lq), db[k][it]);
-            }
+        for (int i = 0; i < IW; ++i) {
+            const int it = it0 + i;
+            if (q <= it / 2) dc[i] = T::mma(bt, T::kfrag(sE + (16 * it + l16) * PS + 32 * q + 4 * lq), dc[i]);
+            if (q >= it / 2) db[i] = T::mma(ct, T::kfrag(sPd + (16 * it + l16) * PS + 32 * q + 4 * lq), db[i]);
         }
+    }
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int i = 16 * it + l16;
-        if (i >= rows) continue;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            const int64_t to = ((t0 + i) * a.groups + g) * N + 16 * (NW * wave + k) + 4 * lq;
-            if (a.slices > 1) {
-                const int64_t plane = a.total * a.groups * N;
-                *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice) * plane + to) = db[k][it];
-                *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice + 1) * plane + to) = dc[k][it];
-            } else {
-                T::store4(static_cast<E *>(a.db) + to, db[k][it]);
-                T::store4(static_cast<E *>(a.dc) + to, dc[k][it]);
-            }
+    for (int i = 0; i < IW; ++i) {
+        const int t = 16 * (it0 + i) + l16;
+        if (t >= rows) continue;
+        const int64_t to = ((t0 + t) * a.groups + g) * N + 16 * nt + 4 * lq;
+        if (a.slices > 1) {
+            const int64_t plane = a.total * a.groups * N;
+            *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice) * plane + to) = db[i];
+            *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice + 1) * plane + to) = dc[i];
+        } else {
+            T::store4(static_cast<E *>(a.db) + to, db[i]);
+            T::store4(static_cast<E *>(a.dc) + to, dc[i]);
         }
+    }
+}
+
+// The gradient of dt, and each chunk's part of dA, dD and dbias, from the
+// token sums of gdr_ssm_grad_kernel: a wave per (chunk, head), lane = token.
+__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
+    __shared__ Gates sg[kSsmThreads / 64];
+    const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kSsmThreads / 64) + wave;
+    if (item >= a.n_chunks * a.heads) return;
+    const int64_t row = item / a.heads;
+    const int h = static_cast<int>(item - row * a.heads);
+    const int4 entry = a.chunks[row];
+    const int rows = entry.y;
+    float *const part = a.head_part + item * 3;
+    if (rows <= 0) {
+        if (l < 3) part[l] = 0.f;
+        return;
+    }
+    const int64_t t0 = entry.x;
+    const bool valid = l < rows;
+    const float raw = valid ? dt_raw(a, t0 + l, h) : 0.f;
+    const float *in = a.token_part + item * kTokenPart;
+    const float rw = in[l], cl = in[64 + l], diag = in[128 + l], m = in[192 + l], st = in[256 + l], et = in[320 + l];
+    const float es_sum = in[384];
+    Gates &s = sg[wave];
+    chunk_gates(a, raw, valid, h, s);
+    lds_wait();
+    const float dt = s.dt[l], far = s.ew[l] * et;
+    const float v = cl + diag + far;
+    float u = rw + s.eg[l] * st - dt * (cl + far);
+    const float z = s.decay * es_sum + sum64(s.w[l] * et);
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) {
+        const float o = __shfl_down(u, k);
+        if (l + k < 64) u += o;
+    }
+    const float dl = z + u;
+    float draw = 0.f;
+    if (valid) {
+        const float x = raw + (a.dt_bias ? a.dt_bias[h] : 0.f);
+        draw = (v + a.A[h] * dl) / (1.f + expf(-x));
+        const int64_t to = (t0 + l) * a.heads + h;
+        if (a.gate_bf16) static_cast<uint16_t *>(a.ddt)[to] = bf16_bits(draw);
+        else static_cast<float *>(a.ddt)[to] = draw;
+    }
+    const float da = sum64(valid ? dt * dl : 0.f), dd = sum64(valid ? m : 0.f), dbias = sum64(draw);
+    if (l == 0) {
+        part[0] = da;
+        part[1] = dd;
+        part[2] = dbias;
     }
 }
 
@@ -452,8 +447,10 @@ hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
                                    dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024)), 2), block, 0, stream, a);
             }
             hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true>), grid, block, 0, stream, a);
-            hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(static_cast<uint32_t>(grads)), block, 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(static_cast<uint32_t>(grads)), dim3(kGradThreads), 0, stream, a);
         }
+        if (walks > 0)
+            hipLaunchKernelGGL(gdr_ssm_dt_kernel, dim3(static_cast<uint32_t>((a.n_chunks * a.heads + 3) / 4)), block, 0, stream, a);
         const int64_t plane = a.total * a.groups * N;
         if (a.slices > 1 && plane > 0)
             hipLaunchKernelGGL((gdr_ssm_bc_kernel<T>), dim3(static_cast<uint32_t>((plane / 4 + kSsmThreads - 1) / kSsmThreads), 2),

@@ -16,6 +16,9 @@ namespace {
 struct BfT {
     typedef uint16_t E;
     typedef bf16x8 F8;
+    typedef bf16x4 F4;
+    static __device__ __forceinline__ F4 raw4(const E *p) { return ld4(p); }
+    static __device__ __forceinline__ f32x4 up(F4 a) { return up4(a); }
     static constexpr bool kBf16 = true;
     static constexpr int kPad = 8;     // elements added to an LDS row: 16-byte rows, spread over the banks
     static constexpr int kParts = 3;   // operands that a split fp32 value takes
@@ -63,6 +66,9 @@ struct FpT {
     struct F8 {
         f32x4 a, b;
     };
+    typedef f32x4 F4;
+    static __device__ __forceinline__ F4 raw4(const E *p) { return *reinterpret_cast<const f32x4 *>(p); }
+    static __device__ __forceinline__ f32x4 up(F4 a) { return a; }
     static constexpr bool kBf16 = false;
     static constexpr int kPad = 4;
     static constexpr int kParts = 1;
@@ -94,25 +100,25 @@ struct FpT {
 constexpr int kSsmThreads = 256;
 
 // A 64-row tile of COLS columns on its way from HBM to LDS through registers.
-template <class T, int COLS>
+template <class T, int COLS, int THREADS = kSsmThreads>
 struct Tile {
     static constexpr int kPitch = COLS + T::kPad;
     static constexpr int kPiece = 16 / sizeof(typename T::E);       // elements of 16 bytes
     static constexpr int kPerRow = COLS / kPiece;
-    static constexpr int kN = 64 * kPerRow / kSsmThreads;
+    static constexpr int kN = 64 * kPerRow / THREADS;
     v4u32 r[kN];
     // rows `ld` bytes apart; rows past the resource's end read as zeros
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, uint32_t ld) {
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-            const int id = threadIdx.x + k * kSsmThreads;
+            const int id = threadIdx.x + k * THREADS;
             r[k] = __builtin_bit_cast(v4u32, buf_load<16>(rsrc, (id / kPerRow) * ld + (id % kPerRow) * 16));
         }
     }
     __device__ __forceinline__ void store(typename T::E *m) const {
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-            const int id = threadIdx.x + k * kSsmThreads;
+            const int id = threadIdx.x + k * THREADS;
             *reinterpret_cast<v4u32 *>(m + (id / kPerRow) * kPitch + (id % kPerRow) * kPiece) = r[k];
         }
     }
@@ -136,26 +142,55 @@ struct Gates {
     float decay;       // e^G_end
 };
 
+// x plus the value that DPP control CTRL moves in (0 where none is), in fp64
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_add64(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, static_cast<uint32_t>(b), CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, static_cast<uint32_t>(b >> 32), CTRL, ROW_MASK, 0xF, false);
+    return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Lane sums without LDS: within the 16 lanes of a row (neighbours, pairs, and
+// two mirrors), and over the four rows (lane swaps).  Every lane gets the sum.
+__device__ __forceinline__ float sum16(float x) {
+    x = dpp_add<0xB1, 0xF>(x);    // quad_perm 1 0 3 2
+    x = dpp_add<0x4E, 0xF>(x);    // quad_perm 2 3 0 1
+    x = dpp_add<0x141, 0xF>(x);   // mirror within 8
+    return dpp_add<0x140, 0xF>(x);   // mirror within 16
+}
+__device__ __forceinline__ float sum_rows(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ float sum64(float x) { return sum_rows(sum16(x)); }
+
 // One wave, lane = token.  Tokens past the end have dt = 0 and write nothing.
 __device__ __forceinline__ void chunk_gates(const SsmArgs &a, float raw, bool valid, int h, Gates &s) {
     const int l = threadIdx.x % 64;
     const float dt = valid ? softplus(raw + (a.dt_bias ? a.dt_bias[h] : 0.f)) : 0.f;
     double g = static_cast<double>(dt) * static_cast<double>(a.A[h]);
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        const double o = __shfl_up(g, m);
-        if (l >= m) g += o;
-    }
-    const double end = __shfl(g, 63);
+    g = dpp_add64<0x111, 0xF>(g);   // inclusive scan, as wave_inclusive_scan
+    g = dpp_add64<0x112, 0xF>(g);
+    g = dpp_add64<0x114, 0xF>(g);
+    g = dpp_add64<0x118, 0xF>(g);
+    g = dpp_add64<0x142, 0xA>(g);
+    g = dpp_add64<0x143, 0xC>(g);
+    const uint64_t b = __builtin_bit_cast(uint64_t, g);
+    const uint64_t end_lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(b), 63));
+    const uint64_t end_hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), 63));
+    const double end = __builtin_bit_cast(double, end_hi << 32 | end_lo);
     const float hi = static_cast<float>(g);
-    const float ew = expf(static_cast<float>(end - g));
+    const float ew = __expf(static_cast<float>(end - g));
     s.dt[l] = dt;
     s.ghi[l] = hi;
     s.glo[l] = static_cast<float>(g - hi);
-    s.eg[l] = expf(hi);
+    s.eg[l] = __expf(hi);
     s.ew[l] = ew;
     s.w[l] = dt * ew;
-    if (l == 63) s.decay = expf(static_cast<float>(end));
+    if (l == 63) s.decay = __expf(static_cast<float>(end));
 }
 
 // A span: consecutive whole chunks of one sequence (its last may be ragged),
@@ -247,7 +282,8 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_ke
     const Span sp = span_of_block(a, si);
     if (a.spans && sp.len < 0) return;                              // surplus entry
     if (MODE == kLocal && (rev ? sp.first : sp.last)) return;       // nothing follows it
-    const int tid = threadIdx.x, wave = tid / 64, l = tid % 64, l16 = l % 16, lq = l / 16;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64);   // the same in every lane
+    const int l = tid % 64, l16 = l % 16, lq = l / 16;
     const int64_t hb = (static_cast<int64_t>(rev ? 1 : 0) * a.n_spans + si) * a.heads + h;   // slot in the span buffers
 
     f32x4 Z[NT][CT];
@@ -337,7 +373,7 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_ke
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float e = (gi - gj[r]) + (gil - gl[r]);
-                    const float v = acc[r] * (T::kBf16 ? __expf(e) : expf(e)) * dj[r];
+                    const float v = acc[r] * __expf(e) * dj[r];
                     p[r] = j0 + r <= 16 * wave + l16 ? v : 0.f;
                 }
                 T::store4(sP + (16 * wave + l16) * PS + j0, p);
