@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
     for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4 *>(hp + (i0 + i) * P + j0);
     if (t < N) s_b[t] = load_scalar<BF16>(a.b, seq * a.ldb + g * N + t);
     else if (t < 2 * N) s_c[t - N] = load_scalar<BF16>(a.c, seq * a.ldc + g * N + t - N);
-    const float dt = softplus(dt_raw(a, seq, h) + (a.dt_bias ? a.dt_bias[h] : 0.f));
+    const float dt = softplus(dt_raw(a, seq, h) + head_bias(a, h));
     const float decay = expf(dt * a.A[h]);
     f32x4 x;
 #pragma unroll
@@ -176,11 +176,11 @@ hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream) {
         if (walks > 0x7FFFFFFF || a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF) return hipErrorInvalidValue;
         const dim3 grid(static_cast<uint32_t>(walks));
         if (a.span_state) {
-            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, false>), grid, block, 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, false>), grid, dim3(walk_threads(kLocal, P)), 0, stream, a);
             hipLaunchKernelGGL((gdr_ssm_join_kernel<N, P, false>), dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024))),
                                block, 0, stream, a);
         }
-        hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kOut, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kOut, false>), grid, dim3(walk_threads(kOut, P)), 0, stream, a);
         return hipGetLastError();
     });
 }

@@ -41,11 +41,11 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     typedef typename T::E E;
     typedef typename T::F8 F8;
     constexpr int NT = N / 16, PT = P / 16, IW = NT / 2, JW = PT / 2;   // i tiles of db, dc and j tiles of dx per wave
-    typedef Tile<T, N, kGradThreads> TileN;
-    typedef Tile<T, P, kGradThreads> TileP;
-    constexpr int PN = TileN::kPitch, PP = TileP::kPitch, PS = 64 + T::kPad;
+    typedef Tile<T, N, true, kGradThreads> TileN;
+    typedef Tile<T, P, true, kGradThreads> TileP;
+    constexpr int PN = TileN::kPitch, PP = TileP::kPitch, PS = T::pitch(64, true), PE = T::pitch(P, false);
     constexpr int kXY = 2 * 64 * PP > 64 * PN ? 2 * 64 * PP : 64 * PN;   // x and dy; c before and after the heads
-    constexpr int kE = T::kBf16 ? (N * PP > 64 * PS ? N * PP : 64 * PS) : 64 * PS;
+    constexpr int kE = T::kBf16 ? (N * PE > 64 * PS ? N * PE : 64 * PS) : 64 * PS;
     __shared__ __attribute__((aligned(16))) E sB[64 * PN], sXY[kXY], sE[kE], sPd[64 * PS];
     __shared__ __attribute__((aligned(16))) Gates sg[2];
     __shared__ __attribute__((aligned(16))) float s_row[4][64], s_col[4][64], s_s[NT][64], s_e[NT][64], s_w[64], s_m[64], s_es[8];
@@ -86,7 +86,13 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             Ev[k] = *reinterpret_cast<const f32x4 *>(Ebase + at + k * 256);
         }
     };
-    auto load_raw = [&](int h) { return l < rows ? dt_raw(a, t0 + l, h) : 0.f; };
+    RawDt raw;   // wave 5: what the next head's gates are made from
+    float bias = 0.f, A = 0.f;
+    auto load_gate = [&](int h) {
+        if (l < rows) raw.load(a, t0 + l, h);
+        bias = head_bias(a, h);
+        A = a.A[h];
+    };
     {
         TileN tb, tc;
         tb.load(tile_rsrc(a.b, a.ldb, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldb * es));
@@ -94,10 +100,9 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
         tb.store(sB);
         tc.store(sC);
     }
-    float raw = 0.f;
     if (wave == 5) {
-        raw = load_raw(h0);
-        chunk_gates(a, raw, l < rows, h0, sg[0]);
+        load_gate(h0);
+        chunk_gates(raw.value(a), bias, A, l < rows, sg[0]);
     }
     load_xy(h0);
     load_states(h0);
@@ -115,16 +120,16 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
         if (idx < 10) {
 #pragma unroll
             for (int q = 0; q < N / 32; ++q)
-                K[k] = T::mma(T::kfrag(sC + (16 * ti[k] + l16) * PN + 32 * q + 4 * lq),
-                              T::kfrag(sB + (16 * tj[k] + l16) * PN + 32 * q + 4 * lq), K[k]);
+                K[k] = T::mma(T::template kfrag<true>(sC + (16 * ti[k] + l16) * PN, q, lq),
+                              T::template kfrag<true>(sB + (16 * tj[k] + l16) * PN, q, lq), K[k]);
         }
     }
     // the values of c beside this wave's rows n of dc (c leaves LDS for x and dy)
     typename T::F4 cd[IW];
 #pragma unroll
-    for (int i = 0; i < IW; ++i) cd[i] = T::raw4(sC + (16 * (it0 + i) + l16) * PN + 16 * nt + 4 * lq);
+    for (int i = 0; i < IW; ++i) cd[i] = T::raw4(sC + (16 * (it0 + i) + l16) * PN + T::template col<true>(16 * nt + 4 * lq));
     // tiles above the diagonal that pairs of tiles reach
-    if (wave == 1 || wave == 3) T::store4(sPd + (16 * wave + l16) * PS + 16 * (wave - 1) + 4 * lq, zero4());
+    if (wave == 1 || wave == 3) T::store4(sPd + (16 * wave + l16) * PS + T::template col<true>(16 * (wave - 1) + 4 * lq), zero4());
     f32x4 dc[IW], db[IW];
 #pragma unroll
     for (int i = 0; i < IW; ++i) dc[i] = db[i] = zero4();
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
         __syncthreads();
         if (h + 1 < h1) {
             load_xy(h + 1);
-            if (wave == 5) raw = load_raw(h + 1);
+            if (wave == 5) load_gate(h + 1);
         }
         // M, W and what they give
 #pragma unroll
@@ -146,8 +151,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             f32x4 m = zero4();
 #pragma unroll
             for (int q = 0; q < P / 32; ++q)
-                m = T::mma(T::kfrag(sY + (16 * ti[k] + l16) * PP + 32 * q + 4 * lq),
-                           T::kfrag(sX + (16 * tj[k] + l16) * PP + 32 * q + 4 * lq), m);
+                m = T::mma(T::template kfrag<true>(sY + (16 * ti[k] + l16) * PP, q, lq),
+                           T::template kfrag<true>(sX + (16 * tj[k] + l16) * PP, q, lq), m);
             const int i0 = 16 * ti[k] + 4 * lq, j = 16 * tj[k] + l16;
             const f32x4 gi = *reinterpret_cast<const f32x4 *>(&s.ghi[i0]), gil = *reinterpret_cast<const f32x4 *>(&s.glo[i0]);
             const float gj = s.ghi[j], gjl = s.glo[j], dtj = s.dt[j];
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                     s_m[j] = m[r];
                 }
             }
-            T::store4(sPd + j * PS + i0, pd);
+            T::store4(sPd + j * PS + T::template col<true>(i0), pd);
 #pragma unroll
             for (int r = 0; r < 4; ++r) rs[r] = sum16(rs[r]);
             if (l16 == 0) *reinterpret_cast<f32x4 *>(&s_row[tj[k]][i0]) = rs;
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 T::split(side ? Ev[2 * q] : Sv[2 * q], side ? Ev[2 * q + 1] : Sv[2 * q + 1], st);
 #pragma unroll
                 for (int i = 0; i < IW; ++i) {
-                    const F8 f = T::kfrag((side ? sX : sY) + (16 * (it0 + i) + l16) * PP + 32 * q + 4 * lq);
+                    const F8 f = T::template kfrag<true>((side ? sX : sY) + (16 * (it0 + i) + l16) * PP, q, lq);
 #pragma unroll
                     for (int e = T::kParts - 1; e >= 0; --e) acc[i] = T::mma(st[e], f, acc[i]);
                 }
@@ -197,7 +202,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             for (int i = 0; i < IW; ++i) {
                 const int at = 16 * (it0 + i) + l16;
                 const float f = side ? s.w[at] : s.eg[at];
-                const f32x4 o = side ? T::load4(sB + at * PN + 16 * nt + 4 * lq) : T::up(cd[i]);
+                const f32x4 o = side ? T::load4(sB + at * PN + T::template col<true>(16 * nt + 4 * lq)) : T::up(cd[i]);
                 float d = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) d += acc[i][r] * o[r];
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             for (int k = 0; k < PT; ++k) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
-                if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PP + 16 * k + 4 * lq, Ev[k]);
+                if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PE + 16 * k + 4 * lq, Ev[k]);
             }
             es_sum = sum64(es_sum);
             if (l == 0) s_es[wave] = es_sum;
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             for (int q = 0; q < N / 32; ++q) {
                 F8 e;
                 if constexpr (T::kBf16) {
-                    e = T::tr(sE, PP, 32 * q, 16 * pt, l16, lq);
+                    e = T::template tr<false>(sE, PE, 32 * q, 16 * pt, l16, lq);
                 } else {
                     // lane p = l16 of E's tile holds p = 4 (lane / 16) + r: gather the four rows n
                     f32x4 v[2];
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 }
 #pragma unroll
                 for (int j = 0; j < JW; ++j)
-                    V[j] = T::mma(e, T::kfrag(sB + (16 * (jt0 + j) + l16) * PN + 32 * q + 4 * lq), V[j]);
+                    V[j] = T::mma(e, T::template kfrag<true>(sB + (16 * (jt0 + j) + l16) * PN, q, lq), V[j]);
             }
             const float dh = a.D ? a.D[h] : 0.f;
             const uint32_t ldx = static_cast<uint32_t>(a.heads * P * es);
@@ -252,21 +257,21 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                                                          static_cast<uint32_t>((rows - 1) * ldx + P * es));
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const F8 y = T::tr(sY, PP, 32 * q, 16 * pt, l16, lq);
+                const F8 y = T::template tr<true>(sY, PP, 32 * q, 16 * pt, l16, lq);
 #pragma unroll
                 for (int j = 0; j < JW; ++j)
-                    if (q >= (jt0 + j) / 2) X[j] = T::mma(y, T::kfrag(sPd + (16 * (jt0 + j) + l16) * PS + 32 * q + 4 * lq), X[j]);
+                    if (q >= (jt0 + j) / 2) X[j] = T::mma(y, T::template kfrag<true>(sPd + (16 * (jt0 + j) + l16) * PS, q, lq), X[j]);
             }
 #pragma unroll
             for (int j = 0; j < JW; ++j) {
                 const int at = 16 * (jt0 + j) + l16, p0 = 16 * pt + 4 * lq;
-                const f32x4 v = (X[j] + V[j] * s.ew[at]) * s.dt[at] + T::load4(sY + at * PP + p0) * dh;
+                const f32x4 v = (X[j] + V[j] * s.ew[at]) * s.dt[at] + T::load4(sY + at * PP + T::template col<true>(p0)) * dh;
                 const uint32_t off = at * ldx + p0 * es;
                 if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(v)), rx, off, 0, 0);
                 else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
             }
         }
-        if (wave == 5 && h + 1 < h1) chunk_gates(a, raw, l < rows, h + 1, sg[(h + 1 - h0) & 1]);
+        if (wave == 5 && h + 1 < h1) chunk_gates(raw.value(a), bias, A, l < rows, sg[(h + 1 - h0) & 1]);
         if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_dt_kernel
             const int tile = l / 16;
             float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f, es_sum = 0.f;
@@ -300,26 +305,26 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (wave + 8 * k >= 10) continue;
-            T::store4(sPd + (16 * tj[k] + l16) * PS + 16 * ti[k] + 4 * lq, R[k]);
+            T::store4(sPd + (16 * tj[k] + l16) * PS + T::template col<true>(16 * ti[k] + 4 * lq), R[k]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int at = (16 * ti[k] + 4 * lq + r) * PS + 16 * tj[k] + l16;
+                const int at = (16 * ti[k] + 4 * lq + r) * PS + T::template col<true>(16 * tj[k] + (l16 & 12)) + (l16 & 3);
                 if constexpr (T::kBf16) sE[at] = bf16_bits(R[k][r]);
                 else sE[at] = R[k][r];
             }
         }
-        if (wave == 0 || wave == 2) T::store4(sE + (16 * wave + l16) * PS + 16 * (wave + 1) + 4 * lq, zero4());
+        if (wave == 0 || wave == 2) T::store4(sE + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
         tc.store(sC);
     }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const F8 bt = T::tr(sB, PN, 32 * q, 16 * nt, l16, lq), ct = T::tr(sC, PN, 32 * q, 16 * nt, l16, lq);
+        const F8 bt = T::template tr<true>(sB, PN, 32 * q, 16 * nt, l16, lq), ct = T::template tr<true>(sC, PN, 32 * q, 16 * nt, l16, lq);
 #pragma unroll
         for (int i = 0; i < IW; ++i) {
             const int it = it0 + i;
-            if (q <= it / 2) dc[i] = T::mma(bt, T::kfrag(sE + (16 * it + l16) * PS + 32 * q + 4 * lq), dc[i]);
-            if (q >= it / 2) db[i] = T::mma(ct, T::kfrag(sPd + (16 * it + l16) * PS + 32 * q + 4 * lq), db[i]);
+            if (q <= it / 2) dc[i] = T::mma(bt, T::template kfrag<true>(sE + (16 * it + l16) * PS, q, lq), dc[i]);
+            if (q >= it / 2) db[i] = T::mma(ct, T::template kfrag<true>(sPd + (16 * it + l16) * PS, q, lq), db[i]);
         }
     }
 #pragma unroll
@@ -356,12 +361,12 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     }
     const int64_t t0 = entry.x;
     const bool valid = l < rows;
-    const float raw = valid ? dt_raw(a, t0 + l, h) : 0.f;
+    const float raw = valid ? dt_raw(a, t0 + l, h) : 0.f, bias = head_bias(a, h), A = a.A[h];
     const float *in = a.token_part + item * kTokenPart;
     const float rw = in[l], cl = in[64 + l], diag = in[128 + l], m = in[192 + l], st = in[256 + l], et = in[320 + l];
     const float es_sum = in[384];
     Gates &s = sg[wave];
-    chunk_gates(a, raw, valid, h, s);
+    chunk_gates(raw, bias, A, valid, s);
     lds_wait();
     const float dt = s.dt[l], far = s.ew[l] * et;
     const float v = cl + diag + far;
@@ -375,8 +380,7 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     const float dl = z + u;
     float draw = 0.f;
     if (valid) {
-        const float x = raw + (a.dt_bias ? a.dt_bias[h] : 0.f);
-        draw = (v + a.A[h] * dl) / (1.f + expf(-x));
+        draw = (v + A * dl) / (1.f + expf(-(raw + bias)));
         const int64_t to = (t0 + l) * a.heads + h;
         if (a.gate_bf16) static_cast<uint16_t *>(a.ddt)[to] = bf16_bits(draw);
         else static_cast<float *>(a.ddt)[to] = draw;
@@ -439,14 +443,14 @@ hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
         const int64_t walks = a.n_spans * a.heads, grads = a.n_chunks * a.groups * a.slices;
         if (walks > 0x7FFFFFFF || grads > 0x7FFFFFFF || a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF)
             return hipErrorInvalidValue;
-        const dim3 grid(static_cast<uint32_t>(walks), 2);
+        const dim3 grid(static_cast<uint32_t>(walks), 2), walk(walk_threads(kStates, P));
         if (walks > 0) {
             if (a.span_state) {
-                hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, true>), grid, block, 0, stream, a);
+                hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, true>), grid, walk, 0, stream, a);
                 hipLaunchKernelGGL((gdr_ssm_join_kernel<N, P, true>),
                                    dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024)), 2), block, 0, stream, a);
             }
-            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true>), grid, block, 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true>), grid, walk, 0, stream, a);
             hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(static_cast<uint32_t>(grads)), dim3(kGradThreads), 0, stream, a);
         }
         if (walks > 0)

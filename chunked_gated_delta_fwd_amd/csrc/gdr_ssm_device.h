@@ -20,14 +20,28 @@ struct BfT {
     static __device__ __forceinline__ F4 raw4(const E *p) { return ld4(p); }
     static __device__ __forceinline__ f32x4 up(F4 a) { return up4(a); }
     static constexpr bool kBf16 = true;
-    static constexpr int kPad = 8;     // elements added to an LDS row: 16-byte rows, spread over the banks
     static constexpr int kParts = 3;   // operands that a split fp32 value takes
     static __device__ __forceinline__ f32x4 mma(F8 a, F8 b, f32x4 c) { return mfma32(a, b, c); }
-    // k contiguous in memory: row pointer + 32 s + 4 lq
-    static __device__ __forceinline__ F8 kfrag(const E *p) { return cat(ld4(p), ld4(p + 16)); }
+    // LDS rows are an odd multiple of 8 banks apart: measured per wave, an
+    // operand read then takes 2.7 units where 4 banks apart take 4.0, and a
+    // transposed one 1.6 instead of 2.4.  Permuted (KP): columns in kpos order,
+    // so that an operand with k along a row is one 16-byte read (two 8-byte
+    // ones take 16 units; a transposed read costs 2.4 for it).  Plain: for
+    // arrays that are only read across their rows.
+    static constexpr int pitch(int cols, bool) { return cols + 16; }
+    template <bool KP>
+    static __device__ __forceinline__ int col(int x) { return KP ? kpos(x) : x; }   // of 4 columns from x, x % 4 == 0
+    // k along a row: columns 32 q ..
+    template <bool KP>
+    static __device__ __forceinline__ F8 kfrag(const E *row, int q, int lq) {
+        if constexpr (KP) return ld8(row + 32 * q + 8 * lq);
+        else return cat(ld4(row + 32 * q + 4 * lq), ld4(row + 32 * q + 16 + 4 * lq));
+    }
     // k along the rows of an LDS array: rows j0 .. j0 + 31, column x0 + l16
+    template <bool KP>
     static __device__ __forceinline__ F8 tr(const E *m, int pitch, int j0, int x0, int l16, int lq) {
-        const E *p = m + (j0 + 4 * lq + l16 / 4) * pitch + x0 + 4 * (l16 % 4);
+        const E *p = m + (j0 + 4 * lq + l16 / 4) * pitch +
+                     (KP ? (x0 & ~31) + ((x0 >> 2) & 4) + 8 * (l16 % 4) : x0 + 4 * (l16 % 4));
         return cat(ld4_tr(p), ld4_tr(p + 16 * pitch));
     }
     static __device__ __forceinline__ F8 round(f32x4 a, f32x4 b) { return cat(cvt4(a), cvt4(b)); }
@@ -70,8 +84,10 @@ struct FpT {
     static __device__ __forceinline__ F4 raw4(const E *p) { return *reinterpret_cast<const f32x4 *>(p); }
     static __device__ __forceinline__ f32x4 up(F4 a) { return a; }
     static constexpr bool kBf16 = false;
-    static constexpr int kPad = 4;
     static constexpr int kParts = 1;
+    static constexpr int pitch(int cols, bool) { return cols + 4; }
+    template <bool KP>
+    static __device__ __forceinline__ int col(int x) { return x; }
     static __device__ __forceinline__ f32x4 mma(F8 a, F8 b, f32x4 c) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[r], b.a[r], c, 0, 0, 0);
@@ -81,7 +97,11 @@ struct FpT {
     }
     static __device__ __forceinline__ f32x4 load4(const E *p) { return *reinterpret_cast<const f32x4 *>(p); }
     static __device__ __forceinline__ void store4(E *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
-    static __device__ __forceinline__ F8 kfrag(const E *p) { return {load4(p), load4(p + 16)}; }
+    template <bool KP>
+    static __device__ __forceinline__ F8 kfrag(const E *row, int q, int lq) {
+        return {load4(row + 32 * q + 4 * lq), load4(row + 32 * q + 16 + 4 * lq)};
+    }
+    template <bool KP>
     static __device__ __forceinline__ F8 tr(const E *m, int pitch, int j0, int x0, int l16, int lq) {
         F8 o;
 #pragma unroll
@@ -100,18 +120,20 @@ struct FpT {
 constexpr int kSsmThreads = 256;
 
 // A 64-row tile of COLS columns on its way from HBM to LDS through registers.
-template <class T, int COLS, int THREADS = kSsmThreads>
+template <class T, int COLS, bool KP, int THREADS = kSsmThreads>
 struct Tile {
-    static constexpr int kPitch = COLS + T::kPad;
+    static constexpr int kPitch = T::pitch(COLS, KP);
     static constexpr int kPiece = 16 / sizeof(typename T::E);       // elements of 16 bytes
     static constexpr int kPerRow = COLS / kPiece;
     static constexpr int kN = 64 * kPerRow / THREADS;
     v4u32 r[kN];
     // rows `ld` bytes apart; rows past the resource's end read as zeros
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, uint32_t ld) {
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));   // offsets are cheap: made anew for each tile, not kept in registers
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-            const int id = threadIdx.x + k * THREADS;
+            const int id = tid + k * THREADS;
             r[k] = __builtin_bit_cast(v4u32, buf_load<16>(rsrc, (id / kPerRow) * ld + (id % kPerRow) * 16));
         }
     }
@@ -119,7 +141,14 @@ struct Tile {
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
             const int id = threadIdx.x + k * THREADS;
-            *reinterpret_cast<v4u32 *>(m + (id / kPerRow) * kPitch + (id % kPerRow) * kPiece) = r[k];
+            typename T::E *const row = m + (id / kPerRow) * kPitch;
+            const int x = (id % kPerRow) * kPiece;
+            if constexpr (T::kBf16 && KP) {
+                *reinterpret_cast<v2u32 *>(row + kpos(x)) = v2u32{r[k][0], r[k][1]};
+                *reinterpret_cast<v2u32 *>(row + kpos(x + 4)) = v2u32{r[k][2], r[k][3]};
+            } else {
+                *reinterpret_cast<v4u32 *>(row + x) = r[k];
+            }
         }
     }
 };
@@ -127,9 +156,25 @@ struct Tile {
 // log(1 + e^v) without overflow; log1p keeps the small values' bits
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
+// The raw dt of a token as it lies in memory, in a float's upper half for bf16
+// once bits() has put it there.  Kept apart from the load, so that a prefetched
+// one is not waited for (and with it every load before it) where it is issued.
+struct RawDt {
+    uint32_t word = 0;
+    __device__ __forceinline__ void load(const SsmArgs &a, int64_t token, int h) {
+        if (a.gate_bf16) word = static_cast<const uint16_t *>(a.dt)[token * a.lddt + h];
+        else word = static_cast<const uint32_t *>(a.dt)[token * a.lddt + h];
+    }
+    __device__ __forceinline__ float value(const SsmArgs &a) const {
+        return __uint_as_float(a.gate_bf16 ? word << 16 : word);
+    }
+};
 __device__ __forceinline__ float dt_raw(const SsmArgs &a, int64_t token, int h) {
-    return a.gate_bf16 ? load_scalar<true>(a.dt, token * a.lddt + h) : load_scalar<false>(a.dt, token * a.lddt + h);
+    RawDt r;
+    r.load(a, token, h);
+    return r.value(a);
 }
+__device__ __forceinline__ float head_bias(const SsmArgs &a, int h) { return a.dt_bias ? a.dt_bias[h] : 0.f; }
 
 // Per-token scalars of a 64-token chunk, G the running sum of dt A from the
 // chunk's start.  The sum is taken in fp64 and kept as two floats, because
@@ -168,10 +213,10 @@ __device__ __forceinline__ float sum_rows(float x) {
 __device__ __forceinline__ float sum64(float x) { return sum_rows(sum16(x)); }
 
 // One wave, lane = token.  Tokens past the end have dt = 0 and write nothing.
-__device__ __forceinline__ void chunk_gates(const SsmArgs &a, float raw, bool valid, int h, Gates &s) {
+__device__ __forceinline__ void chunk_gates(float raw, float bias, float A, bool valid, Gates &s) {
     const int l = threadIdx.x % 64;
-    const float dt = valid ? softplus(raw + (a.dt_bias ? a.dt_bias[h] : 0.f)) : 0.f;
-    double g = static_cast<double>(dt) * static_cast<double>(a.A[h]);
+    const float dt = valid ? softplus(raw + bias) : 0.f;
+    double g = static_cast<double>(dt) * static_cast<double>(A);
     g = dpp_add64<0x111, 0xF>(g);   // inclusive scan, as wave_inclusive_scan
     g = dpp_add64<0x112, 0xF>(g);
     g = dpp_add64<0x114, 0xF>(g);
@@ -262,16 +307,24 @@ __device__ __forceinline__ void store_state_tile(float *m, int nt, int pt, int l
 // state: E <- e^G_end E + sum_i e^G_i c_i dy_i^T, stored at each chunk's end.
 enum WalkMode { kLocal, kStates, kOut };
 
+// Waves of a block: kOut 4, of 16 or 32 columns p each (with 8, a wave's
+// registers for y and its operands do not fit 4 waves a SIMD, and spill); the
+// other walks one per 16 columns.  waves: a SIMD's, at least.
+constexpr int walk_threads(int mode, int p) { return mode == kOut ? 256 : 4 * p; }
+constexpr int walk_waves(int mode, bool bf16, int p) { return mode != kOut && p == 128 ? (bf16 ? 4 : 2) : (bf16 ? 2 : 1); }
+
 template <class T, int N, int P, int MODE, bool OB>
-__global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf16, P)) gdr_ssm_walk_kernel(SsmArgs a) {
     typedef typename T::E E;
     typedef typename T::F8 F8;
-    constexpr int NT = N / 16, PT = P / 16, CT = PT / 4;   // a wave owns CT of the column tiles
+    constexpr int NT = N / 16, PT = P / 16, TH = walk_threads(MODE, P), WAVES = TH / 64, CT = PT / WAVES;   // a wave owns CT of the column tiles
     constexpr bool kY = MODE == kOut;
-    typedef Tile<T, N> TileN;
-    typedef Tile<T, P> TileP;
-    constexpr int PN = TileN::kPitch, PP = TileP::kPitch, PS = 64 + T::kPad;
-    __shared__ __attribute__((aligned(16))) E sU[64 * PN], sV[64 * PP], sC[kY ? 64 * PN : 16], sP[kY ? 64 * PS : 16];
+    constexpr bool KU = kY;   // the scores read U along its rows, the state update across them
+    typedef Tile<T, N, KU, TH> TileU;
+    typedef Tile<T, N, true, TH> TileC;
+    typedef Tile<T, P, false, TH> TileV;
+    constexpr int PU = TileU::kPitch, PC = TileC::kPitch, PV = TileV::kPitch, PS = T::pitch(64, true);
+    __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16], sP[kY ? 64 * PS : 16];
     __shared__ __attribute__((aligned(16))) Gates sg[2];
 
     const int64_t item = gqa_xcd_item(blockIdx.x, gridDim.x, a.heads, a.groups);
@@ -305,9 +358,11 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_ke
     const E *ub = static_cast<const E *>(rev ? a.c : a.b) + g * N;
     const E *vb = static_cast<const E *>(rev ? a.dy : a.x) + h * P;
     const E *cb = static_cast<const E *>(a.c) + g * N;
-    TileN tu, tc;
-    TileP tv;
-    float raw = 0.f;   // wave 0: dt of the chunk after the prefetched one
+    TileU tu;
+    TileC tc;
+    TileV tv;
+    RawDt raw;   // the last wave: dt of the chunk after the prefetched one
+    const float bias = head_bias(a, h), A = a.A[h];
     auto chunk_at = [&](int k) { return rev ? chunks - 1 - k : k; };
     auto rows_of = [&](int c) {
         const int64_t left = sp.len - 64 * static_cast<int64_t>(c);
@@ -327,16 +382,29 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_ke
     };
     auto load_raw = [&](int k) {
         const int c = chunk_at(k);
-        return l < rows_of(c) ? dt_raw(a, sp.t0 + 64 * static_cast<int64_t>(c) + l, h) : 0.f;
+        if (l < rows_of(c)) raw.load(a, sp.t0 + 64 * static_cast<int64_t>(c) + l, h);
+    };
+    auto store_tiles = [&] {
+        tu.store(sU);
+        tv.store(sV);
+        if constexpr (kY) tc.store(sC);
     };
     if (chunks > 0) {
         load_tiles(0);
-        if (wave == 0) {
-            chunk_gates(a, load_raw(0), l < rows_of(chunk_at(0)), h, sg[0]);
-            if (chunks > 1) raw = load_raw(1);
+        if (wave == WAVES - 1) {
+            load_raw(0);
+            chunk_gates(raw.value(a), bias, A, l < rows_of(chunk_at(0)), sg[0]);
+            if (chunks > 1) load_raw(1);
         }
+        store_tiles();
     }
+    if (kY && (wave == 0 || wave == 2))   // tiles above the diagonal that the products' pairs of tiles reach
+        T::store4(sP + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
+    const float dh = kY && a.D ? a.D[h] : 0.f;
     float total = 0.f;   // kLocal: log of the span's decay
+    // all loads so far have arrived: otherwise the compiler would wait for the
+    // initial state inside the loop, and with it for each chunk's prefetch
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
     for (int k = 0; k < chunks; ++k) {
         const int c = chunk_at(k), rows = rows_of(c);
         const int64_t t = sp.t0 + 64 * static_cast<int64_t>(c);
@@ -346,94 +414,94 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_ke
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < CT; ++i)
-                    *reinterpret_cast<f32x4 *>(to + ((nt * PT + CT * wave + i) * 64 + l) * 4) = Z[nt][i];
+                for (int i = 0; i < CT; ++i) *reinterpret_cast<f32x4 *>(to + ((nt * PT + CT * wave + i) * 64 + l) * 4) = Z[nt][i];
         }
-        tu.store(sU);
-        tv.store(sV);
-        if constexpr (kY) tc.store(sC);
-        __syncthreads();
+        __syncthreads();   // this chunk's tiles and gates are in LDS
         if (k + 1 < chunks) load_tiles(k + 1);
 
-        f32x4 Y[4][CT];
         if constexpr (kY) {
-            // scores, transposed: tile (j, i) of B C^T, wave w the rows i of y's tile w
-            F8 ci[N / 32];
+            // scores, transposed: tile (j, i) of B C^T; a wave takes tiles wave, wave + WAVES, .. of the ten
 #pragma unroll
-            for (int q = 0; q < N / 32; ++q) ci[q] = T::kfrag(sC + (16 * wave + l16) * PN + 32 * q + 4 * lq);
-            const float gi = s.ghi[16 * wave + l16], gil = s.glo[16 * wave + l16];
-            for (int jt = 0; jt <= wave; ++jt) {
+            for (int m = 0; m < (10 + WAVES - 1) / WAVES; ++m) {
+                const int idx = wave + WAVES * m;
+                if (idx >= 10) break;
+                const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
                 f32x4 acc = zero4();
 #pragma unroll
-                for (int q = 0; q < N / 32; ++q) acc = T::mma(T::kfrag(sU + (16 * jt + l16) * PN + 32 * q + 4 * lq), ci[q], acc);
-                const int j0 = 16 * jt + 4 * lq;
+                for (int q = 0; q < N / 32; ++q)
+                    acc = T::mma(T::template kfrag<KU>(sU + (16 * jt + l16) * PU, q, lq),
+                                 T::template kfrag<true>(sC + (16 * it + l16) * PC, q, lq), acc);
+                const int i = 16 * it + l16, j0 = 16 * jt + 4 * lq;
+                const float gi = s.ghi[i], gil = s.glo[i];
                 const f32x4 gj = *reinterpret_cast<const f32x4 *>(&s.ghi[j0]), gl = *reinterpret_cast<const f32x4 *>(&s.glo[j0]);
                 const f32x4 dj = *reinterpret_cast<const f32x4 *>(&s.dt[j0]);
                 f32x4 p;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float e = (gi - gj[r]) + (gil - gl[r]);
-                    const float v = acc[r] * __expf(e) * dj[r];
-                    p[r] = j0 + r <= 16 * wave + l16 ? v : 0.f;
+                    const float v = acc[r] * __expf((gi - gj[r]) + (gil - gl[r])) * dj[r];
+                    p[r] = j0 + r <= i ? v : 0.f;
                 }
-                T::store4(sP + (16 * wave + l16) * PS + j0, p);
+                T::store4(sP + i * PS + T::template col<true>(j0), p);
             }
-            if (wave % 2 == 0)   // the upper tile of a K32 pair that the products below read
-                T::store4(sP + (16 * wave + l16) * PS + 16 * (wave + 1) + 4 * lq, zero4());
-            // what the incoming state gives: Y^T = S^T C^T
+        }
+        if (wave == WAVES - 1 && k + 1 < chunks) {   // the next chunk's gates (the first two waves have one score tile more)
+            chunk_gates(raw.value(a), bias, A, l < rows_of(chunk_at(k + 1)), sg[(k + 1) & 1]);
+            if (k + 2 < chunks) load_raw(k + 2);
+        }
+        F8 v[2][CT];   // x (or dy) with tokens as k
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < CT; ++i) v[q][i] = T::template tr<false>(sV, PV, 32 * q, 16 * (CT * wave + i), l16, lq);
+        if constexpr (kY) {
+            // y^T = e^G (S^T C^T) + D x^T + X^T P^T for this wave's columns
+            f32x4 Y[4][CT];
 #pragma unroll
             for (int it = 0; it < 4; ++it)
 #pragma unroll
                 for (int i = 0; i < CT; ++i) Y[it][i] = zero4();
 #pragma unroll
             for (int q = 0; q < N / 32; ++q) {
-                F8 z[CT];
+                F8 z[CT], cf[4];
+#pragma unroll
+                for (int it = 0; it < 4; ++it) cf[it] = T::template kfrag<true>(sC + (16 * it + l16) * PC, q, lq);
 #pragma unroll
                 for (int i = 0; i < CT; ++i) z[i] = T::round(Z[2 * q][i], Z[2 * q + 1][i]);
+                __builtin_amdgcn_sched_barrier(0);   // the reads together, ahead of the products
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const F8 cf = T::kfrag(sC + (16 * it + l16) * PN + 32 * q + 4 * lq);
+                for (int it = 0; it < 4; ++it)
 #pragma unroll
-                    for (int i = 0; i < CT; ++i) Y[it][i] = T::mma(z[i], cf, Y[it][i]);
-                }
+                    for (int i = 0; i < CT; ++i) Y[it][i] = T::mma(z[i], cf[it], Y[it][i]);
             }
-        }
-        if (wave == 0 && k + 1 < chunks) {   // the next chunk's gates (wave 0 has the fewest score tiles)
-            chunk_gates(a, raw, l < rows_of(chunk_at(k + 1)), h, sg[(k + 1) & 1]);
-            if (k + 2 < chunks) raw = load_raw(k + 2);
-        }
-        F8 v[2][CT];   // x (or dy) with tokens as k
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < CT; ++i) v[q][i] = T::tr(sV, PP, 32 * q, 16 * (CT * wave + i), l16, lq);
-        if constexpr (kY) {
-            __syncthreads();
-            const float dh = a.D ? a.D[h] : 0.f;
-            const uint32_t ldy = static_cast<uint32_t>(a.heads * P * sizeof(E));
-            E *yb = static_cast<E *>(a.y) + (t * a.heads + h) * P;
-            const __amdgpu_buffer_rsrc_t ry = chunk_rsrc(yb, static_cast<uint32_t>((rows - 1) * ldy + P * sizeof(E)));
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const float eg = s.eg[16 * it + l16];
 #pragma unroll
-                for (int i = 0; i < CT; ++i) Y[it][i] = Y[it][i] * eg;
+                for (int i = 0; i < CT; ++i)
+                    Y[it][i] = Y[it][i] * eg + T::load4(sV + (16 * it + l16) * PV + 16 * (CT * wave + i) + 4 * lq) * dh;
+            }
+            __syncthreads();   // the scores are in LDS
+            uint32_t ldy = static_cast<uint32_t>(a.heads * P * sizeof(E));
+            asm volatile("" : "+s"(ldy));   // as for the tiles' offsets
+            E *yb = static_cast<E *>(a.y) + (t * a.heads + h) * P;
+            const __amdgpu_buffer_rsrc_t ry = chunk_rsrc(yb, static_cast<uint32_t>((rows - 1) * ldy + P * sizeof(E)));
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
 #pragma unroll
                 for (int q = 0; q <= it / 2; ++q) {
-                    const F8 pf = T::kfrag(sP + (16 * it + l16) * PS + 32 * q + 4 * lq);
+                    const F8 pf = T::template kfrag<true>(sP + (16 * it + l16) * PS, q, lq);
 #pragma unroll
                     for (int i = 0; i < CT; ++i) Y[it][i] = T::mma(v[q][i], pf, Y[it][i]);
                 }
 #pragma unroll
                 for (int i = 0; i < CT; ++i) {
-                    const int p0 = 16 * (CT * wave + i) + 4 * lq;
-                    const f32x4 y = Y[it][i] + T::load4(sV + (16 * it + l16) * PP + p0) * dh;
-                    const uint32_t off = (16 * it + l16) * ldy + p0 * sizeof(E);
-                    if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(y)), ry, off, 0, 0);
-                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, y), ry, off, 0, 0);
+                    const uint32_t off = (16 * it + l16) * ldy + (16 * (CT * wave + i) + 4 * lq) * sizeof(E);
+                    if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(Y[it][i])), ry, off, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, Y[it][i]), ry, off, 0, 0);
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         // Z <- decay Z + U^T (w V)
         const float decay = s.decay;
         if (MODE == kLocal) total += s.ghi[63] + s.glo[63];
@@ -450,16 +518,21 @@ __global__ void __launch_bounds__(kSsmThreads, T::kBf16 ? 2 : 1) gdr_ssm_walk_ke
 #pragma unroll
             for (int i = 0; i < CT; ++i) T::split(T::lo(v[q][i]) * wa, T::hi(v[q][i]) * wb, vs[i]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const F8 u = T::tr(sU, PN, 32 * q, 16 * nt, l16, lq);
+            for (int nt = 0; nt < NT; nt += 2) {   // two tiles at a time: products on one sum do not follow each other
+                F8 u[2];
 #pragma unroll
-                for (int i = 0; i < CT; ++i)
+                for (int k2 = 0; k2 < 2; ++k2) u[k2] = T::template tr<KU>(sU, PU, 32 * q, 16 * (nt + k2), l16, lq);
 #pragma unroll
-                    for (int e = T::kParts - 1; e >= 0; --e)
-                        Z[nt][i] = OB ? T::mma(vs[i][e], u, Z[nt][i]) : T::mma(u, vs[i][e], Z[nt][i]);
+                for (int e = T::kParts - 1; e >= 0; --e)
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                        for (int i = 0; i < CT; ++i)
+                            Z[nt + k2][i] = OB ? T::mma(vs[i][e], u[k2], Z[nt + k2][i]) : T::mma(u[k2], vs[i][e], Z[nt + k2][i]);
             }
         }
-        __syncthreads();
+        __syncthreads();   // the chunk's tiles have been read
+        if (k + 1 < chunks) store_tiles();
     }
 
     float *out = nullptr;
