@@ -106,7 +106,9 @@ def library(path: Optional[str] = None):
     lib.gdr_dispatch_order.restype = ctypes.c_int
     lib.gdr_chunk_local_cumsum.argtypes = [TP] * 3 + [ctypes.c_void_p]
     lib.gdr_chunk_local_cumsum.restype = ctypes.c_int
-    P = ctypes.c_void_p   # the operators of mixer.py take packed descriptors by address
+    # the operators around the recurrence take descriptors by address here
+    # (the tests do; mixer.py calls them through its compiled extension)
+    P = ctypes.c_void_p
     lib.gdr_short_conv_fwd.argtypes = [P] * 7 + [ctypes.c_int, P]
     lib.gdr_short_conv_bwd.argtypes = [P] * 11 + [ctypes.c_int, P, P, P]
     lib.gdr_short_conv_step.argtypes = [P] * 5 + [ctypes.c_int, P]

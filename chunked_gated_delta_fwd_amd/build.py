@@ -1,20 +1,24 @@
-"""Build ``libgdr.so`` (HIP kernels + C ABI) for gfx950 with hipcc, in-tree."""
+"""Build ``libgdr.so`` (HIP kernels + C ABI) for gfx950 with hipcc, and
+``_gdr_torch.so`` (the compiled marshalling of mixer.py), in-tree."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdr.so")
+TORCH_LIB = os.path.join(PKG, "_gdr_torch.so")
 
 SOURCES = ["gdr_kernels.hip", "gdr_bwd.hip", "gdr_kda.hip", "gdr_conv.hip", "gdr_qknorm.hip", "gdr_ssm.hip",
            "gdr_ssm_bwd.hip", "gdr_api.cpp", "gdr_mixer_api.cpp"]
 
-HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
+HIPCC = os.environ.get("HIPCC", os.path.join(ROCM, "bin", "hipcc"))
 
 FLAGS = [
     "--offload-arch=gfx950",
@@ -31,10 +35,31 @@ FLAGS = [
 ]
 
 
+def _torch_command() -> list:
+    """The host compiler's line for the extension that mixer.py calls."""
+    import torch
+    from torch.utils import cpp_extension
+
+    root = os.path.dirname(torch.__file__)
+    include = sum((["-isystem", p] for p in cpp_extension.include_paths()), [])
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-DTORCH_EXTENSION_NAME=_gdr_torch"]
+            + include + ["-isystem", os.path.join(ROCM, "include"), "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE,
+                         os.path.join(CSRC, "gdr_torch.cpp"), "-L", os.path.join(root, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu",
+                         "-ltorch", "-ltorch_python", "-L", PKG, "-lgdr", "-Wl,-rpath,$ORIGIN"])
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source into ``chunked_gated_delta_fwd_amd/libgdr.so``."""
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC] + FLAGS + [os.path.join(CSRC, s) for s in SOURCES] + ["-o", tmp]
+    """Compile every source into ``chunked_gated_delta_fwd_amd/libgdr.so``, then
+    the torch extension that links to it."""
+    _compile([HIPCC] + FLAGS + [os.path.join(CSRC, s) for s in SOURCES], LIB, verbose)
+    _compile(_torch_command(), TORCH_LIB, verbose)
+    return LIB
+
+
+def _compile(cmd: list, lib: str, verbose: bool) -> None:
+    tmp = lib + ".tmp%d" % os.getpid()
+    cmd = cmd + ["-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     proc = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -43,11 +68,10 @@ def build(verbose: bool = False) -> str:
     if proc.returncode != 0:
         if os.path.exists(tmp):
             os.remove(tmp)
-        raise RuntimeError("hipcc failed (%d):\n%s" % (proc.returncode, out))
+        raise RuntimeError("%s failed (%d):\n%s" % (os.path.basename(cmd[0]), proc.returncode, out))
     if verbose and out:
         print(out, flush=True)
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, lib)
 
 
 if __name__ == "__main__":
