@@ -71,10 +71,12 @@ struct SsmArgs {
     int64_t n_seq, seq_len, total;
     int64_t ldx, lddt, ldb, ldc;
     int32_t heads, groups, n, p, bf16, gate_bf16;
-    // Spans of span_len tokens (a multiple of 64) that are walked in parallel;
-    // spans NULL: one per sequence.  {first token, length (< 0: surplus entry),
-    // sequence << 2 | last << 1 | first, chunk row of its first chunk}
+    // Spans of span_len tokens (a multiple of 64) that are walked in parallel.
+    // With cu, from a table, or (NULL) one per sequence: {first token, length
+    // (< 0: surplus entry), sequence << 2 | last << 1 | first, chunk row of its
+    // first chunk}.  Without, row_spans and row_chunks (64 tokens) a sequence.
     const int4 *spans;
+    int32_t row_spans, row_chunks;
     const int32_t *span_first;            // [N + 1] first span of each sequence
     int64_t n_spans;                      // entries: an upper bound on the spans
     int64_t span_len;
@@ -86,7 +88,7 @@ struct SsmArgs {
     int64_t lddy;
     float *chunk_state;                   // [2][n_chunks][H][n p]: states before chunks, gradients after them
     int64_t n_chunks;                     // entries: an upper bound on the 64-token chunks
-    const int4 *chunks;                   // as spans, span_len 64
+    const int4 *chunks;                   // as spans, span_len 64; NULL without cu
     void *dx, *ddt, *db, *dc;
     float *dA, *dD, *dbias, *dh0;         // dD, dbias, dh0 NULL: not written
     int32_t slices, slice_heads;          // the heads of a group in slices, one block each

@@ -450,8 +450,12 @@ void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, SsmTables &t) {
         a.span_len = (longest / 64 + 1) * 64;
     }
     a.n_spans = t.split ? entries(a.span_len) : a.n_seq;
+    a.row_spans = static_cast<int32_t>((a.seq_len + a.span_len - 1) / a.span_len);
+    if (a.row_spans < 1) a.row_spans = 1;
+    a.row_chunks = static_cast<int32_t>((a.seq_len + 63) / 64);
+    if (a.row_chunks < 1) a.row_chunks = 1;
     const int64_t ways = bwd ? 2 : 1;
-    if (t.split || bwd) {
+    if (a.cu && (t.split || bwd)) {
         t.span_first = c.take<int32_t>(a.n_seq + 1);
         t.spans = c.take<int4>(a.n_spans);
     }
@@ -461,8 +465,10 @@ void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, SsmTables &t) {
     }
     if (bwd) {
         a.n_chunks = entries(64);
-        t.chunk_first = c.take<int32_t>(a.n_seq + 1);
-        t.chunks = c.take<int4>(a.n_chunks);
+        if (a.cu) {
+            t.chunk_first = c.take<int32_t>(a.n_seq + 1);
+            t.chunks = c.take<int4>(a.n_chunks);
+        }
         a.chunk_state = c.take<float>(2 * a.n_chunks * H * state);
         a.token_part = c.take<float>(a.n_chunks * H * gdr::kTokenPart);
         a.head_part = c.take<float>(a.n_chunks * H * 3);
@@ -479,7 +485,7 @@ void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, SsmTables &t) {
 // Tables, then the walks.
 hipError_t run_ssm(gdr::SsmArgs &a, const SsmTables &t, bool bwd, hipStream_t stream) {
     hipError_t e = hipSuccess;
-    if (bwd && a.n_seq > 0) {
+    if (t.chunks && a.n_seq > 0) {
         e = gdr::launch_ssm_table(a, 64, a.n_chunks, nullptr, t.chunk_first, t.chunks, stream);
         a.chunks = t.chunks;
     }

@@ -32,8 +32,9 @@ template <int N, int P, bool BF16>
 __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
     constexpr int CG = P / 4, RG = 256 / CG, RPT = N / RG;
     __shared__ float s_b[N], s_c[N], s_part[RG][P];
-    const int64_t seq = blockIdx.x / a.heads;
-    const int h = static_cast<int>(blockIdx.x % a.heads);
+    const uint32_t seq32 = blockIdx.x / static_cast<uint32_t>(a.heads);
+    const int64_t seq = seq32;
+    const int h = static_cast<int>(blockIdx.x - seq32 * a.heads);
     const int g = h / (a.heads / a.groups);
     const int t = threadIdx.x, cg = t % CG, rg = t / CG;
     const int j0 = 4 * cg, i0 = RPT * rg;
@@ -153,12 +154,14 @@ hipError_t by_ssm(const SsmArgs &a, F f) {
 }  // namespace
 
 int64_t ssm_span_len(const SsmArgs &a) {
-    // Enough walks to fill the chip several times; not split when no sequence
-    // can be longer than a span.
+    // About 1024 walks: two rounds over the chip.  With 4096 the joining pass
+    // moves four times the states (91 us where it takes 28, at 65536 tokens and
+    // 32 heads of 128 x 128), with 512 the last round is half empty.  Not split when no sequence
+    // can be longer than a span, or than what a split costs (its three launches
+    // take about as long as a walk over 640 tokens).
     const int64_t longest = a.cu ? a.total : a.seq_len;
-    int64_t len = (a.total * a.heads / 2048 + 63) / 64 * 64;
-    if (len < 64) len = 64;
-    return longest <= len ? 0 : len;
+    const int64_t len = (a.total * a.heads / 1024 + 63) / 64 * 64;
+    return longest <= 640 || longest <= len ? 0 : len < 64 ? 64 : len;
 }
 
 hipError_t launch_ssm_table(const SsmArgs &a, int64_t span_len, int64_t count, const int32_t *chunk_first,

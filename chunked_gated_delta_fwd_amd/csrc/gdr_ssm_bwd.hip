@@ -28,6 +28,20 @@
 namespace gdr {
 namespace {
 
+// First token and number of tokens (none: rows <= 0) of a chunk row.
+__device__ __forceinline__ void chunk_of_row(const SsmArgs &a, int64_t row, int64_t &t0, int &rows) {
+    if (a.chunks) {
+        const int4 v = a.chunks[row];
+        t0 = v.x;
+        rows = v.y;
+    } else {
+        const uint32_t seq = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.row_chunks);
+        const int64_t at = 64 * (row - static_cast<int64_t>(seq) * a.row_chunks), left = a.seq_len - at;
+        t0 = seq * a.seq_len + at;
+        rows = static_cast<int>(left < 64 ? left : 64);
+    }
+}
+
 // One block of 8 waves per (chunk, group, slice of the group's heads); a wave
 // owns one or two of the (i, j) tiles of the lower triangle, one tile of rows
 // n of db and dc (of half the tokens when n is 64) and one tile of rows p of
@@ -52,15 +66,15 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     E *const sX = sXY, *const sY = sXY + 64 * PP, *const sC = sXY;
 
     const int per_group = a.heads / a.groups;
-    const int64_t item = blockIdx.x;
-    const int slice = static_cast<int>(item % a.slices);
-    const int g = static_cast<int>(item / a.slices % a.groups);
-    const int64_t row = item / a.slices / a.groups;
+    const uint32_t slices = a.slices, groups = a.groups, rest = blockIdx.x / slices;
+    const int slice = static_cast<int>(blockIdx.x - rest * slices);
+    const int64_t row = rest / groups;
+    const int g = static_cast<int>(rest - static_cast<uint32_t>(row) * groups);
     const int h0 = g * per_group + slice * a.slice_heads;
     const int h1 = h0 + a.slice_heads < (g + 1) * per_group ? h0 + a.slice_heads : (g + 1) * per_group;
-    const int4 entry = a.chunks[row];
-    const int rows = entry.y;
-    const int64_t t0 = entry.x;
+    int rows;
+    int64_t t0;
+    chunk_of_row(a, row, t0, rows);
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64);   // the same in every lane
     const int l = tid % 64, l16 = l % 16, lq = l / 16;
     if (rows <= 0) return;   // a length-0 sequence's row, or a surplus one
@@ -350,16 +364,16 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t item = static_cast<int64_t>(blockIdx.x) * (kSsmThreads / 64) + wave;
     if (item >= a.n_chunks * a.heads) return;
-    const int64_t row = item / a.heads;
+    const int64_t row = static_cast<uint32_t>(item) / static_cast<uint32_t>(a.heads);
     const int h = static_cast<int>(item - row * a.heads);
-    const int4 entry = a.chunks[row];
-    const int rows = entry.y;
+    int rows;
+    int64_t t0;
+    chunk_of_row(a, row, t0, rows);
     float *const part = a.head_part + item * 3;
     if (rows <= 0) {
         if (l < 3) part[l] = 0.f;
         return;
     }
-    const int64_t t0 = entry.x;
     const bool valid = l < rows;
     const float raw = valid ? dt_raw(a, t0 + l, h) : 0.f, bias = head_bias(a, h), A = a.A[h];
     const float *in = a.token_part + item * kTokenPart;
@@ -441,7 +455,8 @@ hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
     const dim3 block(kSsmThreads);
     auto run = [&]<class T, int N, int P>() {
         const int64_t walks = a.n_spans * a.heads, grads = a.n_chunks * a.groups * a.slices;
-        if (walks > 0x7FFFFFFF || grads > 0x7FFFFFFF || a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF)
+        if (walks > 0x7FFFFFFF || grads > 0x7FFFFFFF || a.n_chunks * a.heads > 0x7FFFFFFF ||
+             a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF)
             return hipErrorInvalidValue;
         const dim3 grid(static_cast<uint32_t>(walks), 2), walk(walk_threads(kStates, P));
         if (walks > 0) {

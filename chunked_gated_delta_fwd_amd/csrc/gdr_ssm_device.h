@@ -247,7 +247,7 @@ struct Span {
     int64_t row0;    // the sequence's chunk rows start here, plus the span's place in it
     bool first, last;
 };
-__device__ __forceinline__ Span span_of_block(const SsmArgs &a, int64_t s) {
+__device__ __forceinline__ Span span_of_block(const SsmArgs &a, uint32_t s) {
     Span r;
     if (a.spans) {
         const int4 v = a.spans[s];
@@ -257,22 +257,47 @@ __device__ __forceinline__ Span span_of_block(const SsmArgs &a, int64_t s) {
         r.first = v.z & 1;
         r.last = v.z & 2;
         r.row0 = v.w;
-    } else {
+    } else if (a.cu) {
+        int64_t b = a.cu[s], e = a.cu[s + 1];
+        b = b < 0 ? 0 : b > a.total ? a.total : b;
+        e = e < b ? b : e > a.total ? a.total : e;
         r.seq = s;
-        r.first = r.last = true;
+        r.t0 = b;
+        r.len = e - b;
         r.row0 = 0;
-        if (a.cu) {
-            int64_t b = a.cu[s], e = a.cu[s + 1];
-            b = b < 0 ? 0 : b > a.total ? a.total : b;
-            e = e < b ? b : e > a.total ? a.total : e;
-            r.t0 = b;
-            r.len = e - b;
-        } else {
-            r.t0 = s * a.seq_len;
-            r.len = a.seq_len;
-        }
+        r.first = r.last = true;
+    } else {   // rows of seq_len tokens, row_spans spans each
+        const uint32_t seq = s / a.row_spans, k = s - seq * a.row_spans;
+        const int64_t at = k * a.span_len, left = a.seq_len - at;
+        r.seq = seq;
+        r.t0 = seq * a.seq_len + at;
+        r.len = left < a.span_len ? left : a.span_len;
+        r.row0 = seq * a.row_chunks + at / 64;
+        r.first = k == 0;
+        r.last = k + 1 == a.row_spans;
     }
     return r;
+}
+// A sequence's first span and their number.
+__device__ __forceinline__ void spans_of_seq(const SsmArgs &a, uint32_t seq, int64_t &first, int &count) {
+    if (a.spans) {
+        first = a.span_first[seq];
+        count = a.span_first[seq + 1] - static_cast<int>(first);
+    } else {
+        first = static_cast<int64_t>(seq) * a.row_spans;
+        count = a.row_spans;
+    }
+}
+
+// Work item of a block, as gqa_xcd_item but in 32 bits: heads that share b and
+// c follow each other on one XCD.
+__device__ __forceinline__ uint32_t shared_item(uint32_t item, uint32_t grid, uint32_t heads, uint32_t groups) {
+    const uint32_t r = heads / groups, span = 8 * r;
+    if (r > 1) {
+        const uint32_t w = item % span;
+        if (item - w + span <= grid) item = (item - w) + (w % 8) * r + w / 8;
+    }
+    return item;
 }
 
 // Element of a [n][p] state that a lane's register r of tile (nt, pt) holds:
@@ -327,10 +352,11 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
     __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16], sP[kY ? 64 * PS : 16];
     __shared__ __attribute__((aligned(16))) Gates sg[2];
 
-    const int64_t item = gqa_xcd_item(blockIdx.x, gridDim.x, a.heads, a.groups);
-    const int64_t si = item / a.heads;
-    const int h = static_cast<int>(item - si * a.heads);
-    const int g = h / (a.heads / a.groups);
+    const uint32_t heads = a.heads, groups = a.groups;
+    const uint32_t item = shared_item(blockIdx.x, gridDim.x, heads, groups);
+    const uint32_t si = item / heads;
+    const int h = static_cast<int>(item - si * heads);
+    const int g = h / static_cast<int>(heads / groups);
     const bool rev = MODE != kOut && blockIdx.y == 1;
     const Span sp = span_of_block(a, si);
     if (a.spans && sp.len < 0) return;                              // surplus entry
@@ -557,38 +583,39 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
 // a thread.  grid.x: (sequence, head, 1024 values), grid.y: direction.
 template <int N, int P, bool OB>
 __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_join_kernel(SsmArgs a) {
-    constexpr int kParts = N * P / (4 * kSsmThreads);
-    const int64_t item = blockIdx.x / kParts;
+    constexpr uint32_t kParts = N * P / (4 * kSsmThreads);
+    const uint32_t item = blockIdx.x / kParts, heads = a.heads;
     const int piece = static_cast<int>(blockIdx.x % kParts) * kSsmThreads + threadIdx.x;   // (tile, lane)
-    const int64_t seq = item / a.heads;
-    const int h = static_cast<int>(item % a.heads);
+    const uint32_t seq = item / heads, h = item - seq * heads;
     const bool rev = blockIdx.y == 1;
-    const int64_t first = a.span_first[seq], count = a.span_first[seq + 1] - first;
+    int64_t first;
+    int count;
+    spans_of_seq(a, seq, first, count);
     const int tile = piece / 64, l16 = piece % 16, lq = (piece % 64) / 16;
     const float *init = rev ? a.dht : a.h0;
     f32x4 s = zero4();
-    if (init) s = load_state_tile<P, OB>(init + (seq * a.heads + h) * (N * P), tile / (P / 16), tile % (P / 16), l16, lq);
-    const int64_t base = rev ? a.n_spans : 0;
-    constexpr int U = 4;   // spans in flight
-    for (int64_t k0 = 0; k0 < count; k0 += U) {
+    if (init) s = load_state_tile<P, OB>(init + (static_cast<int64_t>(seq) * heads + h) * (N * P), tile / (P / 16), tile % (P / 16), l16, lq);
+    const int64_t base = (rev ? a.n_spans : 0) + first;
+    constexpr int U = 8;   // spans in flight
+    for (int k0 = 0; k0 < count; k0 += U) {
         f32x4 v[U];
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u;
+            const int k = k0 + u;
             v[u] = zero4();
             d[u] = 0.f;
             if (k + 1 < count) {   // the last one's own state leads nowhere
-                const int64_t slot = (base + first + (rev ? count - 1 - k : k)) * a.heads + h;
+                const int64_t slot = (base + (rev ? count - 1 - k : k)) * heads + h;
                 v[u] = *reinterpret_cast<const f32x4 *>(a.span_state + slot * (N * P) + piece * 4);
                 d[u] = a.span_decay[slot];
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u;
+            const int k = k0 + u;
             if (k >= count) break;
-            const int64_t slot = (base + first + (rev ? count - 1 - k : k)) * a.heads + h;
+            const int64_t slot = (base + (rev ? count - 1 - k : k)) * heads + h;
             *reinterpret_cast<f32x4 *>(a.span_state + slot * (N * P) + piece * 4) = s;
             s = s * d[u] + v[u];
         }
