@@ -60,6 +60,7 @@ int64_t norm_bwd_blocks(const NormArgs &a);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream);
 
 // Selective state space scan.
+constexpr int kGateRow = 6 * 64 + 4;     // floats of a (chunk, head) in gates
 constexpr int kTokenPart = 6 * 64 + 4;   // floats of a (chunk, head) in token_part
 struct SsmArgs {
     const void *x, *dt, *b, *c;
@@ -80,6 +81,7 @@ struct SsmArgs {
     const int32_t *span_first;            // [N + 1] first span of each sequence
     int64_t n_spans;                      // entries: an upper bound on the spans
     int64_t span_len;
+    float *gates;                         // [n_chunks][H][kGateRow]; NULL: made inside the walks (not split)
     float *span_state;                    // [directions][n_spans][H][n p]; NULL: not split
     float *span_decay;                    // [directions][n_spans][H]
     // backward
@@ -99,11 +101,15 @@ struct SsmArgs {
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream);
 // Tokens of a span, or 0 where each sequence is walked by one block.
 int64_t ssm_span_len(const SsmArgs &a);
-// Table of spans (or, with span_len 64, of chunks) from the content of
-// cu_seqlens: first [N + 1], table [count].  chunk_first: that of the chunks'
-// table, for the spans' chunk rows (NULL: the entry's own index).
-hipError_t launch_ssm_table(const SsmArgs &a, int64_t span_len, int64_t count, const int32_t *chunk_first,
-                            int32_t *first, int4 *table, hipStream_t stream);
+// Tables of spans and of 64-token chunks from the content of cu_seqlens:
+// first spans [N + 1], chunks [N + 1]; tables [n_spans], [n_chunks].
+struct SsmTables {
+    int32_t *span_first, *chunk_first;
+    int4 *spans, *chunks;
+};
+hipError_t launch_ssm_table(const SsmArgs &a, const SsmTables &t, hipStream_t stream);
+// The gates of every (chunk, head).
+hipError_t launch_ssm_gates(const SsmArgs &a, hipStream_t stream);
 hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream);
 // Slices of a group's heads in a backward call (a.n_chunks set).
 int ssm_slices(const SsmArgs &a);

@@ -427,15 +427,10 @@ struct Carve {
     }
 };
 
-struct SsmTables {
-    int32_t *span_first, *chunk_first;
-    int4 *spans, *chunks;
-    bool split;
-};
 // Parts of a call's workspace; also sets the counts that the launches need.
 // The entries of a table bound the spans: each sequence has at least one and
 // at most its length / span + 1.
-void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, SsmTables &t) {
+void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, gdr::SsmTables &t) {
     std::memset(&t, 0, sizeof(t));
     const int64_t state = static_cast<int64_t>(a.n) * a.p, H = a.heads;
     auto entries = [&](int64_t span) {
@@ -444,57 +439,53 @@ void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, SsmTables &t) {
         return a.n_seq * (each < 1 ? 1 : each);
     };
     a.span_len = gdr::ssm_span_len(a);
-    t.split = a.span_len > 0;
-    if (!t.split) {
-        const int64_t longest = a.cu ? a.total : a.seq_len;
-        a.span_len = (longest / 64 + 1) * 64;
-    }
-    a.n_spans = t.split ? entries(a.span_len) : a.n_seq;
+    const bool split = a.span_len > 0;
+    if (!split) a.span_len = ((a.cu ? a.total : a.seq_len) / 64 + 1) * 64;
+    a.n_spans = split ? entries(a.span_len) : a.n_seq;
     a.row_spans = static_cast<int32_t>((a.seq_len + a.span_len - 1) / a.span_len);
     if (a.row_spans < 1) a.row_spans = 1;
     a.row_chunks = static_cast<int32_t>((a.seq_len + 63) / 64);
     if (a.row_chunks < 1) a.row_chunks = 1;
+    if (!split && !bwd) return;
     const int64_t ways = bwd ? 2 : 1;
-    if (a.cu && (t.split || bwd)) {
+    a.n_chunks = entries(64);
+    if (a.cu) {
         t.span_first = c.take<int32_t>(a.n_seq + 1);
+        t.chunk_first = c.take<int32_t>(a.n_seq + 1);
         t.spans = c.take<int4>(a.n_spans);
+        t.chunks = c.take<int4>(a.n_chunks);
     }
-    if (t.split) {
+    a.gates = c.take<float>(a.n_chunks * H * gdr::kGateRow);
+    if (split) {
         a.span_state = c.take<float>(ways * a.n_spans * H * state);
         a.span_decay = c.take<float>(ways * a.n_spans * H);
     }
     if (bwd) {
-        a.n_chunks = entries(64);
-        if (a.cu) {
-            t.chunk_first = c.take<int32_t>(a.n_seq + 1);
-            t.chunks = c.take<int4>(a.n_chunks);
-        }
         a.chunk_state = c.take<float>(2 * a.n_chunks * H * state);
         a.token_part = c.take<float>(a.n_chunks * H * gdr::kTokenPart);
         a.head_part = c.take<float>(a.n_chunks * H * 3);
+        a.slices = 1;
         if (a.n_chunks > 0) {
             a.slices = gdr::ssm_slices(a);
             a.slice_heads = (a.heads / a.groups + a.slices - 1) / a.slices;
-        } else {
-            a.slices = 1;
         }
         if (a.slices > 1) a.bc_part = c.take<float>(2 * a.slices * a.total * a.groups * a.n);
     }
 }
 
-// Tables, then the walks.
-hipError_t run_ssm(gdr::SsmArgs &a, const SsmTables &t, bool bwd, hipStream_t stream) {
+// Tables and gates, then the walks.
+hipError_t run_ssm(gdr::SsmArgs &a, const gdr::SsmTables &t, bool bwd, hipStream_t stream) {
     hipError_t e = hipSuccess;
-    if (t.chunks && a.n_seq > 0) {
-        e = gdr::launch_ssm_table(a, 64, a.n_chunks, nullptr, t.chunk_first, t.chunks, stream);
-        a.chunks = t.chunks;
+    if (a.gates && a.n_seq > 0) {
+        if (a.cu) {
+            e = gdr::launch_ssm_table(a, t, stream);
+            a.spans = t.spans;
+            a.span_first = t.span_first;
+            a.chunks = t.chunks;
+        }
+        if (e == hipSuccess) e = gdr::launch_ssm_gates(a, stream);
+        if (e != hipSuccess) return e;
     }
-    if (e == hipSuccess && t.spans && a.n_seq > 0) {
-        e = gdr::launch_ssm_table(a, a.span_len, a.n_spans, t.chunk_first, t.span_first, t.spans, stream);
-        a.spans = t.spans;
-        a.span_first = t.span_first;
-    }
-    if (e != hipSuccess) return e;
     return bwd ? gdr::launch_ssm_bwd(a, stream) : gdr::launch_ssm_fwd(a, stream);
 }
 
@@ -743,7 +734,7 @@ int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
         a.y = y->data;
         a.ht = ht ? static_cast<float *>(ht->data) : nullptr;
         Carve size{nullptr};
-        SsmTables t;
+        gdr::SsmTables t;
         carve_ssm(a, false, size, t);
         if (workspace || !workspace_bytes) {
             if ((rc = check_device())) return rc;
@@ -826,7 +817,7 @@ int gdr_ssm_scan_bwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
         a.dbias = f32(ddt_bias);
         a.dh0 = f32(dh0);
         Carve size{nullptr};
-        SsmTables t;
+        gdr::SsmTables t;
         carve_ssm(a, true, size, t);
         if (workspace || !workspace_bytes) {
             if ((rc = check_device())) return rc;

@@ -72,74 +72,104 @@ __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
 // --- tables ---------------------------------------------------------------------
 constexpr int kTableThreads = 1024;
 
-// One block: prefix sums of every sequence's number of spans (at least one,
-// so that a length-0 sequence has a walk that hands its state on), then the
-// entries, each of which finds its sequence by bisection.
-__global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a, int64_t span, int64_t count,
-                                                                       const int32_t *chunk_first, int32_t *first,
-                                                                       int4 *table) {
-    __shared__ int32_t s_scan[kTableThreads];
+// One block: prefix sums of every sequence's numbers of spans and chunks (at
+// least one, so that a length-0 sequence has a walk that hands its state on),
+// then the entries, each of which finds its sequence by bisection.
+__global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a, SsmTables t) {
+    __shared__ int32_t s_span[kTableThreads], s_chunk[kTableThreads];
     const int tid = threadIdx.x;
     auto range = [&](int64_t n, int64_t &b, int64_t &e) {
-        if (a.cu) {
-            b = a.cu[n];
-            e = a.cu[n + 1];
-            b = b < 0 ? 0 : b > a.total ? a.total : b;
-            e = e < b ? b : e > a.total ? a.total : e;
-        } else {
-            b = n * a.seq_len;
-            e = b + a.seq_len;
-        }
+        b = a.cu[n];
+        e = a.cu[n + 1];
+        b = b < 0 ? 0 : b > a.total ? a.total : b;
+        e = e < b ? b : e > a.total ? a.total : e;
     };
-    int64_t carry = 0;
+    auto clamp = [](int64_t v, int64_t most) { return static_cast<int32_t>(v < most ? v : most); };
+    int64_t spans = 0, chunks = 0;
     for (int64_t base = 0; base < a.n_seq; base += kTableThreads) {
-        int32_t mine = 0;
+        int32_t ms = 0, mc = 0;
         if (base + tid < a.n_seq) {
             int64_t b, e;
             range(base + tid, b, e);
-            mine = static_cast<int32_t>((e - b + span - 1) / span);
-            if (mine < 1) mine = 1;
+            ms = static_cast<int32_t>((e - b + a.span_len - 1) / a.span_len);
+            mc = static_cast<int32_t>((e - b + 63) / 64);
+            ms = ms < 1 ? 1 : ms;
+            mc = mc < 1 ? 1 : mc;
         }
-        s_scan[tid] = mine;
+        s_span[tid] = ms;
+        s_chunk[tid] = mc;
         __syncthreads();
-        for (int m = 1; m < kTableThreads; m *= 2) {
-            const int32_t o = tid >= m ? s_scan[tid - m] : 0;
+        const int live = static_cast<int>(a.n_seq - base < kTableThreads ? a.n_seq - base : kTableThreads);
+        for (int m = 1; m < live; m *= 2) {
+            const int32_t os = tid >= m ? s_span[tid - m] : 0, oc = tid >= m ? s_chunk[tid - m] : 0;
             __syncthreads();
-            s_scan[tid] += o;
+            s_span[tid] += os;
+            s_chunk[tid] += oc;
             __syncthreads();
         }
         if (base + tid < a.n_seq) {
-            const int64_t v = carry + s_scan[tid] - mine;
-            first[base + tid] = static_cast<int32_t>(v < count ? v : count);
+            t.span_first[base + tid] = clamp(spans + s_span[tid] - ms, a.n_spans);
+            t.chunk_first[base + tid] = clamp(chunks + s_chunk[tid] - mc, a.n_chunks);
         }
-        carry += s_scan[kTableThreads - 1];
+        spans += s_span[live - 1];
+        chunks += s_chunk[live - 1];
         __syncthreads();
     }
-    if (tid == 0) first[a.n_seq] = static_cast<int32_t>(carry < count ? carry : count);
+    if (tid == 0) {
+        t.span_first[a.n_seq] = clamp(spans, a.n_spans);
+        t.chunk_first[a.n_seq] = clamp(chunks, a.n_chunks);
+    }
     __threadfence_block();
     __syncthreads();
-    const int64_t used = first[a.n_seq];
-    for (int64_t i = tid; i < count; i += kTableThreads) {
-        int4 v = make_int4(0, -1, 0, 0);
-        if (i < used) {
-            int64_t lo = 0, hi = a.n_seq;
-            while (hi - lo > 1) {
-                const int64_t m = (lo + hi) / 2;
-                if (first[m] <= i) lo = m;
-                else hi = m;
+    auto fill = [&](const int32_t *first, int64_t unit, int64_t count, int4 *table) {
+        const int64_t used = first[a.n_seq];
+        for (int64_t i = tid; i < count; i += kTableThreads) {
+            int4 v = make_int4(0, -1, 0, 0);
+            if (i < used) {
+                int64_t lo = 0, hi = a.n_seq;
+                while (hi - lo > 1) {
+                    const int64_t m = (lo + hi) / 2;
+                    if (first[m] <= i) lo = m;
+                    else hi = m;
+                }
+                int64_t b, e;
+                range(lo, b, e);
+                const int64_t at = (i - first[lo]) * unit;
+                const int64_t left = e - b - at;
+                v.x = static_cast<int32_t>(b + at);
+                v.y = static_cast<int32_t>(left < 0 ? 0 : left < unit ? left : unit);
+                v.z = static_cast<int32_t>((static_cast<uint32_t>(lo) << 2) | (i + 1 == first[lo + 1] ? 2u : 0u) |
+                                           (i == first[lo] ? 1u : 0u));
+                v.w = static_cast<int32_t>(t.chunk_first[lo] + at / 64);
             }
-            int64_t b, e;
-            range(lo, b, e);
-            const int64_t at = (i - first[lo]) * span;
-            const int64_t left = e - b - at;
-            v.x = static_cast<int32_t>(b + at);
-            v.y = static_cast<int32_t>(left < 0 ? 0 : left < span ? left : span);
-            v.z = static_cast<int32_t>((static_cast<uint32_t>(lo) << 2) | (i + 1 == first[lo + 1] ? 2u : 0u) |
-                                       (i == first[lo] ? 1u : 0u));
-            v.w = static_cast<int32_t>(chunk_first ? chunk_first[lo] + at / 64 : i);
+            table[i] = v;
         }
-        table[i] = v;
-    }
+    };
+    fill(t.span_first, a.span_len, a.n_spans, t.spans);
+    fill(t.chunk_first, 64, a.n_chunks, t.chunks);
+}
+
+// The gates of every chunk and head, a wave each.
+__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_gates_kernel(SsmArgs a) {
+    __shared__ __attribute__((aligned(16))) Gates sg[kSsmThreads / 64];
+    const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t item = blockIdx.x * (kSsmThreads / 64) + wave;
+    if (item >= a.n_chunks * a.heads) return;
+    const uint32_t row = item / static_cast<uint32_t>(a.heads);
+    const int h = static_cast<int>(item - row * a.heads);
+    int rows;
+    int64_t t0;
+    chunk_of_row(a, row, t0, rows);
+    if (rows <= 0) return;   // no chunk: never read
+    const bool valid = l < rows;
+    Gates &s = sg[wave];
+    chunk_gates(valid ? dt_raw(a, t0 + l, h) : 0.f, head_bias(a, h), a.A[h], valid, s);
+    lds_wait();
+    float *to = a.gates + static_cast<int64_t>(item) * kGateRow;
+    const float *from = reinterpret_cast<const float *>(&s);
+#pragma unroll
+    for (int k = 0; k < 6; ++k) to[64 * k + l] = from[64 * k + l];
+    if (l == 0) to[384] = s.decay;
 }
 
 template <class F>
@@ -164,10 +194,15 @@ int64_t ssm_span_len(const SsmArgs &a) {
     return longest <= 640 || longest <= len ? 0 : len < 64 ? 64 : len;
 }
 
-hipError_t launch_ssm_table(const SsmArgs &a, int64_t span_len, int64_t count, const int32_t *chunk_first,
-                            int32_t *first, int4 *table, hipStream_t stream) {
-    hipLaunchKernelGGL(gdr_ssm_table_kernel, dim3(1), dim3(kTableThreads), 0, stream, a, span_len, count, chunk_first, first,
-                       table);
+hipError_t launch_ssm_table(const SsmArgs &a, const SsmTables &t, hipStream_t stream) {
+    hipLaunchKernelGGL(gdr_ssm_table_kernel, dim3(1), dim3(kTableThreads), 0, stream, a, t);
+    return hipGetLastError();
+}
+
+hipError_t launch_ssm_gates(const SsmArgs &a, hipStream_t stream) {
+    const int64_t items = a.n_chunks * a.heads;
+    if (items > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(gdr_ssm_gates_kernel, dim3(static_cast<uint32_t>((items + 3) / 4)), dim3(kSsmThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -178,12 +213,15 @@ hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream) {
         const int64_t walks = (a.span_state ? a.n_spans : a.n_seq) * a.heads;
         if (walks > 0x7FFFFFFF || a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF) return hipErrorInvalidValue;
         const dim3 grid(static_cast<uint32_t>(walks));
+        const dim3 out(walk_threads(kOut, P));
         if (a.span_state) {
-            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, false>), grid, dim3(walk_threads(kLocal, P)), 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, false, true>), grid, dim3(walk_threads(kLocal, P)), 0, stream, a);
             hipLaunchKernelGGL((gdr_ssm_join_kernel<N, P, false>), dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024))),
                                block, 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kOut, false, true>), grid, out, 0, stream, a);
+        } else {
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kOut, false, false>), grid, out, 0, stream, a);
         }
-        hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kOut, false>), grid, dim3(walk_threads(kOut, P)), 0, stream, a);
         return hipGetLastError();
     });
 }

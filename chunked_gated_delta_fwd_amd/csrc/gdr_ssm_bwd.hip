@@ -28,20 +28,6 @@
 namespace gdr {
 namespace {
 
-// First token and number of tokens (none: rows <= 0) of a chunk row.
-__device__ __forceinline__ void chunk_of_row(const SsmArgs &a, int64_t row, int64_t &t0, int &rows) {
-    if (a.chunks) {
-        const int4 v = a.chunks[row];
-        t0 = v.x;
-        rows = v.y;
-    } else {
-        const uint32_t seq = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.row_chunks);
-        const int64_t at = 64 * (row - static_cast<int64_t>(seq) * a.row_chunks), left = a.seq_len - at;
-        t0 = seq * a.seq_len + at;
-        rows = static_cast<int>(left < 64 ? left : 64);
-    }
-}
-
 // One block of 8 waves per (chunk, group, slice of the group's heads); a wave
 // owns one or two of the (i, j) tiles of the lower triangle, one tile of rows
 // n of db and dc (of half the tokens when n is 64) and one tile of rows p of
@@ -61,7 +47,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     constexpr int kXY = 2 * 64 * PP > 64 * PN ? 2 * 64 * PP : 64 * PN;   // x and dy; c before and after the heads
     constexpr int kE = T::kBf16 ? (N * PE > 64 * PS ? N * PE : 64 * PS) : 64 * PS;
     __shared__ __attribute__((aligned(16))) E sB[64 * PN], sXY[kXY], sE[kE], sPd[64 * PS];
-    __shared__ __attribute__((aligned(16))) Gates sg[2];
+    __shared__ __attribute__((aligned(16))) Gates sg;
     __shared__ __attribute__((aligned(16))) float s_row[4][64], s_col[4][64], s_s[NT][64], s_e[NT][64], s_w[64], s_m[64], s_es[8];
     E *const sX = sXY, *const sY = sXY + 64 * PP, *const sC = sXY;
 
@@ -86,9 +72,11 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
         return chunk_rsrc(static_cast<const E *>(base) + t0 * ld + col, static_cast<uint32_t>(((rows - 1) * ld + cols) * es));
     };
     TileP tx, ty;
+    GateTile<kGradThreads> tg;
     auto load_xy = [&](int h) {
         tx.load(tile_rsrc(a.x, a.ldx, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.ldx * es));
         ty.load(tile_rsrc(a.dy, a.lddy, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.lddy * es));
+        tg.load(a, row, h);
     };
     const float *const Sbase = a.chunk_state, *const Ebase = a.chunk_state + a.n_chunks * a.heads * (N * P);
     f32x4 Sv[PT], Ev[PT];   // this wave's rows n of S and E
@@ -100,23 +88,12 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             Ev[k] = *reinterpret_cast<const f32x4 *>(Ebase + at + k * 256);
         }
     };
-    RawDt raw;   // wave 5: what the next head's gates are made from
-    float bias = 0.f, A = 0.f;
-    auto load_gate = [&](int h) {
-        if (l < rows) raw.load(a, t0 + l, h);
-        bias = head_bias(a, h);
-        A = a.A[h];
-    };
     {
         TileN tb, tc;
         tb.load(tile_rsrc(a.b, a.ldb, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldb * es));
         tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
         tb.store(sB);
         tc.store(sC);
-    }
-    if (wave == 5) {
-        load_gate(h0);
-        chunk_gates(raw.value(a), bias, A, l < rows, sg[0]);
     }
     load_xy(h0);
     load_states(h0);
@@ -150,14 +127,12 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     __syncthreads();
 
     for (int h = h0; h < h1; ++h) {
-        const Gates &s = sg[(h - h0) & 1];
+        const Gates &s = sg;
         tx.store(sX);
         ty.store(sY);
+        tg.store(sg);
         __syncthreads();
-        if (h + 1 < h1) {
-            load_xy(h + 1);
-            if (wave == 5) load_gate(h + 1);
-        }
+        if (h + 1 < h1) load_xy(h + 1);
         // M, W and what they give
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -285,7 +260,6 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
             }
         }
-        if (wave == 5 && h + 1 < h1) chunk_gates(raw.value(a), bias, A, l < rows, sg[(h + 1 - h0) & 1]);
         if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_dt_kernel
             const int tile = l / 16;
             float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f, es_sum = 0.f;
@@ -360,7 +334,6 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
 // The gradient of dt, and each chunk's part of dA, dD and dbias, from the
 // token sums of gdr_ssm_grad_kernel: a wave per (chunk, head), lane = token.
 __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
-    __shared__ Gates sg[kSsmThreads / 64];
     const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t item = static_cast<int64_t>(blockIdx.x) * (kSsmThreads / 64) + wave;
     if (item >= a.n_chunks * a.heads) return;
@@ -376,12 +349,10 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     }
     const bool valid = l < rows;
     const float raw = valid ? dt_raw(a, t0 + l, h) : 0.f, bias = head_bias(a, h), A = a.A[h];
+    const Gates &s = *reinterpret_cast<const Gates *>(a.gates + item * kGateRow);
     const float *in = a.token_part + item * kTokenPart;
     const float rw = in[l], cl = in[64 + l], diag = in[128 + l], m = in[192 + l], st = in[256 + l], et = in[320 + l];
     const float es_sum = in[384];
-    Gates &s = sg[wave];
-    chunk_gates(raw, bias, A, valid, s);
-    lds_wait();
     const float dt = s.dt[l], far = s.ew[l] * et;
     const float v = cl + diag + far;
     float u = rw + s.eg[l] * st - dt * (cl + far);
@@ -461,11 +432,11 @@ hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
         const dim3 grid(static_cast<uint32_t>(walks), 2), walk(walk_threads(kStates, P));
         if (walks > 0) {
             if (a.span_state) {
-                hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, true>), grid, walk, 0, stream, a);
+                hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, true, true>), grid, walk, 0, stream, a);
                 hipLaunchKernelGGL((gdr_ssm_join_kernel<N, P, true>),
                                    dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024)), 2), block, 0, stream, a);
             }
-            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true>), grid, walk, 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true, true>), grid, walk, 0, stream, a);
             hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(static_cast<uint32_t>(grads)), dim3(kGradThreads), 0, stream, a);
         }
         if (walks > 0)

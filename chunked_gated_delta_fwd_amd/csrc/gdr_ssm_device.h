@@ -238,6 +238,26 @@ __device__ __forceinline__ void chunk_gates(float raw, float bias, float A, bool
     if (l == 63) s.decay = __expf(static_cast<float>(end));
 }
 
+// Gates that a pass of its own has made (SsmArgs::gates), on their way to LDS.
+template <int THREADS>
+struct GateTile {
+    static constexpr int kFloats = sizeof(Gates) / 4, kN = (kFloats + THREADS - 1) / THREADS;
+    static_assert(kFloats <= kGateRow);
+    float r[kN];
+    __device__ __forceinline__ void load(const SsmArgs &a, int64_t row, int h) {
+        const __amdgpu_buffer_rsrc_t from = chunk_rsrc(a.gates + (row * a.heads + h) * kGateRow, kGateRow * 4);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) r[k] = __builtin_bit_cast(float, buf_load<4>(from, (threadIdx.x + k * THREADS) * 4));
+    }
+    __device__ __forceinline__ void store(Gates &s) const {
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            const int i = threadIdx.x + k * THREADS;
+            if (i < kFloats) reinterpret_cast<float *>(&s)[i] = r[k];
+        }
+    }
+};
+
 // A span: consecutive whole chunks of one sequence (its last may be ragged),
 // walked by one block per head.  Without a table each sequence is one span.
 struct Span {
@@ -278,6 +298,20 @@ __device__ __forceinline__ Span span_of_block(const SsmArgs &a, uint32_t s) {
     }
     return r;
 }
+// First token and number of tokens (none: rows <= 0) of a chunk row.
+__device__ __forceinline__ void chunk_of_row(const SsmArgs &a, int64_t row, int64_t &t0, int &rows) {
+    if (a.chunks) {
+        const int4 v = a.chunks[row];
+        t0 = v.x;
+        rows = v.y;
+    } else {
+        const uint32_t seq = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.row_chunks);
+        const int64_t at = 64 * (row - static_cast<int64_t>(seq) * a.row_chunks), left = a.seq_len - at;
+        t0 = seq * a.seq_len + at;
+        rows = static_cast<int>(left < 64 ? left : 64);
+    }
+}
+
 // A sequence's first span and their number.
 __device__ __forceinline__ void spans_of_seq(const SsmArgs &a, uint32_t seq, int64_t &first, int &count) {
     if (a.spans) {
@@ -324,6 +358,14 @@ __device__ __forceinline__ void store_state_tile(float *m, int nt, int pt, int l
     }
 }
 
+// A state in a work buffer: tile `tile`, 16 bytes a lane (voff = 16 lane).
+__device__ __forceinline__ f32x4 load_tile(__amdgpu_buffer_rsrc_t r, uint32_t voff, int tile) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, tile * 1024, 0));
+}
+__device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t r, uint32_t voff, int tile, f32x4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), r, voff, tile * 1024, 0);
+}
+
 // Walks of the state over the chunks of a span, one block per (span, head):
 //   kLocal   the state that the span's own tokens make from zero, and its decay
 //   kStates  the state before each chunk, stored for the gradients
@@ -335,10 +377,13 @@ enum WalkMode { kLocal, kStates, kOut };
 // Waves of a block: kOut 4, of 16 or 32 columns p each (with 8, a wave's
 // registers for y and its operands do not fit 4 waves a SIMD, and spill); the
 // other walks one per 16 columns.  waves: a SIMD's, at least.
-constexpr int walk_threads(int mode, int p) { return mode == kOut ? 256 : 4 * p; }
-constexpr int walk_waves(int mode, bool bf16, int p) { return mode != kOut && p == 128 ? (bf16 ? 4 : 2) : (bf16 ? 2 : 1); }
+constexpr int walk_threads(int, int p) { return 4 * p; }
+constexpr int walk_waves(int mode, bool bf16, int p) { return p == 128 ? (bf16 ? 4 : 2) : (bf16 ? 2 : 1); }
 
-template <class T, int N, int P, int MODE, bool OB>
+// PRE: the gates come from memory (a.gates); else the last wave makes each
+// chunk's while the others are at work on the one before (short calls, where
+// a launch more would cost more).
+template <class T, int N, int P, int MODE, bool OB, bool PRE>
 __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf16, P)) gdr_ssm_walk_kernel(SsmArgs a) {
     typedef typename T::E E;
     typedef typename T::F8 F8;
@@ -350,7 +395,7 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
     typedef Tile<T, P, false, TH> TileV;
     constexpr int PU = TileU::kPitch, PC = TileC::kPitch, PV = TileV::kPitch, PS = T::pitch(64, true);
     __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16], sP[kY ? 64 * PS : 16];
-    __shared__ __attribute__((aligned(16))) Gates sg[2];
+    __shared__ __attribute__((aligned(16))) Gates sg[PRE ? 1 : 2];
 
     const uint32_t heads = a.heads, groups = a.groups;
     const uint32_t item = shared_item(blockIdx.x, gridDim.x, heads, groups);
@@ -362,12 +407,14 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
     if (a.spans && sp.len < 0) return;                              // surplus entry
     if (MODE == kLocal && (rev ? sp.first : sp.last)) return;       // nothing follows it
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64);   // the same in every lane
-    const int l = tid % 64, l16 = l % 16, lq = l / 16;
+    const int l = tid % 64, lane16 = l % 16, lane4 = l / 16;
+    int l16 = lane16, lq = lane4;
     const int64_t hb = (static_cast<int64_t>(rev ? 1 : 0) * a.n_spans + si) * a.heads + h;   // slot in the span buffers
 
     f32x4 Z[NT][CT];
     const float *init = rev ? a.dht : a.h0;
     const bool split = MODE != kLocal && a.span_state;
+    const __amdgpu_buffer_rsrc_t mine = chunk_rsrc(a.span_state + hb * (N * P), N * P * 4);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -375,7 +422,7 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
             const int pt = CT * wave + c;
             Z[nt][c] = zero4();
             if (MODE == kLocal) continue;
-            if (split) Z[nt][c] = *reinterpret_cast<const f32x4 *>(a.span_state + hb * (N * P) + ((nt * PT + pt) * 64 + l) * 4);
+            if (split) Z[nt][c] = load_tile(mine, 16 * l, nt * PT + pt);
             else if (init) Z[nt][c] = load_state_tile<P, OB>(init + (sp.seq * a.heads + h) * (N * P), nt, pt, l16, lq);
         }
 
@@ -387,8 +434,9 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
     TileU tu;
     TileC tc;
     TileV tv;
-    RawDt raw;   // the last wave: dt of the chunk after the prefetched one
-    const float bias = head_bias(a, h), A = a.A[h];
+    GateTile<TH> tg;
+    RawDt raw;   // not PRE, the last wave: dt of the chunk after the prefetched one
+    const float bias = PRE ? 0.f : head_bias(a, h), A = PRE ? 0.f : a.A[h];
     auto chunk_at = [&](int k) { return rev ? chunks - 1 - k : k; };
     auto rows_of = [&](int c) {
         const int64_t left = sp.len - 64 * static_cast<int64_t>(c);
@@ -405,6 +453,10 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
             const uint32_t w = static_cast<uint32_t>(((rows - 1) * a.ldc + N) * es);
             tc.load(chunk_rsrc(cb + t * a.ldc, w), static_cast<uint32_t>(a.ldc * es));
         }
+        if constexpr (PRE) {
+            const int64_t row = sp.row0 + c;   // within the table, whatever cu_seqlens holds
+            tg.load(a, row < a.n_chunks ? row : a.n_chunks - 1, h);
+        }
     };
     auto load_raw = [&](int k) {
         const int c = chunk_at(k);
@@ -414,10 +466,11 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
         tu.store(sU);
         tv.store(sV);
         if constexpr (kY) tc.store(sC);
+        if constexpr (PRE) tg.store(sg[0]);
     };
     if (chunks > 0) {
         load_tiles(0);
-        if (wave == WAVES - 1) {
+        if (!PRE && wave == WAVES - 1) {
             load_raw(0);
             chunk_gates(raw.value(a), bias, A, l < rows_of(chunk_at(0)), sg[0]);
             if (chunks > 1) load_raw(1);
@@ -434,17 +487,22 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
     for (int k = 0; k < chunks; ++k) {
         const int c = chunk_at(k), rows = rows_of(c);
         const int64_t t = sp.t0 + 64 * static_cast<int64_t>(c);
-        const Gates &s = sg[k & 1];
+        const Gates &s = sg[PRE ? 0 : k & 1];
         if (MODE == kStates && sp.row0 + c < a.n_chunks) {   // always, unless cu_seqlens breaks its preconditions
-            float *to = a.chunk_state + ((static_cast<int64_t>(rev ? 1 : 0) * a.n_chunks + sp.row0 + c) * a.heads + h) * (N * P);
+            const __amdgpu_buffer_rsrc_t to = chunk_rsrc(
+                a.chunk_state + ((static_cast<int64_t>(rev ? 1 : 0) * a.n_chunks + sp.row0 + c) * a.heads + h) * (N * P), N * P * 4);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < CT; ++i) *reinterpret_cast<f32x4 *>(to + ((nt * PT + CT * wave + i) * 64 + l) * 4) = Z[nt][i];
+                for (int i = 0; i < CT; ++i) store_tile(to, 16 * l, nt * PT + CT * wave + i, Z[nt][i]);
         }
         __syncthreads();   // this chunk's tiles and gates are in LDS
         if (k + 1 < chunks) load_tiles(k + 1);
 
+        // The lane's coordinates are opaque to the compiler in each phase: LDS
+        // addresses are made there, not kept over the whole loop, where they
+        // would take the registers that 4 waves a SIMD need
+        asm volatile("" : "+v"(l16), "+v"(lq));
         if constexpr (kY) {
             // scores, transposed: tile (j, i) of B C^T; a wave takes tiles wave, wave + WAVES, .. of the ten
 #pragma unroll
@@ -470,10 +528,11 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
                 T::store4(sP + i * PS + T::template col<true>(j0), p);
             }
         }
-        if (wave == WAVES - 1 && k + 1 < chunks) {   // the next chunk's gates (the first two waves have one score tile more)
+        if (!PRE && wave == WAVES - 1 && k + 1 < chunks) {   // the next chunk's gates (the first two waves have one score tile more)
             chunk_gates(raw.value(a), bias, A, l < rows_of(chunk_at(k + 1)), sg[(k + 1) & 1]);
             if (k + 2 < chunks) load_raw(k + 2);
         }
+        asm volatile("" : "+v"(l16), "+v"(lq));
         F8 v[2][CT];   // x (or dy) with tokens as k
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -507,6 +566,7 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
                     Y[it][i] = Y[it][i] * eg + T::load4(sV + (16 * it + l16) * PV + 16 * (CT * wave + i) + 4 * lq) * dh;
             }
             __syncthreads();   // the scores are in LDS
+            asm volatile("" : "+v"(l16), "+v"(lq));
             uint32_t ldy = static_cast<uint32_t>(a.heads * P * sizeof(E));
             asm volatile("" : "+s"(ldy));   // as for the tiles' offsets
             E *yb = static_cast<E *>(a.y) + (t * a.heads + h) * P;
@@ -528,6 +588,7 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
             }
         }
         __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" : "+v"(l16), "+v"(lq));
         // Z <- decay Z + U^T (w V)
         const float decay = s.decay;
         if (MODE == kLocal) total += s.ghi[63] + s.glo[63];
@@ -561,8 +622,11 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
         if (k + 1 < chunks) store_tiles();
     }
 
+    l16 = lane16;
+    lq = lane4;
+    asm volatile("" : "+v"(l16), "+v"(lq));
     float *out = nullptr;
-    if (MODE == kLocal) out = a.span_state + hb * (N * P);
+    if (MODE == kLocal) out = a.span_state;
     else if (MODE == kOut && sp.last && a.ht) out = a.ht + (sp.seq * a.heads + h) * (N * P);
     else if (MODE == kStates && rev && sp.first && a.dh0) out = a.dh0 + (sp.seq * a.heads + h) * (N * P);
     if (out) {
@@ -571,7 +635,7 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 const int pt = CT * wave + i;
-                if (MODE == kLocal) *reinterpret_cast<f32x4 *>(out + ((nt * PT + pt) * 64 + l) * 4) = Z[nt][i];
+                if (MODE == kLocal) store_tile(mine, 16 * l, nt * PT + pt, Z[nt][i]);
                 else store_state_tile<P, OB>(out, nt, pt, l16, lq, Z[nt][i]);
             }
     }
