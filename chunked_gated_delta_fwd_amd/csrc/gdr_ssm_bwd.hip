@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     int64_t t0;
     chunk_of_row(a, row, t0, rows);
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64);   // the same in every lane
-    const int l = tid % 64, l16 = l % 16, lq = l / 16;
+    const int l = tid % 64;
+    int l16 = l % 16, lq = l / 16;
     if (rows <= 0) return;   // a length-0 sequence's row, or a surplus one
     const int nt = wave % NT, it0 = wave / NT * IW;     // db, dc: rows 16 nt .., tokens 16 it0 ..
     const int pt = wave % PT, jt0 = wave / PT * JW;     // dx: rows 16 pt .., tokens 16 jt0 ..
@@ -73,10 +74,12 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     };
     TileP tx, ty;
     GateTile<kGradThreads> tg;
+    float d_next;
     auto load_xy = [&](int h) {
         tx.load(tile_rsrc(a.x, a.ldx, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.ldx * es));
         ty.load(tile_rsrc(a.dy, a.lddy, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.lddy * es));
         tg.load(a, row, h);
+        d_next = a.D ? a.D[h] : 0.f;
     };
     const float *const Sbase = a.chunk_state, *const Ebase = a.chunk_state + a.n_chunks * a.heads * (N * P);
     f32x4 Sv[PT], Ev[PT];   // this wave's rows n of S and E
@@ -132,7 +135,12 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
         ty.store(sY);
         tg.store(sg);
         __syncthreads();
-        if (h + 1 < h1) load_xy(h + 1);
+        // Unconditional (the last head's own once more), so that a later wait
+        // for the states can count these as still on their way
+        const float dh = d_next;
+        load_xy(h + 1 < h1 ? h + 1 : h);
+        // opaque coordinates, as in the walks: addresses are made in each phase
+        asm volatile("" : "+v"(l16), "+v"(lq));
         // M, W and what they give
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -170,7 +178,19 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             col = sum_rows(col);
             if (lq == 0) s_col[ti[k]][j] = col;
         }
+        asm volatile("" : "+v"(l16), "+v"(lq));
         // S dy^T and E x^T for this wave's rows n
+        if (first_n) {
+            float es_sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < PT; ++k) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
+                if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PE + 16 * k + 4 * lq, Ev[k]);
+            }
+            es_sum = sum64(es_sum);
+            if (l == 0) s_es[wave] = es_sum;
+        }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             f32x4 acc[IW];
@@ -178,14 +198,15 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             for (int i = 0; i < IW; ++i) acc[i] = zero4();
 #pragma unroll
             for (int q = 0; q < P / 32; ++q) {
-                F8 st[T::kParts];
+                F8 st[T::kParts], f[IW];
+#pragma unroll
+                for (int i = 0; i < IW; ++i) f[i] = T::template kfrag<true>((side ? sX : sY) + (16 * (it0 + i) + l16) * PP, q, lq);
                 T::split(side ? Ev[2 * q] : Sv[2 * q], side ? Ev[2 * q + 1] : Sv[2 * q + 1], st);
+                if constexpr (T::kBf16) __builtin_amdgcn_sched_barrier(0);   // the reads together, ahead of the products
 #pragma unroll
-                for (int i = 0; i < IW; ++i) {
-                    const F8 f = T::template kfrag<true>((side ? sX : sY) + (16 * (it0 + i) + l16) * PP, q, lq);
+                for (int e = T::kParts - 1; e >= 0; --e)
 #pragma unroll
-                    for (int e = T::kParts - 1; e >= 0; --e) acc[i] = T::mma(st[e], f, acc[i]);
-                }
+                    for (int i = 0; i < IW; ++i) acc[i] = T::mma(st[e], f[i], acc[i]);
             }
 #pragma unroll
             for (int i = 0; i < IW; ++i) {
@@ -201,20 +222,10 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 if (lq == 0) (side ? s_e : s_s)[nt][at] = d;
             }
         }
-        if (first_n) {
-            float es_sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < PT; ++k) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
-                if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PE + 16 * k + 4 * lq, Ev[k]);
-            }
-            es_sum = sum64(es_sum);
-            if (l == 0) s_es[wave] = es_sum;
-        }
         __syncthreads();
-        if (h + 1 < h1) load_states(h + 1);
+        load_states(h + 1 < h1 ? h + 1 : h);
 
+        asm volatile("" : "+v"(l16), "+v"(lq));
         // dx for this wave's rows p
         {
             f32x4 X[JW], V[JW];
@@ -236,11 +247,12 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                             v[b][r] = Ep[(((2 * q + b) * PT + pt) * 64 + 16 * (l16 / 4) + 4 * lq + r) * 4 + l16 % 4];
                     e = T::round(v[0], v[1]);
                 }
+                F8 f[JW];
 #pragma unroll
-                for (int j = 0; j < JW; ++j)
-                    V[j] = T::mma(e, T::template kfrag<true>(sB + (16 * (jt0 + j) + l16) * PN, q, lq), V[j]);
+                for (int j = 0; j < JW; ++j) f[j] = T::template kfrag<true>(sB + (16 * (jt0 + j) + l16) * PN, q, lq);
+#pragma unroll
+                for (int j = 0; j < JW; ++j) V[j] = T::mma(e, f[j], V[j]);
             }
-            const float dh = a.D ? a.D[h] : 0.f;
             const uint32_t ldx = static_cast<uint32_t>(a.heads * P * es);
             const __amdgpu_buffer_rsrc_t rx = chunk_rsrc(static_cast<E *>(a.dx) + (t0 * a.heads + h) * P,
                                                          static_cast<uint32_t>((rows - 1) * ldx + P * es));
@@ -286,6 +298,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
         __syncthreads();
     }
 
+    asm volatile("" : "+v"(l16), "+v"(lq));
     // the heads' L M dt parts: dc += R B, db += R^T C
     {
         TileN tc;
