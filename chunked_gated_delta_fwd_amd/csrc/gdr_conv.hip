@@ -27,9 +27,10 @@ __device__ __forceinline__ void ldv(const void *base, int64_t i, float (&o)[VEC]
     if constexpr (VEC == 1) {
         o[0] = load_scalar<BF16>(base, i);
     } else if constexpr (BF16) {
-        const v4u32 u = *reinterpret_cast<const v4u32 *>(reinterpret_cast<const uint16_t *>(base) + i);
+        typedef unsigned int Piece __attribute__((ext_vector_type(VEC / 2)));
+        const Piece u = *reinterpret_cast<const Piece *>(reinterpret_cast<const uint16_t *>(base) + i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < VEC / 2; ++e) {
             o[2 * e] = __uint_as_float(u[e] << 16);
             o[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
         }
@@ -45,11 +46,12 @@ __device__ __forceinline__ void stv(void *base, int64_t i, const float (&o)[VEC]
         if constexpr (BF16) reinterpret_cast<uint16_t *>(base)[i] = bf16_bits(o[0]);
         else reinterpret_cast<float *>(base)[i] = o[0];
     } else if constexpr (BF16) {
-        v4u32 u;
+        typedef unsigned int Piece __attribute__((ext_vector_type(VEC / 2)));
+        Piece u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < VEC / 2; ++e)
             u[e] = bf16_bits(o[2 * e]) | (static_cast<uint32_t>(bf16_bits(o[2 * e + 1])) << 16);
-        *reinterpret_cast<v4u32 *>(reinterpret_cast<uint16_t *>(base) + i) = u;
+        *reinterpret_cast<Piece *>(reinterpret_cast<uint16_t *>(base) + i) = u;
     } else {
         f32x4 u;
 #pragma unroll
@@ -231,8 +233,6 @@ __global__ void __launch_bounds__(kThreads) gdr_conv_step_kernel(ConvArgs a) {
 // over the strip in registers, over the block's strips through LDS in a fixed
 // order, over blocks by a second kernel (no atomics: the same bits every run).
 
-constexpr int kBwdStrip = 32;
-
 // lanes of a block along the channels: a power of two up to 64
 __host__ __device__ inline int conv_bwd_lanes(int64_t nvec) {
     int c = 1;
@@ -248,7 +248,8 @@ __device__ __forceinline__ float act_grad(float z, float dy, bool silu) {
 }
 
 template <bool BF16, int W, int VEC>
-__global__ void __launch_bounds__(kThreads) gdr_conv_bwd_kernel(ConvArgs a, int64_t main_blocks, int64_t row_blocks) {
+__global__ void __launch_bounds__(kThreads) gdr_conv_bwd_kernel(ConvArgs a, int64_t strip, int64_t main_blocks,
+                                                                 int64_t row_blocks) {
     const int64_t nvec = a.ch / VEC;
     float w[VEC][W], bias[VEC];
 #pragma unroll
@@ -318,8 +319,8 @@ __global__ void __launch_bounds__(kThreads) gdr_conv_bwd_kernel(ConvArgs a, int6
 #pragma unroll
         for (int j = 0; j <= W; ++j) acc[v][j] = 0.f;
 
-    const int64_t t0 = (rb * strips + sub) * kBwdStrip;
-    const int64_t t1 = t0 + kBwdStrip < a.total ? t0 + kBwdStrip : a.total;
+    const int64_t t0 = (rb * strips + sub) * strip;
+    const int64_t t1 = t0 + strip < a.total ? t0 + strip : a.total;
     for (int64_t t = live ? t0 : t1; t < t1;) {
         const int64_t n = seq_of(a, t);
         int64_t s, e;
@@ -444,8 +445,9 @@ __global__ void __launch_bounds__(64) gdr_conv_wsum_kernel(ConvArgs a, int64_t r
     else if (a.db) a.db[c] = v;
 }
 
-// Calls f.template operator()<BF16, W, VEC>() for the call's type, taps and piece.
-template <class F>
+// Calls f.template operator()<BF16, W, VEC>() for the call's type, taps and
+// piece; VECB: channels of a bf16 piece.
+template <int VECB, class F>
 hipError_t by_conv(const ConvArgs &a, F f) {
     auto width = [&]<bool BF16, int VEC>() {
         switch (a.width) {
@@ -454,16 +456,20 @@ hipError_t by_conv(const ConvArgs &a, F f) {
         default: return f.template operator()<BF16, 4, VEC>();
         }
     };
-    if (a.bf16) return a.vec ? width.template operator()<true, 8>() : width.template operator()<true, 1>();
+    if (a.bf16) return a.vec ? width.template operator()<true, VECB>() : width.template operator()<true, 1>();
     return a.vec ? width.template operator()<false, 4>() : width.template operator()<false, 1>();
 }
 
-int64_t pieces(int32_t ch, int32_t bf16, int32_t vec) { return vec ? ch / (bf16 ? 8 : 4) : ch; }
+int64_t pieces(int32_t ch, int32_t bf16, int32_t vec, int vecb) { return vec ? ch / (bf16 ? vecb : 4) : ch; }
+
+// Channels of a bf16 piece in the backward pass: its windows and sums for 8
+// take over 200 registers, 2 waves a SIMD.
+constexpr int kBwdVec = 4;
 
 }  // namespace
 
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t stream) {
-    const int64_t nvec = pieces(a.ch, a.bf16, a.vec);
+    const int64_t nvec = pieces(a.ch, a.bf16, a.vec, 8);
     // Strips of 64 tokens re-read 3 rows in 67; shorter ones when there would
     // be fewer than 8 waves a CU otherwise.
     int64_t strip = 64;
@@ -471,7 +477,7 @@ hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t stream) {
     const int64_t n_strips = (a.total + strip - 1) / strip;
     const int64_t blocks = ((n_strips + (a.st ? a.n_seq : 0)) * nvec + kThreads - 1) / kThreads;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    return by_conv(a, [&]<bool BF16, int W, int VEC>() {
+    return by_conv<8>(a, [&]<bool BF16, int W, int VEC>() {
         hipLaunchKernelGGL((gdr_conv_fwd_kernel<BF16, W, VEC>), dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0,
                            stream, a, strip, n_strips, blocks);
         return hipGetLastError();
@@ -479,36 +485,50 @@ hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t stream) {
-    const int64_t blocks = (pieces(a.ch, a.bf16, a.vec) * a.n_seq + kThreads - 1) / kThreads;
+    const int64_t blocks = (pieces(a.ch, a.bf16, a.vec, 8) * a.n_seq + kThreads - 1) / kThreads;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    return by_conv(a, [&]<bool BF16, int W, int VEC>() {
+    return by_conv<8>(a, [&]<bool BF16, int W, int VEC>() {
         hipLaunchKernelGGL((gdr_conv_step_kernel<BF16, W, VEC>), dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0,
                            stream, a);
         return hipGetLastError();
     });
 }
 
-int64_t conv_bwd_rows(int64_t total, int32_t ch, int32_t bf16, int32_t vec) {
-    const int64_t per = static_cast<int64_t>(kThreads / conv_bwd_lanes(pieces(ch, bf16, vec))) * kBwdStrip;
-    return (total + per - 1) / per;
+// Strips of 64 tokens (3 rows re-read on either side, one row of sums stored
+// for the block's strips); shorter ones while there are less than 4 blocks a CU.
+struct BwdSplit {
+    int64_t strip, rows, blocks;
+};
+static BwdSplit bwd_split(int64_t total, int32_t ch, int32_t bf16, int32_t vec) {
+    const int64_t nvec = pieces(ch, bf16, vec, kBwdVec);
+    const int lanes = conv_bwd_lanes(nvec);
+    BwdSplit s;
+    s.strip = 128;
+    do {
+        s.strip /= 2;
+        const int64_t per = kThreads / lanes * s.strip;
+        s.rows = (total + per - 1) / per;
+        s.blocks = s.rows * ((nvec + lanes - 1) / lanes);
+    } while (s.strip > 8 && s.blocks < 1024);
+    return s;
 }
 
+int64_t conv_bwd_rows(int64_t total, int32_t ch, int32_t bf16, int32_t vec) { return bwd_split(total, ch, bf16, vec).rows; }
+
 hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t stream) {
-    const int64_t nvec = pieces(a.ch, a.bf16, a.vec);
-    const int lanes = conv_bwd_lanes(nvec);
-    const int64_t rows = conv_bwd_rows(a.total, a.ch, a.bf16, a.vec);
-    const int64_t main_blocks = rows * ((nvec + lanes - 1) / lanes);
-    const int64_t blocks = main_blocks + (a.ds0 ? (a.n_seq * nvec + kThreads - 1) / kThreads : 0);
+    const int64_t nvec = pieces(a.ch, a.bf16, a.vec, kBwdVec);
+    const BwdSplit s = bwd_split(a.total, a.ch, a.bf16, a.vec);
+    const int64_t blocks = s.blocks + (a.ds0 ? (a.n_seq * nvec + kThreads - 1) / kThreads : 0);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    return by_conv(a, [&]<bool BF16, int W, int VEC>() {
+    return by_conv<kBwdVec>(a, [&]<bool BF16, int W, int VEC>() {
         if (blocks > 0)
             hipLaunchKernelGGL((gdr_conv_bwd_kernel<BF16, W, VEC>), dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0,
-                               stream, a, main_blocks, rows);
+                               stream, a, s.strip, s.blocks, s.rows);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int64_t cols = static_cast<int64_t>(a.ch) * (W + 1);
         hipLaunchKernelGGL((gdr_conv_wsum_kernel<W>), dim3(static_cast<uint32_t>((cols + 63) / 64)), dim3(64), 0, stream,
-                           a, rows);
+                           a, s.rows);
         return hipGetLastError();
     });
 }

@@ -52,7 +52,7 @@ struct NormArgs {
     const void *doq, *dok;
     void *dq, *dk;
     float *dwq, *dwk;                     // [d], NULL: no weights
-    float *part;                          // [norm_bwd_blocks][2][d]
+    float *part;                          // [norm_bwd_blocks][d]
     int64_t lddoq, lddok;
 };
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream);

@@ -671,7 +671,7 @@ int gdr_qk_norm_rope_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_ten
         a.dwq = dwq ? static_cast<float *>(dwq->data) : nullptr;
         a.dwk = dwk ? static_cast<float *>(dwk->data) : nullptr;
         const bool sums = a.dwq || a.dwk;
-        const size_t need = sums ? static_cast<size_t>(gdr::norm_bwd_blocks(a)) * 2 * static_cast<size_t>(d) * 4 : 0;
+        const size_t need = sums ? static_cast<size_t>(gdr::norm_bwd_blocks(a)) * static_cast<size_t>(d) * 4 : 0;
         if (workspace || !workspace_bytes)
             if ((rc = check_device())) return rc;
         Workspace ws;

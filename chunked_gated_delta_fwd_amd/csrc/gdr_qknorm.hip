@@ -14,6 +14,7 @@
 // group keeps one token and walks its heads, so cos and sin are read once per
 // token and slice of heads.  All arithmetic is fp32; outputs are rounded once.
 #include "gdr_device.h"
+#include "gdr_lanes.h"
 #include "gdr_mixer.h"
 
 namespace gdr {
@@ -53,14 +54,6 @@ __device__ __forceinline__ void st8f(void *base, int64_t i, const float (&o)[8])
         p[0] = f32x4{o[0], o[1], o[2], o[3]};
         p[1] = f32x4{o[4], o[5], o[6], o[7]};
     }
-}
-
-// sum over the lanes of a row (a power of two of neighbouring lanes)
-template <int LANES>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-    for (int m = 1; m < LANES; m *= 2) x += __shfl_xor(x, m);
-    return x;
 }
 
 // A lane's part of its token's rotation: y = x * c + partner(x) * s
@@ -125,115 +118,133 @@ __device__ __forceinline__ void rotate(const NormArgs &a, const Turn &t, bool ba
     }
 }
 
-// A work item: one token and `per` of its q heads or of its k heads.
-struct Item {
-    int64_t token;
-    int first, end;
-    bool is_k;
+// The q or the k side of a call: a block works on one of them, on items of a
+// token and `per` of its heads.
+struct Side {
+    int heads, per, slices;
+    int64_t items;
 };
-__device__ __forceinline__ Item item_of(const NormArgs &a, int64_t i, int per, int slices_q, int slices) {
-    Item r;
-    r.token = i / slices;
-    int s = static_cast<int>(i - r.token * slices);
-    r.is_k = s >= slices_q;
-    if (r.is_k) s -= slices_q;
-    const int heads = r.is_k ? a.hk : a.hq;
-    r.first = s * per;
-    r.end = r.first + per < heads ? r.first + per : heads;
-    return r;
+__host__ __device__ inline Side side_of(int64_t tokens, int heads, int most) {
+    Side s;
+    s.heads = heads;
+    s.per = heads < most ? heads : most;
+    s.slices = (heads + s.per - 1) / s.per;
+    s.items = tokens * s.slices;
+    return s;
+}
+
+// Of `blocks` blocks, blocks_k work on k, evenly spread among q's: a token's q
+// and k are then read at about the same time (in two runs one after the other
+// the forward pass took 230 us where it takes 213, at 65536 tokens of 16 and 16
+// heads of 128).  The block's number on its side is left in `mine`.
+__device__ __forceinline__ bool side_of_block(int64_t blocks_k, int64_t blocks, int64_t &mine) {
+    const int64_t b = blockIdx.x, k = b * blocks_k / blocks;
+    const bool is_k = (b + 1) * blocks_k / blocks != k;
+    mine = is_k ? k : b - k;
+    return is_k;
 }
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int64_t items, int per, int slices_q,
-                                                                 int slices) {
+__global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int most, int64_t blocks_k) {
     constexpr int LANES = D / 8, ROWS = kThreads / LANES;
     const int l = threadIdx.x % LANES;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / LANES;
-    const bool live = i < items;
-    const Item it = item_of(a, live ? i : items - 1, per, slices_q, slices);
-    const void *in = it.is_k ? a.k : a.q, *wp = it.is_k ? a.wk : a.wq;
-    void *out = it.is_k ? a.ok : a.oq;
-    const int64_t at = it.token * (it.is_k ? a.ldk : a.ldq) + 8 * l;
-    const int64_t to = it.token * (it.is_k ? a.hk : a.hq) * D + 8 * l;
+    int64_t mine;
+    const bool is_k = side_of_block(blocks_k, gridDim.x, mine);
+    const Side sd = side_of(a.tokens, is_k ? a.hk : a.hq, most);
+    const int64_t i0 = mine * ROWS + threadIdx.x / LANES;
+    const bool live = i0 < sd.items;
+    const int64_t i = live ? i0 : sd.items - 1;
+    const int64_t token = sd.slices == 1 ? i : i / sd.slices;
+    const int first = static_cast<int>(i - token * sd.slices) * sd.per;
+    const int count = !live ? 0 : first + sd.per < sd.heads ? sd.per : sd.heads - first;
+    const void *in = is_k ? a.k : a.q, *wp = is_k ? a.wk : a.wq;
+    void *out = is_k ? a.ok : a.oq;
+    const int64_t at = token * (is_k ? a.ldk : a.ldq) + static_cast<int64_t>(first) * D + 8 * l;
+    const int64_t to = (token * sd.heads + first) * D + 8 * l;
     const float inv_m = a.rms ? 1.f / D : 1.f;
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = 1.f;
     if (wp) ld8f<BF16>(wp, 8 * l, w);
     Turn t;
-    if (a.rot) load_turn<LANES>(a, it.token, l, t);
+    if (a.rot) load_turn<LANES>(a, token, l, t);
     constexpr int U = 4;
     // every lane of a wave runs the same number of rows (the exchanges need
-    // them all): `per` of them, those past the slice read and store nothing
-    for (int h0 = 0; h0 < per; h0 += U) {
+    // them all): those past the item's heads read and store nothing
+    for (int h0 = 0; h0 < sd.per; h0 += U) {
         float x[U][8];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = it.first + h0 + u;
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-            if (h0 + u < per && h < it.end) ld8f<BF16>(in, at + static_cast<int64_t>(h) * D, x[u]);
+            if (h0 + u < count) ld8f<BF16>(in, at + static_cast<int64_t>(h0 + u) * D, x[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = it.first + h0 + u;
             float s = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) s += x[u][e] * x[u][e];
-            const float inv = 1.f / sqrtf(row_sum<LANES>(s) * inv_m + a.eps);
+            const float inv = 1.f / sqrtf(lane_sum<LANES>(s) * inv_m + a.eps);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[u][e] *= inv * w[e];
             if (a.rot) rotate(a, t, false, x[u]);
-            if (live && h0 + u < per && h < it.end) st8f<BF16>(out, to + static_cast<int64_t>(h) * D, x[u]);
+            if (h0 + u < count) st8f<BF16>(out, to + static_cast<int64_t>(h0 + u) * D, x[u]);
         }
     }
 }
 
 // Backward.  With g = R^T do (the rotation undone) and r = 1 / sqrt(s + eps):
 //   dw = sum over rows of g x r,   dx = r (g w) - x r^3 (sum g w x) [/ d]
-// A block walks several items; dw is summed in registers, then over the
-// block's rows in a fixed order, then over blocks by a second kernel.
+// A block walks several items, all of q or all of k; dw is summed in registers,
+// then over the block's rows in a fixed order, then over blocks (q's rows of
+// partial sums first) by a second kernel.
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kThreads) gdr_norm_bwd_kernel(NormArgs a, int64_t items, int per, int slices_q,
-                                                                 int slices) {
+__global__ void __launch_bounds__(kThreads) gdr_norm_bwd_kernel(NormArgs a, int most, int64_t blocks_k) {
     constexpr int LANES = D / 8, ROWS = kThreads / LANES;
     const int l = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    int64_t mine;
+    const bool is_k = side_of_block(blocks_k, gridDim.x, mine);
+    const void *in = is_k ? a.k : a.q, *gin = is_k ? a.dok : a.doq, *wp = is_k ? a.wk : a.wq;
+    void *out = is_k ? a.dk : a.dq;
+    const int64_t ld = is_k ? a.ldk : a.ldq, ldg = is_k ? a.lddok : a.lddoq;
+    const Side sd = side_of(a.tokens, is_k ? a.hk : a.hq, most);
+    const int heads = sd.heads, per = sd.per;
+    const int64_t items = sd.items;
+    const int64_t stride = (is_k ? blocks_k : gridDim.x - blocks_k) * ROWS;
     const float inv_m = a.rms ? 1.f / D : 1.f;
-    float aq[8], ak[8];
+    float w[8], acc[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * ROWS;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS; base < items; base += stride) {
-        const int64_t i = base + sub;
-        const bool live = i < items;
-        const Item it = item_of(a, live ? i : items - 1, per, slices_q, slices);
-        const void *in = it.is_k ? a.k : a.q, *gin = it.is_k ? a.dok : a.doq, *wp = it.is_k ? a.wk : a.wq;
-        void *out = it.is_k ? a.dk : a.dq;
-        const int64_t at = it.token * (it.is_k ? a.ldk : a.ldq) + 8 * l;
-        const int64_t gat = it.token * (it.is_k ? a.lddok : a.lddoq) + 8 * l;
-        const int64_t to = it.token * (it.is_k ? a.hk : a.hq) * D + 8 * l;
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.f;
-        if (wp) ld8f<BF16>(wp, 8 * l, w);
+    for (int e = 0; e < 8; ++e) {
+        w[e] = 1.f;
+        acc[e] = 0.f;
+    }
+    if (wp) ld8f<BF16>(wp, 8 * l, w);
+    for (int64_t base = mine * ROWS; base < items; base += stride) {
+        const bool live = base + sub < items;
+        const int64_t i = live ? base + sub : items - 1;
+        const int64_t token = sd.slices == 1 ? i : i / sd.slices;
+        const int first = static_cast<int>(i - token * sd.slices) * per;
+        const int count = !live ? 0 : first + per < heads ? per : heads - first;
+        const int64_t at = token * ld + static_cast<int64_t>(first) * D + 8 * l;
+        const int64_t gat = token * ldg + static_cast<int64_t>(first) * D + 8 * l;
+        const int64_t to = (token * heads + first) * D + 8 * l;
         Turn t;
-        if (a.rot) load_turn<LANES>(a, it.token, l, t);
-        constexpr int U = 2;
+        if (a.rot) load_turn<LANES>(a, token, l, t);
+        constexpr int U = 4;
+        // every lane of a wave runs the same number of rows, for the exchanges
         for (int h0 = 0; h0 < per; h0 += U) {
             float x[U][8], g[U][8];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = it.first + h0 + u;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[u][e] = g[u][e] = 0.f;
-                if (live && h0 + u < per && h < it.end) {
-                    ld8f<BF16>(in, at + static_cast<int64_t>(h) * D, x[u]);
-                    ld8f<BF16>(gin, gat + static_cast<int64_t>(h) * D, g[u]);
+                if (h0 + u < count) {
+                    ld8f<BF16>(in, at + static_cast<int64_t>(h0 + u) * D, x[u]);
+                    ld8f<BF16>(gin, gat + static_cast<int64_t>(h0 + u) * D, g[u]);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = it.first + h0 + u;
                 if (a.rot) rotate(a, t, true, g[u]);
                 float s = 0.f, d = 0.f;
 #pragma unroll
@@ -241,53 +252,51 @@ __global__ void __launch_bounds__(kThreads) gdr_norm_bwd_kernel(NormArgs a, int6
                     s += x[u][e] * x[u][e];
                     d += g[u][e] * w[e] * x[u][e];
                 }
-                const float inv = 1.f / sqrtf(row_sum<LANES>(s) * inv_m + a.eps);
-                const float back = row_sum<LANES>(d) * inv_m * inv * inv * inv;
-                if (live && h0 + u < per && h < it.end) {
+                const float inv = 1.f / sqrtf(lane_sum<LANES>(s) * inv_m + a.eps);
+                const float back = lane_sum<LANES>(d) * inv_m * inv * inv * inv;
+                if (h0 + u < count) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float dw = g[u][e] * (x[u][e] * inv);
-                        aq[e] += it.is_k ? 0.f : dw;
-                        ak[e] += it.is_k ? dw : 0.f;
+                        acc[e] += g[u][e] * (x[u][e] * inv);
                         x[u][e] = inv * (g[u][e] * w[e]) - x[u][e] * back;
                     }
-                    st8f<BF16>(out, to + static_cast<int64_t>(h) * D, x[u]);
+                    st8f<BF16>(out, to + static_cast<int64_t>(h0 + u) * D, x[u]);
                 }
             }
         }
     }
     if (!a.part) return;
-    __shared__ float sum[ROWS][2][D];
+    __shared__ float sum[ROWS][D];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        sum[sub][0][8 * l + e] = aq[e];
-        sum[sub][1][8 * l + e] = ak[e];
-    }
+    for (int e = 0; e < 8; ++e) sum[sub][8 * l + e] = acc[e];
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    if (threadIdx.x < D) {
         float s = 0.f;
-        for (int r = 0; r < ROWS; ++r) s += sum[r][i / D][i % D];
-        a.part[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = s;
+        for (int r = 0; r < ROWS; ++r) s += sum[r][threadIdx.x];
+        a.part[((is_k ? gridDim.x - blocks_k : 0) + mine) * D + threadIdx.x] = s;
     }
 }
 
-// dwq and dwk: 16 columns a block, the rows of partial sums on 64 threads each
-__global__ void __launch_bounds__(1024) gdr_norm_wsum_kernel(NormArgs a, int64_t rows) {
+// dwq (blockIdx.y 0, from the first blocks_q rows of partial sums) and dwk: 16
+// columns a block, the rows on 64 threads each, 4 loads of a thread in flight
+__global__ void __launch_bounds__(1024) gdr_norm_wsum_kernel(NormArgs a, int64_t blocks_q, int64_t blocks) {
     __shared__ float sum[64][17];
     const int col = threadIdx.x % 16, sub = threadIdx.x / 16;
     const int i = blockIdx.x * 16 + col;
-    float s = 0.f;
-    for (int64_t r = sub; r < rows; r += 64) s += a.part[r * 2 * a.d + i];
-    sum[sub][col] = s;
+    const int64_t first = blockIdx.y ? blocks_q : 0, end = blockIdx.y ? blocks : blocks_q;
+    float s[4] = {};
+    int64_t r = first + sub;
+    for (; r + 3 * 64 < end; r += 4 * 64)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] += a.part[(r + 64 * k) * a.d + i];
+    for (; r < end; r += 64) s[0] += a.part[r * a.d + i];
+    sum[sub][col] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
     if (threadIdx.x < 16) {
         float v = 0.f;
         for (int k = 0; k < 64; ++k) v += sum[k][threadIdx.x];
-        if (i < a.d) {
-            if (a.dwq) a.dwq[i] = v;
-        } else if (a.dwk) {
-            a.dwk[i - a.d] = v;
-        }
+        float *to = blockIdx.y ? a.dwk : a.dwq;
+        if (to) to[i] = v;
     }
 }
 
@@ -303,59 +312,62 @@ hipError_t by_norm(const NormArgs &a, F f) {
     return a.bf16 ? dim.template operator()<true>() : dim.template operator()<false>();
 }
 
-struct Split {
-    int per, slices_q, slices;
-    int64_t items;
-};
-// Heads of an item: up to 16, so that the tables are read once for them; fewer
-// when there would be less than 4 waves a CU otherwise.
-Split split_of(const NormArgs &a) {
-    Split s;
-    s.per = a.hq > a.hk ? a.hq : a.hk;
-    if (s.per > 16) s.per = 16;
-    auto count = [&] {
-        s.slices_q = (a.hq + s.per - 1) / s.per;
-        s.slices = s.slices_q + (a.hk + s.per - 1) / s.per;
-        s.items = a.tokens * s.slices;
-    };
-    count();
-    while (s.per > 1 && s.items * (a.d / 8) < 256 * 4 * 64) {
-        s.per = (s.per + 1) / 2;
-        count();
-    }
-    return s;
+// Heads of an item at most: 16, so that the tables are read once for them;
+// fewer when there would be less than 4 waves a CU otherwise.
+int most_heads(const NormArgs &a) {
+    int most = 16;
+    while (most > 1 && (side_of(a.tokens, a.hq, most).items + side_of(a.tokens, a.hk, most).items) * (a.d / 8) < 256 * 4 * 64)
+        most /= 2;
+    return most;
+}
+int64_t blocks_of(const Side &s, int d) {
+    const int64_t rows = kThreads / (d / 8);
+    return (s.items + rows - 1) / rows;
 }
 
 }  // namespace
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream) {
-    const Split s = split_of(a);
+    const int most = most_heads(a);
+    const int64_t blocks_q = blocks_of(side_of(a.tokens, a.hq, most), a.d);
+    const int64_t blocks = blocks_q + blocks_of(side_of(a.tokens, a.hk, most), a.d);
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     return by_norm(a, [&]<bool BF16, int D>() {
-        constexpr int ROWS = kThreads / (D / 8);
-        const int64_t blocks = (s.items + ROWS - 1) / ROWS;
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
         hipLaunchKernelGGL((gdr_norm_fwd_kernel<BF16, D>), dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream, a,
-                           s.items, s.per, s.slices_q, s.slices);
+                           most, blocks - blocks_q);
         return hipGetLastError();
     });
 }
 
-int64_t norm_bwd_blocks(const NormArgs &a) {
-    const int64_t rows = kThreads / (a.d / 8);
-    const int64_t blocks = (split_of(a).items + rows - 1) / rows;
-    return blocks < 2048 ? blocks : 2048;
+namespace {
+struct BwdSplit {
+    int per;
+    int64_t blocks_q, blocks;
+};
+// 8 blocks a CU at most, shared between q and k by their heads
+BwdSplit bwd_split(const NormArgs &a) {
+    BwdSplit s;
+    s.per = most_heads(a);
+    const int64_t nq = blocks_of(side_of(a.tokens, a.hq, s.per), a.d), nk = blocks_of(side_of(a.tokens, a.hk, s.per), a.d);
+    const int64_t most_q = (2048 * a.hq + a.hq + a.hk - 1) / (a.hq + a.hk);
+    s.blocks_q = nq < most_q ? nq : most_q;
+    const int64_t most_k = 2048 - most_q > 0 ? 2048 - most_q : 1;
+    s.blocks = s.blocks_q + (nk < most_k ? nk : most_k);
+    return s;
 }
+}  // namespace
+
+int64_t norm_bwd_blocks(const NormArgs &a) { return bwd_split(a).blocks; }
 
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream) {
-    const Split s = split_of(a);
-    const int64_t blocks = norm_bwd_blocks(a);
+    const BwdSplit s = bwd_split(a);
     return by_norm(a, [&]<bool BF16, int D>() {
-        if (blocks > 0)
-            hipLaunchKernelGGL((gdr_norm_bwd_kernel<BF16, D>), dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0, stream,
-                               a, s.items, s.per, s.slices_q, s.slices);
+        if (s.blocks > 0)
+            hipLaunchKernelGGL((gdr_norm_bwd_kernel<BF16, D>), dim3(static_cast<uint32_t>(s.blocks)), dim3(kThreads), 0, stream,
+                               a, s.per, s.blocks - s.blocks_q);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || !a.part) return e;
-        hipLaunchKernelGGL(gdr_norm_wsum_kernel, dim3(2 * D / 16), dim3(1024), 0, stream, a, blocks);
+        hipLaunchKernelGGL(gdr_norm_wsum_kernel, dim3(D / 16, 2), dim3(1024), 0, stream, a, s.blocks_q, s.blocks);
         return hipGetLastError();
     });
 }

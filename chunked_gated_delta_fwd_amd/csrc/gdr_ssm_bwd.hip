@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             }
             T::store4(sPd + j * PS + T::template col<true>(i0), pd);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) rs[r] = sum16(rs[r]);
+            for (int r = 0; r < 4; ++r) rs[r] = lane_sum<16>(rs[r]);
             if (l16 == 0) *reinterpret_cast<f32x4 *>(&s_row[tj[k]][i0]) = rs;
             col = sum_rows(col);
             if (lq == 0) s_col[ti[k]][j] = col;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
                 if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PE + 16 * k + 4 * lq, Ev[k]);
             }
-            es_sum = sum64(es_sum);
+            es_sum = lane_sum<64>(es_sum);
             if (l == 0) s_es[wave] = es_sum;
         }
 #pragma unroll
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     const float dt = s.dt[l], far = s.ew[l] * et;
     const float v = cl + diag + far;
     float u = rw + s.eg[l] * st - dt * (cl + far);
-    const float z = s.decay * es_sum + sum64(s.w[l] * et);
+    const float z = s.decay * es_sum + lane_sum<64>(s.w[l] * et);
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) {
         const float o = __shfl_down(u, k);
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
         if (a.gate_bf16) static_cast<uint16_t *>(a.ddt)[to] = bf16_bits(draw);
         else static_cast<float *>(a.ddt)[to] = draw;
     }
-    const float da = sum64(valid ? dt * dl : 0.f), dd = sum64(valid ? m : 0.f), dbias = sum64(draw);
+    const float da = lane_sum<64>(valid ? dt * dl : 0.f), dd = lane_sum<64>(valid ? m : 0.f), dbias = lane_sum<64>(draw);
     if (l == 0) {
         part[0] = da;
         part[1] = dd;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_heads_kernel(SsmArgs a) {
         for (int k = 0; k < 3; ++k) s[k] += a.head_part[(r * a.heads + h) * 3 + k];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        s[k] = sum64(s[k]);
+        s[k] = lane_sum<64>(s[k]);
         if (threadIdx.x % 64 == 0) sum[k][threadIdx.x / 64] = s[k];
     }
     __syncthreads();

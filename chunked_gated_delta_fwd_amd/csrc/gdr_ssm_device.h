@@ -2,6 +2,7 @@
 #pragma once
 
 #include "gdr_device.h"
+#include "gdr_lanes.h"
 #include "gdr_mixer.h"
 
 namespace gdr {
@@ -195,22 +196,6 @@ __device__ __forceinline__ double dpp_add64(double x) {
     const uint32_t hi = __builtin_amdgcn_update_dpp(0u, static_cast<uint32_t>(b >> 32), CTRL, ROW_MASK, 0xF, false);
     return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
-
-// Lane sums without LDS: within the 16 lanes of a row (neighbours, pairs, and
-// two mirrors), and over the four rows (lane swaps).  Every lane gets the sum.
-__device__ __forceinline__ float sum16(float x) {
-    x = dpp_add<0xB1, 0xF>(x);    // quad_perm 1 0 3 2
-    x = dpp_add<0x4E, 0xF>(x);    // quad_perm 2 3 0 1
-    x = dpp_add<0x141, 0xF>(x);   // mirror within 8
-    return dpp_add<0x140, 0xF>(x);   // mirror within 16
-}
-__device__ __forceinline__ float sum_rows(float x) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-__device__ __forceinline__ float sum64(float x) { return sum_rows(sum16(x)); }
 
 // One wave, lane = token.  Tokens past the end have dt = 0 and write nothing.
 __device__ __forceinline__ void chunk_gates(float raw, float bias, float A, bool valid, Gates &s) {
