@@ -81,6 +81,7 @@ struct SsmArgs {
     const int32_t *span_first;            // [N + 1] first span of each sequence
     int64_t n_spans;                      // entries: an upper bound on the spans
     int64_t span_len;
+    int64_t whole;                        // spans are this long when no sequence is longer (a multiple of span_len)
     float *gates;                         // [n_chunks][H][kGateRow]; NULL: made inside the walks (not split)
     float *span_state;                    // [directions][n_spans][H][n p]; NULL: not split
     float *span_decay;                    // [directions][n_spans][H]
@@ -99,8 +100,8 @@ struct SsmArgs {
     float *head_part;                     // [n_chunks][H]{dA, dD, dbias}
 };
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream);
-// Tokens of a span, or 0 where each sequence is walked by one block.
-int64_t ssm_span_len(const SsmArgs &a);
+// Sets span_len (0: each sequence is walked by one block) and whole.
+void ssm_spans(SsmArgs &a, bool bwd);
 // Tables of spans and of 64-token chunks from the content of cu_seqlens:
 // first spans [N + 1], chunks [N + 1]; tables [n_spans], [n_chunks].
 struct SsmTables {

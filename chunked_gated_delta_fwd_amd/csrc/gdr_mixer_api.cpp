@@ -438,9 +438,9 @@ void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, gdr::SsmTables &t) {
         const int64_t each = (a.seq_len + span - 1) / span;
         return a.n_seq * (each < 1 ? 1 : each);
     };
-    a.span_len = gdr::ssm_span_len(a);
+    gdr::ssm_spans(a, bwd);
     const bool split = a.span_len > 0;
-    if (!split) a.span_len = ((a.cu ? a.total : a.seq_len) / 64 + 1) * 64;
+    if (!split) a.span_len = a.whole = ((a.cu ? a.total : a.seq_len) / 64 + 1) * 64;
     a.n_spans = split ? entries(a.span_len) : a.n_seq;
     a.row_spans = static_cast<int32_t>((a.seq_len + a.span_len - 1) / a.span_len);
     if (a.row_spans < 1) a.row_spans = 1;

@@ -349,7 +349,7 @@ BwdSplit bwd_split(const NormArgs &a) {
     BwdSplit s;
     s.per = most_heads(a);
     const int64_t nq = blocks_of(side_of(a.tokens, a.hq, s.per), a.d), nk = blocks_of(side_of(a.tokens, a.hk, s.per), a.d);
-    const int64_t most_q = (2048 * a.hq + a.hq + a.hk - 1) / (a.hq + a.hk);
+    const int64_t heads = static_cast<int64_t>(a.hq) + a.hk, most_q = (2048 * static_cast<int64_t>(a.hq) + heads - 1) / heads;
     s.blocks_q = nq < most_q ? nq : most_q;
     const int64_t most_k = 2048 - most_q > 0 ? 2048 - most_q : 1;
     s.blocks = s.blocks_q + (nk < most_k ? nk : most_k);

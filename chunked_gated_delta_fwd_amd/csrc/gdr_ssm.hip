@@ -74,9 +74,10 @@ constexpr int kTableThreads = 1024;
 
 // One block: prefix sums of every sequence's numbers of spans and chunks (at
 // least one, so that a length-0 sequence has a walk that hands its state on),
-// then the entries, each of which finds its sequence by bisection.
+// then the entries, each of which finds its sequence by bisection.  Here the
+// lengths are known: nothing is split when no sequence is longer than a.whole.
 __global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a, SsmTables t) {
-    __shared__ int32_t s_span[kTableThreads], s_chunk[kTableThreads];
+    __shared__ int32_t s_span[kTableThreads], s_chunk[kTableThreads], s_longest;
     const int tid = threadIdx.x;
     auto range = [&](int64_t n, int64_t &b, int64_t &e) {
         b = a.cu[n];
@@ -85,13 +86,24 @@ __global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a,
         e = e < b ? b : e > a.total ? a.total : e;
     };
     auto clamp = [](int64_t v, int64_t most) { return static_cast<int32_t>(v < most ? v : most); };
+    if (tid == 0) s_longest = 0;
+    __syncthreads();
+    int32_t longest = 0;
+    for (int64_t n = tid; n < a.n_seq; n += kTableThreads) {
+        int64_t b, e;
+        range(n, b, e);
+        longest = e - b > longest ? static_cast<int32_t>(e - b) : longest;
+    }
+    atomicMax(&s_longest, longest);
+    __syncthreads();
+    const int64_t span_len = s_longest > a.whole ? a.span_len : a.whole;
     int64_t spans = 0, chunks = 0;
     for (int64_t base = 0; base < a.n_seq; base += kTableThreads) {
         int32_t ms = 0, mc = 0;
         if (base + tid < a.n_seq) {
             int64_t b, e;
             range(base + tid, b, e);
-            ms = static_cast<int32_t>((e - b + a.span_len - 1) / a.span_len);
+            ms = static_cast<int32_t>((e - b + span_len - 1) / span_len);
             mc = static_cast<int32_t>((e - b + 63) / 64);
             ms = ms < 1 ? 1 : ms;
             mc = mc < 1 ? 1 : mc;
@@ -145,7 +157,7 @@ __global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a,
             table[i] = v;
         }
     };
-    fill(t.span_first, a.span_len, a.n_spans, t.spans);
+    fill(t.span_first, span_len, a.n_spans, t.spans);
     fill(t.chunk_first, 64, a.n_chunks, t.chunks);
 }
 
@@ -183,15 +195,38 @@ hipError_t by_ssm(const SsmArgs &a, F f) {
 
 }  // namespace
 
-int64_t ssm_span_len(const SsmArgs &a) {
-    // About 1024 walks: two rounds over the chip.  With 4096 the joining pass
-    // moves four times the states (91 us where it takes 28, at 65536 tokens and
-    // 32 heads of 128 x 128), with 512 the last round is half empty.  Not split when no sequence
-    // can be longer than a span, or than what a split costs (its three launches
-    // take about as long as a walk over 640 tokens).
-    const int64_t longest = a.cu ? a.total : a.seq_len;
-    const int64_t len = (a.total * a.heads / 1024 + 63) / 64 * 64;
-    return longest <= 640 || longest <= len ? 0 : len < 64 ? 64 : len;
+// 512 walks at 8 waves each fill the chip.  Equal rows take that many; in the
+// backward pass, where the walk from the end runs beside the one from the
+// start, half of it (one row of 16384 tokens, 32 heads, n = 128: forward, p =
+// 64, 128, 256, 512, 1024, 2048 walks: 277, 156, 125, 129, 142 us; backward,
+// 256 and 512: 461 and 459, p = 128: 766 and 792).  Packed sequences make walks
+// of all lengths and take twice as many (15 in 65536 tokens, p = 128, 512 and
+// 1024: 797 to 817 and 743 to 749 us; backward of 4 to 16 in 16384, p = 64,
+// 256 and 512: 518 to 576 and 499 to 573).
+//
+// Not split when that takes fewer steps than its extra launches and its second
+// pass over the tokens cost: no sequence longer than `whole` (32 heads, p =
+// 64, 16384 tokens, whole = 2048, packed sequences of up to 1780: 131 us whole,
+// 155 split; of up to 3244: 161 and 145), or none longer than `few` (8 to 32
+// heads; forward bf16, 512 tokens: 28 to 34 us whole, 22 to 43 split, 1024: 53
+// to 64 and 25 to 43; f32, 192: 30 to 40 and 29 to 38; backward bf16, 512: 46
+// to 67 and 46 to 80, 1024: 61 to 103 and 49 to 106; f32, 512: 72 to 114 and 62
+// to 107).
+// The longest of packed sequences is taken for four times their average, and
+// for a third of all tokens at least, so that one long among many short ones
+// costs no more than 3 x few steps (37 sequences in 600 tokens: 20 us whole,
+// 41 split).
+void ssm_spans(SsmArgs &a, bool bwd) {
+    int64_t longest = a.seq_len;
+    if (a.cu) {   // not known here
+        const int64_t four = a.n_seq ? 4 * a.total / a.n_seq : 0;
+        longest = four > a.total ? a.total : four > a.total / 3 ? four : a.total / 3;
+    }
+    const int64_t few = bwd ? (a.bf16 ? 768 : 448) : (a.bf16 ? 512 : 192);
+    const int64_t len = (a.total * a.heads / ((bwd ? 256 : 512) * (a.cu ? 2 : 1)) + 63) / 64 * 64;
+    a.span_len = len < 64 ? 64 : len;
+    a.whole = (a.cu && !bwd ? 4 : 2) * a.span_len;
+    if (longest <= few || (a.cu ? a.total : longest) <= a.whole) a.span_len = 0;
 }
 
 hipError_t launch_ssm_table(const SsmArgs &a, const SsmTables &t, hipStream_t stream) {
@@ -213,9 +248,9 @@ hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream) {
         const int64_t walks = (a.span_state ? a.n_spans : a.n_seq) * a.heads;
         if (walks > 0x7FFFFFFF || a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF) return hipErrorInvalidValue;
         const dim3 grid(static_cast<uint32_t>(walks));
-        const dim3 out(walk_threads(kOut, P));
+        const dim3 out(walk_threads(P));
         if (a.span_state) {
-            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, false, true>), grid, dim3(walk_threads(kLocal, P)), 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, false, true>), grid, dim3(walk_threads(P)), 0, stream, a);
             hipLaunchKernelGGL((gdr_ssm_join_kernel<N, P, false>), dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024))),
                                block, 0, stream, a);
             hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kOut, false, true>), grid, out, 0, stream, a);

@@ -442,7 +442,7 @@ hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
         if (walks > 0x7FFFFFFF || grads > 0x7FFFFFFF || a.n_chunks * a.heads > 0x7FFFFFFF ||
              a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF)
             return hipErrorInvalidValue;
-        const dim3 grid(static_cast<uint32_t>(walks), 2), walk(walk_threads(kStates, P));
+        const dim3 grid(static_cast<uint32_t>(walks), 2), walk(walk_threads(P));
         if (walks > 0) {
             if (a.span_state) {
                 hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kLocal, true, true>), grid, walk, 0, stream, a);

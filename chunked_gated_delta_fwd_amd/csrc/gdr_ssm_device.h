@@ -359,20 +359,20 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo
 // state: E <- e^G_end E + sum_i e^G_i c_i dy_i^T, stored at each chunk's end.
 enum WalkMode { kLocal, kStates, kOut };
 
-// Waves of a block: kOut 4, of 16 or 32 columns p each (with 8, a wave's
-// registers for y and its operands do not fit 4 waves a SIMD, and spill); the
-// other walks one per 16 columns.  waves: a SIMD's, at least.
-constexpr int walk_threads(int, int p) { return 4 * p; }
-constexpr int walk_waves(int mode, bool bf16, int p) { return p == 128 ? (bf16 ? 4 : 2) : (bf16 ? 2 : 1); }
+// Waves of a block: one per 16 columns p, so that its part of the state stays
+// in registers.  32 columns a wave halve the LDS reads but leave 2 waves a SIMD:
+// kOut took 545 us at best instead of 517, 65536 tokens of 32 heads, n = p = 128.
+constexpr int walk_threads(int p) { return 4 * p; }
+constexpr int walk_waves(bool bf16, int p) { return p == 128 ? (bf16 ? 4 : 2) : (bf16 ? 2 : 1); }   // a SIMD's, at least
 
 // PRE: the gates come from memory (a.gates); else the last wave makes each
 // chunk's while the others are at work on the one before (short calls, where
 // a launch more would cost more).
 template <class T, int N, int P, int MODE, bool OB, bool PRE>
-__global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf16, P)) gdr_ssm_walk_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_ssm_walk_kernel(SsmArgs a) {
     typedef typename T::E E;
     typedef typename T::F8 F8;
-    constexpr int NT = N / 16, PT = P / 16, TH = walk_threads(MODE, P), WAVES = TH / 64, CT = PT / WAVES;   // a wave owns CT of the column tiles
+    constexpr int NT = N / 16, PT = P / 16, TH = walk_threads(P), WAVES = TH / 64;   // a wave owns a column tile
     constexpr bool kY = MODE == kOut;
     constexpr bool KU = kY;   // the scores read U along its rows, the state update across them
     typedef Tile<T, N, KU, TH> TileU;
@@ -396,20 +396,17 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
     int l16 = lane16, lq = lane4;
     const int64_t hb = (static_cast<int64_t>(rev ? 1 : 0) * a.n_spans + si) * a.heads + h;   // slot in the span buffers
 
-    f32x4 Z[NT][CT];
+    f32x4 Z[NT];
     const float *init = rev ? a.dht : a.h0;
     const bool split = MODE != kLocal && a.span_state;
     const __amdgpu_buffer_rsrc_t mine = chunk_rsrc(a.span_state + hb * (N * P), N * P * 4);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            const int pt = CT * wave + c;
-            Z[nt][c] = zero4();
-            if (MODE == kLocal) continue;
-            if (split) Z[nt][c] = load_tile(mine, 16 * l, nt * PT + pt);
-            else if (init) Z[nt][c] = load_state_tile<P, OB>(init + (sp.seq * a.heads + h) * (N * P), nt, pt, l16, lq);
-        }
+    for (int nt = 0; nt < NT; ++nt) {
+        Z[nt] = zero4();
+        if (MODE == kLocal) continue;
+        if (split) Z[nt] = load_tile(mine, 16 * l, nt * PT + wave);
+        else if (init) Z[nt] = load_state_tile<P, OB>(init + (sp.seq * a.heads + h) * (N * P), nt, wave, l16, lq);
+    }
 
     const int chunks = static_cast<int>((sp.len + 63) / 64);
     const int64_t ldu = rev ? a.ldc : a.ldb, ldv = rev ? a.lddy : a.ldx;
@@ -477,9 +474,7 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
             const __amdgpu_buffer_rsrc_t to = chunk_rsrc(
                 a.chunk_state + ((static_cast<int64_t>(rev ? 1 : 0) * a.n_chunks + sp.row0 + c) * a.heads + h) * (N * P), N * P * 4);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < CT; ++i) store_tile(to, 16 * l, nt * PT + CT * wave + i, Z[nt][i]);
+            for (int nt = 0; nt < NT; ++nt) store_tile(to, 16 * l, nt * PT + wave, Z[nt]);
         }
         __syncthreads();   // this chunk's tiles and gates are in LDS
         if (k + 1 < chunks) load_tiles(k + 1);
@@ -518,37 +513,28 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
             if (k + 2 < chunks) load_raw(k + 2);
         }
         asm volatile("" : "+v"(l16), "+v"(lq));
-        F8 v[2][CT];   // x (or dy) with tokens as k
+        F8 v[2];   // x (or dy) with tokens as k
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < CT; ++i) v[q][i] = T::template tr<false>(sV, PV, 32 * q, 16 * (CT * wave + i), l16, lq);
+        for (int q = 0; q < 2; ++q) v[q] = T::template tr<false>(sV, PV, 32 * q, 16 * wave, l16, lq);
         if constexpr (kY) {
             // y^T = e^G (S^T C^T) + D x^T + X^T P^T for this wave's columns
-            f32x4 Y[4][CT];
+            f32x4 Y[4];
 #pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int i = 0; i < CT; ++i) Y[it][i] = zero4();
+            for (int it = 0; it < 4; ++it) Y[it] = zero4();
 #pragma unroll
             for (int q = 0; q < N / 32; ++q) {
-                F8 z[CT], cf[4];
+                F8 cf[4];
 #pragma unroll
                 for (int it = 0; it < 4; ++it) cf[it] = T::template kfrag<true>(sC + (16 * it + l16) * PC, q, lq);
-#pragma unroll
-                for (int i = 0; i < CT; ++i) z[i] = T::round(Z[2 * q][i], Z[2 * q + 1][i]);
+                const F8 z = T::round(Z[2 * q], Z[2 * q + 1]);   // the state itself stays fp32; y is rounded to bf16 too
                 __builtin_amdgcn_sched_barrier(0);   // the reads together, ahead of the products
 #pragma unroll
-                for (int it = 0; it < 4; ++it)
-#pragma unroll
-                    for (int i = 0; i < CT; ++i) Y[it][i] = T::mma(z[i], cf[it], Y[it][i]);
+                for (int it = 0; it < 4; ++it) Y[it] = T::mma(z, cf[it], Y[it]);
             }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const float eg = s.eg[16 * it + l16];
-#pragma unroll
-                for (int i = 0; i < CT; ++i)
-                    Y[it][i] = Y[it][i] * eg + T::load4(sV + (16 * it + l16) * PV + 16 * (CT * wave + i) + 4 * lq) * dh;
+                Y[it] = Y[it] * eg + T::load4(sV + (16 * it + l16) * PV + 16 * wave + 4 * lq) * dh;
             }
             __syncthreads();   // the scores are in LDS
             asm volatile("" : "+v"(l16), "+v"(lq));
@@ -561,15 +547,11 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
 #pragma unroll
                 for (int q = 0; q <= it / 2; ++q) {
                     const F8 pf = T::template kfrag<true>(sP + (16 * it + l16) * PS, q, lq);
-#pragma unroll
-                    for (int i = 0; i < CT; ++i) Y[it][i] = T::mma(v[q][i], pf, Y[it][i]);
+                    Y[it] = T::mma(v[q], pf, Y[it]);
                 }
-#pragma unroll
-                for (int i = 0; i < CT; ++i) {
-                    const uint32_t off = (16 * it + l16) * ldy + (16 * (CT * wave + i) + 4 * lq) * sizeof(E);
-                    if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(Y[it][i])), ry, off, 0, 0);
-                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, Y[it][i]), ry, off, 0, 0);
-                }
+                const uint32_t off = (16 * it + l16) * ldy + (16 * wave + 4 * lq) * sizeof(E);
+                if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(Y[it])), ry, off, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, Y[it]), ry, off, 0, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -578,17 +560,14 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
         const float decay = s.decay;
         if (MODE == kLocal) total += s.ghi[63] + s.glo[63];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < CT; ++i) Z[nt][i] = Z[nt][i] * decay;
+        for (int nt = 0; nt < NT; ++nt) Z[nt] = Z[nt] * decay;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const float *w = rev ? s.eg : s.w;
             const f32x4 wa = *reinterpret_cast<const f32x4 *>(w + 32 * q + 4 * lq);
             const f32x4 wb = *reinterpret_cast<const f32x4 *>(w + 32 * q + 16 + 4 * lq);
-            F8 vs[CT][T::kParts];
-#pragma unroll
-            for (int i = 0; i < CT; ++i) T::split(T::lo(v[q][i]) * wa, T::hi(v[q][i]) * wb, vs[i]);
+            F8 vs[T::kParts];
+            T::split(T::lo(v[q]) * wa, T::hi(v[q]) * wb, vs);
 #pragma unroll
             for (int nt = 0; nt < NT; nt += 2) {   // two tiles at a time: products on one sum do not follow each other
                 F8 u[2];
@@ -598,9 +577,7 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
                 for (int e = T::kParts - 1; e >= 0; --e)
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-                        for (int i = 0; i < CT; ++i)
-                            Z[nt + k2][i] = OB ? T::mma(vs[i][e], u[k2], Z[nt + k2][i]) : T::mma(u[k2], vs[i][e], Z[nt + k2][i]);
+                        Z[nt + k2] = OB ? T::mma(vs[e], u[k2], Z[nt + k2]) : T::mma(u[k2], vs[e], Z[nt + k2]);
             }
         }
         __syncthreads();   // the chunk's tiles have been read
@@ -616,13 +593,10 @@ __global__ void __launch_bounds__(walk_threads(MODE, P), walk_waves(MODE, T::kBf
     else if (MODE == kStates && rev && sp.first && a.dh0) out = a.dh0 + (sp.seq * a.heads + h) * (N * P);
     if (out) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < CT; ++i) {
-                const int pt = CT * wave + i;
-                if (MODE == kLocal) store_tile(mine, 16 * l, nt * PT + pt, Z[nt][i]);
-                else store_state_tile<P, OB>(out, nt, pt, l16, lq, Z[nt][i]);
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+            if (MODE == kLocal) store_tile(mine, 16 * l, nt * PT + wave, Z[nt]);
+            else store_state_tile<P, OB>(out, nt, wave, l16, lq, Z[nt]);
+        }
     }
     if (MODE == kLocal && tid == 0) a.span_decay[hb] = expf(total);
 }

@@ -60,6 +60,11 @@ CASES = [
     (1, 190, 4, 2, 128, 64, F, BF, [0, 64, 64, 190], True, True, True),
     (1, 70, 2, 2, 128, 128, F, F, None, True, False, False),
     (1, 66, 1, 1, 64, 128, F, F, [0, 0, 66], False, True, False),
+    # walked in spans, in both directions; rows; and packed sequences that are all short
+    (1, 1100, 2, 1, 64, 64, BF, F, [0, 1000, 1000, 1100], True, True, False),
+    (2, 900, 2, 2, 64, 64, BF, BF, None, True, True, False),
+    (1, 700, 2, 1, 64, 64, F, F, [0, 30, 700], True, True, False),
+    (1, 900, 4, 2, 64, 64, BF, F, list(range(0, 901, 100)), True, True, False),
 ]
 IDS = ["%dx%d H%d/%d n%d p%d %s%s" % (c[0], c[1], c[2], c[3], c[4], c[5], "bf16" if c[6] == BF else "f32",
                                       " packed" if c[8] else "") for c in CASES]
@@ -243,10 +248,11 @@ def test_no_tokens(T, cu):
     assert torch.equal(dh0, d["dht"]) and all((t == 0).all() for t in (dA, dD, dbias))
 
 
-def test_in_a_graph():
-    """Forward with spans and backward, captured with workspaces of their own, replayed with eager work between."""
+@pytest.mark.parametrize("T", [700, 1000])
+def test_in_a_graph(T):
+    """Forward with spans and backward (with spans where T is 1000), captured with workspaces of their own, replayed with eager work between."""
     import chunked_gated_delta_fwd_amd as gdr
-    d, _ = make(9, 1, 700, 2, 1, 64, 64, BF, F, [0, 300, 700])
+    d, _ = make(9, 1, T, 2, 1, 64, 64, BF, F, [0, 300, T])
     eager = list(forward(gdr, d)) + list(backward(gdr, d))
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
