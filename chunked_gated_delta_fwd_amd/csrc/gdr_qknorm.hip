@@ -144,6 +144,8 @@ __device__ __forceinline__ bool side_of_block(int64_t blocks_k, int64_t blocks, 
     return is_k;
 }
 
+// 65536 tokens of 16 + 16 bf16 heads of 128: 213 to 222 us without rotation,
+// 4.9 TB/s of the 1.07 GB, 231 us with (a large copy reaches 5.2 TB/s).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int most, int64_t blocks_k) {
     constexpr int LANES = D / 8, ROWS = kThreads / LANES;
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int 
 //   dw = sum over rows of g x r,   dx = r (g w) - x r^3 (sum g w x) [/ d]
 // A block walks several items, all of q or all of k; dw is summed in registers,
 // then over the block's rows in a fixed order, then over blocks (q's rows of
-// partial sums first) by a second kernel.
+// partial sums first) by a second kernel.  16384 tokens of 32 + 4 bf16 heads of
+// 128: 107 us and 5 for the sums, 4.2 TB/s of the 453 MB.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads) gdr_norm_bwd_kernel(NormArgs a, int most, int64_t blocks_k) {
     constexpr int LANES = D / 8, ROWS = kThreads / LANES;
@@ -313,7 +316,9 @@ hipError_t by_norm(const NormArgs &a, F f) {
 }
 
 // Heads of an item at most: 16, so that the tables are read once for them;
-// fewer when there would be less than 4 waves a CU otherwise.
+// fewer when there would be less than 4 waves a CU otherwise.  16 + 16 bf16
+// heads of 128, rotated, 64 tokens: 5.4 us with one head an item, 10.5 with 16;
+// 65536 tokens: 428 and 231.
 int most_heads(const NormArgs &a) {
     int most = 16;
     while (most > 1 && (side_of(a.tokens, a.hq, most).items + side_of(a.tokens, a.hk, most).items) * (a.d / 8) < 256 * 4 * 64)
@@ -344,7 +349,9 @@ struct BwdSplit {
     int per;
     int64_t blocks_q, blocks;
 };
-// 8 blocks a CU at most, shared between q and k by their heads
+// 8 blocks a CU at most, shared between q and k by their heads: each leaves a
+// row of partial sums (16384 tokens, 32 + 4 heads of 128: 4 blocks a CU 127 us,
+// 8 110, and with half the rows in flight 115 and 120)
 BwdSplit bwd_split(const NormArgs &a) {
     BwdSplit s;
     s.per = most_heads(a);

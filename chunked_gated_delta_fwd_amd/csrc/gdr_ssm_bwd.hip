@@ -34,6 +34,12 @@ namespace {
 // dx (likewise).  db and dc are summed over the slice's heads in registers;
 // their L M parts as one matrix, multiplied once.  8 waves, because with 4 the
 // sums and states of a wave take over 256 registers and spill.
+//
+// 16384 tokens in 4 sequences, 32 heads on one b and c, n = 128, p = 64, bf16:
+// 285 us; 580 MB of states, x and dy read and dx and partial sums written, 2.6
+// TB/s over five rounds of blocks where four would do.  A head takes 5.6 us a
+// block (88 KB a CU in that time: near what HBM gives), a block 8 us around its
+// heads.
 constexpr int kGradThreads = 512;
 
 template <class T, int N, int P>
@@ -346,6 +352,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
 
 // The gradient of dt, and each chunk's part of dA, dD and dbias, from the
 // token sums of gdr_ssm_grad_kernel: a wave per (chunk, head), lane = token.
+// HBM bound: 13 us for 8300 of them.
 __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int64_t item = static_cast<int64_t>(blockIdx.x) * (kSsmThreads / 64) + wave;
@@ -391,7 +398,8 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     }
 }
 
-// db and dc from the slices' parts, added in order
+// db and dc from the slices' parts, added in order: HBM bound, 13 us for 4
+// slices of 16384 tokens, n = 128
 template <class T>
 __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_bc_kernel(SsmArgs a, int64_t plane) {
     const int64_t i = (static_cast<int64_t>(blockIdx.x) * kSsmThreads + threadIdx.x) * 4;
@@ -427,7 +435,9 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_heads_kernel(SsmArgs a) {
 
 int ssm_slices(const SsmArgs &a) {
     // one block sums the heads of a slice: enough slices to fill the chip, as
-    // few as that takes, because db and dc pass through HBM once a slice
+    // few as that takes, because db and dc pass through HBM once a slice (16384
+    // tokens, 32 heads, n = 128, p = 64: about 512, 768, 1024, 2048, 4096 blocks
+    // take 308, 289, 283, 299, 344 us)
     const int64_t per_group = a.heads / a.groups;
     int64_t s = (1024 + a.n_chunks * a.groups - 1) / (a.n_chunks * a.groups);
     s = s < 1 ? 1 : s > per_group ? per_group : s;

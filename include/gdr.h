@@ -439,9 +439,10 @@ int gdr_qk_norm_rope_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_ten
  * bf16 inputs: bf16 matrix operands with fp32 sums for y (rounded once), and a
  * state of fp32 accuracy (its products take exact bf16 parts).  f32 inputs:
  * fp32 products throughout.  A non-finite x can reach the y of earlier tokens
- * of its 64-token chunk.  Workspace: none when no sequence is longer than a
- * span, else 4 H n p bytes a span and tables; spans have about
- * T H / 2048 tokens.
+ * of its 64-token chunk.  Workspace: none where every sequence is walked by
+ * one block (small calls, many short rows); else 4 H n p bytes a span, 1552 H a
+ * 64-token chunk, and tables.  Spans have about T H / 1024 tokens with
+ * cu_seqlens, B T H / 512 without.
  */
 int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
                      const gdr_tensor *b, const gdr_tensor *c, const gdr_tensor *D,
@@ -460,7 +461,9 @@ int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
  *   dh0   [N, H, n, p] out, f32, or NULL (written also when h0 is NULL)
  *
  * ddt, dA, dD, ddt_bias and dh0 are fp32-accurate for bf16 inputs too.
- * Workspace: about 8 n p bytes a (64-token chunk, head).
+ * Workspace: about 8 n p + 3100 bytes a (64-token chunk, head), 8 n p a (span,
+ * head), and for db and dc, where few blocks would sum whole groups, 8 n bytes a
+ * token, group and slice of the heads.
  */
 int gdr_ssm_scan_bwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
                      const gdr_tensor *b, const gdr_tensor *c, const gdr_tensor *D,
