@@ -127,28 +127,30 @@ struct Tile {
     static constexpr int kPiece = 16 / sizeof(typename T::E);       // elements of 16 bytes
     static constexpr int kPerRow = COLS / kPiece;
     static constexpr int kN = 64 * kPerRow / THREADS;
+    static constexpr int kStep = THREADS / kPerRow;                 // rows between a thread's pieces
     v4u32 r[kN];
     // rows `ld` bytes apart; rows past the resource's end read as zeros
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, uint32_t ld) {
-        int tid = threadIdx.x;
+        uint32_t tid = threadIdx.x;
         asm volatile("" : "+v"(tid));   // offsets are cheap: made anew for each tile, not kept in registers
+        const uint32_t at = (tid / kPerRow) * ld + (tid % kPerRow) * 16;
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-            const int id = tid + k * THREADS;
-            r[k] = __builtin_bit_cast(v4u32, buf_load<16>(rsrc, (id / kPerRow) * ld + (id % kPerRow) * 16));
-        }
+        for (int k = 0; k < kN; ++k) r[k] = __builtin_bit_cast(v4u32, buf_load<16>(rsrc, at + k * (kStep * ld)));
     }
     __device__ __forceinline__ void store(typename T::E *m) const {
+        uint32_t tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const uint32_t x = (tid % kPerRow) * kPiece;
+        typename T::E *const row = m + (tid / kPerRow) * kPitch;
+        constexpr bool kPermuted = T::kBf16 && KP;
+        typename T::E *const to = row + (kPermuted ? kpos(x) : x), *const to4 = row + (kPermuted ? kpos(x + 4) : x);
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
-            const int id = threadIdx.x + k * THREADS;
-            typename T::E *const row = m + (id / kPerRow) * kPitch;
-            const int x = (id % kPerRow) * kPiece;
-            if constexpr (T::kBf16 && KP) {
-                *reinterpret_cast<v2u32 *>(row + kpos(x)) = v2u32{r[k][0], r[k][1]};
-                *reinterpret_cast<v2u32 *>(row + kpos(x + 4)) = v2u32{r[k][2], r[k][3]};
+            if constexpr (kPermuted) {
+                *reinterpret_cast<v2u32 *>(to + k * (kStep * kPitch)) = v2u32{r[k][0], r[k][1]};
+                *reinterpret_cast<v2u32 *>(to4 + k * (kStep * kPitch)) = v2u32{r[k][2], r[k][3]};
             } else {
-                *reinterpret_cast<v4u32 *>(row + x) = r[k];
+                *reinterpret_cast<v4u32 *>(to + k * (kStep * kPitch)) = r[k];
             }
         }
     }
@@ -550,6 +552,7 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
             asm volatile("" : "+v"(l16), "+v"(lq));
             uint32_t ldy = static_cast<uint32_t>(a.heads * P * sizeof(E));
             asm volatile("" : "+s"(ldy));   // as for the tiles' offsets
+            const uint32_t y0 = l16 * ldy + (16 * wave + 4 * lq) * sizeof(E);
             E *yb = static_cast<E *>(a.y) + (t * a.heads + h) * P;
             const __amdgpu_buffer_rsrc_t ry = chunk_rsrc(yb, static_cast<uint32_t>((rows - 1) * ldy + P * sizeof(E)));
 #pragma unroll
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
                     const F8 pf = T::template kfrag<true>(sP + (16 * it + l16) * PS, q, lq);
                     Y[it] = T::mma(v[q], pf, Y[it]);
                 }
-                const uint32_t off = (16 * it + l16) * ldy + (16 * wave + 4 * lq) * sizeof(E);
+                const uint32_t off = y0 + it * (16 * ldy);
                 if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(Y[it])), ry, off, 0, 0);
                 else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, Y[it]), ry, off, 0, 0);
             }
