@@ -94,8 +94,9 @@ struct SsmArgs {
     const int4 *chunks;                   // as spans, span_len 64; NULL without cu
     void *dx, *ddt, *db, *dc;
     float *dA, *dD, *dbias, *dh0;         // dD, dbias, dh0 NULL: not written
-    int32_t slices, slice_heads;          // the heads of a group in slices, one block each
-    float *bc_part;                       // [slices][db, dc][total][G][n]; not used with one slice
+    const int32_t *chunks_used;           // entries of chunks in use
+    int32_t grad_blocks, grad_least;      // blocks of the gradient, and the least (chunk, head)s of one
+    float *bc_part;                       // [parts][db, dc][total][G][n]; NULL: one block sums a group
     float *token_part;                    // [n_chunks][H][kTokenPart]: per-token sums
     float *head_part;                     // [n_chunks][H]{dA, dD, dbias}
 };
@@ -112,8 +113,8 @@ hipError_t launch_ssm_table(const SsmArgs &a, const SsmTables &t, hipStream_t st
 // The gates of every (chunk, head).
 hipError_t launch_ssm_gates(const SsmArgs &a, hipStream_t stream);
 hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream);
-// Slices of a group's heads in a backward call (a.n_chunks set).
-int ssm_slices(const SsmArgs &a);
+// Sets grad_blocks and grad_least (a.n_chunks set): how many blocks at most sum one group's db and dc.
+int ssm_grad_parts(SsmArgs &a);
 hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream);
 
 }  // namespace gdr

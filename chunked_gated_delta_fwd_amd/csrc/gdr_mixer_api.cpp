@@ -464,12 +464,8 @@ void carve_ssm(gdr::SsmArgs &a, bool bwd, Carve &c, gdr::SsmTables &t) {
         a.chunk_state = c.take<float>(2 * a.n_chunks * H * state);
         a.token_part = c.take<float>(a.n_chunks * H * gdr::kTokenPart);
         a.head_part = c.take<float>(a.n_chunks * H * 3);
-        a.slices = 1;
-        if (a.n_chunks > 0) {
-            a.slices = gdr::ssm_slices(a);
-            a.slice_heads = (a.heads / a.groups + a.slices - 1) / a.slices;
-        }
-        if (a.slices > 1) a.bc_part = c.take<float>(2 * a.slices * a.total * a.groups * a.n);
+        const int64_t parts = gdr::ssm_grad_parts(a);
+        if (parts > 1) a.bc_part = c.take<float>(2 * parts * a.total * a.groups * a.n);
     }
 }
 
@@ -482,6 +478,7 @@ hipError_t run_ssm(gdr::SsmArgs &a, const gdr::SsmTables &t, bool bwd, hipStream
             a.spans = t.spans;
             a.span_first = t.span_first;
             a.chunks = t.chunks;
+            a.chunks_used = t.chunk_first + a.n_seq;
         }
         if (e == hipSuccess) e = gdr::launch_ssm_gates(a, stream);
         if (e != hipSuccess) return e;

@@ -28,10 +28,34 @@
 namespace gdr {
 namespace {
 
-// One block of 8 waves per (chunk, group, slice of the group's heads); a wave
+// The units of work are (chunk, group, head), in that order; a block takes an
+// equal run of them, so that one round of blocks does all, and where a run ends
+// inside a (chunk, group) the parts of db and dc meet in memory.
+struct GradSplit {
+    uint32_t items, len, per_group;   // len: of a block's run
+    // the block that starts a (chunk, group), and how many blocks share it
+    __device__ __forceinline__ uint32_t first(uint32_t unit) const { return unit * per_group / len; }
+    __device__ __forceinline__ int parts(uint32_t unit) const {
+        return static_cast<int>(((unit + 1) * per_group - 1) / len - first(unit)) + 1;
+    }
+};
+// Of the chunks that there are, not of the table's entries; but not shorter
+// runs than the room for the parts allows (a.grad_least), whatever cu_seqlens holds.
+__device__ __forceinline__ GradSplit grad_split(const SsmArgs &a) {
+    GradSplit s;
+    const uint32_t used = a.chunks ? static_cast<uint32_t>(*a.chunks_used) : static_cast<uint32_t>(a.n_chunks);
+    const uint32_t blocks = static_cast<uint32_t>(a.grad_blocks), least = static_cast<uint32_t>(a.grad_least);
+    s.per_group = static_cast<uint32_t>(a.heads / a.groups);
+    s.items = used * static_cast<uint32_t>(a.heads);
+    const uint32_t len = (s.items + blocks - 1) / blocks;
+    s.len = len < least ? least : len;
+    return s;
+}
+
+// Blocks of 8 waves; a wave
 // owns one or two of the (i, j) tiles of the lower triangle, one tile of rows
 // n of db and dc (of half the tokens when n is 64) and one tile of rows p of
-// dx (likewise).  db and dc are summed over the slice's heads in registers;
+// dx (likewise).  db and dc are summed over the run's heads in registers;
 // their L M parts as one matrix, multiplied once.  8 waves, because with 4 the
 // sums and states of a wave take over 256 registers and spill.
 //
@@ -57,296 +81,303 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     __shared__ __attribute__((aligned(16))) float s_row[4][64], s_col[4][64], s_s[NT][64], s_e[NT][64], s_w[64], s_m[64], s_es[8];
     E *const sX = sXY, *const sY = sXY + 64 * PP, *const sC = sXY;
 
-    const int per_group = a.heads / a.groups;
-    const uint32_t slices = a.slices, groups = a.groups, rest = blockIdx.x / slices;
-    const int slice = static_cast<int>(blockIdx.x - rest * slices);
-    const int64_t row = rest / groups;
-    const int g = static_cast<int>(rest - static_cast<uint32_t>(row) * groups);
-    const int h0 = g * per_group + slice * a.slice_heads;
-    const int h1 = h0 + a.slice_heads < (g + 1) * per_group ? h0 + a.slice_heads : (g + 1) * per_group;
-    int rows;
-    int64_t t0;
-    chunk_of_row(a, row, t0, rows);
+    const uint32_t per_group = static_cast<uint32_t>(a.heads / a.groups), groups = a.groups;
+    const GradSplit split = grad_split(a);
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64);   // the same in every lane
     const int l = tid % 64;
     int l16 = l % 16, lq = l / 16;
-    if (rows <= 0) return;   // a length-0 sequence's row, or a surplus one
     const int nt = wave % NT, it0 = wave / NT * IW;     // db, dc: rows 16 nt .., tokens 16 it0 ..
     const int pt = wave % PT, jt0 = wave / PT * JW;     // dx: rows 16 pt .., tokens 16 jt0 ..
     const bool first_n = wave < NT;
     constexpr int es = sizeof(E);
-    auto tile_rsrc = [&](const void *base, int64_t ld, int64_t col, int cols) {
-        return chunk_rsrc(static_cast<const E *>(base) + t0 * ld + col, static_cast<uint32_t>(((rows - 1) * ld + cols) * es));
-    };
-    TileP tx, ty;
-    GateTile<kGradThreads> tg;
-    float d_next;
-    auto load_xy = [&](int h) {
-        tx.load(tile_rsrc(a.x, a.ldx, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.ldx * es));
-        ty.load(tile_rsrc(a.dy, a.lddy, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.lddy * es));
-        tg.load(a, row, h);
-        d_next = a.D ? a.D[h] : 0.f;
-    };
-    const float *const Sbase = a.chunk_state, *const Ebase = a.chunk_state + a.n_chunks * a.heads * (N * P);
-    f32x4 Sv[PT], Ev[PT];   // this wave's rows n of S and E
-    auto load_states = [&](int h) {
-        const int64_t at = (row * a.heads + h) * (N * P) + (nt * PT * 64 + l) * 4;
-#pragma unroll
-        for (int k = 0; k < PT; ++k) {
-            Sv[k] = *reinterpret_cast<const f32x4 *>(Sbase + at + k * 256);
-            Ev[k] = *reinterpret_cast<const f32x4 *>(Ebase + at + k * 256);
-        }
-    };
-    {
-        TileN tb, tc;
-        tb.load(tile_rsrc(a.b, a.ldb, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldb * es));
-        tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
-        tb.store(sB);
-        tc.store(sC);
-    }
-    load_xy(h0);
-    load_states(h0);
-    __syncthreads();
-
-    // this wave's tiles of the lower triangle's ten: number wave, and wave + 8
-    int ti[2], tj[2];
-    f32x4 K[2], R[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int idx = wave + 8 * k;
-        ti[k] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
-        tj[k] = idx - ti[k] * (ti[k] + 1) / 2;
-        K[k] = R[k] = zero4();
-        if (idx < 10) {
-#pragma unroll
-            for (int q = 0; q < N / 32; ++q)
-                K[k] = T::mma(T::template kfrag<true>(sC + (16 * ti[k] + l16) * PN, q, lq),
-                              T::template kfrag<true>(sB + (16 * tj[k] + l16) * PN, q, lq), K[k]);
-        }
-    }
-    // the values of c beside this wave's rows n of dc (c leaves LDS for x and dy)
-    typename T::F4 cd[IW];
-#pragma unroll
-    for (int i = 0; i < IW; ++i) cd[i] = T::raw4(sC + (16 * (it0 + i) + l16) * PN + T::template col<true>(16 * nt + 4 * lq));
-    // tiles above the diagonal that pairs of tiles reach
-    if (wave == 1 || wave == 3) T::store4(sPd + (16 * wave + l16) * PS + T::template col<true>(16 * (wave - 1) + 4 * lq), zero4());
-    f32x4 dc[IW], db[IW];
-#pragma unroll
-    for (int i = 0; i < IW; ++i) dc[i] = db[i] = zero4();
-    __syncthreads();
-
-    for (int h = h0; h < h1; ++h) {
-        const Gates &s = sg;
-        tx.store(sX);
-        ty.store(sY);
-        tg.store(sg);
-        __syncthreads();
-        // Unconditional (the last head's own once more), so that a later wait
-        // for the states can count these as still on their way
-        const float dh = d_next;
-        load_xy(h + 1 < h1 ? h + 1 : h);
-        // opaque coordinates, as in the walks: addresses are made in each phase
-        asm volatile("" : "+v"(l16), "+v"(lq));
-        // M, W and what they give
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (wave + 8 * k >= 10) continue;
-            f32x4 m = zero4();
-#pragma unroll
-            for (int q = 0; q < P / 32; ++q)
-                m = T::mma(T::template kfrag<true>(sY + (16 * ti[k] + l16) * PP, q, lq),
-                           T::template kfrag<true>(sX + (16 * tj[k] + l16) * PP, q, lq), m);
-            const int i0 = 16 * ti[k] + 4 * lq, j = 16 * tj[k] + l16;
-            const f32x4 gi = *reinterpret_cast<const f32x4 *>(&s.ghi[i0]), gil = *reinterpret_cast<const f32x4 *>(&s.glo[i0]);
-            const float gj = s.ghi[j], gjl = s.glo[j], dtj = s.dt[j];
-            f32x4 pd, rs;
-            float col = 0.f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const bool below = i0 + r > j, on = i0 + r == j;
-                const float e = __expf((gi[r] - gj) + (gil[r] - gjl));
-                const float lk = below || on ? e * K[k][r] : 0.f;
-                const float lm = below || on ? e * m[r] : 0.f;
-                const float w = lk * m[r];
-                pd[r] = lk;
-                R[k][r] += lm * dtj;
-                rs[r] = below ? w * dtj : 0.f;
-                col += below ? w : 0.f;
-                if (on) {
-                    s_w[j] = w;
-                    s_m[j] = m[r];
-                }
-            }
-            T::store4(sPd + j * PS + T::template col<true>(i0), pd);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) rs[r] = lane_sum<16>(rs[r]);
-            if (l16 == 0) *reinterpret_cast<f32x4 *>(&s_row[tj[k]][i0]) = rs;
-            col = sum_rows(col);
-            if (lq == 0) s_col[ti[k]][j] = col;
-        }
-        asm volatile("" : "+v"(l16), "+v"(lq));
-        // S dy^T and E x^T for this wave's rows n
-        if (first_n) {
-            float es_sum = 0.f;
+    uint32_t item = blockIdx.x * split.len;
+    const uint32_t end = item + split.len < split.items ? item + split.len : split.items;
+    while (item < end) {
+        const uint32_t unit = item / per_group;
+        const int64_t row = unit / groups;
+        const int g = static_cast<int>(unit - static_cast<uint32_t>(row) * groups);
+        const int h0 = static_cast<int>(g * per_group + (item - unit * per_group));
+        item = (unit + 1) * per_group < end ? (unit + 1) * per_group : end;
+        const int h1 = static_cast<int>(g * per_group + (item - unit * per_group));
+        int rows;
+        int64_t t0;
+        chunk_of_row(a, row, t0, rows);
+        if (rows <= 0) continue;   // a length-0 sequence's row
+        auto tile_rsrc = [&](const void *base, int64_t ld, int64_t col, int cols) {
+            return chunk_rsrc(static_cast<const E *>(base) + t0 * ld + col, static_cast<uint32_t>(((rows - 1) * ld + cols) * es));
+        };
+        TileP tx, ty;
+        GateTile<kGradThreads> tg;
+        float d_next;
+        auto load_xy = [&](int h) {
+            tx.load(tile_rsrc(a.x, a.ldx, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.ldx * es));
+            ty.load(tile_rsrc(a.dy, a.lddy, static_cast<int64_t>(h) * P, P), static_cast<uint32_t>(a.lddy * es));
+            tg.load(a, row, h);
+            d_next = a.D ? a.D[h] : 0.f;
+        };
+        const float *const Sbase = a.chunk_state, *const Ebase = a.chunk_state + a.n_chunks * a.heads * (N * P);
+        f32x4 Sv[PT], Ev[PT];   // this wave's rows n of S and E
+        auto load_states = [&](int h) {
+            const int64_t at = (row * a.heads + h) * (N * P) + (nt * PT * 64 + l) * 4;
 #pragma unroll
             for (int k = 0; k < PT; ++k) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
-                if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PE + 16 * k + 4 * lq, Ev[k]);
+                Sv[k] = *reinterpret_cast<const f32x4 *>(Sbase + at + k * 256);
+                Ev[k] = *reinterpret_cast<const f32x4 *>(Ebase + at + k * 256);
             }
-            es_sum = lane_sum<64>(es_sum);
-            if (l == 0) s_es[wave] = es_sum;
-        }
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            f32x4 acc[IW];
-#pragma unroll
-            for (int i = 0; i < IW; ++i) acc[i] = zero4();
-#pragma unroll
-            for (int q = 0; q < P / 32; ++q) {
-                F8 st[T::kParts], f[IW];
-#pragma unroll
-                for (int i = 0; i < IW; ++i) f[i] = T::template kfrag<true>((side ? sX : sY) + (16 * (it0 + i) + l16) * PP, q, lq);
-                T::split(side ? Ev[2 * q] : Sv[2 * q], side ? Ev[2 * q + 1] : Sv[2 * q + 1], st);
-                if constexpr (T::kBf16) __builtin_amdgcn_sched_barrier(0);   // the reads together, ahead of the products
-#pragma unroll
-                for (int e = T::kParts - 1; e >= 0; --e)
-#pragma unroll
-                    for (int i = 0; i < IW; ++i) acc[i] = T::mma(st[e], f[i], acc[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < IW; ++i) {
-                const int at = 16 * (it0 + i) + l16;
-                const float f = side ? s.w[at] : s.eg[at];
-                const f32x4 o = side ? T::load4(sB + at * PN + T::template col<true>(16 * nt + 4 * lq)) : T::up(cd[i]);
-                float d = 0.f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) d += acc[i][r] * o[r];
-                if (side) db[i] = db[i] + acc[i] * f;
-                else dc[i] = dc[i] + acc[i] * f;
-                d = sum_rows(d);
-                if (lq == 0) (side ? s_e : s_s)[nt][at] = d;
-            }
-        }
-        __syncthreads();
-        load_states(h + 1 < h1 ? h + 1 : h);
-
-        asm volatile("" : "+v"(l16), "+v"(lq));
-        // dx for this wave's rows p
+        };
         {
-            f32x4 X[JW], V[JW];
-#pragma unroll
-            for (int j = 0; j < JW; ++j) X[j] = V[j] = zero4();
-            const float *Ep = Ebase + (row * a.heads + h) * (N * P);
-#pragma unroll
-            for (int q = 0; q < N / 32; ++q) {
-                F8 e;
-                if constexpr (T::kBf16) {
-                    e = T::template tr<false>(sE, PE, 32 * q, 16 * pt, l16, lq);
-                } else {
-                    // lane p = l16 of E's tile holds p = 4 (lane / 16) + r: gather the four rows n
-                    f32x4 v[2];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            v[b][r] = Ep[(((2 * q + b) * PT + pt) * 64 + 16 * (l16 / 4) + 4 * lq + r) * 4 + l16 % 4];
-                    e = T::round(v[0], v[1]);
-                }
-                F8 f[JW];
-#pragma unroll
-                for (int j = 0; j < JW; ++j) f[j] = T::template kfrag<true>(sB + (16 * (jt0 + j) + l16) * PN, q, lq);
-#pragma unroll
-                for (int j = 0; j < JW; ++j) V[j] = T::mma(e, f[j], V[j]);
-            }
-            const uint32_t ldx = static_cast<uint32_t>(a.heads * P * es);
-            const __amdgpu_buffer_rsrc_t rx = chunk_rsrc(static_cast<E *>(a.dx) + (t0 * a.heads + h) * P,
-                                                         static_cast<uint32_t>((rows - 1) * ldx + P * es));
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const F8 y = T::template tr<true>(sY, PP, 32 * q, 16 * pt, l16, lq);
-#pragma unroll
-                for (int j = 0; j < JW; ++j)
-                    if (q >= (jt0 + j) / 2) X[j] = T::mma(y, T::template kfrag<true>(sPd + (16 * (jt0 + j) + l16) * PS, q, lq), X[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < JW; ++j) {
-                const int at = 16 * (jt0 + j) + l16, p0 = 16 * pt + 4 * lq;
-                const f32x4 v = (X[j] + V[j] * s.ew[at]) * s.dt[at] + T::load4(sY + at * PP + T::template col<true>(p0)) * dh;
-                const uint32_t off = at * ldx + p0 * es;
-                if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(v)), rx, off, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
-            }
+            TileN tb, tc;
+            tb.load(tile_rsrc(a.b, a.ldb, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldb * es));
+            tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+            tb.store(sB);
+            tc.store(sC);
         }
-        if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_dt_kernel
-            const int tile = l / 16;
-            float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f, es_sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k <= tile) rw += s_row[k][l];
-                if (k >= tile) cl += s_col[k][l];
-            }
-#pragma unroll
-            for (int k = 0; k < NT; ++k) {
-                st += s_s[k][l];
-                et += s_e[k][l];
-                es_sum += s_es[k];
-            }
-            float *to = a.token_part + (row * a.heads + h) * kTokenPart + l;
-            to[0] = rw;
-            to[64] = cl;
-            to[128] = s_w[l];
-            to[192] = s_m[l];
-            to[256] = st;
-            to[320] = et;
-            if (l == 0) to[384] = es_sum;
-        }
+        load_xy(h0);
+        load_states(h0);
         __syncthreads();
-    }
 
-    asm volatile("" : "+v"(l16), "+v"(lq));
-    // the heads' L M dt parts: dc += R B, db += R^T C
-    {
-        TileN tc;
-        tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+        // this wave's tiles of the lower triangle's ten: number wave, and wave + 8
+        int ti[2], tj[2];
+        f32x4 K[2], R[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (wave + 8 * k >= 10) continue;
-            T::store4(sPd + (16 * tj[k] + l16) * PS + T::template col<true>(16 * ti[k] + 4 * lq), R[k]);
+            const int idx = wave + 8 * k;
+            ti[k] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
+            tj[k] = idx - ti[k] * (ti[k] + 1) / 2;
+            K[k] = R[k] = zero4();
+            if (idx < 10) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int at = (16 * ti[k] + 4 * lq + r) * PS + T::template col<true>(16 * tj[k] + (l16 & 12)) + (l16 & 3);
-                if constexpr (T::kBf16) sE[at] = bf16_bits(R[k][r]);
-                else sE[at] = R[k][r];
+                for (int q = 0; q < N / 32; ++q)
+                    K[k] = T::mma(T::template kfrag<true>(sC + (16 * ti[k] + l16) * PN, q, lq),
+                                  T::template kfrag<true>(sB + (16 * tj[k] + l16) * PN, q, lq), K[k]);
             }
         }
-        if (wave == 0 || wave == 2) T::store4(sE + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
-        tc.store(sC);
-    }
-    __syncthreads();
+        // the values of c beside this wave's rows n of dc (c leaves LDS for x and dy)
+        typename T::F4 cd[IW];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const F8 bt = T::template tr<true>(sB, PN, 32 * q, 16 * nt, l16, lq), ct = T::template tr<true>(sC, PN, 32 * q, 16 * nt, l16, lq);
+        for (int i = 0; i < IW; ++i) cd[i] = T::raw4(sC + (16 * (it0 + i) + l16) * PN + T::template col<true>(16 * nt + 4 * lq));
+        // tiles above the diagonal that pairs of tiles reach
+        if (wave == 1 || wave == 3) T::store4(sPd + (16 * wave + l16) * PS + T::template col<true>(16 * (wave - 1) + 4 * lq), zero4());
+        f32x4 dc[IW], db[IW];
+#pragma unroll
+        for (int i = 0; i < IW; ++i) dc[i] = db[i] = zero4();
+        __syncthreads();
+
+        for (int h = h0; h < h1; ++h) {
+            const Gates &s = sg;
+            tx.store(sX);
+            ty.store(sY);
+            tg.store(sg);
+            __syncthreads();
+            // Unconditional (the last head's own once more), so that a later wait
+            // for the states can count these as still on their way
+            const float dh = d_next;
+            load_xy(h + 1 < h1 ? h + 1 : h);
+            // opaque coordinates, as in the walks: addresses are made in each phase
+            asm volatile("" : "+v"(l16), "+v"(lq));
+            // M, W and what they give
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (wave + 8 * k >= 10) continue;
+                f32x4 m = zero4();
+#pragma unroll
+                for (int q = 0; q < P / 32; ++q)
+                    m = T::mma(T::template kfrag<true>(sY + (16 * ti[k] + l16) * PP, q, lq),
+                               T::template kfrag<true>(sX + (16 * tj[k] + l16) * PP, q, lq), m);
+                const int i0 = 16 * ti[k] + 4 * lq, j = 16 * tj[k] + l16;
+                const f32x4 gi = *reinterpret_cast<const f32x4 *>(&s.ghi[i0]), gil = *reinterpret_cast<const f32x4 *>(&s.glo[i0]);
+                const float gj = s.ghi[j], gjl = s.glo[j], dtj = s.dt[j];
+                f32x4 pd, rs;
+                float col = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool below = i0 + r > j, on = i0 + r == j;
+                    const float e = __expf((gi[r] - gj) + (gil[r] - gjl));
+                    const float lk = below || on ? e * K[k][r] : 0.f;
+                    const float lm = below || on ? e * m[r] : 0.f;
+                    const float w = lk * m[r];
+                    pd[r] = lk;
+                    R[k][r] += lm * dtj;
+                    rs[r] = below ? w * dtj : 0.f;
+                    col += below ? w : 0.f;
+                    if (on) {
+                        s_w[j] = w;
+                        s_m[j] = m[r];
+                    }
+                }
+                T::store4(sPd + j * PS + T::template col<true>(i0), pd);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) rs[r] = lane_sum<16>(rs[r]);
+                if (l16 == 0) *reinterpret_cast<f32x4 *>(&s_row[tj[k]][i0]) = rs;
+                col = sum_rows(col);
+                if (lq == 0) s_col[ti[k]][j] = col;
+            }
+            asm volatile("" : "+v"(l16), "+v"(lq));
+            // S dy^T and E x^T for this wave's rows n
+            if (first_n) {
+                float es_sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < PT; ++k) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
+                    if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PE + 16 * k + 4 * lq, Ev[k]);
+                }
+                es_sum = lane_sum<64>(es_sum);
+                if (l == 0) s_es[wave] = es_sum;
+            }
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                f32x4 acc[IW];
+#pragma unroll
+                for (int i = 0; i < IW; ++i) acc[i] = zero4();
+#pragma unroll
+                for (int q = 0; q < P / 32; ++q) {
+                    F8 st[T::kParts], f[IW];
+#pragma unroll
+                    for (int i = 0; i < IW; ++i) f[i] = T::template kfrag<true>((side ? sX : sY) + (16 * (it0 + i) + l16) * PP, q, lq);
+                    T::split(side ? Ev[2 * q] : Sv[2 * q], side ? Ev[2 * q + 1] : Sv[2 * q + 1], st);
+                    if constexpr (T::kBf16) __builtin_amdgcn_sched_barrier(0);   // the reads together, ahead of the products
+#pragma unroll
+                    for (int e = T::kParts - 1; e >= 0; --e)
+#pragma unroll
+                        for (int i = 0; i < IW; ++i) acc[i] = T::mma(st[e], f[i], acc[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < IW; ++i) {
+                    const int at = 16 * (it0 + i) + l16;
+                    const float f = side ? s.w[at] : s.eg[at];
+                    const f32x4 o = side ? T::load4(sB + at * PN + T::template col<true>(16 * nt + 4 * lq)) : T::up(cd[i]);
+                    float d = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) d += acc[i][r] * o[r];
+                    if (side) db[i] = db[i] + acc[i] * f;
+                    else dc[i] = dc[i] + acc[i] * f;
+                    d = sum_rows(d);
+                    if (lq == 0) (side ? s_e : s_s)[nt][at] = d;
+                }
+            }
+            __syncthreads();
+            load_states(h + 1 < h1 ? h + 1 : h);
+
+            asm volatile("" : "+v"(l16), "+v"(lq));
+            // dx for this wave's rows p
+            {
+                f32x4 X[JW], V[JW];
+#pragma unroll
+                for (int j = 0; j < JW; ++j) X[j] = V[j] = zero4();
+                const float *Ep = Ebase + (row * a.heads + h) * (N * P);
+#pragma unroll
+                for (int q = 0; q < N / 32; ++q) {
+                    F8 e;
+                    if constexpr (T::kBf16) {
+                        e = T::template tr<false>(sE, PE, 32 * q, 16 * pt, l16, lq);
+                    } else {
+                        // lane p = l16 of E's tile holds p = 4 (lane / 16) + r: gather the four rows n
+                        f32x4 v[2];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                v[b][r] = Ep[(((2 * q + b) * PT + pt) * 64 + 16 * (l16 / 4) + 4 * lq + r) * 4 + l16 % 4];
+                        e = T::round(v[0], v[1]);
+                    }
+                    F8 f[JW];
+#pragma unroll
+                    for (int j = 0; j < JW; ++j) f[j] = T::template kfrag<true>(sB + (16 * (jt0 + j) + l16) * PN, q, lq);
+#pragma unroll
+                    for (int j = 0; j < JW; ++j) V[j] = T::mma(e, f[j], V[j]);
+                }
+                const uint32_t ldx = static_cast<uint32_t>(a.heads * P * es);
+                const __amdgpu_buffer_rsrc_t rx = chunk_rsrc(static_cast<E *>(a.dx) + (t0 * a.heads + h) * P,
+                                                             static_cast<uint32_t>((rows - 1) * ldx + P * es));
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const F8 y = T::template tr<true>(sY, PP, 32 * q, 16 * pt, l16, lq);
+#pragma unroll
+                    for (int j = 0; j < JW; ++j)
+                        if (q >= (jt0 + j) / 2) X[j] = T::mma(y, T::template kfrag<true>(sPd + (16 * (jt0 + j) + l16) * PS, q, lq), X[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < JW; ++j) {
+                    const int at = 16 * (jt0 + j) + l16, p0 = 16 * pt + 4 * lq;
+                    const f32x4 v = (X[j] + V[j] * s.ew[at]) * s.dt[at] + T::load4(sY + at * PP + T::template col<true>(p0)) * dh;
+                    const uint32_t off = at * ldx + p0 * es;
+                    if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(v)), rx, off, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
+                }
+            }
+            if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_dt_kernel
+                const int tile = l / 16;
+                float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f, es_sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k <= tile) rw += s_row[k][l];
+                    if (k >= tile) cl += s_col[k][l];
+                }
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    st += s_s[k][l];
+                    et += s_e[k][l];
+                    es_sum += s_es[k];
+                }
+                float *to = a.token_part + (row * a.heads + h) * kTokenPart + l;
+                to[0] = rw;
+                to[64] = cl;
+                to[128] = s_w[l];
+                to[192] = s_m[l];
+                to[256] = st;
+                to[320] = et;
+                if (l == 0) to[384] = es_sum;
+            }
+            __syncthreads();
+        }
+
+        asm volatile("" : "+v"(l16), "+v"(lq));
+        // the heads' L M dt parts: dc += R B, db += R^T C
+        {
+            TileN tc;
+            tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (wave + 8 * k >= 10) continue;
+                T::store4(sPd + (16 * tj[k] + l16) * PS + T::template col<true>(16 * ti[k] + 4 * lq), R[k]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = (16 * ti[k] + 4 * lq + r) * PS + T::template col<true>(16 * tj[k] + (l16 & 12)) + (l16 & 3);
+                    if constexpr (T::kBf16) sE[at] = bf16_bits(R[k][r]);
+                    else sE[at] = R[k][r];
+                }
+            }
+            if (wave == 0 || wave == 2) T::store4(sE + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
+            tc.store(sC);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const F8 bt = T::template tr<true>(sB, PN, 32 * q, 16 * nt, l16, lq), ct = T::template tr<true>(sC, PN, 32 * q, 16 * nt, l16, lq);
+#pragma unroll
+            for (int i = 0; i < IW; ++i) {
+                const int it = it0 + i;
+                if (q <= it / 2) dc[i] = T::mma(bt, T::template kfrag<true>(sE + (16 * it + l16) * PS, q, lq), dc[i]);
+                if (q >= it / 2) db[i] = T::mma(ct, T::template kfrag<true>(sPd + (16 * it + l16) * PS, q, lq), db[i]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < IW; ++i) {
-            const int it = it0 + i;
-            if (q <= it / 2) dc[i] = T::mma(bt, T::template kfrag<true>(sE + (16 * it + l16) * PS, q, lq), dc[i]);
-            if (q >= it / 2) db[i] = T::mma(ct, T::template kfrag<true>(sPd + (16 * it + l16) * PS, q, lq), db[i]);
+            const int t = 16 * (it0 + i) + l16;
+            if (t >= rows) continue;
+            const int64_t to = ((t0 + t) * a.groups + g) * N + 16 * nt + 4 * lq;
+            if (split.parts(unit) > 1) {
+                const int64_t plane = a.total * a.groups * N;
+                const int part = static_cast<int>(blockIdx.x - split.first(unit));
+                *reinterpret_cast<f32x4 *>(a.bc_part + (2 * part) * plane + to) = db[i];
+                *reinterpret_cast<f32x4 *>(a.bc_part + (2 * part + 1) * plane + to) = dc[i];
+            } else {
+                T::store4(static_cast<E *>(a.db) + to, db[i]);
+                T::store4(static_cast<E *>(a.dc) + to, dc[i]);
+            }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < IW; ++i) {
-        const int t = 16 * (it0 + i) + l16;
-        if (t >= rows) continue;
-        const int64_t to = ((t0 + t) * a.groups + g) * N + 16 * nt + 4 * lq;
-        if (a.slices > 1) {
-            const int64_t plane = a.total * a.groups * N;
-            *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice) * plane + to) = db[i];
-            *reinterpret_cast<f32x4 *>(a.bc_part + (2 * slice + 1) * plane + to) = dc[i];
-        } else {
-            T::store4(static_cast<E *>(a.db) + to, db[i]);
-            T::store4(static_cast<E *>(a.dc) + to, dc[i]);
-        }
+        __syncthreads();   // the tiles have been read
     }
 }
 
@@ -398,16 +429,27 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     }
 }
 
-// db and dc from the slices' parts, added in order: HBM bound, 13 us for 4
-// slices of 16384 tokens, n = 128
-template <class T>
-__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_bc_kernel(SsmArgs a, int64_t plane) {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kSsmThreads + threadIdx.x) * 4;
-    if (i >= plane) return;
-    const int side = blockIdx.y;
+// db and dc of the (chunk, group)s that blocks shared: the parts, added in order
+template <class T, int N>
+__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_bc_kernel(SsmArgs a) {
+    const GradSplit split = grad_split(a);
+    const uint32_t unit = blockIdx.x, groups = a.groups;
+    if (unit >= split.items / split.per_group) return;
+    const int parts = split.parts(unit), side = blockIdx.y;
+    if (parts == 1) return;
+    const int64_t row = unit / groups, plane = a.total * a.groups * N;
+    const int g = static_cast<int>(unit - static_cast<uint32_t>(row) * groups);
+    int rows;
+    int64_t t0;
+    chunk_of_row(a, row, t0, rows);
+    const float *const from = a.bc_part + side * plane;
+    const int i = blockIdx.z * kSsmThreads + threadIdx.x, t = i / (N / 4);
+    if (t >= rows) return;
+    const int64_t to = ((t0 + t) * a.groups + g) * N + 4 * (i % (N / 4));
     f32x4 s = zero4();
-    for (int k = 0; k < a.slices; ++k) s = s + *reinterpret_cast<const f32x4 *>(a.bc_part + (2 * k + side) * plane + i);
-    T::store4(static_cast<typename T::E *>(side ? a.dc : a.db) + i, s);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) s = s + *reinterpret_cast<const f32x4 *>(from + 2 * k * plane + to);
+    T::store4(static_cast<typename T::E *>(side ? a.dc : a.db) + to, s);
 }
 
 // dA, dD and dbias of a head from its chunks
@@ -433,23 +475,23 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_heads_kernel(SsmArgs a) {
 
 }  // namespace
 
-int ssm_slices(const SsmArgs &a) {
-    // one block sums the heads of a slice: enough slices to fill the chip, as
-    // few as that takes, because db and dc pass through HBM once a slice (16384
-    // tokens, 32 heads, n = 128, p = 64: about 512, 768, 1024, 2048, 4096 blocks
-    // take 308, 289, 283, 299, 344 us)
-    const int64_t per_group = a.heads / a.groups;
-    int64_t s = (1024 + a.n_chunks * a.groups - 1) / (a.n_chunks * a.groups);
-    s = s < 1 ? 1 : s > per_group ? per_group : s;
-    const int64_t heads = (per_group + s - 1) / s;
-    return static_cast<int>((per_group + heads - 1) / heads);
+int ssm_grad_parts(SsmArgs &a) {
+    // one block a CU (its registers allow no second one)
+    const int64_t items = a.n_chunks * a.heads, per_group = a.heads / a.groups;
+    a.grad_blocks = static_cast<int32_t>(items < 256 ? items : 256);
+    const int64_t sure = (a.cu ? (a.total + 63) / 64 : a.n_chunks) * a.heads;   // fewer only where cu_seqlens leaves tokens out
+    a.grad_least = a.grad_blocks ? static_cast<int32_t>((sure + a.grad_blocks - 1) / a.grad_blocks) : 1;
+    if (a.grad_least < 1) a.grad_least = 1;
+    if (per_group == 1) return 1;
+    const int64_t parts = (per_group - 2) / a.grad_least + 2;
+    return static_cast<int>(parts < per_group ? parts : per_group);
 }
 
 hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
     const dim3 block(kSsmThreads);
     auto run = [&]<class T, int N, int P>() {
-        const int64_t walks = a.n_spans * a.heads, grads = a.n_chunks * a.groups * a.slices;
-        if (walks > 0x7FFFFFFF || grads > 0x7FFFFFFF || a.n_chunks * a.heads > 0x7FFFFFFF ||
+        const int64_t walks = a.n_spans * a.heads;
+        if (walks > 0x7FFFFFFF || a.n_chunks * a.heads > 0x7FFFFFFF ||
              a.n_seq * a.heads * (N * P / 1024) > 0x7FFFFFFF)
             return hipErrorInvalidValue;
         const dim3 grid(static_cast<uint32_t>(walks), 2), walk(walk_threads(P));
@@ -460,14 +502,13 @@ hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
                                    dim3(static_cast<uint32_t>(a.n_seq * a.heads * (N * P / 1024)), 2), block, 0, stream, a);
             }
             hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true, true>), grid, walk, 0, stream, a);
-            hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(static_cast<uint32_t>(grads)), dim3(kGradThreads), 0, stream, a);
+            hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(a.grad_blocks), dim3(kGradThreads), 0, stream, a);
         }
         if (walks > 0)
             hipLaunchKernelGGL(gdr_ssm_dt_kernel, dim3(static_cast<uint32_t>((a.n_chunks * a.heads + 3) / 4)), block, 0, stream, a);
-        const int64_t plane = a.total * a.groups * N;
-        if (a.slices > 1 && plane > 0)
-            hipLaunchKernelGGL((gdr_ssm_bc_kernel<T>), dim3(static_cast<uint32_t>((plane / 4 + kSsmThreads - 1) / kSsmThreads), 2),
-                               block, 0, stream, a, plane);
+        if (a.bc_part && walks > 0)
+            hipLaunchKernelGGL((gdr_ssm_bc_kernel<T, N>), dim3(static_cast<uint32_t>(a.n_chunks * a.groups), 2, N / 16), block, 0,
+                               stream, a);
         hipLaunchKernelGGL(gdr_ssm_heads_kernel, dim3(a.heads), block, 0, stream, a);
         return hipGetLastError();
     };

@@ -267,3 +267,32 @@ def test_in_a_graph(T):
         backward(gdr, d)
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(eager, out))
+
+
+@pytest.mark.parametrize("cu", [None, [0, 0, 1010, 2500]])
+@pytest.mark.parametrize("T,H,G", [(2500, 12, 4), (2500, 8, 1)])
+def test_groups_alone_and_together(T, H, G, cu):
+    """Gradients of a call whose blocks take several heads, across groups, against calls on one group and one
+    head each (which the tests above hold to fp64): twice the 512 U of the terms' sizes at most, which are some 15
+    times the largest result."""
+    import chunked_gated_delta_fwd_amd as gdr
+    d, _ = make(10, 1, T, H, G, 64, 64, F, F, cu)
+    whole = dict(zip(("dx", "ddt", "dA", "db", "dc", "dD", "dbias", "dh0"), backward(gdr, d)))
+    R = H // G
+    db, dc = torch.zeros_like(whole["db"]), torch.zeros_like(whole["dc"])
+    for h in range(H):
+        g = h // R
+        s = slice(h, h + 1)
+        one = dict(zip(("dx", "ddt", "dA", "db", "dc", "dD", "dbias", "dh0"), gdr.ssm_scan_bwd(
+            d["x"][:, :, s].contiguous(), d["dt"][..., s].contiguous(), d["A"][s], d["b"][:, :, g:g + 1].contiguous(),
+            d["c"][:, :, g:g + 1].contiguous(), d["dy"][:, :, s].contiguous(), d["D"][s], d["dt_bias"][s], d["cu"],
+            d["h0"][:, s].contiguous(), d["dht"][:, s].contiguous())))
+        db[:, :, g] += one["db"][:, :, 0]
+        dc[:, :, g] += one["dc"][:, :, 0]
+        for name, part in (("dx", whole["dx"][:, :, s]), ("ddt", whole["ddt"][..., s]), ("dA", whole["dA"][s]),
+                           ("dD", whole["dD"][s]), ("dbias", whole["dbias"][s]), ("dh0", whole["dh0"][:, s])):
+            scale = one[name].abs().max().item()
+            # one head's results do not depend on the others, but its spans may be cut elsewhere: 512 U as above
+            assert (part - one[name]).abs().max().item() <= 512 * U * 30 * scale, (name, h)
+    for name, want in (("db", db), ("dc", dc)):
+        assert (whole[name] - want).abs().max().item() <= 512 * U * 30 * want.abs().max().item(), name
