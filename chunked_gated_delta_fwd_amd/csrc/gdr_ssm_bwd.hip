@@ -52,18 +52,17 @@ __device__ __forceinline__ GradSplit grad_split(const SsmArgs &a) {
     return s;
 }
 
-// Blocks of 8 waves; a wave
-// owns one or two of the (i, j) tiles of the lower triangle, one tile of rows
-// n of db and dc (of half the tokens when n is 64) and one tile of rows p of
-// dx (likewise).  db and dc are summed over the run's heads in registers;
-// their L M parts as one matrix, multiplied once.  8 waves, because with 4 the
-// sums and states of a wave take over 256 registers and spill.
+// Blocks of 8 waves; a wave owns one or two of the (i, j) tiles of the lower
+// triangle, one tile of rows n of db and dc (of half the tokens when n is 64)
+// and one tile of rows p of dx (likewise).  db and dc are summed over a
+// group's heads in registers; their L M parts as one matrix, multiplied once.
+// 8 waves, because with 4 the sums and states of a wave take over 256
+// registers and spill.
 //
 // 16384 tokens in 4 sequences, 32 heads on one b and c, n = 128, p = 64, bf16:
-// 285 us; 580 MB of states, x and dy read and dx and partial sums written, 2.6
-// TB/s over five rounds of blocks where four would do.  A head takes 5.6 us a
-// block (88 KB a CU in that time: near what HBM gives), a block 8 us around its
-// heads.
+// 220 us; 540 MB of states and 200 MB of x, dy, dx, gates and sums, 3.4 TB/s.
+// A head takes 5.6 us of a block (88 KB a CU in that time: near what HBM
+// gives), and what surrounds a group's heads 8 us.
 constexpr int kGradThreads = 512;
 
 template <class T, int N, int P>
@@ -429,7 +428,8 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     }
 }
 
-// db and dc of the (chunk, group)s that blocks shared: the parts, added in order
+// db and dc of the (chunk, group)s that blocks shared: the parts, added in
+// order; 10 us for two parts of 16384 tokens, n = 128
 template <class T, int N>
 __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_bc_kernel(SsmArgs a) {
     const GradSplit split = grad_split(a);
@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_heads_kernel(SsmArgs a) {
 }  // namespace
 
 int ssm_grad_parts(SsmArgs &a) {
-    // one block a CU (its registers allow no second one)
+    // one block a CU (its registers allow no second one): 16384 tokens, 32 heads,
+    // n = 128, p = 64, 256, 512 and 1024 blocks: 475, 492, 525 us a whole gradient
     const int64_t items = a.n_chunks * a.heads, per_group = a.heads / a.groups;
     a.grad_blocks = static_cast<int32_t>(items < 256 ? items : 256);
     const int64_t sure = (a.cu ? (a.total + 63) / 64 : a.n_chunks) * a.heads;   // fewer only where cu_seqlens leaves tokens out

@@ -462,8 +462,8 @@ int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
  *
  * ddt, dA, dD, ddt_bias and dh0 are fp32-accurate for bf16 inputs too.
  * Workspace: about 8 n p + 3100 bytes a (64-token chunk, head), 8 n p a (span,
- * head), and for db and dc, where few blocks would sum whole groups, 8 n bytes a
- * token, group and slice of the heads.
+ * head), and, where blocks share the heads of a group, 8 n bytes a token, group
+ * and sharing block for db and dc.
  */
 int gdr_ssm_scan_bwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
                      const gdr_tensor *b, const gdr_tensor *c, const gdr_tensor *D,
