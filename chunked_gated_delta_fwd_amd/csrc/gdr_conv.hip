@@ -123,7 +123,7 @@ __device__ __forceinline__ void load_past(const ConvArgs &a, int64_t pos, int64_
     }
 }
 
-constexpr int kBatch = 4;   // rows in flight per thread
+constexpr int kBatch = 4;   // rows in flight per thread (2, 4, 8: 446, 395, 414 us forward, 133, 115, 118 backward at the sizes below)
 
 // 65536 tokens of 8192 bf16 channels, 4 taps: 395 us, 5.4 TB/s of the 2.15 GB
 // read and written once (a large copy reaches 5.2): HBM bound.

@@ -391,7 +391,12 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
     typedef Tile<T, N, true, TH> TileC;
     typedef Tile<T, P, false, TH> TileV;
     constexpr int PU = TileU::kPitch, PC = TileC::kPitch, PV = TileV::kPitch, PS = T::pitch(64, true);
-    __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16], sP[kY ? 64 * PS : 16];
+    // The scores wait in registers until x has been read, and take its place,
+    // where that lets one block more onto a CU.
+    constexpr bool kInV = kY && T::kBf16 && P == 64;
+    static_assert(!kInV || PS <= PV);
+    __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16], sOwnP[kY && !kInV ? 64 * PS : 16];
+    E *const sP = kInV ? sV : sOwnP;
     __shared__ __attribute__((aligned(16))) Gates sg[PRE ? 1 : 2];
 
     const uint32_t heads = a.heads, groups = a.groups;
@@ -471,8 +476,10 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
         }
         store_tiles();
     }
-    if (kY && (wave == 0 || wave == 2))   // tiles above the diagonal that the products' pairs of tiles reach
-        T::store4(sP + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
+    auto store_zeros = [&] {   // tiles above the diagonal that the products' pairs of tiles reach
+        if (wave == 0 || wave == 2) T::store4(sP + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
+    };
+    if (kY && !kInV) store_zeros();
     const float dh = kY && a.D ? a.D[h] : 0.f;
     float total = 0.f;   // kLocal: log of the span's decay
     // all loads so far have arrived: otherwise the compiler would wait for the
@@ -495,13 +502,23 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
         // addresses are made there, not kept over the whole loop, where they
         // would take the registers that 4 waves a SIMD need
         asm volatile("" : "+v"(l16), "+v"(lq));
+        constexpr int kScores = (10 + WAVES - 1) / WAVES;
+        f32x4 scores[kScores];
+        auto score_tile = [&](int m, int &it, int &jt) {   // a wave takes tiles wave, wave + WAVES, .. of the ten
+            const int idx = wave + WAVES * m;
+            it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
+            jt = idx - it * (it + 1) / 2;
+            return idx < 10;
+        };
+        auto store_score = [&](int m, int it, int jt) {
+            T::store4(sP + (16 * it + l16) * PS + T::template col<true>(16 * jt + 4 * lq), scores[m]);
+        };
         if constexpr (kY) {
-            // scores, transposed: tile (j, i) of B C^T; a wave takes tiles wave, wave + WAVES, .. of the ten
+            // scores, transposed: tile (j, i) of B C^T
 #pragma unroll
-            for (int m = 0; m < (10 + WAVES - 1) / WAVES; ++m) {
-                const int idx = wave + WAVES * m;
-                if (idx >= 10) break;
-                const int it = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, jt = idx - it * (it + 1) / 2;
+            for (int m = 0; m < kScores; ++m) {
+                int it, jt;
+                if (!score_tile(m, it, jt)) break;
                 f32x4 acc = zero4();
 #pragma unroll
                 for (int q = 0; q < N / 32; ++q)
@@ -511,13 +528,12 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
                 const float gi = s.ghi[i], gil = s.glo[i];
                 const f32x4 gj = *reinterpret_cast<const f32x4 *>(&s.ghi[j0]), gl = *reinterpret_cast<const f32x4 *>(&s.glo[j0]);
                 const f32x4 dj = *reinterpret_cast<const f32x4 *>(&s.dt[j0]);
-                f32x4 p;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float v = acc[r] * __expf((gi - gj[r]) + (gil - gl[r])) * dj[r];
-                    p[r] = j0 + r <= i ? v : 0.f;
+                    scores[m][r] = j0 + r <= i ? v : 0.f;
                 }
-                T::store4(sP + i * PS + T::template col<true>(j0), p);
+                if constexpr (!kInV) store_score(m, it, jt);
             }
         }
         if (!PRE && wave == WAVES - 1 && k + 1 < chunks) {   // the next chunk's gates (the first two waves have one score tile more)
@@ -547,6 +563,16 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
             for (int it = 0; it < 4; ++it) {
                 const float eg = s.eg[16 * it + l16];
                 Y[it] = Y[it] * eg + T::load4(sV + (16 * it + l16) * PV + 16 * wave + 4 * lq) * dh;
+            }
+            if constexpr (kInV) {
+                __syncthreads();   // x has been read
+                asm volatile("" : "+v"(l16), "+v"(lq));
+#pragma unroll
+                for (int m = 0; m < kScores; ++m) {
+                    int it, jt;
+                    if (score_tile(m, it, jt)) store_score(m, it, jt);
+                }
+                store_zeros();
             }
             __syncthreads();   // the scores are in LDS
             asm volatile("" : "+v"(l16), "+v"(lq));
