@@ -218,7 +218,7 @@ hipError_t by_ssm(const SsmArgs &a, F f) {
 // to 107).
 // The longest of packed sequences is taken for four times their average, and
 // for a third of all tokens at least, so that one long among many short ones
-// costs no more than 3 x few steps (37 sequences in 600 tokens: 20 us whole,
+// costs no more than 3 x few steps (37 sequences in 600 tokens: 16 us whole,
 // 41 split).
 void ssm_spans(SsmArgs &a, bool bwd) {
     int64_t longest = a.seq_len;

@@ -377,9 +377,9 @@ constexpr int walk_waves(bool bf16, int p) { return p == 128 ? (bf16 ? 4 : 2) : 
 
 // PRE: the gates come from memory (a.gates); else the last wave makes each
 // chunk's while the others are at work on the one before (calls that are not
-// split: 32 sequences in 16384 tokens, n = p = 128, 216 us so and 196 + 15 with
-// the gates' and tables' launches, which is as much, but 600 tokens of short
-// sequences, 20 us, would take 13 us more).
+// split: a row of 64 tokens, 8 heads, n = 128, p = 64, 7 us so and 13 with the
+// pass, of 448 tokens 25 and 30; 32 sequences in 16384 tokens, 32 heads, n = p =
+// 128, 216 us so and 211 with the pass and the table).
 template <class T, int N, int P, int MODE, bool OB, bool PRE>
 __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_ssm_walk_kernel(SsmArgs a) {
     typedef typename T::E E;
@@ -392,7 +392,9 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
     typedef Tile<T, P, false, TH> TileV;
     constexpr int PU = TileU::kPitch, PC = TileC::kPitch, PV = TileV::kPitch, PS = T::pitch(64, true);
     // The scores wait in registers until x has been read, and take its place,
-    // where that lets one block more onto a CU.
+    // where that lets one block more onto a CU (with a place of their own 592
+    // blocks of 600 tokens took 18.6 us instead of 16.2, 65536 tokens of 32 heads
+    // 528 instead of 498; a block alone on its CU 24.7 instead of 25.3).
     constexpr bool kInV = kY && T::kBf16 && P == 64;
     static_assert(!kInV || PS <= PV);
     __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16], sOwnP[kY && !kInV ? 64 * PS : 16];

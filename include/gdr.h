@@ -440,7 +440,7 @@ int gdr_qk_norm_rope_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_ten
  * state of fp32 accuracy (its products take exact bf16 parts).  f32 inputs:
  * fp32 products throughout.  A non-finite x can reach the y of earlier tokens
  * of its 64-token chunk.  Workspace: none where every sequence is walked by
- * one block (small calls, many short rows); else 4 H n p bytes a span, 1552 H a
+ * one block (small calls, rows of 512 tokens or, f32, 192 and less); else 4 H n p bytes a span, 1552 H a
  * 64-token chunk, and tables.  Spans have about T H / 1024 tokens with
  * cu_seqlens, B T H / 512 without.
  */
