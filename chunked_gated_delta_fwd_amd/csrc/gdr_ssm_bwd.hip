@@ -15,10 +15,13 @@
 // l is the gradient of dt A.  Its recursion starts anew in every chunk from
 // the inner product of E and the state after the chunk, so its rounding does
 // not grow with the sequence; the diagonal of W is left out of it because it
-// would cancel.  W's sums use fp32 products of exact bf16 inputs, the states
-// enter c^T S dy and b^T E x as exact sums of bf16 parts, so ddt, dA and dbias
-// are fp32-accurate also for bf16 inputs; operands that only reach bf16
-// outputs (L K, L M, E in dx) are rounded once to bf16.
+// would cancel, and what does cancel, W's sums along rows and columns, is
+// summed in fp64 (51 tokens of 2 heads: dA is off by 4.3e-7 of itself, 1.3e-6
+// with sums in fp32, the geometric mean of ten draws; it costs 1.5 % of a call).
+// W's sums use fp32 products of exact bf16 inputs, the states enter c^T S dy
+// and b^T E x as exact sums of bf16 parts, so ddt, dA and dbias are
+// fp32-accurate also for bf16 inputs; operands that only reach dx (L K, E),
+// which is bf16 itself, are rounded once to bf16.
 //
 // S and E of every chunk come from the walks of gdr_ssm_device.h.
 #include <type_traits>
@@ -77,7 +80,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     constexpr int kE = T::kBf16 ? (N * PE > 64 * PS ? N * PE : 64 * PS) : 64 * PS;
     __shared__ __attribute__((aligned(16))) E sB[64 * PN], sXY[kXY], sE[kE], sPd[64 * PS];
     __shared__ __attribute__((aligned(16))) Gates sg;
-    __shared__ __attribute__((aligned(16))) float s_row[4][64], s_col[4][64], s_s[NT][64], s_e[NT][64], s_w[64], s_m[64], s_es[8];
+    __shared__ __attribute__((aligned(16))) float s_s[NT][64], s_e[NT][64], s_w[64], s_m[64], s_es[8];
+    __shared__ double s_row[4][64], s_col[4][64];
     E *const sX = sXY, *const sY = sXY + 64 * PP, *const sC = sXY;
 
     const uint32_t per_group = static_cast<uint32_t>(a.heads / a.groups), groups = a.groups;
@@ -186,8 +190,9 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 const int i0 = 16 * ti[k] + 4 * lq, j = 16 * tj[k] + l16;
                 const f32x4 gi = *reinterpret_cast<const f32x4 *>(&s.ghi[i0]), gil = *reinterpret_cast<const f32x4 *>(&s.glo[i0]);
                 const float gj = s.ghi[j], gjl = s.glo[j], dtj = s.dt[j];
-                f32x4 pd, rs;
-                float col = 0.f;
+                f32x4 pd;
+                double rs[4];
+                double col = 0.;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const bool below = i0 + r > j, on = i0 + r == j;
@@ -197,8 +202,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                     const float w = lk * m[r];
                     pd[r] = lk;
                     R[k][r] += lm * dtj;
-                    rs[r] = below ? w * dtj : 0.f;
-                    col += below ? w : 0.f;
+                    rs[r] = below ? static_cast<double>(w) * dtj : 0.;
+                    col += below ? w : 0.f;   // in fp64, as rs: their difference counts
                     if (on) {
                         s_w[j] = w;
                         s_m[j] = m[r];
@@ -206,9 +211,12 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 }
                 T::store4(sPd + j * PS + T::template col<true>(i0), pd);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) rs[r] = lane_sum<16>(rs[r]);
-                if (l16 == 0) *reinterpret_cast<f32x4 *>(&s_row[tj[k]][i0]) = rs;
-                col = sum_rows(col);
+                for (int r = 0; r < 4; ++r) rs[r] = row_sum64(rs[r]);
+                if (l16 == 0) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s_row[tj[k]][i0 + r] = rs[r];
+                }
+                col = sum_rows64(col);
                 if (lq == 0) s_col[ti[k]][j] = col;
             }
             asm volatile("" : "+v"(l16), "+v"(lq));
@@ -307,7 +315,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
             }
             if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_dt_kernel
                 const int tile = l / 16;
-                float rw = 0.f, cl = 0.f, st = 0.f, et = 0.f, es_sum = 0.f;
+                double rw = 0., cl = 0.;
+                float st = 0.f, et = 0.f, es_sum = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (k <= tile) rw += s_row[k][l];
@@ -320,8 +329,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                     es_sum += s_es[k];
                 }
                 float *to = a.token_part + (row * a.heads + h) * kTokenPart + l;
-                to[0] = rw;
-                to[64] = cl;
+                to[0] = static_cast<float>(rw - s.dt[l] * cl);
+                to[64] = static_cast<float>(cl);
                 to[128] = s_w[l];
                 to[192] = s_m[l];
                 to[256] = st;
@@ -332,33 +341,39 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
         }
 
         asm volatile("" : "+v"(l16), "+v"(lq));
-        // the heads' L M dt parts: dc += R B, db += R^T C
-        {
-            TileN tc;
-            tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+        // the heads' L M dt parts: dc += R B, db += R^T C, with R (once for all
+        // heads) as two bf16 parts: one would add a rounding to db's and dc's own
+        TileN tc;
+        tc.load(tile_rsrc(a.c, a.ldc, static_cast<int64_t>(g) * N, N), static_cast<uint32_t>(a.ldc * es));
+        if (wave == 0 || wave == 2) T::store4(sE + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
+        tc.store(sC);
+#pragma unroll
+        for (int part = 0; part < (T::kBf16 ? 2 : 1); ++part) {
+            if (part) __syncthreads();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (wave + 8 * k >= 10) continue;
-                T::store4(sPd + (16 * tj[k] + l16) * PS + T::template col<true>(16 * ti[k] + 4 * lq), R[k]);
+                f32x4 v = R[k];
+                if constexpr (T::kBf16) v = up4(cvt4(v));
+                R[k] = R[k] - v;
+                T::store4(sPd + (16 * tj[k] + l16) * PS + T::template col<true>(16 * ti[k] + 4 * lq), v);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int at = (16 * ti[k] + 4 * lq + r) * PS + T::template col<true>(16 * tj[k] + (l16 & 12)) + (l16 & 3);
-                    if constexpr (T::kBf16) sE[at] = bf16_bits(R[k][r]);
-                    else sE[at] = R[k][r];
+                    if constexpr (T::kBf16) sE[at] = bf16_bits(v[r]);
+                    else sE[at] = v[r];
                 }
             }
-            if (wave == 0 || wave == 2) T::store4(sE + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
-            tc.store(sC);
-        }
-        __syncthreads();
+            __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const F8 bt = T::template tr<true>(sB, PN, 32 * q, 16 * nt, l16, lq), ct = T::template tr<true>(sC, PN, 32 * q, 16 * nt, l16, lq);
+            for (int q = 0; q < 2; ++q) {
+                const F8 bt = T::template tr<true>(sB, PN, 32 * q, 16 * nt, l16, lq), ct = T::template tr<true>(sC, PN, 32 * q, 16 * nt, l16, lq);
 #pragma unroll
-            for (int i = 0; i < IW; ++i) {
-                const int it = it0 + i;
-                if (q <= it / 2) dc[i] = T::mma(bt, T::template kfrag<true>(sE + (16 * it + l16) * PS, q, lq), dc[i]);
-                if (q >= it / 2) db[i] = T::mma(ct, T::template kfrag<true>(sPd + (16 * it + l16) * PS, q, lq), db[i]);
+                for (int i = 0; i < IW; ++i) {
+                    const int it = it0 + i;
+                    if (q <= it / 2) dc[i] = T::mma(bt, T::template kfrag<true>(sE + (16 * it + l16) * PS, q, lq), dc[i]);
+                    if (q >= it / 2) db[i] = T::mma(ct, T::template kfrag<true>(sPd + (16 * it + l16) * PS, q, lq), db[i]);
+                }
             }
         }
 #pragma unroll
@@ -401,26 +416,26 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     const float raw = valid ? dt_raw(a, t0 + l, h) : 0.f, bias = head_bias(a, h), A = a.A[h];
     const Gates &s = *reinterpret_cast<const Gates *>(a.gates + item * kGateRow);
     const float *in = a.token_part + item * kTokenPart;
-    const float rw = in[l], cl = in[64 + l], diag = in[128 + l], m = in[192 + l], st = in[256 + l], et = in[320 + l];
+    const float diff = in[l], cl = in[64 + l], diag = in[128 + l], m = in[192 + l], st = in[256 + l], et = in[320 + l];
     const float es_sum = in[384];
-    const float dt = s.dt[l], far = s.ew[l] * et;
-    const float v = cl + diag + far;
-    float u = rw + s.eg[l] * st - dt * (cl + far);
-    const float z = s.decay * es_sum + lane_sum<64>(s.w[l] * et);
+    const float dt = s.dt[l], v = cl + diag + s.ew[l] * et;
+    const double write = static_cast<double>(s.w[l]) * et;
+    double u = diff + static_cast<double>(s.eg[l]) * st - write;
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) {
-        const float o = __shfl_down(u, k);
+        const double o = __shfl_down(u, k);
         if (l + k < 64) u += o;
     }
-    const float dl = z + u;
-    float draw = 0.f;
+    const double dl = static_cast<double>(s.decay) * es_sum + sum_rows64(row_sum64(write)) + u;
+    double draw = 0.;
     if (valid) {
         draw = (v + A * dl) / (1.f + expf(-(raw + bias)));
         const int64_t to = (t0 + l) * a.heads + h;
-        if (a.gate_bf16) static_cast<uint16_t *>(a.ddt)[to] = bf16_bits(draw);
-        else static_cast<float *>(a.ddt)[to] = draw;
+        if (a.gate_bf16) static_cast<uint16_t *>(a.ddt)[to] = bf16_bits(static_cast<float>(draw));
+        else static_cast<float *>(a.ddt)[to] = static_cast<float>(draw);
     }
-    const float da = lane_sum<64>(valid ? dt * dl : 0.f), dd = lane_sum<64>(valid ? m : 0.f), dbias = lane_sum<64>(draw);
+    auto sum = [](double x) { return static_cast<float>(sum_rows64(row_sum64(x))); };
+    const float da = sum(valid ? dt * dl : 0.), dd = sum(valid ? m : 0.), dbias = sum(draw);
     if (l == 0) {
         part[0] = da;
         part[1] = dd;

@@ -190,15 +190,6 @@ struct Gates {
     float decay;       // e^G_end
 };
 
-// x plus the value that DPP control CTRL moves in (0 where none is), in fp64
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ double dpp_add64(double x) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, static_cast<uint32_t>(b), CTRL, ROW_MASK, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, static_cast<uint32_t>(b >> 32), CTRL, ROW_MASK, 0xF, false);
-    return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-
 // One wave, lane = token.  Tokens past the end have dt = 0 and write nothing.
 __device__ __forceinline__ void chunk_gates(float raw, float bias, float A, bool valid, Gates &s) {
     const int l = threadIdx.x % 64;
