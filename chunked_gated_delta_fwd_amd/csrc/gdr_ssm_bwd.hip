@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                     else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), rx, off, 0, 0);
                 }
             }
-            if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_dt_kernel
+            if (wave == 7) {   // lane = token: the sums of this head's parts, for gdr_ssm_finish_kernel
                 const int tile = l / 16;
                 double rw = 0., cl = 0.;
                 float st = 0.f, et = 0.f, es_sum = 0.f;
@@ -397,10 +397,9 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
 
 // The gradient of dt, and each chunk's part of dA, dD and dbias, from the
 // token sums of gdr_ssm_grad_kernel: a wave per (chunk, head), lane = token.
-// HBM bound: 13 us for 8300 of them.
-__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
+__device__ __forceinline__ void finish_dt(const SsmArgs &a, uint32_t block) {
     const int l = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kSsmThreads / 64) + wave;
+    const int64_t item = static_cast<int64_t>(block) * (kSsmThreads / 64) + wave;
     if (item >= a.n_chunks * a.heads) return;
     const int64_t row = static_cast<uint32_t>(item) / static_cast<uint32_t>(a.heads);
     const int h = static_cast<int>(item - row * a.heads);
@@ -443,14 +442,14 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_dt_kernel(SsmArgs a) {
     }
 }
 
-// db and dc of the (chunk, group)s that blocks shared: the parts, added in
-// order; 10 us for two parts of 16384 tokens, n = 128
+// db and dc of the (chunk, group)s that blocks shared: the parts, added in order
 template <class T, int N>
-__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_bc_kernel(SsmArgs a) {
+__device__ __forceinline__ void finish_bc(const SsmArgs &a, uint32_t block) {
     const GradSplit split = grad_split(a);
-    const uint32_t unit = blockIdx.x, groups = a.groups;
+    constexpr uint32_t kPieces = N / 16;
+    const uint32_t unit = block / (2 * kPieces), groups = a.groups;
     if (unit >= split.items / split.per_group) return;
-    const int parts = split.parts(unit), side = blockIdx.y;
+    const int parts = split.parts(unit), side = block / kPieces % 2;
     if (parts == 1) return;
     const int64_t row = unit / groups, plane = a.total * a.groups * N;
     const int g = static_cast<int>(unit - static_cast<uint32_t>(row) * groups);
@@ -458,13 +457,23 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_bc_kernel(SsmArgs a) {
     int64_t t0;
     chunk_of_row(a, row, t0, rows);
     const float *const from = a.bc_part + side * plane;
-    const int i = blockIdx.z * kSsmThreads + threadIdx.x, t = i / (N / 4);
+    const int i = block % kPieces * kSsmThreads + threadIdx.x, t = i / (N / 4);
     if (t >= rows) return;
     const int64_t to = ((t0 + t) * a.groups + g) * N + 4 * (i % (N / 4));
     f32x4 s = zero4();
 #pragma unroll 4
     for (int k = 0; k < parts; ++k) s = s + *reinterpret_cast<const f32x4 *>(from + 2 * k * plane + to);
     T::store4(static_cast<typename T::E *>(side ? a.dc : a.db) + to, s);
+}
+
+// What the gradient's blocks left: dt_blocks blocks of the first kind, the others
+// of the second.  One launch for both, whose loads wait beside each other: with
+// one each the gradient took 486 us instead of 481 (16384 tokens, 32 heads, n =
+// 128, p = 64).
+template <class T, int N>
+__global__ void __launch_bounds__(kSsmThreads) gdr_ssm_finish_kernel(SsmArgs a, uint32_t dt_blocks) {
+    if (blockIdx.x < dt_blocks) finish_dt(a, blockIdx.x);
+    else finish_bc<T, N>(a, blockIdx.x - dt_blocks);
 }
 
 // dA, dD and dbias of a head from its chunks
@@ -520,11 +529,13 @@ hipError_t launch_ssm_bwd(const SsmArgs &a, hipStream_t stream) {
             hipLaunchKernelGGL((gdr_ssm_walk_kernel<T, N, P, kStates, true, true>), grid, walk, 0, stream, a);
             hipLaunchKernelGGL((gdr_ssm_grad_kernel<T, N, P>), dim3(a.grad_blocks), dim3(kGradThreads), 0, stream, a);
         }
-        if (walks > 0)
-            hipLaunchKernelGGL(gdr_ssm_dt_kernel, dim3(static_cast<uint32_t>((a.n_chunks * a.heads + 3) / 4)), block, 0, stream, a);
-        if (a.bc_part && walks > 0)
-            hipLaunchKernelGGL((gdr_ssm_bc_kernel<T, N>), dim3(static_cast<uint32_t>(a.n_chunks * a.groups), 2, N / 16), block, 0,
-                               stream, a);
+        if (walks > 0) {
+            const int64_t dt_blocks = (a.n_chunks * a.heads + 3) / 4;
+            const int64_t blocks = dt_blocks + (a.bc_part ? a.n_chunks * a.groups * (N / 8) : 0);
+            if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+            hipLaunchKernelGGL((gdr_ssm_finish_kernel<T, N>), dim3(static_cast<uint32_t>(blocks)), block, 0, stream, a,
+                               static_cast<uint32_t>(dt_blocks));
+        }
         hipLaunchKernelGGL(gdr_ssm_heads_kernel, dim3(a.heads), block, 0, stream, a);
         return hipGetLastError();
     };
