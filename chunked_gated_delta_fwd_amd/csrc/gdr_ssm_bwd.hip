@@ -63,7 +63,7 @@ __device__ __forceinline__ GradSplit grad_split(const SsmArgs &a) {
 // registers and spill.
 //
 // 16384 tokens in 4 sequences, 32 heads on one b and c, n = 128, p = 64, bf16:
-// 220 us; 540 MB of states and 200 MB of x, dy, dx, gates and sums, 3.4 TB/s.
+// 230 us; 540 MB of states and 200 MB of x, dy, dx, gates and sums, 3.2 TB/s.
 // A head takes 5.6 us of a block (88 KB a CU in that time: near what HBM
 // gives), and what surrounds a group's heads 8 us.
 constexpr int kGradThreads = 512;

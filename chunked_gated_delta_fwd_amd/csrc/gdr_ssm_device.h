@@ -352,7 +352,7 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo
 // state: E <- e^G_end E + sum_i e^G_i c_i dy_i^T, stored at each chunk's end.
 //
 // 65536 tokens in 15 sequences, 32 heads on 16 groups, n = p = 128, bf16:
-// kLocal 202 us, kOut 520 to 600 us, which is 3 TB/s of x, y, b, c and gates
+// kLocal 170 to 200 us, kOut 500 to 600 us, which is 3 TB/s of x, y, b, c and gates
 // and 0.6 PFLOP/s of matrix work.  kOut issues 78 matrix, 449 vector and 102 LDS
 // instructions a wave and chunk; LDS reads (315 us of the CU's LDS cycles), the
 // vector unit (190 us) and the three barriers of a chunk bound it: with no loads
