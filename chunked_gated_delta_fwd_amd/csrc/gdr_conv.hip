@@ -40,7 +40,7 @@ __device__ __forceinline__ void ldv(const void *base, int64_t i, float (&o)[VEC]
         for (int e = 0; e < 4; ++e) o[e] = u[e];
     }
 }
-template <bool BF16, int VEC>
+template <bool BF16, int VEC, bool PAST = false>
 __device__ __forceinline__ void stv(void *base, int64_t i, const float (&o)[VEC]) {
     if constexpr (VEC == 1) {
         if constexpr (BF16) reinterpret_cast<uint16_t *>(base)[i] = bf16_bits(o[0]);
@@ -51,12 +51,16 @@ __device__ __forceinline__ void stv(void *base, int64_t i, const float (&o)[VEC]
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e)
             u[e] = bf16_bits(o[2 * e]) | (static_cast<uint32_t>(bf16_bits(o[2 * e + 1])) << 16);
-        *reinterpret_cast<Piece *>(reinterpret_cast<uint16_t *>(base) + i) = u;
+        Piece *const to = reinterpret_cast<Piece *>(reinterpret_cast<uint16_t *>(base) + i);
+        if constexpr (PAST) __builtin_nontemporal_store(u, to);
+        else *to = u;
     } else {
         f32x4 u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[e] = o[e];
-        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(base) + i) = u;
+        f32x4 *const to = reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(base) + i);
+        if constexpr (PAST) __builtin_nontemporal_store(u, to);
+        else *to = u;
     }
 }
 
@@ -125,10 +129,12 @@ __device__ __forceinline__ void load_past(const ConvArgs &a, int64_t pos, int64_
 
 constexpr int kBatch = 4;   // rows in flight per thread (2, 4, 8: 446, 395, 414 us forward, 133, 115, 118 backward at the sizes below)
 
-// 65536 tokens of 8192 bf16 channels, 4 taps: 395 us, 5.4 TB/s of the 2.15 GB
+// 65536 tokens of 8192 bf16 channels, 4 taps: 383 us, 5.6 TB/s of the 2.15 GB
 // read and written once (a large copy reaches 5.2): HBM bound.
 
-template <bool BF16, int W, int VEC>
+// PAST: y is stored past the caches (compiled apart: a branch at each store
+// takes 24 us).
+template <bool BF16, int W, int VEC, bool PAST>
 __global__ void __launch_bounds__(kThreads) gdr_conv_fwd_kernel(ConvArgs a, int64_t strip, int64_t n_strips,
                                                                  int64_t blocks) {
     const int64_t nvec = a.ch / VEC;
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) gdr_conv_fwd_kernel(ConvArgs a, int6
             for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
             win[W - 2][v] = x[v];
         }
-        stv<BF16, VEC>(a.y, t * a.ch + c, o);
+        stv<BF16, VEC, PAST>(a.y, t * a.ch + c, o);
     };
     for (int64_t t = t0; t < t1;) {
         const int64_t n = seq_of(a, t);
@@ -490,8 +496,13 @@ hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t stream) {
     const int64_t blocks = ((n_strips + (a.st ? a.n_seq : 0)) * nvec + kThreads - 1) / kThreads;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     return by_conv<8>(a, [&]<bool BF16, int W, int VEC>() {
-        hipLaunchKernelGGL((gdr_conv_fwd_kernel<BF16, W, VEC>), dim3(static_cast<uint32_t>(blocks)), dim3(kThreads), 0,
-                           stream, a, strip, n_strips, blocks);
+        const dim3 grid(static_cast<uint32_t>(blocks));
+        if (VEC > 1 && past_caches(a.total * a.ch * (BF16 ? 2 : 4)))
+            hipLaunchKernelGGL((gdr_conv_fwd_kernel<BF16, W, VEC, (VEC > 1)>), grid, dim3(kThreads), 0, stream, a, strip,
+                               n_strips, blocks);
+        else
+            hipLaunchKernelGGL((gdr_conv_fwd_kernel<BF16, W, VEC, false>), grid, dim3(kThreads), 0, stream, a, strip, n_strips,
+                               blocks);
         return hipGetLastError();
     });
 }

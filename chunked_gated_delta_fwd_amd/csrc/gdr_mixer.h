@@ -17,6 +17,24 @@ __device__ __forceinline__ int64_t xcd_run(int64_t block, int64_t count) {
     return x * q + (x < r ? x : r) + block / 8;
 }
 
+// Whether an output of so many bytes is stored past the caches.  A convolution
+// of 4096 channels and the norm that reads it, us with plain and with such
+// stores: 32 MB 31 and 35, 64 MB 48 and 52, 128 MB 112 and 107, 512 MB 464 and
+// 439; a norm gradient of 151 MB alone 109 and 106.  (Not the convolution's
+// gradient, 114.8 and 114.4.)
+__host__ __device__ inline bool past_caches(int64_t bytes) { return bytes >= (int64_t{1} << 27); }
+// Stores a piece of 8 or 16 bytes.
+template <class V>
+__device__ __forceinline__ void store_piece(V *to, V v, bool past) {
+    if (past) {
+        asm volatile("");   // otherwise the compiler joins the two stores into a plain one
+        __builtin_nontemporal_store(v, to);
+        asm volatile("");
+    } else {
+        *to = v;
+    }
+}
+
 // Short causal depthwise convolution; rows of x and dy are ld* elements apart.
 struct ConvArgs {
     const void *x, *w, *bias;   // bias NULL: none

@@ -42,17 +42,17 @@ __device__ __forceinline__ void ld8f(const void *base, int64_t i, float (&o)[8])
     }
 }
 template <bool BF16>
-__device__ __forceinline__ void st8f(void *base, int64_t i, const float (&o)[8]) {
+__device__ __forceinline__ void st8f(void *base, int64_t i, const float (&o)[8], bool past) {
     if constexpr (BF16) {
         v4u32 u;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             u[e] = bf16_bits(o[2 * e]) | (static_cast<uint32_t>(bf16_bits(o[2 * e + 1])) << 16);
-        *reinterpret_cast<v4u32 *>(reinterpret_cast<uint16_t *>(base) + i) = u;
+        store_piece(reinterpret_cast<v4u32 *>(reinterpret_cast<uint16_t *>(base) + i), u, past);
     } else {
         f32x4 *p = reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(base) + i);
-        p[0] = f32x4{o[0], o[1], o[2], o[3]};
-        p[1] = f32x4{o[4], o[5], o[6], o[7]};
+        store_piece(p, f32x4{o[0], o[1], o[2], o[3]}, past);
+        store_piece(p + 1, f32x4{o[4], o[5], o[6], o[7]}, past);
     }
 }
 
@@ -144,7 +144,7 @@ __device__ __forceinline__ bool side_of_block(int64_t blocks_k, int64_t blocks, 
     return is_k;
 }
 
-// 65536 tokens of 16 + 16 bf16 heads of 128: 213 to 222 us without rotation,
+// 65536 tokens of 16 + 16 bf16 heads of 128: 216 to 219 us without rotation,
 // 4.9 TB/s of the 1.07 GB, 231 us with (a large copy reaches 5.2 TB/s).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int most, int64_t blocks_k) {
@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int 
     if (wp) ld8f<BF16>(wp, 8 * l, w);
     Turn t;
     if (a.rot) load_turn<LANES>(a, token, l, t);
+    const bool past = past_caches(a.tokens * (a.hq + a.hk) * D * (BF16 ? 2 : 4));
     constexpr int U = 4;
     // every lane of a wave runs the same number of rows (the exchanges need
     // them all): those past the item's heads read and store nothing
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int 
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[u][e] *= inv * w[e];
             if (a.rot) rotate(a, t, false, x[u]);
-            if (h0 + u < count) st8f<BF16>(out, to + static_cast<int64_t>(h0 + u) * D, x[u]);
+            if (h0 + u < count) st8f<BF16>(out, to + static_cast<int64_t>(h0 + u) * D, x[u], past);
         }
     }
 }
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) gdr_norm_fwd_kernel(NormArgs a, int 
 // A block walks several items, all of q or all of k; dw is summed in registers,
 // then over the block's rows in a fixed order, then over blocks (q's rows of
 // partial sums first) by a second kernel.  16384 tokens of 32 + 4 bf16 heads of
-// 128: 107 us and 5 for the sums, 4.2 TB/s of the 453 MB.
+// 128: 102 us and 5 for the sums, 4.4 TB/s of the 453 MB.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads) gdr_norm_bwd_kernel(NormArgs a, int most, int64_t blocks_k) {
     constexpr int LANES = D / 8, ROWS = kThreads / LANES;
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) gdr_norm_bwd_kernel(NormArgs a, int 
         acc[e] = 0.f;
     }
     if (wp) ld8f<BF16>(wp, 8 * l, w);
+    const bool past = past_caches(a.tokens * (a.hq + a.hk) * D * (BF16 ? 2 : 4));
     for (int64_t base = mine * ROWS; base < items; base += stride) {
         const bool live = base + sub < items;
         const int64_t i = live ? base + sub : items - 1;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) gdr_norm_bwd_kernel(NormArgs a, int 
                         acc[e] += g[u][e] * (x[u][e] * inv);
                         x[u][e] = inv * (g[u][e] * w[e]) - x[u][e] * back;
                     }
-                    st8f<BF16>(out, to + static_cast<int64_t>(h0 + u) * D, x[u]);
+                    st8f<BF16>(out, to + static_cast<int64_t>(h0 + u) * D, x[u], past);
                 }
             }
         }

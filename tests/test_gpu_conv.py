@@ -182,3 +182,18 @@ def test_conv_backward_in_a_graph():
         gdr.short_conv_bwd(*args)
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(eager, out))
+
+
+def test_large_outputs():
+    """An output that is stored past the caches has the bits of its rows computed alone."""
+    import chunked_gated_delta_fwd_amd as gdr
+    g = torch.Generator(device="cuda").manual_seed(21)
+    for dtype, ch in ((BF, 4096), (F, 2048)):
+        x = torch.randn(2, 8192, ch, generator=g, device="cuda").to(dtype)
+        w = torch.randn(ch, 4, generator=g, device="cuda").to(dtype)
+        s0 = torch.randn(2, 3, ch, generator=g, device="cuda").to(dtype)
+        y, st = gdr.short_conv_fwd(x, w, s0=s0)
+        assert y.numel() * y.element_size() >= 1 << 27
+        for i in range(2):
+            one, s1 = gdr.short_conv_fwd(x[i:i + 1], w, s0=s0[i:i + 1])
+            assert torch.equal(one[0], y[i]) and torch.equal(s1[0], st[i])

@@ -143,3 +143,23 @@ def test_norm_positions_outside_the_table_stay_inside():
     a = gdr.qk_norm_rope_fwd(dv["q"], dv["k"], None, None, dv["cos"], dv["sin"], dv["pos"])
     b = gdr.qk_norm_rope_fwd(dv["q"], dv["k"], None, None, dv["cos"], dv["sin"], near)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_large_outputs():
+    """Outputs that are stored past the caches have the bits of their rows computed alone."""
+    import chunked_gated_delta_fwd_amd as gdr
+    g = torch.Generator(device="cuda").manual_seed(22)
+    for dtype, hq in ((torch.bfloat16, 28), (torch.float32, 12)):
+        q = torch.randn(2, 8192, hq, 128, generator=g, device="cuda").to(dtype)
+        k = torch.randn(2, 8192, 4, 128, generator=g, device="cuda").to(dtype)
+        cos, sin = torch.randn(2, 8192, 32, generator=g, device="cuda")
+        wq = torch.randn(128, generator=g, device="cuda").to(dtype)
+        oq, ok = gdr.qk_norm_rope_fwd(q, k, wq, None, cos, sin)
+        assert (oq.numel() + ok.numel()) * oq.element_size() >= 1 << 27
+        dq, dk, _, _ = gdr.qk_norm_rope_bwd(q, k, oq, ok, wq, None, cos, sin)
+        for i in range(2):
+            s = slice(i, i + 1)
+            a, b = gdr.qk_norm_rope_fwd(q[s], k[s], wq, None, cos, sin)
+            assert torch.equal(a[0], oq[i]) and torch.equal(b[0], ok[i])
+            a, b, _, _ = gdr.qk_norm_rope_bwd(q[s], k[s], oq[s], ok[s], wq, None, cos, sin)
+            assert torch.equal(a[0], dq[i]) and torch.equal(b[0], dk[i])
