@@ -468,7 +468,7 @@ __device__ __forceinline__ void finish_bc(const SsmArgs &a, uint32_t block) {
 
 // What the gradient's blocks left: dt_blocks blocks of the first kind, the others
 // of the second.  One launch for both, whose loads wait beside each other: with
-// one each the gradient took 486 us instead of 481 (16384 tokens, 32 heads, n =
+// one each the gradient took 486 us where it took 481 so (16384 tokens, 32 heads, n =
 // 128, p = 64).
 template <class T, int N>
 __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_finish_kernel(SsmArgs a, uint32_t dt_blocks) {

@@ -340,8 +340,9 @@ __device__ __forceinline__ void store_state_tile(float *m, int nt, int pt, int l
 __device__ __forceinline__ f32x4 load_tile(__amdgpu_buffer_rsrc_t r, uint32_t voff, int tile) {
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, tile * 1024, 0));
 }
+template <int AUX = 0>   // 2: past the caches
 __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t r, uint32_t voff, int tile, f32x4 v) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), r, voff, tile * 1024, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, v), r, voff, tile * 1024, AUX);
 }
 
 // Walks of the state over the chunks of a span, one block per (span, head):
@@ -418,6 +419,10 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
         else if (init) Z[nt] = load_state_tile<P, OB>(init + (sp.seq * a.heads + h) * (N * P), nt, wave, l16, lq);
     }
 
+    // The states of both directions go past the caches from 256 MiB (32 heads,
+    // n = p = 128, a gradient of 2048 tokens, 134 MB: 132 us, 139 so; 4096: 220 and
+    // 217; 8192: 399 and 375).
+    const bool past = MODE == kStates && past_caches(a.n_chunks * a.heads * (N * P * 4));
     const int chunks = static_cast<int>((sp.len + 63) / 64);
     const int64_t ldu = rev ? a.ldc : a.ldb, ldv = rev ? a.lddy : a.ldx;
     const E *ub = static_cast<const E *>(rev ? a.c : a.b) + g * N;
@@ -485,8 +490,13 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
         if (MODE == kStates && sp.row0 + c < a.n_chunks) {   // always, unless cu_seqlens breaks its preconditions
             const __amdgpu_buffer_rsrc_t to = chunk_rsrc(
                 a.chunk_state + ((static_cast<int64_t>(rev ? 1 : 0) * a.n_chunks + sp.row0 + c) * a.heads + h) * (N * P), N * P * 4);
+            if (past) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) store_tile(to, 16 * l, nt * PT + wave, Z[nt]);
+                for (int nt = 0; nt < NT; ++nt) store_tile<2>(to, 16 * l, nt * PT + wave, Z[nt]);
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) store_tile(to, 16 * l, nt * PT + wave, Z[nt]);
+            }
         }
         __syncthreads();   // this chunk's tiles and gates are in LDS
         if (k + 1 < chunks) load_tiles(k + 1);
