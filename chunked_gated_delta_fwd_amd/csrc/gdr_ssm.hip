@@ -28,8 +28,9 @@ namespace {
 // owns one (sequence, head) with the whole state in registers, 16 bytes a
 // lane, so all of its loads are in flight at once; y is summed over the rows
 // each thread holds, then over row groups through LDS.  256 sequences of 32
-// heads of 128 x 128: 210 us, 5.1 TB/s of 1.08 GB (a large copy reaches 5.2).
-template <int N, int P, bool BF16>
+// heads of 128 x 128: 180 us, 6.0 TB/s of 1.08 GB (a large copy reaches 5.2).
+// PAST: the state goes past the caches both ways.
+template <int N, int P, bool BF16, bool PAST>
 __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
     constexpr int CG = P / 4, RG = 256 / CG, RPT = N / RG;
     __shared__ float s_b[N], s_c[N], s_part[RG][P];
@@ -42,7 +43,11 @@ __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
     float *hp = a.ht + (seq * a.heads + h) * N * P;
     f32x4 S[RPT];
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) S[i] = *reinterpret_cast<const f32x4 *>(hp + (i0 + i) * P + j0);
+    for (int i = 0; i < RPT; ++i) {
+        const f32x4 *from = reinterpret_cast<const f32x4 *>(hp + (i0 + i) * P + j0);
+        if constexpr (PAST) S[i] = __builtin_nontemporal_load(from);
+        else S[i] = *from;
+    }
     if (t < N) s_b[t] = load_scalar<BF16>(a.b, seq * a.ldb + g * N + t);
     else if (t < 2 * N) s_c[t - N] = load_scalar<BF16>(a.c, seq * a.ldc + g * N + t - N);
     const float dt = softplus(dt_raw(a, seq, h) + head_bias(a, h));
@@ -55,7 +60,9 @@ __global__ void __launch_bounds__(256) gdr_ssm_step_kernel(SsmArgs a) {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         S[i] = S[i] * decay + x * (dt * s_b[i0 + i]);
-        *reinterpret_cast<f32x4 *>(hp + (i0 + i) * P + j0) = S[i];
+        f32x4 *const to = reinterpret_cast<f32x4 *>(hp + (i0 + i) * P + j0);
+        if constexpr (PAST) __builtin_nontemporal_store(S[i], to);
+        else *to = S[i];
         y = y + S[i] * s_c[i0 + i];
     }
     *reinterpret_cast<f32x4 *>(&s_part[rg][j0]) = y;
@@ -267,8 +274,16 @@ hipError_t launch_ssm_fwd(const SsmArgs &a, hipStream_t stream) {
 
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream) {
     return by_ssm(a, [&]<int N, int P, bool BF16>() {
-        hipLaunchKernelGGL((gdr_ssm_step_kernel<N, P, BF16>), dim3(static_cast<uint32_t>(a.n_seq * a.heads)), dim3(256), 0,
-                           stream, a);
+        const dim3 grid(static_cast<uint32_t>(a.n_seq * a.heads)), block(256);
+        // A layer's state comes round again after every other layer's, and is
+        // in no cache then.  States of 2, 17, 67, 134, 268 and 537 MB in turn with
+        // others, us kept in the caches and past them: 4.1 and 4.6, 9.7 and 7.8, 30
+        // and 22, 55 and 46, 104 and 90, 209 and 180.  (The same state over and
+        // over: 6.1 and 6.0, 20 and 20, 40 and 45, 79 and 90 from 17 to 268 MB.)
+        if (a.n_seq * a.heads * (N * P * 4) >= (1 << 24))
+            hipLaunchKernelGGL((gdr_ssm_step_kernel<N, P, BF16, true>), grid, block, 0, stream, a);
+        else
+            hipLaunchKernelGGL((gdr_ssm_step_kernel<N, P, BF16, false>), grid, block, 0, stream, a);
         return hipGetLastError();
     });
 }

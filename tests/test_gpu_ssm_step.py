@@ -42,3 +42,21 @@ def test_three_tokens(B, H, G, n, p, dtype, gate, extras):
     worst = 3 * (1 + (step * c["A"].abs()).max().item())   # three tokens' roundings
     check("state", h, ht, 16 * U * worst * mh)
     check("y", torch.stack(ys, 1), y, (n + 32 + 16 * worst) * U * my + (half_step(dtype) * y.abs() if dtype == BF else 0))
+
+
+@pytest.mark.parametrize("dtype,n,p", [(BF, 128, 128), (F, 64, 128)])
+def test_large_states(dtype, n, p):
+    """States that go past the caches have the bits of each sequence alone, over three tokens."""
+    import chunked_gated_delta_fwd_amd as gdr
+    B, H = 5 * 128 // n, 65
+    d, _ = make(B, H, 5, n, p, dtype, dtype, seed=2)
+    h = d["h"].clone()
+    assert h.numel() * 4 >= 1 << 24
+    ys = [gdr.ssm_step(d["x"][:, t], d["dt"][:, t], d["A"], d["b"][:, t], d["c"][:, t], h, d["D"], d["dt_bias"]) for t in range(3)]
+    for i in range(B):
+        s = slice(i, i + 1)
+        one = d["h"][s].clone()
+        for t in range(3):
+            y = gdr.ssm_step(d["x"][s, t], d["dt"][s, t], d["A"], d["b"][s, t], d["c"][s, t], one, d["D"], d["dt_bias"])
+            assert torch.equal(y[0], ys[t][i])
+        assert torch.equal(one[0], h[i])
