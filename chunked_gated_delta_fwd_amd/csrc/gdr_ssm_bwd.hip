@@ -21,7 +21,7 @@
 // W's sums use fp32 products of exact bf16 inputs, the states enter c^T S dy
 // and b^T E x as exact sums of bf16 parts, so ddt, dA and dbias are
 // fp32-accurate also for bf16 inputs; operands that only reach dx (L K, E),
-// which is bf16 itself, are rounded once to bf16.
+// which is bf16 itself, are taken as two bf16 parts.
 //
 // S and E of every chunk come from the walks of gdr_ssm_device.h.
 #include <type_traits>
@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
     constexpr int kXY = 2 * 64 * PP > 64 * PN ? 2 * 64 * PP : 64 * PN;   // x and dy; c before and after the heads
     constexpr int kE = T::kBf16 ? (N * PE > 64 * PS ? N * PE : 64 * PS) : 64 * PS;
     __shared__ __attribute__((aligned(16))) E sB[64 * PN], sXY[kXY], sE[kE], sPd[64 * PS];
+    // the second parts of what only reaches dx (E and L K)
+    __shared__ __attribute__((aligned(16))) E sE2[T::kBf16 ? N * PE : 16], sPd2[T::kBf16 ? 64 * PS : 16];
     __shared__ __attribute__((aligned(16))) Gates sg;
     __shared__ __attribute__((aligned(16))) float s_s[NT][64], s_e[NT][64], s_w[64], s_m[64], s_es[8];
     __shared__ double s_row[4][64], s_col[4][64];
@@ -160,7 +162,10 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
 #pragma unroll
         for (int i = 0; i < IW; ++i) cd[i] = T::raw4(sC + (16 * (it0 + i) + l16) * PN + T::template col<true>(16 * nt + 4 * lq));
         // tiles above the diagonal that pairs of tiles reach
-        if (wave == 1 || wave == 3) T::store4(sPd + (16 * wave + l16) * PS + T::template col<true>(16 * (wave - 1) + 4 * lq), zero4());
+        if (wave == 1 || wave == 3) {
+            const int at = (16 * wave + l16) * PS + T::template col<true>(16 * (wave - 1) + 4 * lq);
+            T::store_two(sPd + at, sPd2 + at, zero4());
+        }
         f32x4 dc[IW], db[IW];
 #pragma unroll
         for (int i = 0; i < IW; ++i) dc[i] = db[i] = zero4();
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                         s_m[j] = m[r];
                     }
                 }
-                T::store4(sPd + j * PS + T::template col<true>(i0), pd);
+                T::store_two(sPd + j * PS + T::template col<true>(i0), sPd2 + j * PS + T::template col<true>(i0), pd);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) rs[r] = row_sum64(rs[r]);
                 if (l16 == 0) {
@@ -227,7 +232,8 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 for (int k = 0; k < PT; ++k) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) es_sum += Ev[k][r] * Sv[k][r];
-                    if constexpr (T::kBf16) T::store4(sE + (16 * nt + l16) * PE + 16 * k + 4 * lq, Ev[k]);
+                    const int at = (16 * nt + l16) * PE + 16 * k + 4 * lq;
+                    if constexpr (T::kBf16) T::store_two(sE + at, sE2 + at, Ev[k]);
                 }
                 es_sum = lane_sum<64>(es_sum);
                 if (l == 0) s_es[wave] = es_sum;
@@ -275,9 +281,10 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 const float *Ep = Ebase + (row * a.heads + h) * (N * P);
 #pragma unroll
                 for (int q = 0; q < N / 32; ++q) {
-                    F8 e;
+                    F8 e[T::kOutParts];
                     if constexpr (T::kBf16) {
-                        e = T::template tr<false>(sE, PE, 32 * q, 16 * pt, l16, lq);
+                        e[0] = T::template tr<false>(sE, PE, 32 * q, 16 * pt, l16, lq);
+                        e[1] = T::template tr<false>(sE2, PE, 32 * q, 16 * pt, l16, lq);
                     } else {
                         // lane p = l16 of E's tile holds p = 4 (lane / 16) + r: gather the four rows n
                         f32x4 v[2];
@@ -286,13 +293,15 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 v[b][r] = Ep[(((2 * q + b) * PT + pt) * 64 + 16 * (l16 / 4) + 4 * lq + r) * 4 + l16 % 4];
-                        e = T::round(v[0], v[1]);
+                        T::two(v[0], v[1], e);
                     }
                     F8 f[JW];
 #pragma unroll
                     for (int j = 0; j < JW; ++j) f[j] = T::template kfrag<true>(sB + (16 * (jt0 + j) + l16) * PN, q, lq);
 #pragma unroll
-                    for (int j = 0; j < JW; ++j) V[j] = T::mma(e, f[j], V[j]);
+                    for (int k = T::kOutParts - 1; k >= 0; --k)
+#pragma unroll
+                        for (int j = 0; j < JW; ++j) V[j] = T::mma(e[k], f[j], V[j]);
                 }
                 const uint32_t ldx = static_cast<uint32_t>(a.heads * P * es);
                 const __amdgpu_buffer_rsrc_t rx = chunk_rsrc(static_cast<E *>(a.dx) + (t0 * a.heads + h) * P,
@@ -301,8 +310,11 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                 for (int q = 0; q < 2; ++q) {
                     const F8 y = T::template tr<true>(sY, PP, 32 * q, 16 * pt, l16, lq);
 #pragma unroll
-                    for (int j = 0; j < JW; ++j)
-                        if (q >= (jt0 + j) / 2) X[j] = T::mma(y, T::template kfrag<true>(sPd + (16 * (jt0 + j) + l16) * PS, q, lq), X[j]);
+                    for (int k = T::kOutParts - 1; k >= 0; --k)
+#pragma unroll
+                        for (int j = 0; j < JW; ++j)
+                            if (q >= (jt0 + j) / 2)
+                                X[j] = T::mma(y, T::template kfrag<true>((k ? sPd2 : sPd) + (16 * (jt0 + j) + l16) * PS, q, lq), X[j]);
                 }
 #pragma unroll
                 for (int j = 0; j < JW; ++j) {

@@ -1,6 +1,8 @@
 // Device code shared by the state space scan's kernels (gdr_ssm.hip, gdr_ssm_bwd.hip).
 #pragma once
 
+#include <cfloat>
+
 #include "gdr_device.h"
 #include "gdr_lanes.h"
 #include "gdr_mixer.h"
@@ -45,16 +47,49 @@ struct BfT {
                      (KP ? (x0 & ~31) + ((x0 >> 2) & 4) + 8 * (l16 % 4) : x0 + 4 * (l16 % 4));
         return cat(ld4_tr(p), ld4_tr(p + 16 * pitch));
     }
-    static __device__ __forceinline__ F8 round(f32x4 a, f32x4 b) { return cat(cvt4(a), cvt4(b)); }
     static __device__ __forceinline__ f32x4 lo(F8 a) { return up4(__builtin_shufflevector(a, a, 0, 1, 2, 3)); }
     static __device__ __forceinline__ f32x4 hi(F8 a) { return up4(__builtin_shufflevector(a, a, 4, 5, 6, 7)); }
     static __device__ __forceinline__ f32x4 load4(const E *p) { return up4(ld4(p)); }
     static __device__ __forceinline__ void store4(E *p, f32x4 v) { st4(p, cvt4(v)); }
+    // An fp32 value as two bf16 ones: its top 8 bits and the rest, rounded.  The
+    // sum is within 2^-15 of the value, so an operand that only reaches a bf16
+    // output leaves that output its own rounding (2^-8) alone; one bf16 operand
+    // added as much again (y of 600 tokens in 37 sequences was 2.2e-3 off and is
+    // 1.7e-3 so, which is y's rounding; 65536 tokens take 830 us for 760, 55 of
+    // them for the state's second part).  Infinite values stay so in both.
+    static constexpr int kOutParts = 2;
+    static __device__ __forceinline__ void two(f32x4 a, F4 (&o)[2]) {
+        v2u32 top;
+        f32x4 rest;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            top[e] = __builtin_amdgcn_perm(__float_as_uint(a[2 * e + 1]), __float_as_uint(a[2 * e]), 0x07060302u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float t = __uint_as_float(__float_as_uint(a[e]) & 0xFFFF0000u);
+            rest[e] = a[e] - __builtin_amdgcn_fmed3f(t, -FLT_MAX, FLT_MAX);
+        }
+        o[0] = __builtin_bit_cast(F4, top);
+        o[1] = cvt4(rest);
+    }
+    static __device__ __forceinline__ void two(f32x4 a, f32x4 b, F8 (&o)[2]) {
+        F4 x[2], y[2];
+        two(a, x);
+        two(b, y);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) o[k] = cat(x[k], y[k]);
+    }
+    static __device__ __forceinline__ void store_two(E *top, E *rest, f32x4 v) {
+        F4 o[2];
+        two(v, o);
+        st4(top, o[0]);
+        st4(rest, o[1]);
+    }
     // An fp32 value as a sum of three bf16 ones: each takes the top 8 bits of
     // what is left, so the sum is the value exactly (a bf16 product keeps all
     // 16 bits of its operands' product in fp32).  This keeps the states, and
     // everything a gradient sums from them, at fp32 accuracy at three times
-    // the matrix work; one rounded operand would leave 2^-9.
+    // the matrix work; one rounded operand would leave 2^-8.
     static __device__ __forceinline__ void split(f32x4 a, f32x4 b, F8 (&o)[3]) {
         typedef unsigned int u8v __attribute__((ext_vector_type(4)));
         u8v w[3];
@@ -112,9 +147,11 @@ struct FpT {
         }
         return o;
     }
-    static __device__ __forceinline__ F8 round(f32x4 a, f32x4 b) { return {a, b}; }
     static __device__ __forceinline__ f32x4 lo(F8 a) { return a.a; }
     static __device__ __forceinline__ f32x4 hi(F8 a) { return a.b; }
+    static constexpr int kOutParts = 1;
+    static __device__ __forceinline__ void two(f32x4 a, f32x4 b, F8 (&o)[1]) { o[0] = {a, b}; }
+    static __device__ __forceinline__ void store_two(E *top, E *, f32x4 v) { store4(top, v); }
     static __device__ __forceinline__ void split(f32x4 a, f32x4 b, F8 (&o)[1]) { o[0] = {a, b}; }
 };
 
@@ -383,14 +420,16 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
     typedef Tile<T, N, true, TH> TileC;
     typedef Tile<T, P, false, TH> TileV;
     constexpr int PU = TileU::kPitch, PC = TileC::kPitch, PV = TileV::kPitch, PS = T::pitch(64, true);
-    // The scores wait in registers until x has been read, and take its place,
-    // where that lets one block more onto a CU (with a place of their own 592
-    // blocks of 600 tokens took 18.6 us instead of 16.2, 65536 tokens of 32 heads
-    // 528 instead of 498; a block alone on its CU 24.7 instead of 25.3).
+    // The scores wait in registers until x and c have been read, and take their
+    // places, where that lets one block more onto a CU (of one part each, with a
+    // place of their own 592 blocks of 600 tokens took 18.6 us instead of 16.2,
+    // 65536 tokens of 32 heads 528 instead of 498; a block alone on its CU 24.7
+    // instead of 25.3).
     constexpr bool kInV = kY && T::kBf16 && P == 64;
-    static_assert(!kInV || PS <= PV);
-    __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16], sOwnP[kY && !kInV ? 64 * PS : 16];
-    E *const sP = kInV ? sV : sOwnP;
+    static_assert(!kInV || (PS <= PV && PS <= PC));
+    __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16];
+    __shared__ __attribute__((aligned(16))) E sOwnP[kY && !kInV ? T::kOutParts * 64 * PS : 16];
+    E *const sP = kInV ? sV : sOwnP, *const sP2 = kInV ? sC : sOwnP + (T::kOutParts - 1) * 64 * PS;   // the scores' parts
     __shared__ __attribute__((aligned(16))) Gates sg[PRE ? 1 : 2];
 
     const uint32_t heads = a.heads, groups = a.groups;
@@ -475,7 +514,10 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
         store_tiles();
     }
     auto store_zeros = [&] {   // tiles above the diagonal that the products' pairs of tiles reach
-        if (wave == 0 || wave == 2) T::store4(sP + (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq), zero4());
+        if (wave == 0 || wave == 2) {
+            const int at = (16 * wave + l16) * PS + T::template col<true>(16 * (wave + 1) + 4 * lq);
+            T::store_two(sP + at, sP2 + at, zero4());
+        }
     };
     if (kY && !kInV) store_zeros();
     const float dh = kY && a.D ? a.D[h] : 0.f;
@@ -514,7 +556,8 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
             return idx < 10;
         };
         auto store_score = [&](int m, int it, int jt) {
-            T::store4(sP + (16 * it + l16) * PS + T::template col<true>(16 * jt + 4 * lq), scores[m]);
+            const int at = (16 * it + l16) * PS + T::template col<true>(16 * jt + 4 * lq);
+            T::store_two(sP + at, sP2 + at, scores[m]);
         };
         if constexpr (kY) {
             // scores, transposed: tile (j, i) of B C^T
@@ -557,10 +600,12 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
                 F8 cf[4];
 #pragma unroll
                 for (int it = 0; it < 4; ++it) cf[it] = T::template kfrag<true>(sC + (16 * it + l16) * PC, q, lq);
-                const F8 z = T::round(Z[2 * q], Z[2 * q + 1]);   // the state itself stays fp32; y is rounded to bf16 too
-                __builtin_amdgcn_sched_barrier(0);   // the reads together, ahead of the products
+                F8 z[T::kOutParts];
+                T::two(Z[2 * q], Z[2 * q + 1], z);
 #pragma unroll
-                for (int it = 0; it < 4; ++it) Y[it] = T::mma(z, cf[it], Y[it]);
+                for (int e = T::kOutParts - 1; e >= 0; --e)
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) Y[it] = T::mma(z[e], cf[it], Y[it]);
             }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
@@ -568,7 +613,7 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
                 Y[it] = Y[it] * eg + T::load4(sV + (16 * it + l16) * PV + 16 * wave + 4 * lq) * dh;
             }
             if constexpr (kInV) {
-                __syncthreads();   // x has been read
+                __syncthreads();   // x and c have been read
                 asm volatile("" : "+v"(l16), "+v"(lq));
 #pragma unroll
                 for (int m = 0; m < kScores; ++m) {
@@ -587,10 +632,10 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
 #pragma unroll
-                for (int q = 0; q <= it / 2; ++q) {
-                    const F8 pf = T::template kfrag<true>(sP + (16 * it + l16) * PS, q, lq);
-                    Y[it] = T::mma(v[q], pf, Y[it]);
-                }
+                for (int e = T::kOutParts - 1; e >= 0; --e)
+#pragma unroll
+                    for (int q = 0; q <= it / 2; ++q)
+                        Y[it] = T::mma(v[q], T::template kfrag<true>((e ? sP2 : sP) + (16 * it + l16) * PS, q, lq), Y[it]);
                 const uint32_t off = y0 + it * (16 * ldy);
                 if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(Y[it])), ry, off, 0, 0);
                 else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, Y[it]), ry, off, 0, 0);
