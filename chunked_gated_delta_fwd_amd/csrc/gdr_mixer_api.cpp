@@ -128,6 +128,9 @@ int sequences(const gdr_tensor *cu, int64_t B, int64_t T, int64_t *N) {
     *N = cu->shape[0] - 1;
     return GDR_OK;
 }
+// Tokens that the kernels look at.  Without a sequence there are none, whatever
+// T is: cu_seqlens has no second offset that a token could be looked up in.
+int64_t live_tokens(int64_t N, int64_t B, int64_t T) { return N == 0 ? 0 : B * T; }
 
 // A call's workspace: the caller's, or the library's (the ring, or the large
 // buffer over 1 MiB).  `get` returns 1 when the call only asked for the size.
@@ -162,7 +165,7 @@ class Workspace {
 
 // The opt-in check of the content of cu_seqlens, on a small workspace of its own.
 int check_cu(const gdr_tensor *cu, int64_t N, int64_t total, hipStream_t stream) {
-    if (!cu || N == 0 || !g_check_cu.load(std::memory_order_relaxed)) return GDR_OK;
+    if (!cu || !g_check_cu.load(std::memory_order_relaxed)) return GDR_OK;
     WsLease lease;
     void *ws = nullptr;
     int rc;
@@ -230,7 +233,7 @@ int plan_conv(ConvIn &c, int lead, gdr::ConvArgs &a) {
     a.s0 = c.s0 ? c.s0->data : nullptr;
     a.n_seq = c.N;
     a.seq_len = c.T;
-    a.total = c.B * c.T;
+    a.total = live_tokens(c.N, c.B, c.T);
     a.ch = static_cast<int32_t>(ch);
     a.width = static_cast<int32_t>(W);
     a.bf16 = c.x->dtype == GDR_BF16;
@@ -404,7 +407,7 @@ int plan_ssm(SsmIn &s, int lead, gdr::SsmArgs &a) {
     a.h0 = s.h0 ? static_cast<const float *>(s.h0->data) : nullptr;
     a.n_seq = s.N;
     a.seq_len = s.T;
-    a.total = s.B * s.T;
+    a.total = live_tokens(s.N, s.B, s.T);
     a.heads = static_cast<int32_t>(H);
     a.groups = static_cast<int32_t>(G);
     a.n = static_cast<int32_t>(nn);
@@ -510,8 +513,8 @@ int gdr_short_conv_fwd(const gdr_tensor *x, const gdr_tensor *w, const gdr_tenso
                                  {{"y", span_of(y, ny)}, {"st", span_of(st, nst)}})))
             return rc;
         if ((rc = check_device())) return rc;
+        if ((rc = check_cu(cu_seqlens, a.n_seq, c.B * c.T, stream))) return rc;
         if (a.n_seq == 0 || (a.total == 0 && !st)) return ok();
-        if ((rc = check_cu(cu_seqlens, a.n_seq, a.total, stream))) return rc;
         a.y = y->data;
         a.st = st ? st->data : nullptr;
         a.vec = a.vec && aligned16(y) && aligned16(st);
@@ -563,7 +566,7 @@ int gdr_short_conv_bwd(const gdr_tensor *x, const gdr_tensor *w, const gdr_tenso
                             static_cast<size_t>(ch * (W + 1)) * 4;
         if (workspace || !workspace_bytes) {
             if ((rc = check_device())) return rc;
-            if ((rc = check_cu(cu_seqlens, a.n_seq, a.total, stream))) return rc;
+            if ((rc = check_cu(cu_seqlens, a.n_seq, c.B * c.T, stream))) return rc;
         }
         Workspace ws;
         void *p;
@@ -735,7 +738,7 @@ int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
         carve_ssm(a, false, size, t);
         if (workspace || !workspace_bytes) {
             if ((rc = check_device())) return rc;
-            if ((rc = check_cu(cu_seqlens, a.n_seq, a.total, stream))) return rc;
+            if ((rc = check_cu(cu_seqlens, a.n_seq, s.B * s.T, stream))) return rc;
         }
         Workspace ws;
         void *p;
@@ -818,7 +821,7 @@ int gdr_ssm_scan_bwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
         carve_ssm(a, true, size, t);
         if (workspace || !workspace_bytes) {
             if ((rc = check_device())) return rc;
-            if ((rc = check_cu(cu_seqlens, a.n_seq, a.total, stream))) return rc;
+            if ((rc = check_cu(cu_seqlens, a.n_seq, s.B * s.T, stream))) return rc;
         }
         Workspace ws;
         void *p;

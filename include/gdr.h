@@ -327,7 +327,9 @@ int gdr_decode_step(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *
  * needs and enqueues nothing; with both set, `workspace` (device memory,
  * 16-byte aligned, *workspace_bytes long) is used and must stay untouched
  * until the call's work is done.  All sums run in a fixed order: repeated
- * calls give the same bits.
+ * calls give the same bits.  Without a sequence (cu_seqlens of one offset) no
+ * token is looked at: gradients that are sums over tokens are zero, and rows
+ * of tokens are not written.
  * ------------------------------------------------------------------------ */
 
 typedef enum { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_activation;
