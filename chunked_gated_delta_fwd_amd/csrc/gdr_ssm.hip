@@ -86,7 +86,9 @@ constexpr int kTableThreads = 1024;
 // lengths are known: nothing is split when no sequence is longer than a.whole.
 // 17 sequences in 65536 tokens: 10 us, one block's latency.
 __global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a, SsmTables t) {
-    __shared__ int32_t s_span[kTableThreads], s_chunk[kTableThreads], s_longest;
+    // 64 bits: sequences that cu_seqlens makes overlap can sum to any number
+    __shared__ int64_t s_span[kTableThreads], s_chunk[kTableThreads];
+    __shared__ int32_t s_longest;
     const int tid = threadIdx.x;
     auto range = [&](int64_t n, int64_t &b, int64_t &e) {
         b = a.cu[n];
@@ -108,12 +110,12 @@ __global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a,
     const int64_t span_len = s_longest > a.whole ? a.span_len : a.whole;
     int64_t spans = 0, chunks = 0;
     for (int64_t base = 0; base < a.n_seq; base += kTableThreads) {
-        int32_t ms = 0, mc = 0;
+        int64_t ms = 0, mc = 0;
         if (base + tid < a.n_seq) {
             int64_t b, e;
             range(base + tid, b, e);
-            ms = static_cast<int32_t>((e - b + span_len - 1) / span_len);
-            mc = static_cast<int32_t>((e - b + 63) / 64);
+            ms = (e - b + span_len - 1) / span_len;
+            mc = (e - b + 63) / 64;
             ms = ms < 1 ? 1 : ms;
             mc = mc < 1 ? 1 : mc;
         }
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kTableThreads) gdr_ssm_table_kernel(SsmArgs a,
         __syncthreads();
         const int live = static_cast<int>(a.n_seq - base < kTableThreads ? a.n_seq - base : kTableThreads);
         for (int m = 1; m < live; m *= 2) {
-            const int32_t os = tid >= m ? s_span[tid - m] : 0, oc = tid >= m ? s_chunk[tid - m] : 0;
+            const int64_t os = tid >= m ? s_span[tid - m] : 0, oc = tid >= m ? s_chunk[tid - m] : 0;
             __syncthreads();
             s_span[tid] += os;
             s_chunk[tid] += oc;
