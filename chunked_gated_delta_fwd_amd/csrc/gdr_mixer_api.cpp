@@ -133,23 +133,25 @@ int sequences(const gdr_tensor *cu, int64_t B, int64_t T, int64_t *N) {
 int64_t live_tokens(int64_t N, int64_t B, int64_t T) { return N == 0 ? 0 : B * T; }
 
 // A call's workspace: the caller's, or the library's (the ring, or the large
-// buffer over 1 MiB).  `get` returns 1 when the call only asked for the size.
+// buffer over 1 MiB).  `check` comes before the device is touched and returns 1
+// when the call only asked for the size.
 class Workspace {
   public:
-    int get(size_t need, void *given, int64_t *given_bytes, hipStream_t stream, void **out) {
-        *out = nullptr;
+    static int check(size_t need, const void *given, int64_t *given_bytes) {
         if (!given && given_bytes) {
             *given_bytes = static_cast<int64_t>(need);
             return 1;
         }
-        if (given) {
-            if (!given_bytes) return fail(GDR_EINVAL, "workspace: its size is missing");
-            if (*given_bytes < static_cast<int64_t>(need))
-                return fail(GDR_EINVAL, "workspace: %lld bytes given, %zu needed", (long long)*given_bytes, need);
-            if (reinterpret_cast<uintptr_t>(given) % 16) return fail(GDR_EINVAL, "workspace: must be 16-byte aligned");
-            *out = given;
-            return GDR_OK;
-        }
+        if (!given) return GDR_OK;
+        if (!given_bytes) return fail(GDR_EINVAL, "workspace: its size is missing");
+        if (*given_bytes < static_cast<int64_t>(need))
+            return fail(GDR_EINVAL, "workspace: %lld bytes given, %zu needed", (long long)*given_bytes, need);
+        if (reinterpret_cast<uintptr_t>(given) % 16) return fail(GDR_EINVAL, "workspace: must be 16-byte aligned");
+        return GDR_OK;
+    }
+    int get(size_t need, void *given, hipStream_t stream, void **out) {
+        *out = given;
+        if (given) return GDR_OK;
         if (need == 0) return GDR_OK;
         hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
         if (hipStreamIsCapturing(stream, &st) == hipSuccess && st != hipStreamCaptureStatusNone)
@@ -564,13 +566,12 @@ int gdr_short_conv_bwd(const gdr_tensor *x, const gdr_tensor *w, const gdr_tenso
                 aligned16(ds0);
         const size_t need = static_cast<size_t>(gdr::conv_bwd_rows(a.total, a.ch, a.bf16, a.vec)) *
                             static_cast<size_t>(ch * (W + 1)) * 4;
-        if (workspace || !workspace_bytes) {
-            if ((rc = check_device())) return rc;
-            if ((rc = check_cu(cu_seqlens, a.n_seq, c.B * c.T, stream))) return rc;
-        }
+        if ((rc = Workspace::check(need, workspace, workspace_bytes))) return rc == 1 ? ok() : rc;
+        if ((rc = check_device())) return rc;
+        if ((rc = check_cu(cu_seqlens, a.n_seq, c.B * c.T, stream))) return rc;
         Workspace ws;
         void *p;
-        if ((rc = ws.get(need, workspace, workspace_bytes, stream, &p))) return rc == 1 ? ok() : rc;
+        if ((rc = ws.get(need, workspace, stream, &p))) return rc;
         a.part = static_cast<float *>(p);
         rc = launch([&] { return gdr::launch_conv_bwd(a, stream); }, "short convolution backward kernels");
         const int rr = ws.release();
@@ -672,11 +673,11 @@ int gdr_qk_norm_rope_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_ten
         a.dwk = dwk ? static_cast<float *>(dwk->data) : nullptr;
         const bool sums = a.dwq || a.dwk;
         const size_t need = sums ? static_cast<size_t>(gdr::norm_bwd_blocks(a)) * static_cast<size_t>(d) * 4 : 0;
-        if (workspace || !workspace_bytes)
-            if ((rc = check_device())) return rc;
+        if ((rc = Workspace::check(need, workspace, workspace_bytes))) return rc == 1 ? ok() : rc;
+        if ((rc = check_device())) return rc;
         Workspace ws;
         void *p;
-        if ((rc = ws.get(need, workspace, workspace_bytes, stream, &p))) return rc == 1 ? ok() : rc;
+        if ((rc = ws.get(need, workspace, stream, &p))) return rc;
         // without tokens the sums are zero: the second kernel reads no partial row
         a.part = sums ? static_cast<float *>(p ? p : static_cast<void *>(dwq ? dwq->data : dwk->data)) : nullptr;
         if (a.tokens == 0 && !sums) return ok();
@@ -736,13 +737,12 @@ int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
         Carve size{nullptr};
         gdr::SsmTables t;
         carve_ssm(a, false, size, t);
-        if (workspace || !workspace_bytes) {
-            if ((rc = check_device())) return rc;
-            if ((rc = check_cu(cu_seqlens, a.n_seq, s.B * s.T, stream))) return rc;
-        }
+        if ((rc = Workspace::check(size.used, workspace, workspace_bytes))) return rc == 1 ? ok() : rc;
+        if ((rc = check_device())) return rc;
+        if ((rc = check_cu(cu_seqlens, a.n_seq, s.B * s.T, stream))) return rc;
         Workspace ws;
         void *p;
-        if ((rc = ws.get(size.used, workspace, workspace_bytes, stream, &p))) return rc == 1 ? ok() : rc;
+        if ((rc = ws.get(size.used, workspace, stream, &p))) return rc;
         if (a.n_seq == 0 || (a.total == 0 && !ht)) return ok();
         Carve parts{static_cast<unsigned char *>(p)};
         carve_ssm(a, false, parts, t);
@@ -819,13 +819,12 @@ int gdr_ssm_scan_bwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
         Carve size{nullptr};
         gdr::SsmTables t;
         carve_ssm(a, true, size, t);
-        if (workspace || !workspace_bytes) {
-            if ((rc = check_device())) return rc;
-            if ((rc = check_cu(cu_seqlens, a.n_seq, s.B * s.T, stream))) return rc;
-        }
+        if ((rc = Workspace::check(size.used, workspace, workspace_bytes))) return rc == 1 ? ok() : rc;
+        if ((rc = check_device())) return rc;
+        if ((rc = check_cu(cu_seqlens, a.n_seq, s.B * s.T, stream))) return rc;
         Workspace ws;
         void *p;
-        if ((rc = ws.get(size.used, workspace, workspace_bytes, stream, &p))) return rc == 1 ? ok() : rc;
+        if ((rc = ws.get(size.used, workspace, stream, &p))) return rc;
         Carve parts{static_cast<unsigned char *>(p)};
         carve_ssm(a, true, parts, t);
         rc = launch([&] { return run_ssm(a, t, true, stream); }, "state space scan backward kernels");
