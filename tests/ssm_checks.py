@@ -76,9 +76,20 @@ def check_backward(got, c, cu, dtype, gate, device="cuda"):
     for name, key in (("dx", "x"), ("db", "b"), ("dc", "c")):
         check(name, got[name], r[key].cpu(), (terms(dtype) * s[key] + half * r[key].abs()).cpu())
     check("dh0", got["dh0"], r["h0"].cpu(), (k * s["h0"]).cpu())
-    # the gradient of a decay's logarithm is a sum over the rest of the chunk:
-    # the rest's c . dc and dt v, and <E, S> at its end
-    per = (a["c"] * s["c"]).sum(-1).repeat_interleave(H // G, 2) + step * s["st"]
+    # the gradient of a decay's logarithm is a sum over the rest of the chunk: what its tokens read of earlier
+    # writes, and what later ones read of theirs (not a token's read of its own write), and <E, S> at its end
+    R = H // G
+    a["bh"], a["ch"] = a["b"].repeat_interleave(R, 2), a["c"].repeat_interleave(R, 2)
+    own = step * (a["bh"] * a["ch"]).sum(-1) * (a["x"] * a["dy"]).sum(-1)
+    reads = torch.zeros_like(own)
+    for i, (b0, e0) in enumerate(seqs):   # |c|^T |S| |dy| of each token, head by head
+        S = m["h0"].detach()[i]
+        for t in range(b0, e0):
+            f = lambda v: v.reshape((-1,) + v.shape[2:])[t]   # noqa: E731
+            S = f(dec)[:, None, None] * S
+            reads.reshape(-1, H)[t] = ((f(a["ch"])[:, :, None] * S).sum(1) * f(a["dy"])).sum(-1)
+            S = S + (f(step)[:, None] * f(a["bh"]))[:, :, None] * f(a["x"])[:, None]
+    per = reads + (step * s["st"] - own).clamp(min=0)
     size = torch.zeros_like(per).reshape(-1, H)
     P_, E_ = per.reshape(-1, H), (dec * s["dec"]).reshape(-1, H)
     tail = (dht.abs() * hm.detach()).sum((2, 3))
