@@ -51,6 +51,16 @@ struct BfT {
     static __device__ __forceinline__ f32x4 hi(F8 a) { return up4(__builtin_shufflevector(a, a, 4, 5, 6, 7)); }
     static __device__ __forceinline__ f32x4 load4(const E *p) { return up4(ld4(p)); }
     static __device__ __forceinline__ void store4(E *p, f32x4 v) { st4(p, cvt4(v)); }
+    // 0 in every lane, or NaN in some where a value of the wave's is not finite
+    static __device__ __forceinline__ float probe(F8 a, F8 b) {
+        const f32x4 d = mma(b, F8{}, mma(a, F8{}, zero4()));
+        return (d[0] + d[1]) + (d[2] + d[3]);
+    }
+    // A part that is taken off a value: what is left of an infinite one is
+    // infinite too, not NaN.
+    static __device__ __forceinline__ float below_inf(uint32_t bits) {
+        return __builtin_amdgcn_fmed3f(__uint_as_float(bits), -FLT_MAX, FLT_MAX);
+    }
     // An fp32 value as two bf16 ones: its top 8 bits and the rest, rounded.  The
     // sum is within 2^-15 of the value, so an operand that only reaches a bf16
     // output leaves that output its own rounding (2^-8) alone; one bf16 operand
@@ -65,10 +75,7 @@ struct BfT {
         for (int e = 0; e < 2; ++e)
             top[e] = __builtin_amdgcn_perm(__float_as_uint(a[2 * e + 1]), __float_as_uint(a[2 * e]), 0x07060302u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float t = __uint_as_float(__float_as_uint(a[e]) & 0xFFFF0000u);
-            rest[e] = a[e] - __builtin_amdgcn_fmed3f(t, -FLT_MAX, FLT_MAX);
-        }
+        for (int e = 0; e < 4; ++e) rest[e] = a[e] - below_inf(__float_as_uint(a[e]) & 0xFFFF0000u);
         o[0] = __builtin_bit_cast(F4, top);
         o[1] = cvt4(rest);
     }
@@ -101,8 +108,8 @@ struct BfT {
                 const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
                 w[k][e] = __builtin_amdgcn_perm(yb, xb, 0x07060302u);   // top halves of x (low) and y (high)
                 if (k < 2) {
-                    x -= __uint_as_float(xb & 0xFFFF0000u);
-                    y -= __uint_as_float(yb & 0xFFFF0000u);
+                    x -= below_inf(xb & 0xFFFF0000u);
+                    y -= below_inf(yb & 0xFFFF0000u);
                 }
             }
         }
@@ -149,6 +156,12 @@ struct FpT {
     }
     static __device__ __forceinline__ f32x4 lo(F8 a) { return a.a; }
     static __device__ __forceinline__ f32x4 hi(F8 a) { return a.b; }
+    static __device__ __forceinline__ float probe(F8 a, F8 b) {
+        float t = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t = fmaf(a.a[r], 0.f, fmaf(a.b[r], 0.f, fmaf(b.a[r], 0.f, fmaf(b.b[r], 0.f, t))));
+        return t;
+    }
     static constexpr int kOutParts = 1;
     static __device__ __forceinline__ void two(f32x4 a, f32x4 b, F8 (&o)[1]) { o[0] = {a, b}; }
     static __device__ __forceinline__ void store_two(E *top, E *, f32x4 v) { store4(top, v); }
@@ -629,13 +642,35 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
             const uint32_t y0 = l16 * ldy + (16 * wave + 4 * lq) * sizeof(E);
             E *yb = static_cast<E *>(a.y) + (t * a.heads + h) * P;
             const __amdgpu_buffer_rsrc_t ry = chunk_rsrc(yb, static_cast<uint32_t>((rows - 1) * ldy + P * sizeof(E)));
+            // An x that is not finite must not meet the zeros of earlier tokens'
+            // scores: such a chunk is summed one token at a time, up to its own
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(!(T::probe(v[0], v[1]) == 0.f)) != 0, 0)) {
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int i = 16 * it + l16;
+                        float sum = 0.f;
+#pragma unroll 1
+                        for (int j = 0; j <= i && j < rows; ++j) {
+                            const int at = i * PS + T::template col<true>(j & ~3) + (j & 3);
+                            float score = load_scalar<T::kBf16>(sP, at);
+                            if constexpr (T::kOutParts > 1) score += load_scalar<T::kBf16>(sP2, at);
+                            sum += score * load_scalar<T::kBf16>(vb, (t + j) * ldv + 16 * wave + 4 * lq + r);
+                        }
+                        Y[it][r] += sum;
+                    }
+            } else {
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int e = T::kOutParts - 1; e >= 0; --e)
+#pragma unroll
+                        for (int q = 0; q <= it / 2; ++q)
+                            Y[it] = T::mma(v[q], T::template kfrag<true>((e ? sP2 : sP) + (16 * it + l16) * PS, q, lq), Y[it]);
+            }
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-#pragma unroll
-                for (int e = T::kOutParts - 1; e >= 0; --e)
-#pragma unroll
-                    for (int q = 0; q <= it / 2; ++q)
-                        Y[it] = T::mma(v[q], T::template kfrag<true>((e ? sP2 : sP) + (16 * it + l16) * PS, q, lq), Y[it]);
                 const uint32_t off = y0 + it * (16 * ldy);
                 if constexpr (T::kBf16) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u32, cvt4(Y[it])), ry, off, 0, 0);
                 else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32, Y[it]), ry, off, 0, 0);

@@ -441,8 +441,9 @@ int gdr_qk_norm_rope_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_ten
  * bf16 inputs: bf16 matrix operands with fp32 sums, of which those that are no
  * inputs take two bf16 parts for y (rounded once, and off by no more than that
  * and 2^-15 of its terms) and exact ones for the state (fp32 accuracy).  f32 inputs:
- * fp32 products throughout.  A non-finite x can reach the y of earlier tokens
- * of its 64-token chunk.  Workspace: none where every sequence is walked by
+ * fp32 products throughout.  An x that is not finite
+ * reaches its column of y and of the state from its token on, as in the
+ * recurrence, and an infinite state stays infinite.  Workspace: none where every sequence is walked by
  * one block (small calls, rows of 512 tokens or, f32, 192 and less); else 4 H n p bytes a span, 1552 H a
  * 64-token chunk, and tables.  Spans have about T H / 1024 tokens with
  * cu_seqlens, B T H / 512 without.
@@ -464,7 +465,8 @@ int gdr_ssm_scan_fwd(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor
  *   dh0   [N, H, n, p] out, f32, or NULL (written also when h0 is NULL)
  *
  * ddt, dA, dD, ddt_bias and dh0 are fp32-accurate for bf16 inputs too; dx, db
- * and dc are rounded once.
+ * and dc are rounded once.  A dy, b or c that is not finite can reach dx, dc
+ * and db, in this order, of any token of its 64-token chunk.
  * Workspace: about 8 n p + 3100 bytes a (64-token chunk, head), 8 n p a (span,
  * head), and, where blocks share the heads of a group, 8 n bytes a token, group
  * and sharing block for db and dc.
