@@ -331,7 +331,7 @@ int plan_norm(NormIn &c, gdr::NormArgs &a) {
 
 // --- state space scan ---------------------------------------------------------------
 
-// Chunk tiles are addressed with 32-bit byte offsets over 64 rows.
+// The scan's chunk tiles are addressed with 32-bit byte offsets over 64 rows.
 constexpr int64_t kMaxRow = 1 << 25;
 
 struct SsmIn {
@@ -396,7 +396,7 @@ int plan_ssm(SsmIn &s, int lead, gdr::SsmArgs &a) {
         return rc;
     if (s.N * H > 0x3FFFFFFFLL) return fail(GDR_ESHAPE, "N * H exceeds the launch grid limit");
     const int64_t e = static_cast<int64_t>(dtype_size(s.x->dtype));
-    if (a.ldx * e > kMaxRow || a.ldb * e > kMaxRow || a.ldc * e > kMaxRow)
+    if (!step && (a.ldx * e > kMaxRow || a.ldb * e > kMaxRow || a.ldc * e > kMaxRow))
         return fail(GDR_ESTRIDE, "x, b and c: rows may be at most %lld bytes apart", (long long)kMaxRow);
     a.x = s.x->data;
     a.dt = s.dt->data;
