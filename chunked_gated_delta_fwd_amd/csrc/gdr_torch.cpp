@@ -73,10 +73,19 @@ at::Tensor empty(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType t
 at::Tensor given_or(const Opt &given, at::IntArrayRef shape, const at::Tensor &like, at::ScalarType type) {
     return given ? *given : empty(shape, like, type);
 }
-int64_t sequences(const at::Tensor &x, const Opt &cu) { return cu ? cu->size(0) - 1 : x.size(0); }
 void want_dims(const at::Tensor &t, int64_t n, const char *name) {
     if (t.dim() != n)
         raise(GDR_ESHAPE, std::string(name) + ": expected " + std::to_string(n) + " dimensions, got " + std::to_string(t.dim()));
+}
+// for the shape of a state that the call makes; a cu_seqlens without an offset is refused by the library
+int64_t sequences(const at::Tensor &x, const Opt &cu) {
+    if (!cu) return x.size(0);
+    want_dims(*cu, 1, "cu_seqlens");
+    return cu->size(0) > 0 ? cu->size(0) - 1 : 0;
+}
+
+at::Tensor conv_state(const at::Tensor &x, const at::Tensor &w, const Opt &cu) {
+    return empty({sequences(x, cu), w.size(1) > 0 ? w.size(1) - 1 : 0, x.size(2)}, x, x.scalar_type());
 }
 
 // f(workspace, workspace_bytes) with the library's workspace, or in a stream
@@ -102,7 +111,7 @@ std::tuple<at::Tensor, Opt> short_conv_fwd(const at::Tensor &x, const at::Tensor
     Call c(x);
     at::Tensor y = given_or(y_, x.sizes(), x, x.scalar_type());
     Opt st = st_;
-    if (!st && want_st) st = empty({sequences(x, cu), w.size(1) - 1, x.size(2)}, x, x.scalar_type());
+    if (!st && want_st) st = conv_state(x, w, cu);
     check(gdr_short_conv_fwd(Desc(x, c).p(), Desc(w, c).p(), Desc(bias, c).p(), Desc(cu, c).p(), Desc(s0, c).p(),
                              Desc(y, c).p(), Desc(st, c).p(), act, c.stream()));
     return {y, st};
@@ -118,7 +127,7 @@ std::tuple<at::Tensor, at::Tensor, Opt, Opt> short_conv_bwd(const at::Tensor &x,
     at::Tensor dx = given_or(dx_, x.sizes(), x, x.scalar_type()), dw = given_or(dw_, w.sizes(), x, at::kFloat);
     Opt db = db_, ds0 = ds0_;
     if (!db && bias) db = empty(bias->sizes(), x, at::kFloat);
-    if (!ds0 && want_ds0) ds0 = empty({sequences(x, cu), w.size(1) - 1, x.size(2)}, x, x.scalar_type());
+    if (!ds0 && want_ds0) ds0 = conv_state(x, w, cu);
     const Desc d[] = {Desc(x, c),  Desc(w, c),   Desc(bias, c), Desc(cu, c), Desc(s0, c), Desc(dy, c),
                       Desc(dst, c), Desc(dx, c), Desc(dw, c),   Desc(db, c), Desc(ds0, c)};
     with_workspace(c, [&](void *ws, int64_t *bytes) {
