@@ -63,7 +63,7 @@ inline int check_tensor(const gdr_tensor *t, const char *name, int ndim, int64_t
             return fail(GDR_ESHAPE, "%s: too many elements", name);
         n *= t->shape[i];
     }
-    if (t->strides) {
+    if (t->strides && n > 0) {   // no element is at any place in an empty one
         int64_t expect = 1;
         for (int i = ndim - 1; i >= 0; --i) {
             if (t->shape[i] != 1 && t->strides[i] != expect)
