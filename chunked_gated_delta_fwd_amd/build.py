@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -36,12 +37,18 @@ FLAGS = [
 
 
 def _torch_command() -> list:
-    """The host compiler's line for the extension that mixer.py calls."""
+    """The host compiler's line for the extension that mixer.py calls; raises
+    ImportError where torch, its headers or a host compiler are missing."""
     import torch
     from torch.utils import cpp_extension
 
     root = os.path.dirname(torch.__file__)
-    include = sum((["-isystem", p] for p in cpp_extension.include_paths()), [])
+    paths = cpp_extension.include_paths()
+    if not any(os.path.exists(os.path.join(p, "torch", "extension.h")) for p in paths):
+        raise ImportError("torch's headers are not installed")
+    if shutil.which("g++") is None:
+        raise ImportError("g++ was not found")
+    include = sum((["-isystem", p] for p in paths), [])
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
              "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-DTORCH_EXTENSION_NAME=_gdr_torch"]
             + include + ["-isystem", os.path.join(ROCM, "include"), "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE,
@@ -51,9 +58,18 @@ def _torch_command() -> list:
 
 def build(verbose: bool = False) -> str:
     """Compile every source into ``chunked_gated_delta_fwd_amd/libgdr.so``, then
-    the torch extension that links to it."""
+    the torch extension that links to it.  The C ABI does not need the
+    extension: without torch, its headers or g++ the library is built alone, and
+    mixer.py says what is missing when it is imported."""
     _compile([HIPCC] + FLAGS + [os.path.join(CSRC, s) for s in SOURCES], LIB, verbose)
-    _compile(_torch_command(), TORCH_LIB, verbose)
+    try:
+        command = _torch_command()
+    except ImportError as e:
+        if os.path.exists(TORCH_LIB):   # of other sources
+            os.remove(TORCH_LIB)
+        print("_gdr_torch.so is not built (%s): the Python calls of mixer.py need it" % e, file=sys.stderr, flush=True)
+        return LIB
+    _compile(command, TORCH_LIB, verbose)
     return LIB
 
 
