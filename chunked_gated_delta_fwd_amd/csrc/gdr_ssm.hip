@@ -211,24 +211,25 @@ hipError_t by_ssm(const SsmArgs &a, F f) {
 // 512 walks at 8 waves each fill the chip.  Equal rows take that many; in the
 // backward pass, where the walk from the end runs beside the one from the
 // start, half of it (one row of 16384 tokens, 32 heads, n = 128: forward, p =
-// 64, 128, 256, 512, 1024, 2048 walks: 277, 156, 125, 129, 142 us; backward,
-// 256 and 512: 461 and 459, p = 128: 766 and 792).  Packed sequences make walks
+// 64, 128, 256, 512, 1024, 2048 walks: 333, 184, 140, 136, 143 us; backward,
+// 256 and 512: 417 and 411, p = 128: 777 and 787).  Packed sequences make walks
 // of all lengths and take twice as many (15 in 65536 tokens, p = 128, 512 and
-// 1024: 797 to 817 and 743 to 749 us; backward of 4 to 16 in 16384, p = 64,
-// 256 and 512: 518 to 576 and 499 to 573).
+// 1024: 834 to 1172 and 778 to 792 us; backward of 4 to 16 in 16384, p = 64,
+// 256 and 512: 464 to 482 and 461 to 464).
 //
 // Not split when that takes fewer steps than its extra launches and its second
 // pass over the tokens cost: no sequence longer than `whole` (32 heads, p =
-// 64, 16384 tokens, whole = 2048, packed sequences of up to 1780: 131 us whole,
-// 155 split; of up to 3244: 161 and 145), or none longer than `few` (8 to 32
-// heads; forward bf16, 512 tokens: 28 to 34 us whole, 22 to 43 split, 1024: 53
-// to 64 and 25 to 43; f32, 192: 30 to 40 and 29 to 38; backward bf16, 512: 46
-// to 67 and 46 to 80, 1024: 61 to 103 and 49 to 106; f32, 512: 72 to 114 and 62
-// to 107).
+// 64, 16384 tokens, whole = 2048, packed sequences of up to 1930: 141 us whole,
+// 188 split; of up to 2489: 163 and 155, 3529: 265 and 161), or none longer
+// than `few` (8 and 32 heads, p = 64 and 128; forward bf16, 320 tokens: 23 to 26
+// us whole, 22 to 32 split, 512: 35 to 39 and 23 to 45, 1024: 65 to 74 and 26 to
+// 46; f32, 192: 30 and 29 to 32, 320: 47 and 30 to 35; backward bf16, 512: 46 to
+// 69 and 46 to 82, 768: 54 to 86 and 50 to 91, 1024: 62 to 100 and 50 to 104;
+// f32, 384: 64 to 71 and 57 to 70, 512: 71 to 77 and 60 to 75).
 // The longest of packed sequences is taken for four times their average, and
 // for a third of all tokens at least, so that one long among many short ones
-// costs no more than 3 x few steps (37 sequences in 600 tokens: 16 us whole,
-// 41 split).
+// costs no more than 3 x few steps (37 sequences in 600 tokens: 14 us whole,
+// 45 split).
 void ssm_spans(SsmArgs &a, bool bwd) {
     int64_t longest = a.seq_len;
     if (a.cu) {   // not known here

@@ -63,9 +63,9 @@ __device__ __forceinline__ GradSplit grad_split(const SsmArgs &a) {
 // registers and spill.
 //
 // 16384 tokens in 4 sequences, 32 heads on one b and c, n = 128, p = 64, bf16:
-// 230 us; 540 MB of states and 200 MB of x, dy, dx, gates and sums, 3.2 TB/s.
-// A head takes 5.6 us of a block (88 KB a CU in that time: near what HBM
-// gives), and what surrounds a group's heads 8 us.
+// 235 to 250 us; 540 MB of states and 200 MB of x, dy, dx, gates and sums, 3
+// TB/s.  A head takes some 6 us of a block (88 KB a CU in that time: near what
+// HBM gives), and what surrounds a group's heads 8 us.
 constexpr int kGradThreads = 512;
 
 template <class T, int N, int P>
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kSsmThreads) gdr_ssm_heads_kernel(SsmArgs a) {
 
 int ssm_grad_parts(SsmArgs &a) {
     // one block a CU (its registers allow no second one): 16384 tokens, 32 heads,
-    // n = 128, p = 64, 256, 512 and 1024 blocks: 475, 492, 525 us a whole gradient
+    // n = 128, p = 64, 256, 512 and 1024 blocks: 461, 481, 526 us a whole gradient
     const int64_t items = a.n_chunks * a.heads, per_group = a.heads / a.groups;
     a.grad_blocks = static_cast<int32_t>(items < 256 ? items : 256);
     const int64_t sure = (a.cu ? (a.total + 63) / 64 : a.n_chunks) * a.heads;   // fewer only where cu_seqlens leaves tokens out

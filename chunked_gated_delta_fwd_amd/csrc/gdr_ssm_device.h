@@ -403,17 +403,21 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo
 // state: E <- e^G_end E + sum_i e^G_i c_i dy_i^T, stored at each chunk's end.
 //
 // 65536 tokens in 15 sequences, 32 heads on 16 groups, n = p = 128, bf16:
-// kLocal 170 to 200 us, kOut 500 to 600 us, which is 3 TB/s of x, y, b, c and gates
-// and 0.6 PFLOP/s of matrix work.  kOut issues 78 matrix, 449 vector and 102 LDS
-// instructions a wave and chunk; LDS reads (315 us of the CU's LDS cycles), the
-// vector unit (190 us) and the three barriers of a chunk bound it: with no loads
-// from HBM it took 487 us.  16384 tokens, 32 heads, n = 128, p = 64: kLocal 80
+// kLocal 170 to 200 us, kOut 580 to 650 us, which is 2.7 TB/s of x, y, b, c and
+// gates.  kOut issues 103 matrix, 588 vector and 102 LDS instructions a wave and
+// chunk (counted; 78, 413 and 96, and 500 to 550 us, with y's operands in one
+// bf16 part).  At 2.4 GHz the vector unit is busy for 245 us of it, LDS for 205
+// and 58 more of bank conflicts, the matrix unit for 170, and a chunk has three
+// barriers: no single one of them bounds it, and HBM does not (with one part and
+// no loads from HBM 487 us).  16384 tokens, 32 heads, n = 128, p = 64: kLocal 80
 // us, kStates 145 us for both directions, 272 MB of states each.
 enum WalkMode { kLocal, kStates, kOut };
 
 // Waves of a block: one per 16 columns p, so that its part of the state stays
-// in registers.  32 columns a wave halve the LDS reads but leave 2 waves a SIMD:
-// kOut took 545 us at best instead of 517, 65536 tokens of 32 heads, n = p = 128.
+// in registers.  32 columns a wave halve the LDS reads but leave 2 waves a SIMD
+// in blocks of 67 KB, two to a CU: kOut took 545 us at best instead of 517 (65536
+// tokens of 32 heads, n = p = 128, y's operands in one part; smaller blocks, three
+// to a CU, were not measured).
 constexpr int walk_threads(int p) { return 4 * p; }
 constexpr int walk_waves(bool bf16, int p) { return p == 128 ? (bf16 ? 4 : 2) : (bf16 ? 2 : 1); }   // a SIMD's, at least
 
@@ -421,7 +425,7 @@ constexpr int walk_waves(bool bf16, int p) { return p == 128 ? (bf16 ? 4 : 2) : 
 // chunk's while the others are at work on the one before (calls that are not
 // split: a row of 64 tokens, 8 heads, n = 128, p = 64, 7 us so and 13 with the
 // pass, of 448 tokens 25 and 30; 32 sequences in 16384 tokens, 32 heads, n = p =
-// 128, 216 us so and 211 with the pass and the table).
+// 128, 216 us so and 211 with the pass and the table; y's operands in one part).
 template <class T, int N, int P, int MODE, bool OB, bool PRE>
 __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_ssm_walk_kernel(SsmArgs a) {
     typedef typename T::E E;
@@ -434,10 +438,9 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
     typedef Tile<T, P, false, TH> TileV;
     constexpr int PU = TileU::kPitch, PC = TileC::kPitch, PV = TileV::kPitch, PS = T::pitch(64, true);
     // The scores wait in registers until x and c have been read, and take their
-    // places, where that lets one block more onto a CU (of one part each, with a
-    // place of their own 592 blocks of 600 tokens took 18.6 us instead of 16.2,
-    // 65536 tokens of 32 heads 528 instead of 498; a block alone on its CU 24.7
-    // instead of 25.3).
+    // places, where that lets one block more onto a CU (with a place of their own
+    // 592 blocks of 600 tokens took 15.3 us instead of 13.6, 65536 tokens of 32
+    // heads 545 instead of 514; a block alone on its CU 31.6 instead of 33.2).
     constexpr bool kInV = kY && T::kBf16 && P == 64;
     static_assert(!kInV || (PS <= PV && PS <= PC));
     __shared__ __attribute__((aligned(16))) E sU[64 * PU], sV[64 * PV], sC[kY ? 64 * PC : 16];

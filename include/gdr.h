@@ -106,8 +106,13 @@ typedef struct {
  * o = scale H^T q for each token in turn, with no bf16 rounding anywhere
  * (error against an fp64 evaluation at fp32 rounding level, about 1e-7
  * relative to the state).  It is latency-bound, one token after another, and
- * meant for checking and for f32 callers, not for throughput.  Results do not
- * depend on scheduling: ghost padding and repeated calls are bitwise
+ * meant for checking and for f32 callers, not for throughput.  Known limit of
+ * the bf16 kernel: it inverts each 16-token block of beta e^(G_i - G_j) k_i.k_j
+ * with bf16 factors, which cancel when the keys of a head are alike, beta is near
+ * 1 and there is hardly any decay (beta 0.985, g = -0.001, mean k.k = 0.5: o off
+ * by 0.02 of 0.34; 0.7: by half; from 0.8 on the state grows without bound where
+ * the recurrence stays below 1).  With beta = 0.5, or independent keys, it is at
+ * bf16 level.  Results do not depend on scheduling: ghost padding and repeated calls are bitwise
  * reproducible.
  *
  * Uses a small device workspace (4*N + 16 bytes) when cu_seqlens is given.
