@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_ssm_grad_kernel(SsmArgs a) {
                     F8 st[T::kParts], f[IW];
 #pragma unroll
                     for (int i = 0; i < IW; ++i) f[i] = T::template kfrag<true>((side ? sX : sY) + (16 * (it0 + i) + l16) * PP, q, lq);
-                    T::split(side ? Ev[2 * q] : Sv[2 * q], side ? Ev[2 * q + 1] : Sv[2 * q + 1], st);
+                    T::template split<false>(side ? Ev[2 * q] : Sv[2 * q], side ? Ev[2 * q + 1] : Sv[2 * q + 1], st);
                     if constexpr (T::kBf16) __builtin_amdgcn_sched_barrier(0);   // the reads together, ahead of the products
 #pragma unroll
                     for (int e = T::kParts - 1; e >= 0; --e)

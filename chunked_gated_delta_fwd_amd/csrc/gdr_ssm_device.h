@@ -56,18 +56,23 @@ struct BfT {
         const f32x4 d = mma(b, F8{}, mma(a, F8{}, zero4()));
         return (d[0] + d[1]) + (d[2] + d[3]);
     }
-    // A part that is taken off a value: what is left of an infinite one is
-    // infinite too, not NaN.
-    static __device__ __forceinline__ float below_inf(uint32_t bits) {
-        return __builtin_amdgcn_fmed3f(__uint_as_float(bits), -FLT_MAX, FLT_MAX);
+    // A part that is taken off a value.  INF: what is left of an infinite one is
+    // infinite too, not NaN; only where that can be told apart in a result, the
+    // state and a score with one x (65536 tokens take 847 us without, 878 with it
+    // everywhere).
+    template <bool INF>
+    static __device__ __forceinline__ float part(uint32_t bits) {
+        const float t = __uint_as_float(bits);
+        return INF ? __builtin_amdgcn_fmed3f(t, -FLT_MAX, FLT_MAX) : t;
     }
     // An fp32 value as two bf16 ones: its top 8 bits and the rest, rounded.  The
     // sum is within 2^-15 of the value, so an operand that only reaches a bf16
     // output leaves that output its own rounding (2^-8) alone; one bf16 operand
     // added as much again (y of 600 tokens in 37 sequences was 2.2e-3 off and is
     // 1.7e-3 so, which is y's rounding; 65536 tokens take 830 us for 760, 55 of
-    // them for the state's second part).  Infinite values stay so in both.
+    // them for the state's second part).
     static constexpr int kOutParts = 2;
+    template <bool INF>
     static __device__ __forceinline__ void two(f32x4 a, F4 (&o)[2]) {
         v2u32 top;
         f32x4 rest;
@@ -75,20 +80,20 @@ struct BfT {
         for (int e = 0; e < 2; ++e)
             top[e] = __builtin_amdgcn_perm(__float_as_uint(a[2 * e + 1]), __float_as_uint(a[2 * e]), 0x07060302u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rest[e] = a[e] - below_inf(__float_as_uint(a[e]) & 0xFFFF0000u);
+        for (int e = 0; e < 4; ++e) rest[e] = a[e] - part<INF>(__float_as_uint(a[e]) & 0xFFFF0000u);
         o[0] = __builtin_bit_cast(F4, top);
         o[1] = cvt4(rest);
     }
     static __device__ __forceinline__ void two(f32x4 a, f32x4 b, F8 (&o)[2]) {
         F4 x[2], y[2];
-        two(a, x);
-        two(b, y);
+        two<false>(a, x);
+        two<false>(b, y);
 #pragma unroll
         for (int k = 0; k < 2; ++k) o[k] = cat(x[k], y[k]);
     }
     static __device__ __forceinline__ void store_two(E *top, E *rest, f32x4 v) {
         F4 o[2];
-        two(v, o);
+        two<true>(v, o);
         st4(top, o[0]);
         st4(rest, o[1]);
     }
@@ -97,6 +102,7 @@ struct BfT {
     // 16 bits of its operands' product in fp32).  This keeps the states, and
     // everything a gradient sums from them, at fp32 accuracy at three times
     // the matrix work; one rounded operand would leave 2^-8.
+    template <bool INF>
     static __device__ __forceinline__ void split(f32x4 a, f32x4 b, F8 (&o)[3]) {
         typedef unsigned int u8v __attribute__((ext_vector_type(4)));
         u8v w[3];
@@ -108,8 +114,8 @@ struct BfT {
                 const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
                 w[k][e] = __builtin_amdgcn_perm(yb, xb, 0x07060302u);   // top halves of x (low) and y (high)
                 if (k < 2) {
-                    x -= below_inf(xb & 0xFFFF0000u);
-                    y -= below_inf(yb & 0xFFFF0000u);
+                    x -= part<INF>(xb & 0xFFFF0000u);
+                    y -= part<INF>(yb & 0xFFFF0000u);
                 }
             }
         }
@@ -165,6 +171,7 @@ struct FpT {
     static constexpr int kOutParts = 1;
     static __device__ __forceinline__ void two(f32x4 a, f32x4 b, F8 (&o)[1]) { o[0] = {a, b}; }
     static __device__ __forceinline__ void store_two(E *top, E *, f32x4 v) { store4(top, v); }
+    template <bool INF>
     static __device__ __forceinline__ void split(f32x4 a, f32x4 b, F8 (&o)[1]) { o[0] = {a, b}; }
 };
 
@@ -692,7 +699,7 @@ __global__ void __launch_bounds__(walk_threads(P), walk_waves(T::kBf16, P)) gdr_
             const f32x4 wa = *reinterpret_cast<const f32x4 *>(w + 32 * q + 4 * lq);
             const f32x4 wb = *reinterpret_cast<const f32x4 *>(w + 32 * q + 16 + 4 * lq);
             F8 vs[T::kParts];
-            T::split(T::lo(v[q]) * wa, T::hi(v[q]) * wb, vs);
+            T::template split<!OB>(T::lo(v[q]) * wa, T::hi(v[q]) * wb, vs);
 #pragma unroll
             for (int nt = 0; nt < NT; nt += 2) {   // two tiles at a time: products on one sum do not follow each other
                 F8 u[2];
