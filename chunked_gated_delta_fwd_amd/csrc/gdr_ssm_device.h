@@ -411,9 +411,9 @@ __device__ __forceinline__ void store_tile(__amdgpu_buffer_rsrc_t r, uint32_t vo
 //
 // 65536 tokens in 15 sequences, 32 heads on 16 groups, n = p = 128, bf16:
 // kLocal 170 to 200 us, kOut 580 to 650 us, which is 2.7 TB/s of x, y, b, c and
-// gates.  kOut issues 103 matrix, 588 vector and 102 LDS instructions a wave and
+// gates.  kOut issues 103 matrix, 555 vector and 102 LDS instructions a wave and
 // chunk (counted; 78, 413 and 96, and 500 to 550 us, with y's operands in one
-// bf16 part).  At 2.4 GHz the vector unit is busy for 245 us of it, LDS for 205
+// bf16 part).  At 2.4 GHz the vector unit is busy for 230 us of it, LDS for 205
 // and 58 more of bank conflicts, the matrix unit for 170, and a chunk has three
 // barriers: no single one of them bounds it, and HBM does not (with one part and
 // no loads from HBM 487 us).  16384 tokens, 32 heads, n = 128, p = 64: kLocal 80
