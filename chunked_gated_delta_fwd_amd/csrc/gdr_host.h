@@ -1,5 +1,5 @@
-// Host-side pieces shared by the library's C ABI sources (gdr_api.cpp and
-// gdr_mixer_api.cpp): error text, descriptor checks, the device check, the
+// Host-side pieces shared by the library's C ABI sources (gdr_api.cpp,
+// gdr_mixer_api.cpp, gdr_attn_api.cpp): error text, descriptor checks, the device check, the
 // workspace ring and the debug options.  One copy of each for the library
 // (inline variables).  Not installed; not part of the C ABI.
 #pragma once
