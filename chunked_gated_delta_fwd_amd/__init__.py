@@ -30,17 +30,24 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_checkpoints", "gdr_chunk_bwd", "gdr_c
            "gdr_chunk_local_cumsum", "gdr_last_error", "gdr_version", "gdr_selftest_mfma",
            "gdr_debug_set", "gdr_device_status", "gdr_free_workspaces", "gdr_chunk_fwd_noalloc",
            "gdr_chunk_fwd_checkpoints_n", "gdr_short_conv_fwd", "gdr_short_conv_bwd", "gdr_short_conv_step",
-           "gdr_qk_norm_rope_fwd", "gdr_qk_norm_rope_bwd", "gdr_ssm_scan_fwd", "gdr_ssm_scan_bwd", "gdr_ssm_step")
+           "gdr_qk_norm_rope_fwd", "gdr_qk_norm_rope_bwd", "gdr_ssm_scan_fwd", "gdr_ssm_scan_bwd", "gdr_ssm_step",
+           "gdr_attn_fwd", "gdr_attn_bwd", "gdr_attn_paged_step", "gdr_page_plan", "gdr_page_store")
 
 # the operators around the recurrence (mixer.py), loaded on first use
 _MIXER = ("short_conv_fwd", "short_conv_bwd", "short_conv_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "ssm_scan_fwd",
           "ssm_scan_bwd", "ssm_step")
+# attention and its paged cache (attention.py), likewise
+_ATTENTION = ("attn_fwd", "attn_bwd", "attn_paged_step", "page_plan", "page_store")
 
 
 def __getattr__(name):
     if name in _MIXER:
         from . import mixer
         globals().update({n: getattr(mixer, n) for n in _MIXER})
+        return globals()[name]
+    if name in _ATTENTION:
+        from . import attention
+        globals().update({n: getattr(attention, n) for n in _ATTENTION})
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
@@ -117,7 +124,12 @@ def library(path: Optional[str] = None):
     lib.gdr_ssm_scan_fwd.argtypes = [P] * 14
     lib.gdr_ssm_scan_bwd.argtypes = [P] * 22
     lib.gdr_ssm_step.argtypes = [P] * 10
-    for name in _MIXER:
+    lib.gdr_attn_fwd.argtypes = [P] * 7 + [ctypes.c_int, ctypes.c_int64, ctypes.c_float, P]
+    lib.gdr_attn_bwd.argtypes = [P] * 11 + [ctypes.c_int, ctypes.c_int64, ctypes.c_float, P, P, P]
+    lib.gdr_attn_paged_step.argtypes = [P] * 6 + [ctypes.c_int64, ctypes.c_float, P, P, P]
+    lib.gdr_page_plan.argtypes = [P] * 9 + [ctypes.c_int32, P]
+    lib.gdr_page_store.argtypes = [P] * 6
+    for name in _MIXER + _ATTENTION:
         getattr(lib, "gdr_" + name).restype = ctypes.c_int
     lib.gdr_last_error.argtypes = []
     lib.gdr_last_error.restype = ctypes.c_char_p

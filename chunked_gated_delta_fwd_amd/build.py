@@ -1,5 +1,5 @@
 """Build ``libgdr.so`` (HIP kernels + C ABI) for gfx950 with hipcc, and
-``_gdr_torch.so`` (the compiled marshalling of mixer.py), in-tree."""
+``_gdr_torch.so`` (the compiled marshalling of mixer.py and attention.py), in-tree."""
 from __future__ import annotations
 
 import os
@@ -16,7 +16,8 @@ LIB = os.path.join(PKG, "libgdr.so")
 TORCH_LIB = os.path.join(PKG, "_gdr_torch.so")
 
 SOURCES = ["gdr_kernels.hip", "gdr_bwd.hip", "gdr_kda.hip", "gdr_conv.hip", "gdr_qknorm.hip", "gdr_ssm.hip",
-           "gdr_ssm_bwd.hip", "gdr_api.cpp", "gdr_mixer_api.cpp"]
+           "gdr_ssm_bwd.hip", "gdr_attn.hip", "gdr_attn_bwd.hip", "gdr_paged.hip", "gdr_api.cpp", "gdr_mixer_api.cpp",
+           "gdr_attn_api.cpp"]
 
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.environ.get("HIPCC", os.path.join(ROCM, "bin", "hipcc"))

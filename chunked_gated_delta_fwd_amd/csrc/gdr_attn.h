@@ -1,0 +1,73 @@
+// Internal interface between the host API (gdr_attn_api.cpp) and the kernels
+// of softmax attention (gdr_attn.hip, gdr_attn_bwd.hip) and of the paged cache
+// (gdr_paged.hip).  Not installed; not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdr {
+
+constexpr int kAttnRows = 128;   // query rows (gradient of keys: key rows) of a block, 32 a wave
+
+struct AttnArgs {
+    const void *q, *k, *v;       // rows ldq, ldk, ldv elements apart, heads and channels compact
+    const int32_t *cu, *cuk;     // [N + 1] of queries and keys; NULL: n_seq rows of seq_q and seq_k tokens
+    void *o;                     // [total_q, hq, d]; backward: input, rows ldo apart
+    float *lse;                  // [total_q, hq], NULL: not written
+    int64_t ldq, ldk, ldv, ldo;
+    int64_t n_seq, seq_q, seq_k, total_q, total_k;
+    int32_t hq, hk, d, bf16, causal;
+    int64_t window;              // keys that a query sees back from its own place, itself included; 0: all
+    float scale;
+    // backward
+    const void *dout;            // rows lddo apart
+    int64_t lddo;
+    void *dq, *dk, *dv;          // compact
+    float *stat;                 // [2][hq][total_q]: lse in powers of two, and do . o
+    float *part;                 // [parts][2][total_k][hk][d]: sums of dk and dv over a part of a group; NULL: one part
+    int32_t parts;
+};
+hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream);
+// How many blocks share the query heads of a group for the gradient of keys and values.
+int32_t attn_bwd_parts(const AttnArgs &a);
+hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t stream);
+
+// Keys and values in pages: row r of page p is row p * page + r of [pages * page, hk, d].
+struct PagedArgs {
+    const void *q;               // [N, hq, d], rows ldq apart
+    const void *k, *v;
+    const int32_t *table, *lens; // [N, width] pages of each sequence in order; keys of each
+    void *o;                     // [N, hq, d]
+    int64_t ldq, n_seq, pages, width, window;
+    int32_t page, hq, hk, d, bf16;
+    float scale;
+    uint32_t magic;              // j / page = j * magic >> shift, for 0 <= j < 2^31
+    int32_t shift;
+    // each sequence's keys are split in chunks of `chunk`, `splits` at most
+    int64_t splits;
+    int32_t chunk;
+    float *part, *stat;          // [N, hq, splits][d] outputs before they are scaled, [N, hq, splits][2] their reference and sum
+};
+// Sets chunk and splits.
+void paged_split(PagedArgs &a);
+hipError_t launch_paged_step(const PagedArgs &a, hipStream_t stream);
+
+struct StoreArgs {
+    const void *k, *v;           // [tokens] rows of row_bytes, ldk and ldv bytes apart
+    const int32_t *slots;        // [tokens]; outside the pages: not stored
+    void *kp, *vp;               // [rows] of row_bytes
+    int64_t tokens, rows, row_bytes, ldk, ldv;
+};
+hipError_t launch_page_store(const StoreArgs &a, hipStream_t stream);
+
+struct PlanArgs {
+    const int32_t *past, *fresh, *pool;   // [N], [N], [pool_size]
+    int32_t *table;                       // [N, width]
+    int32_t *cu, *lens, *positions, *slots, *used;   // [N + 1], [N], [tokens], [tokens], [2]
+    int64_t n_seq, pool_size, width, tokens;
+    int32_t page;
+};
+hipError_t launch_page_plan(const PlanArgs &a, hipStream_t stream);
+
+}  // namespace gdr

@@ -1,0 +1,211 @@
+// Softmax attention over packed or equal rows, forward.  Per sequence and head,
+// over the keys j that query i sees,
+//
+//     s_ij = scale q_i . k_j,   lse_i = log sum_j e^{s_ij},   o_i = sum_j e^{s_ij - lse_i} v_j.
+//
+// One pass over the keys with the running maximum and sum of each row.
+#include "gdr_attn_device.h"
+
+namespace gdr {
+namespace {
+
+// A block takes 128 query rows of one head, 32 a wave, and walks the keys in
+// tiles.  Scores are made transposed (keys x queries), so that a lane holds one
+// query's scores and the maximum and sum cross lanes once a tile, and the
+// result registers are the next product's operand.  The next tile's keys and
+// values load to LDS while this one is worked on.
+template <class T, int D>
+struct AttnFwd {
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    static constexpr int kKeys = T::kBf16 ? 64 : 32;   // a tile
+    typedef AttnTile<T, D, kKeys> Tile;
+    static constexpr int kSteps = D / 16, kParts = D / 32, kSub = kKeys / 32;
+    struct Lds {
+        alignas(16) char k[2][Tile::kBytes];
+        alignas(16) char v[2][Tile::kBytes];
+    };
+    // A row's scores may pass its reference value by so many powers of two
+    // before sums and outputs are rescaled to a new one.
+    static constexpr float kSlack = 8.f;
+
+    struct Row {
+        F8 q[kSteps];
+        f32x16 o[kParts];   // transposed: channels x queries
+        float ref, sum;     // ref: in powers of two; sum: of this lane's half
+    };
+
+    // CAREFUL: a value that is not finite reaches the rows that see its key and no other.  A product
+    // gives every row of a tile each of its keys, zero times those it does not see, which a value that
+    // is not finite would turn into NaN; there one key after another is added to the rows that see it.
+    template <bool CAREFUL>
+    static __device__ __forceinline__ void walk(Row &w, const AttnSight &sight, float c, int32_t i0, int32_t i1,
+                                                int32_t begin, int32_t end, const E *k, const E *v, uint32_t step_k,
+                                                uint32_t step_v, int32_t lk, Lds &lds, int wave, int lane) {
+        const int col = lane & 31, h = lane >> 5;
+        const typename Tile::From fk = Tile::from(wave, lane, step_k), fv = Tile::from(wave, lane, step_v);
+        const int32_t lo = i0 + 32 * wave, at = sight.at(lo + col);
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) w.o[t] = zero16();
+        w.ref = -__builtin_inff();
+        w.sum = 0.f;
+        int buf = 0;
+        auto load = [&](int32_t j, int b) {
+            Tile::load(fk, reinterpret_cast<const E *>(reinterpret_cast<const char *>(k) + static_cast<int64_t>(j) * step_k),
+                       step_k, lk - j, lds.k[b], wave);
+            Tile::load(fv, reinterpret_cast<const E *>(reinterpret_cast<const char *>(v) + static_cast<int64_t>(j) * step_v),
+                       step_v, lk - j, lds.v[b], wave);
+        };
+        if (begin < end) load(begin, 0);
+        for (int32_t j = begin; j < end; j += kKeys, buf ^= 1) {
+            loads_landed();
+            __syncthreads();
+            if (j + kKeys < end) load(j + kKeys, buf ^ 1);
+            const int32_t hi = lo + 31 < i1 ? lo + 31 : i1;
+            if (lo > i1 || !sight.any(lo, hi, j, kKeys)) continue;
+            f32x16 s[kSub];
+#pragma unroll
+            for (int t = 0; t < kSub; ++t) {
+                s[t] = zero16();
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) s[t] = T::mma(Tile::rows(lds.k[buf], 32 * t, ks, col, h), w.q[ks], s[t]);
+            }
+            const bool whole = sight.all(lo, hi, j, kKeys);
+            const int32_t d0 = at - j - 4 * h;
+            if (!whole) {
+#pragma unroll
+                for (int t = 0; t < kSub; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (!sight.sees(d0, 32 * t + 8 * (r / 4) + r % 4)) s[t][r] = -__builtin_inff();
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int t = 0; t < kSub; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+            top = half_max(top) * c;
+            if (__builtin_amdgcn_ballot_w64(top > w.ref + kSlack)) {
+                // c >= 0; a row that has seen no key keeps -inf, and a factor of 1 for its zeros
+                const float now = fmaxf(top, w.ref), f = now == w.ref ? 1.f : fast_exp2(w.ref - now);
+                w.ref = now;
+                w.sum *= f;
+#pragma unroll
+                for (int t = 0; t < kParts; ++t) w.o[t] *= f;
+            }
+            const float ref = w.ref == -__builtin_inff() ? 0.f : w.ref;
+#pragma unroll
+            for (int t = 0; t < kSub; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float p = fast_exp2(__builtin_fmaf(s[t][r], c, -ref));
+                    s[t][r] = whole || sight.sees(d0, 32 * t + 8 * (r / 4) + r % 4) ? p : 0.f;
+                    w.sum += s[t][r];
+                }
+            // bf16: probabilities are rounded to nearest for the product with the values (relative 2^-9 each, of
+            // independent signs); their sum is not
+#pragma unroll
+            for (int kb = 0; kb < 2 * kSub; ++kb) {
+                const F8 p = T::part(s[kb / 2], kb % 2);
+                if (!CAREFUL || whole) {
+#pragma unroll
+                    for (int t = 0; t < kParts; ++t)
+                        w.o[t] = T::mma(Tile::across(lds.v[buf], 16 * kb, 32 * t, lane), p, w.o[t]);
+                } else {
+                    for (int key = 0; key < 16; ++key) {   // slot s of half h holds key 4 h + s % 4 + 2 (s & 4)
+                        const int slot = (key >> 2 & 1) == h ? (key & 3) + (key >> 1 & 4) : -1;
+                        const bool seen = sight.sees(at, j + 16 * kb + key);
+#pragma unroll
+                        for (int t = 0; t < kParts; ++t) {
+                            const f32x16 x = T::mma(T::only(Tile::across(lds.v[buf], 16 * kb, 32 * t, lane), slot),
+                                                    T::only(p, slot), zero16());
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) w.o[t][r] += seen ? x[r] : 0.f;
+                        }
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <class T, int D>
+__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_fwd_kernel(AttnArgs a, int64_t tiles) {
+    typedef AttnFwd<T, D> F;
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    __shared__ typename F::Lds lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
+    const int group = a.hq / a.hk;
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const AttnItem item = attn_item(blockIdx.x, pairs, tiles, group);
+    if (item.tile < 0) return;
+    const int64_t n = a.cu ? attn_find(a.cu, a.n_seq, a.total_q, item.tile, lane) : item.pair / a.hk;
+    const int hk = static_cast<int>(item.pair % a.hk), hq = hk * group + item.way;
+    const AttnSeq seq = attn_seq(a, n);
+    const int64_t tile = a.cu ? item.tile - (attn_clamp(a.cu[n], 0, a.total_q) / kAttnRows + n) : item.tile;
+    if (tile < 0 || tile * kAttnRows >= seq.lq) return;
+    const AttnSight sight(a, seq);
+    const int32_t i0 = static_cast<int32_t>(tile * kAttnRows);
+    const int32_t i1 = i0 + kAttnRows < seq.lq ? i0 + kAttnRows - 1 : seq.lq - 1;   // last row
+
+    // keys that some row of the block sees, from a whole tile on
+    const int64_t first = static_cast<int64_t>(sight.at(i0)) - sight.back + 1;
+    const int32_t begin = first > 0 ? static_cast<int32_t>(first) / F::kKeys * F::kKeys : 0;
+    const int32_t end = sight.at(i1) + 1 < seq.lk ? sight.at(i1) + 1 : seq.lk;
+
+    const float c = a.scale * kLog2e;
+    typename F::Row w;
+    {
+        const int32_t i = i0 + 32 * wave + col < seq.lq ? i0 + 32 * wave + col : seq.lq - 1;
+        const E *q = static_cast<const E *>(a.q) + (seq.q0 + i) * a.ldq + static_cast<int64_t>(hq) * D + 8 * h;
+#pragma unroll
+        for (int ks = 0; ks < F::kSteps; ++ks) {
+            const F8 x = T::load(q + 16 * ks);
+            w.q[ks] = c < 0.f ? T::flip(x) : x;
+        }
+    }
+    const E *k = static_cast<const E *>(a.k) + seq.k0 * a.ldk + static_cast<int64_t>(hk) * D;
+    const E *v = static_cast<const E *>(a.v) + seq.k0 * a.ldv + static_cast<int64_t>(hk) * D;
+    const uint32_t step_k = static_cast<uint32_t>(a.ldk * sizeof(E)), step_v = static_cast<uint32_t>(a.ldv * sizeof(E));
+    F::template walk<false>(w, sight, __builtin_fabsf(c), i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    {
+        float x = 0.f;   // 0, or NaN where an output is not finite
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.o[t][r], 0.f, x);
+        if (__syncthreads_or(x != 0.f))
+            F::template walk<true>(w, sight, __builtin_fabsf(c), i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    }
+    const int32_t i = i0 + 32 * wave + col;
+    // no key seen (or scores of -inf alone): 0, and NaN stays NaN
+    const float sum = half_sum(w.sum), inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (i < seq.lq) {
+        E *o = static_cast<E *>(a.o) + ((seq.q0 + i) * a.hq + hq) * D;
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t) attn_store<T>(o + 32 * t, w.o[t], inv, h);
+        if (a.lse && h == 0)
+            a.lse[(seq.q0 + i) * a.hq + hq] =
+                sum == 0.f ? -__builtin_inff() : (w.ref + __builtin_log2f(sum)) * 0.69314718055994530942f;
+    }
+}
+
+template <class T, int D>
+hipError_t run(const AttnArgs &a, hipStream_t stream) {
+    const int64_t tiles = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const int64_t grid = attn_grid(pairs, tiles, a.hq / a.hk);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    gdr_attn_fwd_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a, tiles);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream) {
+    if (a.bf16) return a.d == 64 ? run<AttnBf, 64>(a, stream) : run<AttnBf, 128>(a, stream);
+    return a.d == 64 ? run<AttnF32, 64>(a, stream) : run<AttnF32, 128>(a, stream);
+}
+
+}  // namespace gdr

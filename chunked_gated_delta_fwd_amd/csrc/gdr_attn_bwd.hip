@@ -1,0 +1,425 @@
+// Softmax attention, backward.  With the forward's lse the probabilities are
+// made again, p_ij = e^{s_ij - lse_i}, and with delta_i = do_i . o_i
+//
+//     dv_j = sum_i p_ij do_i,   ds_ij = p_ij (do_i . v_j - delta_i),
+//     dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i,
+//
+// dk and dv over every query head that shares the key head.  Two passes, one
+// that holds query rows and walks the keys (dq, delta), one that holds key rows
+// and walks the queries (dk, dv): scores and do . v are made twice, seven
+// products for five, so that every sum stays in registers in a fixed order.
+#include "gdr_attn_device.h"
+
+namespace gdr {
+namespace {
+
+// dq: a block takes 128 query rows of one head, 32 a wave, as the forward does.
+template <class T, int D>
+struct AttnDq {
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    static constexpr int kKeys = T::kBf16 ? 64 : 32;
+    typedef AttnTile<T, D, kKeys> Tile;
+    static constexpr int kSteps = D / 16, kParts = D / 32, kSub = kKeys / 32;
+    struct Lds {
+        alignas(16) char k[2][Tile::kBytes];
+        alignas(16) char v[2][Tile::kBytes];
+    };
+    struct Row {
+        F8 q[kSteps], dout[kSteps];
+        f32x16 dq[kParts];   // transposed: channels x queries
+        float lse, delta;    // lse in powers of two
+    };
+
+    // CAREFUL as in the forward: a key that is not finite reaches the rows that see it and no other.
+    template <bool CAREFUL>
+    static __device__ __forceinline__ void walk(Row &w, const AttnSight &sight, float c, int32_t i0, int32_t i1,
+                                                int32_t begin, int32_t end, const E *k, const E *v, uint32_t step_k,
+                                                uint32_t step_v, int32_t lk, Lds &lds, int wave, int lane) {
+        const int col = lane & 31, h = lane >> 5;
+        const typename Tile::From fk = Tile::from(wave, lane, step_k), fv = Tile::from(wave, lane, step_v);
+        const int32_t lo = i0 + 32 * wave, at = sight.at(lo + col);
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) w.dq[t] = zero16();
+        int buf = 0;
+        auto load = [&](int32_t j, int b) {
+            Tile::load(fk, reinterpret_cast<const E *>(reinterpret_cast<const char *>(k) + static_cast<int64_t>(j) * step_k),
+                       step_k, lk - j, lds.k[b], wave);
+            Tile::load(fv, reinterpret_cast<const E *>(reinterpret_cast<const char *>(v) + static_cast<int64_t>(j) * step_v),
+                       step_v, lk - j, lds.v[b], wave);
+        };
+        if (begin < end) load(begin, 0);
+        for (int32_t j = begin; j < end; j += kKeys, buf ^= 1) {
+            loads_landed();
+            __syncthreads();
+            if (j + kKeys < end) load(j + kKeys, buf ^ 1);
+            const int32_t hi = lo + 31 < i1 ? lo + 31 : i1;
+            if (lo > i1) continue;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                const int32_t ju = j + 32 * u;
+                if (!sight.any(lo, hi, ju, 32)) continue;
+                f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) s = T::mma(Tile::rows(lds.k[buf], 32 * u, ks, col, h), w.q[ks], s);
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) dp = T::mma(Tile::rows(lds.v[buf], 32 * u, ks, col, h), w.dout[ks], dp);
+                const bool whole = sight.all(lo, hi, ju, 32);
+                const int32_t d0 = at - ju - 4 * h;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float p = fast_exp2(__builtin_fmaf(s[r], c, -w.lse));
+                    s[r] = whole || sight.sees(d0, 8 * (r / 4) + r % 4) ? p * (dp[r] - w.delta) : 0.f;
+                }
+                // bf16: ds is rounded to nearest for the product with the keys
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const F8 ds = T::part(s, kb);
+                    if (!CAREFUL || whole) {
+#pragma unroll
+                        for (int t = 0; t < kParts; ++t)
+                            w.dq[t] = T::mma(Tile::across(lds.k[buf], 32 * u + 16 * kb, 32 * t, lane), ds, w.dq[t]);
+                    } else {
+                        for (int key = 0; key < 16; ++key) {
+                            const int slot = (key >> 2 & 1) == h ? (key & 3) + (key >> 1 & 4) : -1;
+                            const bool seen = sight.sees(at, ju + 16 * kb + key);
+#pragma unroll
+                            for (int t = 0; t < kParts; ++t) {
+                                const f32x16 x =
+                                    T::mma(T::only(Tile::across(lds.k[buf], 32 * u + 16 * kb, 32 * t, lane), slot),
+                                           T::only(ds, slot), zero16());
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) w.dq[t][r] += seen ? x[r] : 0.f;
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <class T, int D>
+__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dq_kernel(AttnArgs a, int64_t tiles) {
+    typedef AttnDq<T, D> F;
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    __shared__ typename F::Lds lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
+    const int group = a.hq / a.hk;
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const AttnItem item = attn_item(blockIdx.x, pairs, tiles, group);
+    if (item.tile < 0) return;
+    const int64_t n = a.cu ? attn_find(a.cu, a.n_seq, a.total_q, item.tile, lane) : item.pair / a.hk;
+    const int hk = static_cast<int>(item.pair % a.hk), hq = hk * group + item.way;
+    const AttnSeq seq = attn_seq(a, n);
+    const int64_t tile = a.cu ? item.tile - (attn_clamp(a.cu[n], 0, a.total_q) / kAttnRows + n) : item.tile;
+    if (tile < 0 || tile * kAttnRows >= seq.lq) return;
+    const AttnSight sight(a, seq);
+    const int32_t i0 = static_cast<int32_t>(tile * kAttnRows);
+    const int32_t i1 = i0 + kAttnRows < seq.lq ? i0 + kAttnRows - 1 : seq.lq - 1;
+    const int64_t first = static_cast<int64_t>(sight.at(i0)) - sight.back + 1;
+    const int32_t begin = first > 0 ? static_cast<int32_t>(first) / F::kKeys * F::kKeys : 0;
+    const int32_t end = sight.at(i1) + 1 < seq.lk ? sight.at(i1) + 1 : seq.lk;
+
+    typename F::Row w;
+    {
+        const int32_t i = i0 + 32 * wave + col < seq.lq ? i0 + 32 * wave + col : seq.lq - 1;
+        const int64_t row = seq.q0 + i, head = static_cast<int64_t>(hq) * D + 8 * h;
+        const E *q = static_cast<const E *>(a.q) + row * a.ldq + head;
+        const E *o = static_cast<const E *>(a.o) + row * a.ldo + head;
+        const E *dout = static_cast<const E *>(a.dout) + row * a.lddo + head;
+        float sum = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < F::kSteps; ++ks) {
+            w.q[ks] = T::load(q + 16 * ks);
+            w.dout[ks] = T::load(dout + 16 * ks);
+            const F8 x = T::load(o + 16 * ks);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) sum = __builtin_fmaf(T::up(w.dout[ks], s), T::up(x, s), sum);
+        }
+        w.delta = half_sum(sum);
+        w.lse = a.lse[row * a.hq + hq] * kLog2e;
+        if (i0 + 32 * wave + col < seq.lq && h == 0) {
+            float *stat = a.stat + static_cast<int64_t>(hq) * a.total_q + row;
+            stat[0] = w.lse;
+            stat[a.hq * a.total_q] = w.delta;
+        }
+    }
+    const float c = a.scale * kLog2e;
+    const E *k = static_cast<const E *>(a.k) + seq.k0 * a.ldk + static_cast<int64_t>(hk) * D;
+    const E *v = static_cast<const E *>(a.v) + seq.k0 * a.ldv + static_cast<int64_t>(hk) * D;
+    const uint32_t step_k = static_cast<uint32_t>(a.ldk * sizeof(E)), step_v = static_cast<uint32_t>(a.ldv * sizeof(E));
+    F::template walk<false>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    {
+        float x = 0.f;   // 0, or NaN where a gradient is not finite
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.dq[t][r], 0.f, x);
+        if (__syncthreads_or(x != 0.f))
+            F::template walk<true>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    }
+    const int32_t i = i0 + 32 * wave + col;
+    if (i < seq.lq) {
+        E *dq = static_cast<E *>(a.dq) + ((seq.q0 + i) * a.hq + hq) * D;
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t) attn_store<T>(dq + 32 * t, w.dq[t], a.scale, h);
+    }
+}
+
+// dk and dv: a block takes 128 key rows of one key head, 32 a wave, and walks
+// the query rows that see them, head after head of its part of the group.
+template <class T, int D>
+struct AttnDkv {
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    static constexpr int kQueries = 32;
+    typedef AttnTile<T, D, kQueries> Tile;
+    static constexpr int kSteps = D / 16, kParts = D / 32;
+    struct Lds {
+        alignas(16) char q[2][Tile::kBytes];
+        alignas(16) char dout[2][Tile::kBytes];
+        alignas(16) float lse[2][64], delta[2][64];   // a load of a wave each, half of it used
+    };
+    struct Row {
+        F8 k[kSteps], v[kSteps];
+        f32x16 dk[kParts], dv[kParts];   // transposed: channels x keys
+    };
+    struct Where {
+        const E *q, *dout;               // first row of the sequence, first head of the part
+        const float *lse, *delta;
+        int64_t total;                   // between two heads' lse
+        uint32_t step_q, step_do;
+        int32_t heads, lq;
+    };
+
+    // CAREFUL: a query or output gradient that is not finite reaches the keys that its row sees and no other.
+    template <bool CAREFUL>
+    static __device__ __forceinline__ void walk(Row &w, const Where &from, const AttnSight &sight, float c, int32_t j0,
+                                                int32_t j1, int32_t begin, int32_t end, Lds &lds, int wave, int lane) {
+        const int col = lane & 31, h = lane >> 5;
+        const typename Tile::From fq = Tile::from(wave, lane, from.step_q), fo = Tile::from(wave, lane, from.step_do);
+        const int32_t lo = j0 + 32 * wave, j = lo + col;
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) w.dk[t] = w.dv[t] = zero16();
+        if (begin >= end) return;
+        auto load = [&](int head, int32_t i, int b) {
+            const int32_t rows = from.lq - i;
+            Tile::load(fq, reinterpret_cast<const E *>(reinterpret_cast<const char *>(from.q + head * D) +
+                                                       static_cast<int64_t>(i) * from.step_q), from.step_q, rows, lds.q[b], wave);
+            Tile::load(fo, reinterpret_cast<const E *>(reinterpret_cast<const char *>(from.dout + head * D) +
+                                                       static_cast<int64_t>(i) * from.step_do), from.step_do, rows, lds.dout[b], wave);
+            if (wave < 2) {
+                const float *x = (wave == 0 ? from.lse : from.delta) + head * from.total + i;
+                lds_load4(uniform_rsrc(x, 4 * (rows < 32 ? rows : 32)), 4 * lane, lds_address(wave == 0 ? lds.lse[b] : lds.delta[b]));
+            }
+        };
+        load(0, begin, 0);
+        int buf = 0;
+        int32_t i = begin, head = 0;
+        while (true) {
+            int32_t next = i + kQueries, nhead = head;
+            if (next >= end) next = begin, ++nhead;
+            loads_landed();
+            __syncthreads();
+            if (nhead < from.heads) load(nhead, next, buf ^ 1);
+            const int32_t last = i + 31 < from.lq ? i + 31 : from.lq - 1;
+            if (lo <= j1 && sight.any(i, last, lo, 32)) {
+                f32x16 p = zero16(), dp = zero16();
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) p = T::mma(Tile::rows(lds.q[buf], 0, ks, col, h), w.k[ks], p);
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks) dp = T::mma(Tile::rows(lds.dout[buf], 0, ks, col, h), w.v[ks], dp);
+                const bool whole = sight.all(i, last, lo, 32);
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const f32x4 lse = *reinterpret_cast<const f32x4 *>(&lds.lse[buf][8 * r4 + 4 * h]);
+                    const f32x4 delta = *reinterpret_cast<const f32x4 *>(&lds.delta[buf][8 * r4 + 4 * h]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int r = 4 * r4 + q;
+                        const bool seen = whole || sight.sees(sight.at(i + 8 * r4 + 4 * h + q), j);
+                        p[r] = seen ? fast_exp2(__builtin_fmaf(p[r], c, -lse[q])) : 0.f;
+                        dp[r] = seen ? p[r] * (dp[r] - delta[q]) : 0.f;
+                    }
+                }
+                // bf16: p and ds are rounded to nearest for the products over the queries
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const F8 pp = T::part(p, kb), ds = T::part(dp, kb);
+                    if (!CAREFUL || whole) {
+#pragma unroll
+                        for (int t = 0; t < kParts; ++t) {
+                            w.dv[t] = T::mma(Tile::across(lds.dout[buf], 16 * kb, 32 * t, lane), pp, w.dv[t]);
+                            w.dk[t] = T::mma(Tile::across(lds.q[buf], 16 * kb, 32 * t, lane), ds, w.dk[t]);
+                        }
+                    } else {
+                        for (int row = 0; row < 16; ++row) {
+                            const int slot = (row >> 2 & 1) == h ? (row & 3) + (row >> 1 & 4) : -1;
+                            const bool seen = sight.sees(sight.at(i + 16 * kb + row), j);
+#pragma unroll
+                            for (int t = 0; t < kParts; ++t) {
+                                const f32x16 x = T::mma(T::only(Tile::across(lds.dout[buf], 16 * kb, 32 * t, lane), slot),
+                                                        T::only(pp, slot), zero16());
+                                const f32x16 y = T::mma(T::only(Tile::across(lds.q[buf], 16 * kb, 32 * t, lane), slot),
+                                                        T::only(ds, slot), zero16());
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) {
+                                    w.dv[t][r] += seen ? x[r] : 0.f;
+                                    w.dk[t][r] += seen ? y[r] : 0.f;
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            if (nhead >= from.heads) break;
+            i = next;
+            head = nhead;
+            buf ^= 1;
+        }
+    }
+};
+
+template <class T, int D>
+__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(AttnArgs a, int64_t tiles) {
+    typedef AttnDkv<T, D> F;
+    typedef typename T::E E;
+    __shared__ typename F::Lds lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
+    const int group = a.hq / a.hk;
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const AttnItem item = attn_item(blockIdx.x, pairs, tiles, a.parts);
+    if (item.tile < 0) return;
+    const int32_t *cuk = a.cuk ? a.cuk : a.cu;
+    const int64_t n = a.cu ? attn_find(cuk, a.n_seq, a.total_k, item.tile, lane) : item.pair / a.hk;
+    const int hk = static_cast<int>(item.pair % a.hk);
+    const AttnSeq seq = attn_seq(a, n);
+    const int64_t tile = a.cu ? item.tile - (attn_clamp(cuk[n], 0, a.total_k) / kAttnRows + n) : item.tile;
+    if (tile < 0 || tile * kAttnRows >= seq.lk) return;
+    const AttnSight sight(a, seq);
+    const int32_t j0 = static_cast<int32_t>(tile * kAttnRows);
+    const int32_t j1 = j0 + kAttnRows < seq.lk ? j0 + kAttnRows - 1 : seq.lk - 1;
+    // queries of which some sees a key of the block: at(i) >= j0 and at(i) - j1 < back
+    int64_t begin = 0, end = seq.lq;
+    if (sight.slope) {
+        begin = static_cast<int64_t>(j0) - sight.first;
+        if (begin < 0) begin = 0;
+        const int64_t e = static_cast<int64_t>(j1) + sight.back - sight.first;
+        if (e < end) end = e;
+    }
+    begin = begin / F::kQueries * F::kQueries;
+
+    const int head0 = group * item.way / a.parts, heads = group * (item.way + 1) / a.parts - head0;
+    const int64_t hq = static_cast<int64_t>(hk) * group + head0;
+    typename F::Where from;
+    from.q = static_cast<const E *>(a.q) + seq.q0 * a.ldq + hq * D;
+    from.dout = static_cast<const E *>(a.dout) + seq.q0 * a.lddo + hq * D;
+    from.lse = a.stat + hq * a.total_q + seq.q0;
+    from.delta = from.lse + a.hq * a.total_q;
+    from.total = a.total_q;
+    from.step_q = static_cast<uint32_t>(a.ldq * sizeof(E));
+    from.step_do = static_cast<uint32_t>(a.lddo * sizeof(E));
+    from.heads = heads;
+    from.lq = seq.lq;
+    typename F::Row w;
+    {
+        const int64_t row = seq.k0 + (j0 + 32 * wave + col < seq.lk ? j0 + 32 * wave + col : seq.lk - 1);
+        const int64_t head = static_cast<int64_t>(hk) * D + 8 * h;
+        const E *k = static_cast<const E *>(a.k) + row * a.ldk + head, *v = static_cast<const E *>(a.v) + row * a.ldv + head;
+#pragma unroll
+        for (int ks = 0; ks < F::kSteps; ++ks) {
+            w.k[ks] = T::load(k + 16 * ks);
+            w.v[ks] = T::load(v + 16 * ks);
+        }
+    }
+    const float c = a.scale * kLog2e;
+    const int32_t b = static_cast<int32_t>(begin), e = static_cast<int32_t>(end);
+    F::template walk<false>(w, from, sight, c, j0, j1, b, e, lds, wave, lane);
+    {
+        float x = 0.f;
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.dk[t][r], 0.f, __builtin_fmaf(w.dv[t][r], 0.f, x));
+        if (__syncthreads_or(x != 0.f)) F::template walk<true>(w, from, sight, c, j0, j1, b, e, lds, wave, lane);
+    }
+    const int32_t j = j0 + 32 * wave + col;
+    if (j >= seq.lk) return;
+    const int64_t at = ((seq.k0 + j) * a.hk + hk) * D;
+    if (a.part) {
+        const int64_t all = a.total_k * a.hk * D;
+        float *part = a.part + 2 * item.way * all + at;
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t) {
+            attn_store<AttnF32>(part + 32 * t, w.dk[t], a.scale, h);
+            attn_store<AttnF32>(part + all + 32 * t, w.dv[t], 1.f, h);
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t) {
+            attn_store<T>(static_cast<E *>(a.dk) + at + 32 * t, w.dk[t], a.scale, h);
+            attn_store<T>(static_cast<E *>(a.dv) + at + 32 * t, w.dv[t], 1.f, h);
+        }
+    }
+}
+
+// Sums the parts of dk and dv in order, for the rows of one tile's sequence.
+template <class T>
+__global__ __launch_bounds__(256) void gdr_attn_join_kernel(AttnArgs a, int64_t tiles) {
+    const int lane = threadIdx.x & 63;
+    const int64_t slot = blockIdx.x % tiles, which = blockIdx.x / tiles;
+    const int32_t *cuk = a.cuk ? a.cuk : a.cu;
+    const int64_t n = a.cu ? attn_find(cuk, a.n_seq, a.total_k, slot, lane) : which;
+    const AttnSeq seq = attn_seq(a, n);
+    const int64_t tile = a.cu ? slot - (attn_clamp(cuk[n], 0, a.total_k) / kAttnRows + n) : slot;
+    if (tile < 0 || tile * kAttnRows >= seq.lk) return;
+    const int64_t row = static_cast<int64_t>(a.hk) * a.d, all = a.total_k * row;
+    const int64_t j0 = tile * kAttnRows, rows = seq.lk - j0 < kAttnRows ? seq.lk - j0 : kAttnRows;
+    const int64_t from = (seq.k0 + j0) * row, count = rows * row;
+    for (int64_t x = threadIdx.x * 4 + blockIdx.y * 1024; x < count; x += gridDim.y * 1024)
+#pragma unroll
+        for (int what = 0; what < 2; ++what) {
+            f32x4 sum = zero4();
+            for (int p = 0; p < a.parts; ++p) sum += *reinterpret_cast<const f32x4 *>(a.part + (2 * p + what) * all + from + x);
+            typename T::E *to = static_cast<typename T::E *>(what ? a.dv : a.dk) + from + x;
+            if constexpr (T::kBf16) *reinterpret_cast<bf16x4 *>(to) = cvt4(sum);
+            else *reinterpret_cast<f32x4 *>(to) = sum;
+        }
+}
+
+template <class T, int D>
+hipError_t run(const AttnArgs &a, hipStream_t stream) {
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const int64_t tiles_q = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
+    const int64_t tiles_k = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k);
+    const int64_t grid_q = attn_grid(pairs, tiles_q, a.hq / a.hk), grid_k = attn_grid(pairs, tiles_k, a.parts);
+    if (grid_q > 0x7FFFFFFF || grid_k > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (a.total_q > 0) gdr_attn_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid_q)), 256, 0, stream>>>(a, tiles_q);
+    if (a.total_k > 0) {
+        gdr_attn_dkv_kernel<T, D><<<dim3(static_cast<unsigned>(grid_k)), 256, 0, stream>>>(a, tiles_k);
+        if (a.part) {
+            const int64_t blocks = tiles_k * (a.cu ? 1 : a.n_seq);
+            gdr_attn_join_kernel<T><<<dim3(static_cast<unsigned>(blocks), 8), 256, 0, stream>>>(a, tiles_k);
+        }
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int32_t attn_bwd_parts(const AttnArgs &a) {
+    const int64_t blocks = (a.cu ? 1 : a.n_seq) * a.hk * attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k);
+    const int32_t group = a.hq / a.hk;
+    int32_t parts = 1;
+    while (parts < group && blocks * parts < 1024) parts *= 2;
+    return parts < group ? parts : group;
+}
+
+hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t stream) {
+    if (a.bf16) return a.d == 64 ? run<AttnBf, 64>(a, stream) : run<AttnBf, 128>(a, stream);
+    return a.d == 64 ? run<AttnF32, 64>(a, stream) : run<AttnF32, 128>(a, stream);
+}
+
+}  // namespace gdr

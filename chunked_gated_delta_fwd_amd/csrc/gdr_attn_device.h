@@ -1,0 +1,326 @@
+// Device code shared by the attention kernels (gdr_attn.hip, gdr_attn_bwd.hip,
+// gdr_paged.hip): the 32x32 matrix products, tiles in LDS, and which block
+// works on what.
+//
+// Matrix operands.  A product contracts 16 indices k: lane (c, h), c = lane %
+// 32, h = lane / 32, supplies row (or column) c with eight values of k.
+//   natural order:  k = 8 h + s, s = 0..7              (two operands along rows)
+//   result order:   k = 4 h + s, s < 4;  8 + 4 h + s - 4, s >= 4
+// A result tile holds, in lane (c, h), column c and rows 8 (r / 4) + 4 h + r % 4
+// for its registers r = 0..15: registers 0..7 and 8..15 are operands in result
+// order of a product over its rows, so scores feed the next product without
+// leaving their lane.  bf16 takes one 32x32x16 instruction, f32 eight 32x32x2.
+#pragma once
+
+#include "gdr_attn.h"
+#include "gdr_device.h"
+
+namespace gdr {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    return z;
+}
+
+// Both halves' values of a lane pair (c, 0), (c, 1).
+__device__ __forceinline__ float half_max(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+struct AttnBf {
+    typedef uint16_t E;
+    typedef bf16x8 F8;
+    static constexpr bool kBf16 = true;
+    static __device__ __forceinline__ f32x16 mma(F8 a, F8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ F8 load(const E *p) { return *reinterpret_cast<const F8 *>(p); }
+    static __device__ __forceinline__ float up(F8 x, int i) { return (float)x[i]; }
+    static __device__ __forceinline__ F8 flip(F8 x) {   // -x, exact
+        return __builtin_bit_cast(F8, __builtin_bit_cast(v4u32, x) ^ 0x80008000u);
+    }
+    // registers 8 kb .. 8 kb + 7, rounded to nearest even
+    static __device__ __forceinline__ F8 part(const f32x16 &x, int kb) {
+        F8 r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = (__bf16)x[8 * kb + i];
+        return r;
+    }
+    static __device__ __forceinline__ F8 only(F8 x, int i) {   // element i, zeros elsewhere (i at run time)
+        F8 r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = j == i ? x[j] : (__bf16)0.f;
+        return r;
+    }
+};
+
+struct AttnF32 {
+    typedef float E;
+    typedef f32x8 F8;
+    static constexpr bool kBf16 = false;
+    static __device__ __forceinline__ f32x16 mma(F8 a, F8 b, f32x16 c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ F8 load(const E *p) {
+        return __builtin_shufflevector(*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 4), 0, 1, 2, 3,
+                                       4, 5, 6, 7);
+    }
+    static __device__ __forceinline__ float up(F8 x, int i) { return x[i]; }
+    static __device__ __forceinline__ F8 flip(F8 x) { return -x; }
+    static __device__ __forceinline__ F8 part(const f32x16 &x, int kb) {
+        F8 r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = x[8 * kb + i];
+        return r;
+    }
+    static __device__ __forceinline__ F8 only(F8 x, int i) {
+        F8 r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = j == i ? x[j] : 0.f;
+        return r;
+    }
+};
+
+// --- tiles in LDS ------------------------------------------------------------------
+
+// Loads to LDS past the registers: lane l's 16 (4) bytes land at `lds` + 16 l (4 l).
+// Not the builtin: the compiler waits for such loads before every LDS read that
+// follows, and a tile is loaded while another one is read.  A load past the
+// buffer's end stores zeros.
+__device__ __forceinline__ void lds_load16(v4u32 rsrc, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 : : "s"(lds), "v"(off), "s"(rsrc) : "memory");
+}
+__device__ __forceinline__ void lds_load4(v4u32 rsrc, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 : : "s"(lds), "v"(off), "s"(rsrc) : "memory");
+}
+__device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ v4u32 uniform_rsrc(const void *base, uint32_t bytes) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    v4u32 r;
+    r[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
+    r[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32) & 0xFFFFu);
+    r[2] = __builtin_amdgcn_readfirstlane(bytes);
+    r[3] = 0x00020000u;
+    return r;
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p)));
+}
+
+// ROWS rows of D elements, compact, in 16-byte pieces.  Piece c of row r lies
+// at place c ^ turn(r): 16 rows' reads of one piece, and 4 rows' reads of 4
+// neighbouring pieces (transposed reads), each touch all 64 banks once.
+template <class T, int D, int ROWS>
+struct AttnTile {
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    static constexpr int kRow = D * sizeof(E), kPieces = kRow / 16, kBytes = ROWS * kRow, kWaves = 4;
+    static constexpr int kLoads = kBytes / 1024 / kWaves;    // of a wave
+    static constexpr int kWays = kRow == 512 ? 2 : 1;        // places that a lane's pieces alternate between
+    static_assert(kBytes % (1024 * kWaves) == 0);
+
+    static __device__ __forceinline__ int turn(int r) {
+        if constexpr (kPieces == 8) return (r << 1 & 4) | (r >> 2 & 3);
+        else return (r << 2 & 12) | (r >> 2 & 3);
+    }
+    // Byte offset of a piece in the tile.
+    static __device__ __forceinline__ int place(int row, int piece) { return row * kRow + ((piece ^ turn(row)) << 4); }
+
+    // Where lane `lane` of wave `wave` loads from, for rows `step` bytes apart.
+    struct From {
+        uint32_t off[kWays];
+        uint32_t hop;                                        // from one load of a wave to the next
+    };
+    static __device__ __forceinline__ From from(int wave, int lane, uint32_t step) {
+        From f;
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+            const int at = (wave + w * kWaves) * 1024 + lane * 16, row = at / kRow, piece = at % kRow / 16;
+            f.off[w] = (wave * 1024 + lane * 16) / kRow * step + ((piece ^ turn(row)) << 4);
+        }
+        f.hop = kWaves * 1024 / kRow * step;
+        return f;
+    }
+    // Starts loading the tile at `base`, of which `rows` rows are there.
+    static __device__ __forceinline__ void load(const From &f, const E *base, uint32_t step, int rows, const void *lds,
+                                                int wave) {
+        const int there = rows < ROWS ? rows : ROWS;
+        const v4u32 rsrc = uniform_rsrc(base, there > 0 ? (there - 1) * step + kRow : 0);
+        const uint32_t to = lds_address(lds) + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) lds_load16(rsrc, f.off[i % kWays] + i * f.hop, to + i * kWaves * 1024);
+    }
+    // Operand along rows: row r0 + c, elements 16 ks + 8 h .., natural order.
+    static __device__ __forceinline__ F8 rows(const char *tile, int r0, int ks, int c, int h) {
+        if constexpr (T::kBf16) {
+            return *reinterpret_cast<const F8 *>(tile + place(r0 + c, 2 * ks + h));
+        } else {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + place(r0 + c, 4 * ks + 2 * h));
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + place(r0 + c, 4 * ks + 2 * h + 1));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+    // Operand across rows: element x0 + c of the rows r0 .. r0 + 15, result order.
+    static __device__ __forceinline__ F8 across(const char *tile, int r0, int x0, int lane) {
+        const int h = lane >> 5;
+        if constexpr (T::kBf16) {
+            const int j = lane & 15, r = r0 + 4 * h + (j >> 2), x = x0 + (lane & 16) + 4 * (j & 3);
+            const int e = (x & 7) * 2;
+            return cat(ld4_tr(reinterpret_cast<const uint16_t *>(tile + place(r, x >> 3) + e)),
+                       ld4_tr(reinterpret_cast<const uint16_t *>(tile + place(r + 8, x >> 3) + e)));
+        } else {
+            F8 v;
+            const int x = x0 + (lane & 31);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                v[s] = *reinterpret_cast<const float *>(tile + place(r0 + 4 * h + (s & 3) + 2 * (s & 4), x >> 2) + (x & 3) * 4);
+            return v;
+        }
+    }
+};
+
+// 32 channels of a lane's row (a transposed result tile), scaled by f, to
+// `row`: bf16 in 16-byte pieces, for which the halves swap a register pair.
+// Every lane of a pair (c, 0), (c, 1) calls it or neither does.
+template <class T>
+__device__ __forceinline__ void attn_store(typename T::E *row, const f32x16 &x, float f, int h) {
+    if constexpr (T::kBf16) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            v2u32 y[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                f32x4 z;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) z[r] = x[8 * p + 4 * q + r] * f;
+                y[q] = __builtin_bit_cast(v2u32, cvt4(z));
+            }
+            const auto a = __builtin_amdgcn_permlane32_swap(y[0][0], y[1][0], false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(y[0][1], y[1][1], false, false);
+            *reinterpret_cast<v4u32 *>(row + 16 * p + 8 * h) = v4u32{a[0], b[0], a[1], b[1]};
+        }
+    } else {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            f32x4 z;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) z[r] = x[4 * p + r] * f;
+            *reinterpret_cast<f32x4 *>(row + 8 * p + 4 * h) = z;
+        }
+    }
+}
+
+// --- sequences and blocks -----------------------------------------------------------
+
+struct AttnSeq {
+    int64_t q0, k0;   // first rows
+    int32_t lq, lk;
+};
+__device__ __forceinline__ int64_t attn_clamp(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+// Sequence n, whatever cu_seqlens holds within the tensors.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int64_t n) {
+    AttnSeq s;
+    if (!a.cu) {
+        s.q0 = n * a.seq_q;
+        s.k0 = n * a.seq_k;
+        s.lq = static_cast<int32_t>(a.seq_q);
+        s.lk = static_cast<int32_t>(a.seq_k);
+        return s;
+    }
+    const int32_t *ck = a.cuk ? a.cuk : a.cu;
+    s.q0 = attn_clamp(a.cu[n], 0, a.total_q);
+    s.lq = static_cast<int32_t>(attn_clamp(a.cu[n + 1], s.q0, a.total_q) - s.q0);
+    s.k0 = attn_clamp(ck[n], 0, a.total_k);
+    s.lk = static_cast<int32_t>(attn_clamp(ck[n + 1], s.k0, a.total_k) - s.k0);
+    return s;
+}
+
+// Tiles of kAttnRows rows.  Packed sequences start at tile cu[n] / kAttnRows +
+// n: at least one tile later than the last of sequence n - 1, so no table is
+// needed, and some tiles are empty.
+__host__ __device__ inline int64_t attn_tiles(bool packed, int64_t n_seq, int64_t seq, int64_t total) {
+    return packed ? total / kAttnRows + n_seq : (seq + kAttnRows - 1) / kAttnRows;
+}
+// Last sequence that starts at or before `tile`: a wave narrows 64 sequences at a time.
+__device__ __forceinline__ int64_t attn_find(const int32_t *cu, int64_t n_seq, int64_t total, int64_t tile, int lane) {
+    int64_t lo = 0, hi = n_seq;
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
+        const bool before = at < hi && attn_clamp(cu[at], 0, total) / kAttnRows + at <= tile;
+        const int count = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before));
+        lo += (count > 0 ? count - 1 : 0) * step;
+        hi = hi < lo + step ? hi : lo + step;
+    }
+    return __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lo));
+}
+
+// Blocks b, b + 8, .. run on one XCD (with an L2 of its own): they work on the
+// same key head (of the same row of the batch), where the counts divide.  Late
+// tiles first: causal ones see the most keys.
+struct AttnItem {
+    int64_t pair, tile;   // (row, key head), tile of the row (packed: of all)
+    int32_t way;          // query head of the group, or part of it
+};
+__host__ __device__ inline int64_t attn_grid(int64_t pairs, int64_t tiles, int64_t ways) {
+    return pairs < 8 && 8 % pairs == 0 ? 8 * ways * ((tiles * pairs + 7) / 8) : pairs * tiles * ways;
+}
+__device__ __forceinline__ AttnItem attn_item(int64_t block, int64_t pairs, int64_t tiles, int64_t ways) {
+    AttnItem t;
+    if (pairs % 8 == 0) {
+        const int64_t each = tiles * ways, at = block / 8;
+        t.pair = at / each * 8 + block % 8;
+        t.tile = at % each / ways;
+        t.way = static_cast<int32_t>(at % ways);
+    } else if (8 % pairs == 0) {
+        const int64_t at = block / 8, x = block % 8;
+        t.pair = x % pairs;
+        t.tile = at / ways * (8 / pairs) + x / pairs;
+        t.way = static_cast<int32_t>(at % ways);
+    } else {
+        t.pair = block % pairs;
+        t.way = static_cast<int32_t>(block / pairs % ways);
+        t.tile = block / pairs / ways;
+    }
+    t.tile = tiles - 1 - t.tile;   // negative: none
+    return t;
+}
+
+// Which keys a query sees.  Query i stands behind key at(i) (causal: the last
+// one it sees, i + lk - lq; else the sequence's last key), and sees key j where
+// 0 <= at(i) - j < back, one unsigned comparison that also ends the sequence.
+struct AttnSight {
+    int32_t first, slope;
+    uint32_t back;
+    __device__ __forceinline__ AttnSight(const AttnArgs &a, const AttnSeq &s)
+        : first(a.causal ? s.lk - s.lq : s.lk - 1), slope(a.causal ? 1 : 0),
+          back(a.window ? static_cast<uint32_t>(a.window) : 0x7FFFFFFFu) {}
+    __device__ __forceinline__ int32_t at(int32_t i) const { return first + slope * i; }
+    __device__ __forceinline__ bool sees(int32_t at, int32_t j) const { return static_cast<uint32_t>(at - j) < back; }
+    // Queries lo .. hi and keys j .. j + n - 1: all pairs seen, any pair seen.
+    __device__ __forceinline__ bool all(int32_t lo, int32_t hi, int32_t j, int32_t n) const {
+        return at(lo) - (j + n - 1) >= 0 && static_cast<int64_t>(at(hi)) - j < back;
+    }
+    __device__ __forceinline__ bool any(int32_t lo, int32_t hi, int32_t j, int32_t n) const {
+        return at(hi) - j >= 0 && static_cast<int64_t>(at(lo)) - (j + n - 1) < back;
+    }
+};
+
+}  // namespace
+}  // namespace gdr

@@ -1,0 +1,328 @@
+// A key-value cache in pages: attention of one new token of every sequence over
+// it, the store of new keys and values, and the tables and slots of new tokens.
+#include "gdr_attn_device.h"
+
+namespace gdr {
+namespace {
+
+// --- one token over the cache ---------------------------------------------------------
+
+// A wave takes a chunk of one sequence's keys and one key head with its group
+// of query heads (32 at most), in tiles of 32 keys.  Keys go from memory to the
+// matrix operand, values through 32 rows of LDS of the wave's own that are read
+// transposed.  The next tile's loads start once this one's keys are multiplied
+// and its values are in LDS.
+template <class T, int D>
+__global__ __launch_bounds__(64, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(PagedArgs a) {
+    typedef typename T::E E;
+    typedef typename T::F8 F8;
+    typedef AttnTile<T, D, 32> Tile;
+    constexpr int kSteps = D / 16, kParts = D / 32, kRow = D * sizeof(E), kLoads = 32 * kRow / 1024;
+    __shared__ alignas(16) char vals[32 * kRow];
+    const int lane = threadIdx.x, col = lane & 31, h = lane >> 5;
+    const int group = a.hq / a.hk, blocks = (group + 31) / 32;
+    int64_t item = blockIdx.x;
+    const int64_t split = item % a.splits;
+    item /= a.splits;
+    const int head0 = static_cast<int>(item % blocks) * 32;
+    item /= blocks;
+    const int hk = static_cast<int>(item % a.hk);
+    const int64_t n = item / a.hk;
+
+    int64_t len = a.lens[n];
+    len = len < 0 ? 0 : len > a.width * a.page ? a.width * a.page : len;
+    const int64_t first = a.window > 0 && len > a.window ? len - a.window : 0;
+    const int64_t begin64 = first + split * a.chunk, end64 = begin64 + a.chunk < len ? begin64 + a.chunk : len;
+    if (begin64 >= end64 && split > 0) return;   // the first chunk of no keys writes zeros
+    const int32_t begin = static_cast<int32_t>(begin64), end = static_cast<int32_t>(end64);
+
+    const int head = head0 + col < group ? head0 + col : group - 1;
+    const float c0 = a.scale * kLog2e, c = __builtin_fabsf(c0);
+    F8 q[kSteps];
+    {
+        const E *x = static_cast<const E *>(a.q) + n * a.ldq + (static_cast<int64_t>(hk) * group + head) * D + 8 * h;
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+            q[ks] = T::load(x + 16 * ks);
+            if (c0 < 0.f) q[ks] = T::flip(q[ks]);
+        }
+    }
+    const int32_t *table = a.table + n * a.width;
+    const int64_t row_step = static_cast<int64_t>(a.hk) * kRow;
+    const char *kbase = static_cast<const char *>(a.k) + static_cast<int64_t>(hk) * kRow;
+    const char *vbase = static_cast<const char *>(a.v) + static_cast<int64_t>(hk) * kRow;
+    // The cache row of this lane's key of the tile at j, -1 where there is none.
+    auto entry = [&](int32_t j, int32_t &in_page) {
+        const int32_t key = j + col < end ? j + col : end - 1;
+        const uint32_t p = static_cast<uint32_t>((static_cast<uint64_t>(key) * a.magic) >> a.shift);
+        in_page = j + col < end ? key - static_cast<int32_t>(p) * a.page : -1;
+        return table[p];
+    };
+    auto row_of = [&](int32_t page, int32_t in_page) {
+        return in_page >= 0 && page >= 0 && page < a.pages ? page * a.page + in_page : -1;
+    };
+    F8 kreg[kSteps];
+    v4u32 vreg[kLoads];
+    auto load = [&](int32_t row) {
+        const char *k = kbase + (row < 0 ? 0 : row) * row_step + h * 8 * sizeof(E);
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) kreg[ks] = T::load(reinterpret_cast<const E *>(k + ks * 16 * sizeof(E)));
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = i * 1024 + lane * 16;
+            const int32_t r = __shfl(row, at / kRow);
+            vreg[i] = v4u32{0, 0, 0, 0};   // a row that is not there: zeros, whatever the memory holds
+            if (r >= 0) vreg[i] = *reinterpret_cast<const v4u32 *>(vbase + r * row_step + at % kRow);
+        }
+    };
+    f32x16 o[kParts];
+#pragma unroll
+    for (int t = 0; t < kParts; ++t) o[t] = zero16();
+    float ref = -__builtin_inff(), sum = 0.f;
+    if (begin < end) {
+        int32_t in_page, next_in = -1, next_page = -1;
+        const int32_t page = entry(begin, in_page);
+        int32_t row = row_of(page, in_page);
+        if (begin + 32 < end) next_page = entry(begin + 32, next_in);
+        load(row);
+        for (int32_t j = begin; j < end; j += 32) {
+            f32x16 s = zero16();
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) s = T::mma(kreg[ks], q[ks], s);
+            // LDS of one wave: its accesses stay in order
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int at = i * 1024 + lane * 16;
+                *reinterpret_cast<v4u32 *>(vals + Tile::place(at / kRow, at % kRow / 16)) = vreg[i];
+            }
+            const uint64_t there = __builtin_amdgcn_ballot_w64(row >= 0);   // bit k: key j + k
+            if (j + 32 < end) {
+                row = row_of(next_page, next_in);
+                if (j + 64 < end) next_page = entry(j + 64, next_in);
+                load(row);
+            }
+            const uint32_t mine = static_cast<uint32_t>(there) >> (4 * h);
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                if (!(mine >> (8 * (r / 4) + r % 4) & 1)) s[r] = -__builtin_inff();
+                top = fmaxf(top, s[r]);
+            }
+            top = half_max(top) * c;
+            if (__builtin_amdgcn_ballot_w64(top > ref + 8.f)) {
+                const float now = fmaxf(top, ref), f = now == ref ? 1.f : fast_exp2(ref - now);
+                ref = now;
+                sum *= f;
+#pragma unroll
+                for (int t = 0; t < kParts; ++t) o[t] *= f;
+            }
+            const float base = ref == -__builtin_inff() ? 0.f : ref;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float p = fast_exp2(__builtin_fmaf(s[r], c, -base));
+                s[r] = mine >> (8 * (r / 4) + r % 4) & 1 ? p : 0.f;
+                sum += s[r];
+            }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const F8 p = T::part(s, kb);
+#pragma unroll
+                for (int t = 0; t < kParts; ++t) o[t] = T::mma(Tile::across(vals, 16 * kb, 32 * t, lane), p, o[t]);
+            }
+        }
+    }
+    sum = half_sum(sum);
+    if (head0 + col >= group) return;
+    const int64_t out = n * a.hq + static_cast<int64_t>(hk) * group + head;
+    if (a.splits == 1) {
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) attn_store<T>(static_cast<E *>(a.o) + out * D + 32 * t, o[t], f, h);
+    } else {
+        const int64_t at = out * a.splits + split;
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) attn_store<AttnF32>(a.part + at * D + 32 * t, o[t], 1.f, h);
+        if (h == 0) {
+            a.stat[2 * at] = ref;
+            a.stat[2 * at + 1] = sum;
+        }
+    }
+}
+
+// Joins the chunks of a query head: a block takes 32 channels, eight chunks at a time.
+template <class T>
+__global__ __launch_bounds__(256) void gdr_paged_join_kernel(PagedArgs a) {
+    __shared__ float best[4], all[8][32], each[8];
+    const int parts = a.d / 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t out = blockIdx.x / parts, n = out / a.hq;
+    const int channel = static_cast<int>(blockIdx.x % parts) * 32 + x;
+    int64_t len = a.lens[n];
+    len = len < 0 ? 0 : len > a.width * a.page ? a.width * a.page : len;
+    if (a.window > 0 && len > a.window) len = a.window;
+    const int64_t count = len > 0 ? (len + a.chunk - 1) / a.chunk : 1;
+    const float *stat = a.stat + out * a.splits * 2;
+    float top = -__builtin_inff();
+    for (int64_t s = threadIdx.x; s < count; s += 256) top = fmaxf(top, stat[2 * s]);
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
+    if ((threadIdx.x & 63) == 0) best[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
+    if (top == -__builtin_inff()) top = 0.f;
+    float sum = 0.f, total = 0.f;
+    for (int64_t s = y; s < count; s += 8) {
+        const float f = fast_exp2(stat[2 * s] - top);
+        total = __builtin_fmaf(f, stat[2 * s + 1], total);
+        sum = __builtin_fmaf(f, a.part[(out * a.splits + s) * a.d + channel], sum);
+    }
+    all[y][x] = sum;
+    if (x == 0) each[y] = total;
+    __syncthreads();
+    if (y) return;
+    sum = total = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        sum += all[i][x];
+        total += each[i];
+    }
+    const float o = total == 0.f ? 0.f : sum / total;
+    if constexpr (T::kBf16) static_cast<uint16_t *>(a.o)[out * a.d + channel] = bf16_bits(o);
+    else static_cast<float *>(a.o)[out * a.d + channel] = o;
+}
+
+template <class T, int D>
+hipError_t run_step(const PagedArgs &a, hipStream_t stream) {
+    const int64_t group = a.hq / a.hk, grid = a.n_seq * a.hk * ((group + 31) / 32) * a.splits;
+    const int64_t join = a.n_seq * a.hq * (a.d / 32);
+    if (grid > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
+    gdr_paged_step_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 64, 0, stream>>>(a);
+    if (a.splits > 1) gdr_paged_join_kernel<T><<<dim3(static_cast<unsigned>(join)), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+// --- store ------------------------------------------------------------------------------
+
+__global__ __launch_bounds__(256) void gdr_page_store_kernel(StoreArgs a) {
+    const int64_t pieces = a.row_bytes / 16, count = 2 * a.tokens * pieces;
+    const int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
+    if (i >= count) return;
+    const bool v = i >= a.tokens * pieces;
+    const int64_t at = v ? i - a.tokens * pieces : i, t = at / pieces, piece = at % pieces * 16;
+    const int32_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.rows) return;
+    const char *from = v ? static_cast<const char *>(a.v) + t * a.ldv : static_cast<const char *>(a.k) + t * a.ldk;
+    char *to = static_cast<char *>(v ? a.vp : a.kp) + slot * a.row_bytes;
+    *reinterpret_cast<v4u32 *>(to + piece) = *reinterpret_cast<const v4u32 *>(from + piece);
+}
+
+// --- plan -------------------------------------------------------------------------------
+
+struct PlanSeq {
+    uint32_t past, fresh, held, need;   // sums of two stay below 2^32
+};
+__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs &a, int64_t n) {
+    PlanSeq s;
+    const uint32_t page = a.page;
+    s.past = a.past[n] > 0 ? a.past[n] : 0;
+    s.fresh = a.fresh[n] > 0 ? a.fresh[n] : 0;
+    s.held = s.past / page + (s.past % page != 0);
+    const uint32_t len = s.past + s.fresh;
+    s.need = len / page + (len % page != 0) - s.held;
+    return s;
+}
+__device__ __forceinline__ int32_t plan_int(int64_t x) { return x > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int32_t>(x); }
+
+// Each block has a run of sequences (and the place behind the last one, which
+// stands for the totals).  The tokens and pages before its run are sums over the
+// lengths, which every block makes for itself, N values from the caches, so that
+// one launch does.  Blocks along y share a sequence's tokens.
+__global__ __launch_bounds__(256) void gdr_page_plan_kernel(PlanArgs a, int64_t run) {
+    __shared__ int64_t sums[2][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t start = blockIdx.x * run, stop = start + run < a.n_seq + 1 ? start + run : a.n_seq + 1;
+    const int64_t i0 = blockIdx.y * static_cast<int64_t>(256) + threadIdx.x, hop = gridDim.y * static_cast<int64_t>(256);
+    int64_t tokens = 0, pages = 0;
+    for (int64_t m = threadIdx.x; m < start && m < a.n_seq; m += 256) {
+        const PlanSeq s = plan_seq(a, m);
+        tokens += s.fresh;
+        pages += s.need;
+    }
+    for (int m = 1; m < 64; m *= 2) {
+        tokens += __shfl_xor(tokens, m);
+        pages += __shfl_xor(pages, m);
+    }
+    if (lane == 0) {
+        sums[0][wave] = tokens;
+        sums[1][wave] = pages;
+    }
+    __syncthreads();
+    tokens = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
+    pages = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
+    for (int64_t n = start; n < stop; ++n) {
+        if (i0 == 0) a.cu[n] = plan_int(tokens < a.tokens ? tokens : a.tokens);
+        if (n == a.n_seq) {
+            if (i0 == 0) {
+                a.used[0] = plan_int(tokens);
+                a.used[1] = plan_int(pages);
+            }
+            for (int64_t t = tokens + i0; t < a.tokens; t += hop) {
+                a.positions[t] = 0;
+                a.slots[t] = -1;
+            }
+            return;
+        }
+        const PlanSeq s = plan_seq(a, n);
+        if (i0 == 0) a.lens[n] = plan_int(static_cast<int64_t>(s.past) + s.fresh);
+        int32_t *row = a.table + n * a.width;
+        const auto taken = [&](int64_t i) { return pages + i < a.pool_size ? a.pool[pages + i] : -1; };
+        for (int64_t i = i0; i < s.need && s.held + i < a.width; i += hop) row[s.held + i] = taken(i);
+        for (int64_t i = i0; i < s.fresh && tokens + i < a.tokens; i += hop) {
+            const uint32_t at = s.past + static_cast<uint32_t>(i), p = at / static_cast<uint32_t>(a.page);
+            // a page taken now comes from the pool again: the row may not be written yet
+            const int64_t page = p >= a.width ? -1 : p >= s.held ? taken(p - s.held) : row[p];
+            const int64_t slot = page * a.page + at % static_cast<uint32_t>(a.page);
+            a.positions[tokens + i] = plan_int(at);
+            a.slots[tokens + i] = page < 0 || slot > 0x7FFFFFFF ? -1 : static_cast<int32_t>(slot);
+        }
+        tokens += s.fresh;
+        pages += s.need;
+    }
+}
+
+}  // namespace
+
+// Chunks of a multiple of 32 keys, 64 at least, of which the sequences at their
+// longest have about 4096 together: two for each wave that the chip holds.
+void paged_split(PagedArgs &a) {
+    int64_t keys = a.width * a.page;
+    if (a.window > 0 && keys > a.window) keys = a.window;
+    if (keys < 1) keys = 1;
+    const int64_t rows = a.n_seq * a.hk * ((a.hq / a.hk + 31) / 32);
+    int64_t chunk = (rows * keys / 4096 + 31) / 32 * 32;
+    if (chunk < 64) chunk = 64;
+    if (chunk > 1 << 20) chunk = 1 << 20;
+    a.chunk = static_cast<int32_t>(chunk);
+    a.splits = (keys + chunk - 1) / chunk;
+}
+
+hipError_t launch_paged_step(const PagedArgs &a, hipStream_t stream) {
+    if (a.bf16) return a.d == 64 ? run_step<AttnBf, 64>(a, stream) : run_step<AttnBf, 128>(a, stream);
+    return a.d == 64 ? run_step<AttnF32, 64>(a, stream) : run_step<AttnF32, 128>(a, stream);
+}
+
+hipError_t launch_page_store(const StoreArgs &a, hipStream_t stream) {
+    const int64_t blocks = (2 * a.tokens * (a.row_bytes / 16) + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    gdr_page_store_kernel<<<dim3(static_cast<unsigned>(blocks)), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_page_plan(const PlanArgs &a, hipStream_t stream) {
+    const int64_t run = (a.n_seq + 1024) / 1024, blocks = (a.n_seq + run) / run;   // places 0 .. n_seq
+    const int64_t share = a.tokens / (a.n_seq + 1) / 512;
+    const unsigned y = share < 1 ? 1 : share > 32 ? 32 : static_cast<unsigned>(share);
+    gdr_page_plan_kernel<<<dim3(static_cast<unsigned>(blocks), y), 256, 0, stream>>>(a, run);
+    return hipGetLastError();
+}
+
+}  // namespace gdr

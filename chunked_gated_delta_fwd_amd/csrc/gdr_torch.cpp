@@ -1,4 +1,4 @@
-// Python calls of the operators in mixer.py: torch tensors in, the C ABI of
+// Python calls of the operators in mixer.py and attention.py: torch tensors in, the C ABI of
 // include/gdr.h called on torch's current stream, torch tensors out.  These
 // operators run once per layer and token while decoding, in a few
 // microseconds, so the marshalling is compiled.  No arithmetic here.
@@ -9,6 +9,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <optional>
 #include <string>
 
@@ -229,6 +230,77 @@ at::Tensor ssm_step(const at::Tensor &x, const at::Tensor &dt, const at::Tensor 
     return y;
 }
 
+float scale_or(const std::optional<double> &scale, const at::Tensor &q) {
+    const int64_t d = q.size(-1);
+    return scale ? static_cast<float>(*scale) : 1.f / std::sqrt(static_cast<float>(d > 0 ? d : 1));
+}
+
+std::tuple<at::Tensor, Opt> attn_fwd(const at::Tensor &q, const at::Tensor &k, const at::Tensor &v, const Opt &cu,
+                                     const Opt &cuk, bool causal, int64_t window, const std::optional<double> &scale,
+                                     bool want_lse, const Opt &o_, const Opt &lse_) {
+    want_dims(q, 4, "q");
+    Call c(q);
+    at::Tensor o = given_or(o_, q.sizes(), q, q.scalar_type());
+    Opt lse = lse_;
+    if (!lse && want_lse) lse = empty({q.size(0), q.size(1), q.size(2)}, q, at::kFloat);
+    check(gdr_attn_fwd(Desc(q, c).p(), Desc(k, c).p(), Desc(v, c).p(), Desc(cu, c).p(), Desc(cuk, c).p(), Desc(o, c).p(),
+                       Desc(lse, c).p(), causal, window, scale_or(scale, q), c.stream()));
+    return {o, lse};
+}
+
+std::tuple<at::Tensor, at::Tensor, at::Tensor> attn_bwd(const at::Tensor &q, const at::Tensor &k, const at::Tensor &v,
+                                                        const at::Tensor &o, const at::Tensor &lse, const at::Tensor &dout,
+                                                        const Opt &cu, const Opt &cuk, bool causal, int64_t window,
+                                                        const std::optional<double> &scale, const Opt &dq_, const Opt &dk_,
+                                                        const Opt &dv_) {
+    want_dims(q, 4, "q");
+    Call c(q);
+    at::Tensor dq = given_or(dq_, q.sizes(), q, q.scalar_type()), dk = given_or(dk_, k.sizes(), q, k.scalar_type());
+    at::Tensor dv = given_or(dv_, v.sizes(), q, v.scalar_type());
+    const Desc d[] = {Desc(q, c), Desc(k, c),   Desc(v, c),    Desc(cu, c), Desc(cuk, c), Desc(o, c),
+                      Desc(lse, c), Desc(dout, c), Desc(dq, c), Desc(dk, c), Desc(dv, c)};
+    with_workspace(c, [&](void *ws, int64_t *bytes) {
+        return gdr_attn_bwd(d[0].p(), d[1].p(), d[2].p(), d[3].p(), d[4].p(), d[5].p(), d[6].p(), d[7].p(), d[8].p(), d[9].p(),
+                            d[10].p(), causal, window, scale_or(scale, q), ws, bytes, c.stream());
+    });
+    return {dq, dk, dv};
+}
+
+at::Tensor attn_paged_step(const at::Tensor &q, const at::Tensor &kp, const at::Tensor &vp, const at::Tensor &table,
+                           const at::Tensor &lens, int64_t window, const std::optional<double> &scale, const Opt &o_) {
+    want_dims(q, 3, "q");
+    Call c(q);
+    at::Tensor o = given_or(o_, q.sizes(), q, q.scalar_type());
+    const Desc d[] = {Desc(q, c), Desc(kp, c), Desc(vp, c), Desc(table, c), Desc(lens, c), Desc(o, c)};
+    with_workspace(c, [&](void *ws, int64_t *bytes) {
+        return gdr_attn_paged_step(d[0].p(), d[1].p(), d[2].p(), d[3].p(), d[4].p(), d[5].p(), window, scale_or(scale, q), ws,
+                                   bytes, c.stream());
+    });
+    return o;
+}
+
+py::tuple page_plan(const at::Tensor &past, const at::Tensor &fresh, const at::Tensor &pool, const at::Tensor &table,
+                    int64_t page, int64_t tokens, const Opt &cu_, const Opt &lens_, const Opt &positions_, const Opt &slots_,
+                    const Opt &used_) {
+    want_dims(past, 1, "past");
+    if (tokens < 0) raise(GDR_EINVAL, "tokens must not be negative");
+    if (page < 1 || page > 65536) raise(GDR_ESHAPE, "page: 1 to 65536 tokens are supported, got " + std::to_string(page));
+    Call c(past);
+    const int64_t n = past.size(0);
+    at::Tensor cu = given_or(cu_, {n + 1}, past, at::kInt), lens = given_or(lens_, {n}, past, at::kInt);
+    at::Tensor positions = given_or(positions_, {1, tokens}, past, at::kInt);
+    at::Tensor slots = given_or(slots_, {1, tokens}, past, at::kInt), used = given_or(used_, {2}, past, at::kInt);
+    check(gdr_page_plan(Desc(past, c).p(), Desc(fresh, c).p(), Desc(pool, c).p(), Desc(table, c).p(), Desc(cu, c).p(),
+                        Desc(lens, c).p(), Desc(positions, c).p(), Desc(slots, c).p(), Desc(used, c).p(),
+                        static_cast<int32_t>(page), c.stream()));
+    return py::make_tuple(cu, lens, positions, slots, used);
+}
+
+void page_store(const at::Tensor &k, const at::Tensor &v, const at::Tensor &slots, const at::Tensor &kp, const at::Tensor &vp) {
+    Call c(k);
+    check(gdr_page_store(Desc(k, c).p(), Desc(v, c).p(), Desc(slots, c).p(), Desc(kp, c).p(), Desc(vp, c).p(), c.stream()));
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
@@ -241,4 +313,9 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     m.def("ssm_scan_fwd", &ssm_scan_fwd);
     m.def("ssm_scan_bwd", &ssm_scan_bwd);
     m.def("ssm_step", &ssm_step);
+    m.def("attn_fwd", &attn_fwd);
+    m.def("attn_bwd", &attn_bwd);
+    m.def("attn_paged_step", &attn_paged_step);
+    m.def("page_plan", &page_plan);
+    m.def("page_store", &page_store);
 }

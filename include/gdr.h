@@ -504,6 +504,125 @@ int gdr_ssm_step(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
                  const gdr_tensor *c, const gdr_tensor *D, const gdr_tensor *dt_bias,
                  const gdr_tensor *h, const gdr_tensor *y, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax attention and the paged key-value cache it decodes from, for the
+ * layers of a stack that are not recurrent.  Rows, workspaces and the order of
+ * sums as for the operators above.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * gdr_attn_fwd - softmax attention, query heads in groups that share a key
+ * head.  Per sequence and query head, over the keys j that query i sees,
+ *
+ *     s_ij = scale q_i . k_j,  lse_i = log sum_j e^(s_ij),  o_i = sum_j e^(s_ij - lse_i) v_j
+ *
+ *   q             [B, Tq, Hq, d] rows, bf16 or f32 (one dtype with k, v, o); d 64 or 128
+ *   k, v          [B, Tk, Hk, d] rows, Hq % Hk == 0; head h reads key head h / (Hq/Hk)
+ *   cu_seqlens    [N+1] int32 or NULL, as gdr_chunk_fwd (preconditions too)
+ *   cu_seqlens_k  [N+1] int32 offsets of the keys, or NULL: those of the queries (Tk == Tq)
+ *   o             [B, Tq, Hq, d] out;  lse [B, Tq, Hq] f32 out, or NULL.
+ *                 Rows of tokens outside every segment are not written.
+ *   causal        0: a query sees every key of its sequence.  Else the last
+ *                 query of a sequence is beside its last key: query i of Lq
+ *                 sees keys j <= i + Lk - Lq (none where that is negative).
+ *   window        with causal, 0 or the number of keys that a query sees, back
+ *                 from the last one.  A query that sees no key: o 0, lse -inf.
+ *
+ * bf16 inputs: bf16 matrix operands with fp32 sums; the probabilities are
+ * rounded to bf16 for the product with v, o is rounded once, lse is fp32.  f32
+ * inputs: fp32 products throughout.  A k or v that is not finite reaches the
+ * queries that see it and no others; a query whose scores are all -inf counts
+ * as one that sees no key.  No workspace.  q, k, v rows and o on 16-byte
+ * addresses, rows at most 32 MiB apart, at most 2^30 tokens.  Errors as
+ * gdr_chunk_fwd, GDR_EINVAL for a negative window or one without causal.
+ */
+int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
+                 const gdr_tensor *cu_seqlens, const gdr_tensor *cu_seqlens_k, const gdr_tensor *o,
+                 const gdr_tensor *lse, int causal, int64_t window, float scale,
+                 hipStream_t stream);
+
+/*
+ * gdr_attn_bwd - gradients of gdr_attn_fwd, from its o and lse.
+ *
+ *   o, do   [B, Tq, Hq, d] rows, dtype of q;  lse [B, Tq, Hq] f32
+ *   dq      [B, Tq, Hq, d] out;  dk, dv [B, Tk, Hk, d] out, summed over each
+ *           key head's query heads; dtype of q.  Rows of tokens outside every
+ *           segment are not written.
+ *
+ * The probabilities are made again from q, k and lse.  bf16 inputs: they and
+ * the scores' gradients are rounded to bf16 for the products over queries and
+ * keys; sums are fp32 and each gradient is rounded once.  Whatever is not
+ * finite reaches the rows whose sums hold it and no others.  Workspace: 8 bytes
+ * a query and query head, and 8 d bytes a key, key head and part where several
+ * blocks share a group's heads (small calls; as many parts at most as a group
+ * has heads).
+ */
+int gdr_attn_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
+                 const gdr_tensor *cu_seqlens, const gdr_tensor *cu_seqlens_k, const gdr_tensor *o,
+                 const gdr_tensor *lse, const gdr_tensor *dout, const gdr_tensor *dq,
+                 const gdr_tensor *dk, const gdr_tensor *dv, int causal, int64_t window,
+                 float scale, void *workspace, int64_t *workspace_bytes, hipStream_t stream);
+
+/*
+ * gdr_attn_paged_step - attention of one new token of each of N sequences over
+ * keys and values in pages (the token's own among them: store it first).
+ *
+ *   q            [N, Hq, d] rows, bf16 or f32 (one dtype with the pages and o); d 64 or 128
+ *   k_pages, v_pages  [P, page, Hk, d], page 1 .. 65536, Hq % Hk == 0, P * page < 2^31
+ *   block_table  [N, M] int32: the pages of a sequence in order.  An entry
+ *                outside 0 .. P-1 stands for a page without keys.
+ *   lens         [N] int32 keys of each sequence, taken as 0 .. M * page
+ *   o            [N, Hq, d] out, rounded once; zeros for a sequence without keys
+ *   window       0, or the number of last keys that are seen
+ *
+ * Arithmetic as gdr_attn_fwd.  The keys are split in chunks that are joined by
+ * a second kernel; workspace: 4 (d + 2) Hq bytes a sequence and chunk of the
+ * longest one that the table holds (chunks of 64 keys and more, about 4096 in
+ * a call), none for one chunk.
+ */
+int gdr_attn_paged_step(const gdr_tensor *q, const gdr_tensor *k_pages, const gdr_tensor *v_pages,
+                        const gdr_tensor *block_table, const gdr_tensor *lens, const gdr_tensor *o,
+                        int64_t window, float scale, void *workspace, int64_t *workspace_bytes,
+                        hipStream_t stream);
+
+/*
+ * gdr_page_plan - page tables, slots and positions of the next tokens of N
+ * requests, from their lengths.
+ *
+ *   past         [N] int32 tokens that a request has in its pages
+ *   fresh        [N] int32 tokens that are added now (negative values count as 0, here and in past)
+ *   free_pages   [F] int32 pages that are free, taken in order from the first
+ *   block_table  [N, M] int32, read and written: entries ceil(past / page) ..
+ *                ceil((past + fresh) / page) - 1 get free pages, request after
+ *                request, or -1 where none is left; the others are kept
+ *   cu_seqlens   [N+1] int32 out: sums of fresh, at most T
+ *   lens         [N] int32 out: past + fresh
+ *   positions    [1, T] int32 out: each new token's place in its request
+ *   slots        [1, T] int32 out: its row in the pages, page * page size +
+ *                place in the page; -1 without a page
+ *   used         [2] int32 out: all fresh tokens and all pages wanted, whether
+ *                or not T, F and M held them
+ *
+ * Tokens past the last request: position 0, slot -1.  No workspace.
+ */
+int gdr_page_plan(const gdr_tensor *past, const gdr_tensor *fresh, const gdr_tensor *free_pages,
+                  const gdr_tensor *block_table, const gdr_tensor *cu_seqlens,
+                  const gdr_tensor *lens, const gdr_tensor *positions, const gdr_tensor *slots,
+                  const gdr_tensor *used, int32_t page, hipStream_t stream);
+
+/*
+ * gdr_page_store - copies the keys and values of tokens into their slots.
+ *
+ *   k, v     [B, T, Hk, d] rows, bf16 or f32, Hk * d a multiple of 16 bytes
+ *   slots    [B, T] int32 rows of the pages; a slot outside 0 .. P * page - 1
+ *            stores nothing.  A slot that is named twice gets pieces of both.
+ *   k_pages, v_pages  [P, page, Hk, d] out, dtype of k; other rows are kept
+ *
+ * No workspace.  k, v rows and the pages on 16-byte addresses.
+ */
+int gdr_page_store(const gdr_tensor *k, const gdr_tensor *v, const gdr_tensor *slots,
+                   const gdr_tensor *k_pages, const gdr_tensor *v_pages, hipStream_t stream);
+
 /*
  * Launch plan of a gdr_chunk_fwd call, computed from shapes only (no device
  * access, no allocation).  gdr_plan validates exactly like gdr_chunk_fwd and
