@@ -129,22 +129,23 @@ struct AttnFwd {
     }
 };
 
-template <class T, int D>
-__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_fwd_kernel(AttnArgs a, int64_t tiles) {
+// A block's rows.  Returns, for every wave alike, whether some output is not
+// finite and the rows have to be done again with care.
+template <class T, int D, bool CAREFUL>
+__device__ __forceinline__ bool attn_fwd_block(const AttnArgs &a, uint32_t tiles, typename AttnFwd<T, D>::Lds &lds) {
     typedef AttnFwd<T, D> F;
     typedef typename T::E E;
     typedef typename T::F8 F8;
-    __shared__ typename F::Lds lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     const int group = a.hq / a.hk;
-    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk;
     const AttnItem item = attn_item(blockIdx.x, pairs, tiles, group);
-    if (item.tile < 0) return;
-    const int64_t n = a.cu ? attn_find(a.cu, a.n_seq, a.total_q, item.tile, lane) : item.pair / a.hk;
-    const int hk = static_cast<int>(item.pair % a.hk), hq = hk * group + item.way;
+    if (item.tile < 0) return false;
+    const int32_t n = a.cu ? attn_find(a.cu, static_cast<int32_t>(a.n_seq), a.total_q, item.tile, lane) : item.pair / a.hk;
+    const int hk = item.pair % a.hk, hq = hk * group + item.way;
     const AttnSeq seq = attn_seq(a, n);
     const int64_t tile = a.cu ? item.tile - (attn_clamp(a.cu[n], 0, a.total_q) / kAttnRows + n) : item.tile;
-    if (tile < 0 || tile * kAttnRows >= seq.lq) return;
+    if (tile < 0 || tile * kAttnRows >= seq.lq) return false;
     const AttnSight sight(a, seq);
     const int32_t i0 = static_cast<int32_t>(tile * kAttnRows);
     const int32_t i1 = i0 + kAttnRows < seq.lq ? i0 + kAttnRows - 1 : seq.lq - 1;   // last row
@@ -168,16 +169,13 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_fwd_kernel(Att
     const E *k = static_cast<const E *>(a.k) + seq.k0 * a.ldk + static_cast<int64_t>(hk) * D;
     const E *v = static_cast<const E *>(a.v) + seq.k0 * a.ldv + static_cast<int64_t>(hk) * D;
     const uint32_t step_k = static_cast<uint32_t>(a.ldk * sizeof(E)), step_v = static_cast<uint32_t>(a.ldv * sizeof(E));
-    F::template walk<false>(w, sight, __builtin_fabsf(c), i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
-    {
-        float x = 0.f;   // 0, or NaN where an output is not finite
+    F::template walk<CAREFUL>(w, sight, __builtin_fabsf(c), i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    float x = 0.f;   // 0, or NaN where an output is not finite
 #pragma unroll
-        for (int t = 0; t < F::kParts; ++t)
+    for (int t = 0; t < F::kParts; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.o[t][r], 0.f, x);
-        if (__syncthreads_or(x != 0.f))
-            F::template walk<true>(w, sight, __builtin_fabsf(c), i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
-    }
+        for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.o[t][r], 0.f, x);
+    if (!CAREFUL && __syncthreads_or(x != 0.f)) return true;
     const int32_t i = i0 + 32 * wave + col;
     // no key seen (or scores of -inf alone): 0, and NaN stays NaN
     const float sum = half_sum(w.sum), inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -189,6 +187,19 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_fwd_kernel(Att
             a.lse[(seq.q0 + i) * a.hq + hq] =
                 sum == 0.f ? -__builtin_inff() : (w.ref + __builtin_log2f(sum)) * 0.69314718055994530942f;
     }
+    return false;
+}
+
+// A function of its own: inside the kernel it would cost the other walk registers.
+template <class T, int D>
+__device__ __attribute__((noinline)) void attn_fwd_careful(AttnArgsAt at, uint32_t tiles, typename AttnFwd<T, D>::Lds *lds) {
+    (void)attn_fwd_block<T, D, true>(attn_args(at), tiles, *lds);
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_fwd_kernel(AttnArgs a, uint32_t tiles) {
+    __shared__ typename AttnFwd<T, D>::Lds lds;
+    if (attn_fwd_block<T, D, false>(a, tiles, lds)) attn_fwd_careful<T, D>(attn_args_at(), tiles, &lds);
 }
 
 template <class T, int D>
@@ -196,8 +207,8 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
     const int64_t tiles = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
     const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
     const int64_t grid = attn_grid(pairs, tiles, a.hq / a.hk);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    gdr_attn_fwd_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a, tiles);
+    if (grid > 0x7FFFFFFF || tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+    gdr_attn_fwd_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
     return hipGetLastError();
 }
 

@@ -99,22 +99,21 @@ struct AttnDq {
     }
 };
 
-template <class T, int D>
-__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dq_kernel(AttnArgs a, int64_t tiles) {
+template <class T, int D, bool CAREFUL>
+__device__ __forceinline__ bool attn_dq_block(const AttnArgs &a, uint32_t tiles, typename AttnDq<T, D>::Lds &lds) {
     typedef AttnDq<T, D> F;
     typedef typename T::E E;
     typedef typename T::F8 F8;
-    __shared__ typename F::Lds lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     const int group = a.hq / a.hk;
-    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk;
     const AttnItem item = attn_item(blockIdx.x, pairs, tiles, group);
-    if (item.tile < 0) return;
-    const int64_t n = a.cu ? attn_find(a.cu, a.n_seq, a.total_q, item.tile, lane) : item.pair / a.hk;
-    const int hk = static_cast<int>(item.pair % a.hk), hq = hk * group + item.way;
+    if (item.tile < 0) return false;
+    const int32_t n = a.cu ? attn_find(a.cu, static_cast<int32_t>(a.n_seq), a.total_q, item.tile, lane) : item.pair / a.hk;
+    const int hk = item.pair % a.hk, hq = hk * group + item.way;
     const AttnSeq seq = attn_seq(a, n);
     const int64_t tile = a.cu ? item.tile - (attn_clamp(a.cu[n], 0, a.total_q) / kAttnRows + n) : item.tile;
-    if (tile < 0 || tile * kAttnRows >= seq.lq) return;
+    if (tile < 0 || tile * kAttnRows >= seq.lq) return false;
     const AttnSight sight(a, seq);
     const int32_t i0 = static_cast<int32_t>(tile * kAttnRows);
     const int32_t i1 = i0 + kAttnRows < seq.lq ? i0 + kAttnRows - 1 : seq.lq - 1;
@@ -150,22 +149,31 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dq_kernel(Attn
     const E *k = static_cast<const E *>(a.k) + seq.k0 * a.ldk + static_cast<int64_t>(hk) * D;
     const E *v = static_cast<const E *>(a.v) + seq.k0 * a.ldv + static_cast<int64_t>(hk) * D;
     const uint32_t step_k = static_cast<uint32_t>(a.ldk * sizeof(E)), step_v = static_cast<uint32_t>(a.ldv * sizeof(E));
-    F::template walk<false>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
-    {
-        float x = 0.f;   // 0, or NaN where a gradient is not finite
+    F::template walk<CAREFUL>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    float x = 0.f;   // 0, or NaN where a gradient is not finite
 #pragma unroll
-        for (int t = 0; t < F::kParts; ++t)
+    for (int t = 0; t < F::kParts; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.dq[t][r], 0.f, x);
-        if (__syncthreads_or(x != 0.f))
-            F::template walk<true>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
-    }
+        for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.dq[t][r], 0.f, x);
+    if (!CAREFUL && __syncthreads_or(x != 0.f)) return true;
     const int32_t i = i0 + 32 * wave + col;
     if (i < seq.lq) {
         E *dq = static_cast<E *>(a.dq) + ((seq.q0 + i) * a.hq + hq) * D;
 #pragma unroll
         for (int t = 0; t < F::kParts; ++t) attn_store<T>(dq + 32 * t, w.dq[t], a.scale, h);
     }
+    return false;
+}
+
+template <class T, int D>
+__device__ __attribute__((noinline)) void attn_dq_careful(AttnArgsAt at, uint32_t tiles, typename AttnDq<T, D>::Lds *lds) {
+    (void)attn_dq_block<T, D, true>(attn_args(at), tiles, *lds);
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dq_kernel(AttnArgs a, uint32_t tiles) {
+    __shared__ typename AttnDq<T, D>::Lds lds;
+    if (attn_dq_block<T, D, false>(a, tiles, lds)) attn_dq_careful<T, D>(attn_args_at(), tiles, &lds);
 }
 
 // dk and dv: a block takes 128 key rows of one key head, 32 a wave, and walks
@@ -282,22 +290,21 @@ struct AttnDkv {
     }
 };
 
-template <class T, int D>
-__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(AttnArgs a, int64_t tiles) {
+template <class T, int D, bool CAREFUL>
+__device__ __forceinline__ bool attn_dkv_block(const AttnArgs &a, uint32_t tiles, typename AttnDkv<T, D>::Lds &lds) {
     typedef AttnDkv<T, D> F;
     typedef typename T::E E;
-    __shared__ typename F::Lds lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     const int group = a.hq / a.hk;
-    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk;
     const AttnItem item = attn_item(blockIdx.x, pairs, tiles, a.parts);
-    if (item.tile < 0) return;
+    if (item.tile < 0) return false;
     const int32_t *cuk = a.cuk ? a.cuk : a.cu;
-    const int64_t n = a.cu ? attn_find(cuk, a.n_seq, a.total_k, item.tile, lane) : item.pair / a.hk;
-    const int hk = static_cast<int>(item.pair % a.hk);
+    const int32_t n = a.cu ? attn_find(cuk, static_cast<int32_t>(a.n_seq), a.total_k, item.tile, lane) : item.pair / a.hk;
+    const int hk = item.pair % a.hk;
     const AttnSeq seq = attn_seq(a, n);
     const int64_t tile = a.cu ? item.tile - (attn_clamp(cuk[n], 0, a.total_k) / kAttnRows + n) : item.tile;
-    if (tile < 0 || tile * kAttnRows >= seq.lk) return;
+    if (tile < 0 || tile * kAttnRows >= seq.lk) return false;
     const AttnSight sight(a, seq);
     const int32_t j0 = static_cast<int32_t>(tile * kAttnRows);
     const int32_t j1 = j0 + kAttnRows < seq.lk ? j0 + kAttnRows - 1 : seq.lk - 1;
@@ -336,17 +343,15 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(Att
     }
     const float c = a.scale * kLog2e;
     const int32_t b = static_cast<int32_t>(begin), e = static_cast<int32_t>(end);
-    F::template walk<false>(w, from, sight, c, j0, j1, b, e, lds, wave, lane);
-    {
-        float x = 0.f;
+    F::template walk<CAREFUL>(w, from, sight, c, j0, j1, b, e, lds, wave, lane);
+    float x = 0.f;
 #pragma unroll
-        for (int t = 0; t < F::kParts; ++t)
+    for (int t = 0; t < F::kParts; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.dk[t][r], 0.f, __builtin_fmaf(w.dv[t][r], 0.f, x));
-        if (__syncthreads_or(x != 0.f)) F::template walk<true>(w, from, sight, c, j0, j1, b, e, lds, wave, lane);
-    }
+        for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.dk[t][r], 0.f, __builtin_fmaf(w.dv[t][r], 0.f, x));
+    if (!CAREFUL && __syncthreads_or(x != 0.f)) return true;
     const int32_t j = j0 + 32 * wave + col;
-    if (j >= seq.lk) return;
+    if (j >= seq.lk) return false;
     const int64_t at = ((seq.k0 + j) * a.hk + hk) * D;
     if (a.part) {
         const int64_t all = a.total_k * a.hk * D;
@@ -363,15 +368,27 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(Att
             attn_store<T>(static_cast<E *>(a.dv) + at + 32 * t, w.dv[t], 1.f, h);
         }
     }
+    return false;
+}
+
+template <class T, int D>
+__device__ __attribute__((noinline)) void attn_dkv_careful(AttnArgsAt at, uint32_t tiles, typename AttnDkv<T, D>::Lds *lds) {
+    (void)attn_dkv_block<T, D, true>(attn_args(at), tiles, *lds);
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(AttnArgs a, uint32_t tiles) {
+    __shared__ typename AttnDkv<T, D>::Lds lds;
+    if (attn_dkv_block<T, D, false>(a, tiles, lds)) attn_dkv_careful<T, D>(attn_args_at(), tiles, &lds);
 }
 
 // Sums the parts of dk and dv in order, for the rows of one tile's sequence.
 template <class T>
-__global__ __launch_bounds__(256) void gdr_attn_join_kernel(AttnArgs a, int64_t tiles) {
+__global__ __launch_bounds__(256) void gdr_attn_join_kernel(AttnArgs a, uint32_t tiles) {
     const int lane = threadIdx.x & 63;
-    const int64_t slot = blockIdx.x % tiles, which = blockIdx.x / tiles;
+    const int32_t slot = blockIdx.x % tiles, which = blockIdx.x / tiles;
     const int32_t *cuk = a.cuk ? a.cuk : a.cu;
-    const int64_t n = a.cu ? attn_find(cuk, a.n_seq, a.total_k, slot, lane) : which;
+    const int32_t n = a.cu ? attn_find(cuk, static_cast<int32_t>(a.n_seq), a.total_k, slot, lane) : which;
     const AttnSeq seq = attn_seq(a, n);
     const int64_t tile = a.cu ? slot - (attn_clamp(cuk[n], 0, a.total_k) / kAttnRows + n) : slot;
     if (tile < 0 || tile * kAttnRows >= seq.lk) return;
@@ -395,13 +412,13 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
     const int64_t tiles_q = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
     const int64_t tiles_k = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k);
     const int64_t grid_q = attn_grid(pairs, tiles_q, a.hq / a.hk), grid_k = attn_grid(pairs, tiles_k, a.parts);
-    if (grid_q > 0x7FFFFFFF || grid_k > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (a.total_q > 0) gdr_attn_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid_q)), 256, 0, stream>>>(a, tiles_q);
+    if (grid_q > 0x7FFFFFFF || grid_k > 0x7FFFFFFF || tiles_q > 0x7FFFFFFF || tiles_k > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (a.total_q > 0) gdr_attn_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid_q)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_q));
     if (a.total_k > 0) {
-        gdr_attn_dkv_kernel<T, D><<<dim3(static_cast<unsigned>(grid_k)), 256, 0, stream>>>(a, tiles_k);
+        gdr_attn_dkv_kernel<T, D><<<dim3(static_cast<unsigned>(grid_k)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
         if (a.part) {
             const int64_t blocks = tiles_k * (a.cu ? 1 : a.n_seq);
-            gdr_attn_join_kernel<T><<<dim3(static_cast<unsigned>(blocks), 8), 256, 0, stream>>>(a, tiles_k);
+            gdr_attn_join_kernel<T><<<dim3(static_cast<unsigned>(blocks), 8), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
         }
     }
     return hipGetLastError();

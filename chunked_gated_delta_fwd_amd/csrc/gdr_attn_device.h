@@ -259,47 +259,60 @@ __host__ __device__ inline int64_t attn_tiles(bool packed, int64_t n_seq, int64_
     return packed ? total / kAttnRows + n_seq : (seq + kAttnRows - 1) / kAttnRows;
 }
 // Last sequence that starts at or before `tile`: a wave narrows 64 sequences at a time.
-__device__ __forceinline__ int64_t attn_find(const int32_t *cu, int64_t n_seq, int64_t total, int64_t tile, int lane) {
-    int64_t lo = 0, hi = n_seq;
+__device__ __forceinline__ int32_t attn_find(const int32_t *cu, int32_t n_seq, int64_t total, int32_t tile, int lane) {
+    int32_t lo = 0, hi = n_seq;
     while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
+        const int32_t step = (hi - lo + 63) / 64, at = lo + lane * step;
         const bool before = at < hi && attn_clamp(cu[at], 0, total) / kAttnRows + at <= tile;
         const int count = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before));
         lo += (count > 0 ? count - 1 : 0) * step;
         hi = hi < lo + step ? hi : lo + step;
     }
-    return __builtin_amdgcn_readfirstlane(static_cast<int32_t>(lo));
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Blocks b, b + 8, .. run on one XCD (with an L2 of its own): they work on the
 // same key head (of the same row of the batch), where the counts divide.  Late
 // tiles first: causal ones see the most keys.
 struct AttnItem {
-    int64_t pair, tile;   // (row, key head), tile of the row (packed: of all)
+    int32_t pair, tile;   // (row, key head), tile of the row (packed: of all)
     int32_t way;          // query head of the group, or part of it
 };
 __host__ __device__ inline int64_t attn_grid(int64_t pairs, int64_t tiles, int64_t ways) {
     return pairs < 8 && 8 % pairs == 0 ? 8 * ways * ((tiles * pairs + 7) / 8) : pairs * tiles * ways;
 }
-__device__ __forceinline__ AttnItem attn_item(int64_t block, int64_t pairs, int64_t tiles, int64_t ways) {
+// All counts are below 2^31, as the grid is.
+__device__ __forceinline__ AttnItem attn_item(uint32_t block, uint32_t pairs, uint32_t tiles, uint32_t ways) {
     AttnItem t;
+    uint32_t tile;
     if (pairs % 8 == 0) {
-        const int64_t each = tiles * ways, at = block / 8;
-        t.pair = at / each * 8 + block % 8;
-        t.tile = at % each / ways;
-        t.way = static_cast<int32_t>(at % ways);
+        const uint32_t at = block / 8, head = at / ways;
+        t.way = at % ways;
+        tile = head % tiles;
+        t.pair = head / tiles * 8 + block % 8;
     } else if (8 % pairs == 0) {
-        const int64_t at = block / 8, x = block % 8;
+        const uint32_t at = block / 8, x = block % 8;
         t.pair = x % pairs;
-        t.tile = at / ways * (8 / pairs) + x / pairs;
-        t.way = static_cast<int32_t>(at % ways);
+        t.way = at % ways;
+        tile = at / ways * (8 / pairs) + x / pairs;
     } else {
+        const uint32_t at = block / pairs;
         t.pair = block % pairs;
-        t.way = static_cast<int32_t>(block / pairs % ways);
-        t.tile = block / pairs / ways;
+        t.way = at % ways;
+        tile = at / ways;
     }
-    t.tile = tiles - 1 - t.tile;   // negative: none
+    t.tile = static_cast<int32_t>(tiles) - 1 - static_cast<int32_t>(tile);   // negative: none
     return t;
+}
+
+// The arguments where the kernel was given them, for functions that are not
+// inlined: a reference to the kernel's own copy would put it on the stack.
+typedef __attribute__((address_space(4))) const AttnArgs *AttnArgsAt;
+__device__ __forceinline__ AttnArgsAt attn_args_at() { return (AttnArgsAt)__builtin_amdgcn_kernarg_segment_ptr(); }
+__device__ __forceinline__ AttnArgs attn_args(AttnArgsAt at) {
+    AttnArgs a;
+    __builtin_memcpy(&a, (const AttnArgs *)at, sizeof(a));
+    return a;
 }
 
 // Which keys a query sees.  Query i stands behind key at(i) (causal: the last
