@@ -49,7 +49,7 @@ struct AttnFwd {
         for (int t = 0; t < kParts; ++t) w.o[t] = zero16();
         w.ref = -__builtin_inff();
         w.sum = 0.f;
-        int buf = 0;
+        const typename Tile::Lane places = Tile::lane_places(lane);
         auto load = [&](int32_t j, int b) {
             Tile::load(fk, reinterpret_cast<const E *>(reinterpret_cast<const char *>(k) + static_cast<int64_t>(j) * step_k),
                        step_k, lk - j, lds.k[b], wave);
@@ -57,18 +57,20 @@ struct AttnFwd {
                        step_v, lk - j, lds.v[b], wave);
         };
         if (begin < end) load(begin, 0);
-        for (int32_t j = begin; j < end; j += kKeys, buf ^= 1) {
+        const auto tile = [&](auto which, int32_t j) {
+            constexpr int buf = decltype(which)::value;
+            const typename Tile::Lane l = attn_here(places);
             loads_landed();
             __syncthreads();
             if (j + kKeys < end) load(j + kKeys, buf ^ 1);
             const int32_t hi = lo + 31 < i1 ? lo + 31 : i1;
-            if (lo > i1 || !sight.any(lo, hi, j, kKeys)) continue;
+            if (lo > i1 || !sight.any(lo, hi, j, kKeys)) return;
             f32x16 s[kSub];
 #pragma unroll
             for (int t = 0; t < kSub; ++t) {
                 s[t] = zero16();
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) s[t] = T::mma(Tile::rows(lds.k[buf], 32 * t, ks, col, h), w.q[ks], s[t]);
+                for (int ks = 0; ks < kSteps; ++ks) s[t] = T::mma(Tile::rows(lds.k[buf], l, 32 * t, ks), w.q[ks], s[t]);
             }
             const bool whole = sight.all(lo, hi, j, kKeys);
             const int32_t d0 = at - j - 4 * h;
@@ -94,14 +96,18 @@ struct AttnFwd {
                 for (int t = 0; t < kParts; ++t) w.o[t] *= f;
             }
             const float ref = w.ref == -__builtin_inff() ? 0.f : w.ref;
+            const auto exponentials = [&](auto masked) {
 #pragma unroll
-            for (int t = 0; t < kSub; ++t)
+                for (int t = 0; t < kSub; ++t)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float p = fast_exp2(__builtin_fmaf(s[t][r], c, -ref));
-                    s[t][r] = whole || sight.sees(d0, 32 * t + 8 * (r / 4) + r % 4) ? p : 0.f;
-                    w.sum += s[t][r];
-                }
+                    for (int r = 0; r < 16; ++r) {
+                        const float p = fast_exp2(__builtin_fmaf(s[t][r], c, -ref));
+                        s[t][r] = !decltype(masked)::value || sight.sees(d0, 32 * t + 8 * (r / 4) + r % 4) ? p : 0.f;
+                        w.sum += s[t][r];
+                    }
+            };
+            if (whole) exponentials(IntC<0>{});
+            else exponentials(IntC<1>{});
             // bf16: probabilities are rounded to nearest for the product with the values (relative 2^-9 each, of
             // independent signs); their sum is not
 #pragma unroll
@@ -110,14 +116,14 @@ struct AttnFwd {
                 if (!CAREFUL || whole) {
 #pragma unroll
                     for (int t = 0; t < kParts; ++t)
-                        w.o[t] = T::mma(Tile::across(lds.v[buf], 16 * kb, 32 * t, lane), p, w.o[t]);
+                        w.o[t] = T::mma(Tile::across(lds.v[buf], l, 16 * kb, t), p, w.o[t]);
                 } else {
                     for (int key = 0; key < 16; ++key) {   // slot s of half h holds key 4 h + s % 4 + 2 (s & 4)
                         const int slot = (key >> 2 & 1) == h ? (key & 3) + (key >> 1 & 4) : -1;
                         const bool seen = sight.sees(at, j + 16 * kb + key);
 #pragma unroll
                         for (int t = 0; t < kParts; ++t) {
-                            const f32x16 x = T::mma(T::only(Tile::across(lds.v[buf], 16 * kb, 32 * t, lane), slot),
+                            const f32x16 x = T::mma(T::only(Tile::across(lds.v[buf], l, 16 * kb, t), slot),
                                                     T::only(p, slot), zero16());
 #pragma unroll
                             for (int r = 0; r < 16; ++r) w.o[t][r] += seen ? x[r] : 0.f;
@@ -125,6 +131,10 @@ struct AttnFwd {
                     }
                 }
             }
+        };
+        for (int32_t j = begin; j < end; j += 2 * kKeys) {
+            tile(IntC<0>{}, j);
+            if (j + kKeys < end) tile(IntC<1>{}, j + kKeys);
         }
     }
 };

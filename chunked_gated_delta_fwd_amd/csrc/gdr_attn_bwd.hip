@@ -41,7 +41,7 @@ struct AttnDq {
         const int32_t lo = i0 + 32 * wave, at = sight.at(lo + col);
 #pragma unroll
         for (int t = 0; t < kParts; ++t) w.dq[t] = zero16();
-        int buf = 0;
+        const typename Tile::Lane places = Tile::lane_places(lane);
         auto load = [&](int32_t j, int b) {
             Tile::load(fk, reinterpret_cast<const E *>(reinterpret_cast<const char *>(k) + static_cast<int64_t>(j) * step_k),
                        step_k, lk - j, lds.k[b], wave);
@@ -49,28 +49,34 @@ struct AttnDq {
                        step_v, lk - j, lds.v[b], wave);
         };
         if (begin < end) load(begin, 0);
-        for (int32_t j = begin; j < end; j += kKeys, buf ^= 1) {
+        const auto tile = [&](auto which, int32_t j) {
+            constexpr int buf = decltype(which)::value;
+            const typename Tile::Lane l = attn_here(places);
             loads_landed();
             __syncthreads();
             if (j + kKeys < end) load(j + kKeys, buf ^ 1);
             const int32_t hi = lo + 31 < i1 ? lo + 31 : i1;
-            if (lo > i1) continue;
+            if (lo > i1) return;
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
                 const int32_t ju = j + 32 * u;
                 if (!sight.any(lo, hi, ju, 32)) continue;
                 f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) s = T::mma(Tile::rows(lds.k[buf], 32 * u, ks, col, h), w.q[ks], s);
+                for (int ks = 0; ks < kSteps; ++ks) s = T::mma(Tile::rows(lds.k[buf], l, 32 * u, ks), w.q[ks], s);
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) dp = T::mma(Tile::rows(lds.v[buf], 32 * u, ks, col, h), w.dout[ks], dp);
+                for (int ks = 0; ks < kSteps; ++ks) dp = T::mma(Tile::rows(lds.v[buf], l, 32 * u, ks), w.dout[ks], dp);
                 const bool whole = sight.all(lo, hi, ju, 32);
                 const int32_t d0 = at - ju - 4 * h;
+                const auto scores = [&](auto masked) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float p = fast_exp2(__builtin_fmaf(s[r], c, -w.lse));
-                    s[r] = whole || sight.sees(d0, 8 * (r / 4) + r % 4) ? p * (dp[r] - w.delta) : 0.f;
-                }
+                    for (int r = 0; r < 16; ++r) {
+                        const float p = fast_exp2(__builtin_fmaf(s[r], c, -w.lse)), ds = p * (dp[r] - w.delta);
+                        s[r] = !decltype(masked)::value || sight.sees(d0, 8 * (r / 4) + r % 4) ? ds : 0.f;
+                    }
+                };
+                if (whole) scores(IntC<0>{});
+                else scores(IntC<1>{});
                 // bf16: ds is rounded to nearest for the product with the keys
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
@@ -78,7 +84,7 @@ struct AttnDq {
                     if (!CAREFUL || whole) {
 #pragma unroll
                         for (int t = 0; t < kParts; ++t)
-                            w.dq[t] = T::mma(Tile::across(lds.k[buf], 32 * u + 16 * kb, 32 * t, lane), ds, w.dq[t]);
+                            w.dq[t] = T::mma(Tile::across(lds.k[buf], l, 32 * u + 16 * kb, t), ds, w.dq[t]);
                     } else {
                         for (int key = 0; key < 16; ++key) {
                             const int slot = (key >> 2 & 1) == h ? (key & 3) + (key >> 1 & 4) : -1;
@@ -86,7 +92,7 @@ struct AttnDq {
 #pragma unroll
                             for (int t = 0; t < kParts; ++t) {
                                 const f32x16 x =
-                                    T::mma(T::only(Tile::across(lds.k[buf], 32 * u + 16 * kb, 32 * t, lane), slot),
+                                    T::mma(T::only(Tile::across(lds.k[buf], l, 32 * u + 16 * kb, t), slot),
                                            T::only(ds, slot), zero16());
 #pragma unroll
                                 for (int r = 0; r < 16; ++r) w.dq[t][r] += seen ? x[r] : 0.f;
@@ -95,6 +101,10 @@ struct AttnDq {
                     }
                 }
             }
+        };
+        for (int32_t j = begin; j < end; j += 2 * kKeys) {
+            tile(IntC<0>{}, j);
+            if (j + kKeys < end) tile(IntC<1>{}, j + kKeys);
         }
     }
 };
@@ -185,21 +195,24 @@ struct AttnDkv {
     static constexpr int kQueries = 32;
     typedef AttnTile<T, D, kQueries> Tile;
     static constexpr int kSteps = D / 16, kParts = D / 32;
+    typedef AttnTile<T, D, kAttnRows> Values;
     struct Lds {
+        alignas(16) float lse[2][64], delta[2][64];   // a load of a wave each, half of it used
         alignas(16) char q[2][Tile::kBytes];
         alignas(16) char dout[2][Tile::kBytes];
-        alignas(16) float lse[2][64], delta[2][64];   // a load of a wave each, half of it used
+        alignas(16) char v[Values::kBytes];           // the block's values, which registers have no room for
     };
     struct Row {
-        F8 k[kSteps], v[kSteps];
+        F8 k[kSteps];
         f32x16 dk[kParts], dv[kParts];   // transposed: channels x keys
     };
     struct Where {
         const E *q, *dout;               // first row of the sequence, first head of the part
+        const E *v;                      // the block's first key
         const float *lse, *delta;
         int64_t total;                   // between two heads' lse
-        uint32_t step_q, step_do;
-        int32_t heads, lq;
+        uint32_t step_q, step_do, step_v;
+        int32_t heads, lq, keys;          // keys: from the block's first to the sequence's last
     };
 
     // CAREFUL: a query or output gradient that is not finite reaches the keys that its row sees and no other.
@@ -212,6 +225,7 @@ struct AttnDkv {
 #pragma unroll
         for (int t = 0; t < kParts; ++t) w.dk[t] = w.dv[t] = zero16();
         if (begin >= end) return;
+        Values::load(Values::from(wave, lane, from.step_v), from.v, from.step_v, from.keys, lds.v, wave);
         auto load = [&](int head, int32_t i, int b) {
             const int32_t rows = from.lq - i;
             Tile::load(fq, reinterpret_cast<const E *>(reinterpret_cast<const char *>(from.q + head * D) +
@@ -224,9 +238,13 @@ struct AttnDkv {
             }
         };
         load(0, begin, 0);
-        int buf = 0;
+        const typename Tile::Lane places = Tile::lane_places(lane);
+        const typename Tile::Lane own{places.along + 32 * wave * Tile::kRow, 4 * h * 4u};   // values; statistics
         int32_t i = begin, head = 0;
-        while (true) {
+        // one tile of queries; returns whether there is a next one
+        const auto tile = [&](auto which) {
+            constexpr int buf = decltype(which)::value;
+            const typename Tile::Lane l = attn_here(places), mine = attn_here(own);
             int32_t next = i + kQueries, nhead = head;
             if (next >= end) next = begin, ++nhead;
             loads_landed();
@@ -236,22 +254,30 @@ struct AttnDkv {
             if (lo <= j1 && sight.any(i, last, lo, 32)) {
                 f32x16 p = zero16(), dp = zero16();
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) p = T::mma(Tile::rows(lds.q[buf], 0, ks, col, h), w.k[ks], p);
+                for (int ks = 0; ks < kSteps; ++ks) p = T::mma(Tile::rows(lds.q[buf], l, 0, ks), w.k[ks], p);
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) dp = T::mma(Tile::rows(lds.dout[buf], 0, ks, col, h), w.v[ks], dp);
+                for (int ks = 0; ks < kSteps; ++ks) 
+                    dp = T::mma(Tile::rows(lds.dout[buf], l, 0, ks), Tile::rows(lds.v, mine, 0, ks), dp);
                 const bool whole = sight.all(i, last, lo, 32);
+                __builtin_amdgcn_sched_barrier(0);   // rows' statistics wait: earlier they cost spilled operands
+                const char *stats = reinterpret_cast<const char *>(lds.lse[buf]) + mine.across;
+                const auto scores = [&](auto masked) {
 #pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    const f32x4 lse = *reinterpret_cast<const f32x4 *>(&lds.lse[buf][8 * r4 + 4 * h]);
-                    const f32x4 delta = *reinterpret_cast<const f32x4 *>(&lds.delta[buf][8 * r4 + 4 * h]);
+                    for (int r4 = 0; r4 < 4; ++r4) {
+                        const f32x4 lse = *reinterpret_cast<const f32x4 *>(stats + 32 * r4);
+                        const f32x4 delta = *reinterpret_cast<const f32x4 *>(stats + 32 * r4 + sizeof(lds.lse));
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int r = 4 * r4 + q;
-                        const bool seen = whole || sight.sees(sight.at(i + 8 * r4 + 4 * h + q), j);
-                        p[r] = seen ? fast_exp2(__builtin_fmaf(p[r], c, -lse[q])) : 0.f;
-                        dp[r] = seen ? p[r] * (dp[r] - delta[q]) : 0.f;
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = 4 * r4 + q;
+                            const float e = fast_exp2(__builtin_fmaf(p[r], c, -lse[q])), ds = e * (dp[r] - delta[q]);
+                            const bool seen = !decltype(masked)::value || sight.sees(sight.at(i + 8 * r4 + 4 * h + q), j);
+                            p[r] = seen ? e : 0.f;
+                            dp[r] = seen ? ds : 0.f;
+                        }
                     }
-                }
+                };
+                if (whole) scores(IntC<0>{});
+                else scores(IntC<1>{});
                 // bf16: p and ds are rounded to nearest for the products over the queries
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
@@ -259,8 +285,8 @@ struct AttnDkv {
                     if (!CAREFUL || whole) {
 #pragma unroll
                         for (int t = 0; t < kParts; ++t) {
-                            w.dv[t] = T::mma(Tile::across(lds.dout[buf], 16 * kb, 32 * t, lane), pp, w.dv[t]);
-                            w.dk[t] = T::mma(Tile::across(lds.q[buf], 16 * kb, 32 * t, lane), ds, w.dk[t]);
+                            w.dv[t] = T::mma(Tile::across(lds.dout[buf], l, 16 * kb, t), pp, w.dv[t]);
+                            w.dk[t] = T::mma(Tile::across(lds.q[buf], l, 16 * kb, t), ds, w.dk[t]);
                         }
                     } else {
                         for (int row = 0; row < 16; ++row) {
@@ -268,9 +294,9 @@ struct AttnDkv {
                             const bool seen = sight.sees(sight.at(i + 16 * kb + row), j);
 #pragma unroll
                             for (int t = 0; t < kParts; ++t) {
-                                const f32x16 x = T::mma(T::only(Tile::across(lds.dout[buf], 16 * kb, 32 * t, lane), slot),
+                                const f32x16 x = T::mma(T::only(Tile::across(lds.dout[buf], l, 16 * kb, t), slot),
                                                         T::only(pp, slot), zero16());
-                                const f32x16 y = T::mma(T::only(Tile::across(lds.q[buf], 16 * kb, 32 * t, lane), slot),
+                                const f32x16 y = T::mma(T::only(Tile::across(lds.q[buf], l, 16 * kb, t), slot),
                                                         T::only(ds, slot), zero16());
 #pragma unroll
                                 for (int r = 0; r < 16; ++r) {
@@ -282,10 +308,11 @@ struct AttnDkv {
                     }
                 }
             }
-            if (nhead >= from.heads) break;
             i = next;
             head = nhead;
-            buf ^= 1;
+            return head < from.heads;
+        };
+        while (tile(IntC<0>{}) && tile(IntC<1>{})) {
         }
     }
 };
@@ -303,8 +330,9 @@ __device__ __forceinline__ bool attn_dkv_block(const AttnArgs &a, uint32_t tiles
     const int32_t n = a.cu ? attn_find(cuk, static_cast<int32_t>(a.n_seq), a.total_k, item.tile, lane) : item.pair / a.hk;
     const int hk = item.pair % a.hk;
     const AttnSeq seq = attn_seq(a, n);
-    const int64_t tile = a.cu ? item.tile - (attn_clamp(cuk[n], 0, a.total_k) / kAttnRows + n) : item.tile;
+    int64_t tile = a.cu ? item.tile - (attn_clamp(cuk[n], 0, a.total_k) / kAttnRows + n) : item.tile;
     if (tile < 0 || tile * kAttnRows >= seq.lk) return false;
+    tile = (seq.lk - 1) / kAttnRows - tile;   // early keys first: causal ones are seen by the most queries
     const AttnSight sight(a, seq);
     const int32_t j0 = static_cast<int32_t>(tile * kAttnRows);
     const int32_t j1 = j0 + kAttnRows < seq.lk ? j0 + kAttnRows - 1 : seq.lk - 1;
@@ -328,18 +356,18 @@ __device__ __forceinline__ bool attn_dkv_block(const AttnArgs &a, uint32_t tiles
     from.total = a.total_q;
     from.step_q = static_cast<uint32_t>(a.ldq * sizeof(E));
     from.step_do = static_cast<uint32_t>(a.lddo * sizeof(E));
+    from.v = static_cast<const E *>(a.v) + (seq.k0 + j0) * a.ldv + static_cast<int64_t>(hk) * D;
+    from.step_v = static_cast<uint32_t>(a.ldv * sizeof(E));
     from.heads = heads;
     from.lq = seq.lq;
+    from.keys = seq.lk - j0;
     typename F::Row w;
     {
         const int64_t row = seq.k0 + (j0 + 32 * wave + col < seq.lk ? j0 + 32 * wave + col : seq.lk - 1);
         const int64_t head = static_cast<int64_t>(hk) * D + 8 * h;
-        const E *k = static_cast<const E *>(a.k) + row * a.ldk + head, *v = static_cast<const E *>(a.v) + row * a.ldv + head;
+        const E *k = static_cast<const E *>(a.k) + row * a.ldk + head;
 #pragma unroll
-        for (int ks = 0; ks < F::kSteps; ++ks) {
-            w.k[ks] = T::load(k + 16 * ks);
-            w.v[ks] = T::load(v + 16 * ks);
-        }
+        for (int ks = 0; ks < F::kSteps; ++ks) w.k[ks] = T::load(k + 16 * ks);
     }
     const float c = a.scale * kLog2e;
     const int32_t b = static_cast<int32_t>(begin), e = static_cast<int32_t>(end);

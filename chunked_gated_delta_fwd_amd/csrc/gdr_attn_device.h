@@ -167,34 +167,58 @@ struct AttnTile {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) lds_load16(rsrc, f.off[i % kWays] + i * f.hop, to + i * kWaves * 1024);
     }
-    // Operand along rows: row r0 + c, elements 16 ks + 8 h .., natural order.
-    static __device__ __forceinline__ F8 rows(const char *tile, int r0, int ks, int c, int h) {
+    // Places that a lane reads, from which those of other steps differ by an exclusive or: kept apart from
+    // the loop over the tiles (attn_here), so that registers hold these two and not all of them.
+    struct Lane {
+        uint32_t along, across;
+    };
+    static __device__ __forceinline__ Lane lane_places(int lane) {
+        const int c = lane & 31, h = lane >> 5;
+        Lane l;
         if constexpr (T::kBf16) {
-            return *reinterpret_cast<const F8 *>(tile + place(r0 + c, 2 * ks + h));
+            const int j = lane & 15, r = 4 * h + (j >> 2);
+            l.along = place(c, h);
+            l.across = place(r, (lane >> 3 & 2) | (j >> 1 & 1)) + (j & 1) * 8;
         } else {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + place(r0 + c, 4 * ks + 2 * h));
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + place(r0 + c, 4 * ks + 2 * h + 1));
+            l.along = place(c, 2 * h);
+            l.across = place(4 * h, c >> 2) + (c & 3) * 4;
+        }
+        return l;
+    }
+    // Operand along rows: row r0 + c (r0 a multiple of 32), elements 16 ks + 8 h .., natural order.
+    static __device__ __forceinline__ F8 rows(const char *tile, const Lane &l, int r0, int ks) {
+        if constexpr (T::kBf16) {
+            return *reinterpret_cast<const F8 *>(tile + (l.along ^ (ks * 32)) + r0 * kRow);
+        } else {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + (l.along ^ (ks * 64)) + r0 * kRow);
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + (l.along ^ (ks * 64 + 16)) + r0 * kRow);
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
-    // Operand across rows: element x0 + c of the rows r0 .. r0 + 15, result order.
-    static __device__ __forceinline__ F8 across(const char *tile, int r0, int x0, int lane) {
-        const int h = lane >> 5;
+    // Operand across rows: element 32 t + c of the rows r0 .. r0 + 15 (r0 a multiple of 16), result order.
+    static __device__ __forceinline__ F8 across(const char *tile, const Lane &l, int r0, int t) {
         if constexpr (T::kBf16) {
-            const int j = lane & 15, r = r0 + 4 * h + (j >> 2), x = x0 + (lane & 16) + 4 * (j & 3);
-            const int e = (x & 7) * 2;
-            return cat(ld4_tr(reinterpret_cast<const uint16_t *>(tile + place(r, x >> 3) + e)),
-                       ld4_tr(reinterpret_cast<const uint16_t *>(tile + place(r + 8, x >> 3) + e)));
+            // turn(r + 8) is turn(r) ^ 2
+            return cat(ld4_tr(reinterpret_cast<const uint16_t *>(tile + (l.across ^ (t * 64)) + r0 * kRow)),
+                       ld4_tr(reinterpret_cast<const uint16_t *>(tile + (l.across ^ (t * 64 + 32)) + (r0 + 8) * kRow)));
         } else {
+            static_assert(T::kBf16 || kPieces >= 16);
             F8 v;
-            const int x = x0 + (lane & 31);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-                v[s] = *reinterpret_cast<const float *>(tile + place(r0 + 4 * h + (s & 3) + 2 * (s & 4), x >> 2) + (x & 3) * 4);
+            for (int s = 0; s < 8; ++s)   // row 4 h + s % 4 + 2 (s & 4)
+                v[s] = *reinterpret_cast<const float *>(tile + (l.across ^ (t * 128) ^ ((s & 3) * 64 + (s >> 2) * 32)) +
+                                                        (r0 + (s & 3) + 2 * (s & 4)) * kRow);
             return v;
         }
     }
 };
+
+// The same value, which the compiler takes for a new one.
+template <class L>
+__device__ __forceinline__ L attn_here(L l) {
+    asm volatile("" : "+v"(l.along), "+v"(l.across));
+    return l;
+}
 
 // 32 channels of a lane's row (a transposed result tile), scaled by f, to
 // `row`: bf16 in 16-byte pieces, for which the halves swap a register pair.

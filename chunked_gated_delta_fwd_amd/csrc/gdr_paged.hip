@@ -75,6 +75,7 @@ __global__ __launch_bounds__(64, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(Pa
             if (r >= 0) vreg[i] = *reinterpret_cast<const v4u32 *>(vbase + r * row_step + at % kRow);
         }
     };
+    const typename Tile::Lane places = Tile::lane_places(lane);
     f32x16 o[kParts];
 #pragma unroll
     for (int t = 0; t < kParts; ++t) o[t] = zero16();
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(64, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(Pa
             for (int kb = 0; kb < 2; ++kb) {
                 const F8 p = T::part(s, kb);
 #pragma unroll
-                for (int t = 0; t < kParts; ++t) o[t] = T::mma(Tile::across(vals, 16 * kb, 32 * t, lane), p, o[t]);
+                for (int t = 0; t < kParts; ++t) o[t] = T::mma(Tile::across(vals, places, 16 * kb, t), p, o[t]);
             }
         }
     }
