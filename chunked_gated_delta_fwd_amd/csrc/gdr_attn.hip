@@ -207,7 +207,7 @@ __device__ __attribute__((noinline)) void attn_fwd_careful(AttnArgsAt at, uint32
 }
 
 template <class T, int D>
-__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_fwd_kernel(AttnArgs a, uint32_t tiles) {
+__global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_attn_fwd_kernel(AttnArgs a, uint32_t tiles) {
     __shared__ typename AttnFwd<T, D>::Lds lds;
     if (attn_fwd_block<T, D, false>(a, tiles, lds)) attn_fwd_careful<T, D>(attn_args_at(), tiles, &lds);
 }

@@ -181,7 +181,7 @@ __device__ __attribute__((noinline)) void attn_dq_careful(AttnArgsAt at, uint32_
 }
 
 template <class T, int D>
-__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dq_kernel(AttnArgs a, uint32_t tiles) {
+__global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_attn_dq_kernel(AttnArgs a, uint32_t tiles) {
     __shared__ typename AttnDq<T, D>::Lds lds;
     if (attn_dq_block<T, D, false>(a, tiles, lds)) attn_dq_careful<T, D>(attn_args_at(), tiles, &lds);
 }

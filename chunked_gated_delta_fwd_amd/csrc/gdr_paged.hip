@@ -7,26 +7,32 @@ namespace {
 
 // --- one token over the cache ---------------------------------------------------------
 
-// A wave takes a chunk of one sequence's keys and one key head with its group
-// of query heads (32 at most), in tiles of 32 keys.  Keys go from memory to the
-// matrix operand, values through 32 rows of LDS of the wave's own that are read
-// transposed.  The next tile's loads start once this one's keys are multiplied
-// and its values are in LDS.
+// A block takes a chunk of one sequence's keys and one key head with its group
+// of query heads (32 at most), a quarter a wave, in tiles of 32 keys.  Keys go
+// from memory to the matrix operand, values through 32 rows of LDS of the
+// wave's own that are read transposed.  The next tile's loads start once this
+// one's keys are multiplied and its values are in LDS.  The waves' sums are
+// joined in LDS, the blocks' by a second kernel.
 template <class T, int D>
-__global__ __launch_bounds__(64, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(PagedArgs a) {
+__global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(PagedArgs a) {
     typedef typename T::E E;
     typedef typename T::F8 F8;
     typedef AttnTile<T, D, 32> Tile;
     constexpr int kSteps = D / 16, kParts = D / 32, kRow = D * sizeof(E), kLoads = 32 * kRow / 1024;
-    __shared__ alignas(16) char vals[32 * kRow];
-    const int lane = threadIdx.x, col = lane & 31, h = lane >> 5;
-    const int group = a.hq / a.hk, blocks = (group + 31) / 32;
-    int64_t item = blockIdx.x;
-    const int64_t split = item % a.splits;
-    item /= a.splits;
-    const int head0 = static_cast<int>(item % blocks) * 32;
+    __shared__ union {
+        alignas(16) char vals[4][32 * kRow];
+        float o[4][kParts][16][64];
+    } lds;
+    __shared__ float refs[4][32], sums[4][32];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
+    char *vals = lds.vals[wave];
+    const uint32_t group = a.hq / a.hk, blocks = (group + 31) / 32, splits = static_cast<uint32_t>(a.splits);
+    uint32_t item = blockIdx.x;
+    const int64_t split = item % splits;
+    item /= splits;
+    const uint32_t head0 = item % blocks * 32;
     item /= blocks;
-    const int hk = static_cast<int>(item % a.hk);
+    const int hk = item % a.hk;
     const int64_t n = item / a.hk;
 
     int64_t len = a.lens[n];
@@ -34,9 +40,11 @@ __global__ __launch_bounds__(64, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(Pa
     const int64_t first = a.window > 0 && len > a.window ? len - a.window : 0;
     const int64_t begin64 = first + split * a.chunk, end64 = begin64 + a.chunk < len ? begin64 + a.chunk : len;
     if (begin64 >= end64 && split > 0) return;   // the first chunk of no keys writes zeros
-    const int32_t begin = static_cast<int32_t>(begin64), end = static_cast<int32_t>(end64);
+    const int32_t share = begin64 < end64 ? static_cast<int32_t>((end64 - begin64 + 127) / 128 * 32) : 0;
+    const int32_t begin = static_cast<int32_t>(begin64) + wave * share;
+    const int32_t end = begin + share < end64 ? begin + share : static_cast<int32_t>(end64);
 
-    const int head = head0 + col < group ? head0 + col : group - 1;
+    const uint32_t head = head0 + col < group ? head0 + col : group - 1;
     const float c0 = a.scale * kLog2e, c = __builtin_fabsf(c0);
     F8 q[kSteps];
     {
@@ -133,19 +141,36 @@ __global__ __launch_bounds__(64, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(Pa
         }
     }
     sum = half_sum(sum);
-    if (head0 + col >= group) return;
+    if (h == 0) {
+        refs[wave][col] = ref;
+        sums[wave][col] = sum;
+    }
+    __syncthreads();   // every wave is done with its values too: o takes their place
+    const float top = fmaxf(fmaxf(refs[0][col], refs[1][col]), fmaxf(refs[2][col], refs[3][col]));
+    const float base = top == -__builtin_inff() ? 0.f : top;
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) total = __builtin_fmaf(fast_exp2(refs[w][col] - base), sums[w][col], total);
+    const float f = fast_exp2(ref - base);
+#pragma unroll
+    for (int t = 0; t < kParts; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) lds.o[wave][t][r][lane] = o[t][r] * f;
+    __syncthreads();
+    if (wave >= kParts || head0 + col >= group) return;
+    f32x16 x;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        x[r] = (lds.o[0][wave][r][lane] + lds.o[1][wave][r][lane]) + (lds.o[2][wave][r][lane] + lds.o[3][wave][r][lane]);
     const int64_t out = n * a.hq + static_cast<int64_t>(hk) * group + head;
-    if (a.splits == 1) {
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-        for (int t = 0; t < kParts; ++t) attn_store<T>(static_cast<E *>(a.o) + out * D + 32 * t, o[t], f, h);
+    if (splits == 1) {
+        attn_store<T>(static_cast<E *>(a.o) + out * D + 32 * wave, x, total == 0.f ? 0.f : 1.f / total, h);
     } else {
-        const int64_t at = out * a.splits + split;
-#pragma unroll
-        for (int t = 0; t < kParts; ++t) attn_store<AttnF32>(a.part + at * D + 32 * t, o[t], 1.f, h);
-        if (h == 0) {
-            a.stat[2 * at] = ref;
-            a.stat[2 * at + 1] = sum;
+        const int64_t at = out * splits + split;
+        attn_store<AttnF32>(a.part + at * D + 32 * wave, x, 1.f, h);
+        if (h == 0 && wave == 0) {
+            a.stat[2 * at] = top;
+            a.stat[2 * at + 1] = total;
         }
     }
 }
@@ -196,7 +221,7 @@ hipError_t run_step(const PagedArgs &a, hipStream_t stream) {
     const int64_t group = a.hq / a.hk, grid = a.n_seq * a.hk * ((group + 31) / 32) * a.splits;
     const int64_t join = a.n_seq * a.hq * (a.d / 32);
     if (grid > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
-    gdr_paged_step_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 64, 0, stream>>>(a);
+    gdr_paged_step_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a);
     if (a.splits > 1) gdr_paged_join_kernel<T><<<dim3(static_cast<unsigned>(join)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -292,15 +317,16 @@ __global__ __launch_bounds__(256) void gdr_page_plan_kernel(PlanArgs a, int64_t 
 
 }  // namespace
 
-// Chunks of a multiple of 32 keys, 64 at least, of which the sequences at their
-// longest have about 4096 together: two for each wave that the chip holds.
+// Chunks of a multiple of 128 keys, kLeastChunk at least, of which the sequences
+// at their longest have about 1024 together: two for each block that the chip holds.
+constexpr int64_t kLeastChunk = 512;
 void paged_split(PagedArgs &a) {
     int64_t keys = a.width * a.page;
     if (a.window > 0 && keys > a.window) keys = a.window;
     if (keys < 1) keys = 1;
     const int64_t rows = a.n_seq * a.hk * ((a.hq / a.hk + 31) / 32);
-    int64_t chunk = (rows * keys / 4096 + 31) / 32 * 32;
-    if (chunk < 64) chunk = 64;
+    int64_t chunk = (rows * keys / 1024 + 127) / 128 * 128;
+    if (chunk < kLeastChunk) chunk = kLeastChunk;
     if (chunk > 1 << 20) chunk = 1 << 20;
     a.chunk = static_cast<int32_t>(chunk);
     a.splits = (keys + chunk - 1) / chunk;
