@@ -124,7 +124,7 @@ def library(path: Optional[str] = None):
     lib.gdr_ssm_scan_fwd.argtypes = [P] * 14
     lib.gdr_ssm_scan_bwd.argtypes = [P] * 22
     lib.gdr_ssm_step.argtypes = [P] * 10
-    lib.gdr_attn_fwd.argtypes = [P] * 7 + [ctypes.c_int, ctypes.c_int64, ctypes.c_float, P]
+    lib.gdr_attn_fwd.argtypes = [P] * 7 + [ctypes.c_int, ctypes.c_int64, ctypes.c_float, P, P, P]
     lib.gdr_attn_bwd.argtypes = [P] * 11 + [ctypes.c_int, ctypes.c_int64, ctypes.c_float, P, P, P]
     lib.gdr_attn_paged_step.argtypes = [P] * 6 + [ctypes.c_int64, ctypes.c_float, P, P, P]
     lib.gdr_page_plan.argtypes = [P] * 9 + [ctypes.c_int32, P]

@@ -20,6 +20,10 @@ struct AttnArgs {
     int32_t hq, hk, d, bf16, causal;
     int64_t window;              // keys that a query sees back from its own place, itself included; 0: all
     float scale;
+    // Forward: the keys of a block are split in `splits` runs at most, each of at least `least` tiles, whose
+    // outputs before they are scaled and whose reference and sum are joined by a second kernel.
+    int32_t splits, least;
+    float *run_o, *run_stat;     // [splits][total_q][hq][d], [splits][total_q][hq][2]; splits 1: none
     // backward
     const void *dout;            // rows lddo apart
     int64_t lddo;
@@ -28,6 +32,20 @@ struct AttnArgs {
     float *part;                 // [parts][2][total_k][hk][d]: sums of dk and dv over a part of a group; NULL: one part
     int32_t parts;
 };
+// How long a launch takes, in us, by a model: blocks go through the chip `slots`
+// at a time, and a step of one takes `full` where the CUs are full and `half`
+// where a block has one for itself; the longest block takes its own time.
+struct AttnCost {
+    double slots, full, half;
+};
+inline double attn_time(const AttnCost &c, double blocks, double mean_steps, double most_steps) {
+    const double rounds = static_cast<double>(static_cast<int64_t>(blocks / c.slots)), rest = blocks - rounds * c.slots;
+    const double last = rest > 256 ? c.full : rest > 0.5 ? c.half : 0;
+    const double all = (rounds * c.full + last) * mean_steps, longest = (blocks > 256 ? 0.85 * c.full : c.half) * most_steps;
+    return all > longest ? all : longest;
+}
+// Sets splits and least.
+void attn_split(AttnArgs &a);
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream);
 // How many blocks share the query heads of a group for the gradient of keys and values.
 int32_t attn_bwd_parts(const AttnArgs &a);

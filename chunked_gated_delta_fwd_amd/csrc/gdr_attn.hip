@@ -139,6 +139,46 @@ struct AttnFwd {
     }
 };
 
+__device__ __forceinline__ float attn_lse(float ref, float sum) {
+    return sum == 0.f ? -__builtin_inff() : (ref + __builtin_log2f(sum)) * 0.69314718055994530942f;
+}
+
+// The run of key tiles that one of a block's splits walks, of `count` in all.
+struct AttnRun {
+    int32_t first, last, count;   // tiles first .. last - 1; count: runs that hold any
+};
+__device__ __forceinline__ AttnRun attn_run(const AttnArgs &a, int32_t tiles, int32_t split) {
+    const int32_t even = (tiles + a.splits - 1) / a.splits, share = even > a.least ? even : a.least;
+    AttnRun r;
+    r.count = tiles > share ? (tiles + share - 1) / share : 1;
+    r.first = split * share;
+    r.last = r.first + share < tiles ? r.first + share : tiles;
+    return r;
+}
+
+// A block's rows, and which keys some of them sees, from a whole tile on.
+struct AttnBlock {
+    AttnSeq seq;
+    int32_t hk, hq, i0, i1, begin, end;   // rows i0 .. i1
+};
+template <int KEYS>
+__device__ __forceinline__ bool attn_block(const AttnArgs &a, const AttnItem &item, int lane, AttnBlock &b) {
+    if (item.tile < 0) return false;
+    const int32_t n = a.cu ? attn_find(a.cu, static_cast<int32_t>(a.n_seq), a.total_q, item.tile, lane) : item.pair / a.hk;
+    b.hk = item.pair % a.hk;
+    b.hq = b.hk * (a.hq / a.hk) + item.way;
+    b.seq = attn_seq(a, n);
+    const int64_t tile = a.cu ? item.tile - (attn_clamp(a.cu[n], 0, a.total_q) / kAttnRows + n) : item.tile;
+    if (tile < 0 || tile * kAttnRows >= b.seq.lq) return false;
+    const AttnSight sight(a, b.seq);
+    b.i0 = static_cast<int32_t>(tile * kAttnRows);
+    b.i1 = b.i0 + kAttnRows < b.seq.lq ? b.i0 + kAttnRows - 1 : b.seq.lq - 1;
+    const int64_t first = static_cast<int64_t>(sight.at(b.i0)) - sight.back + 1;
+    b.begin = first > 0 ? static_cast<int32_t>(first) / KEYS * KEYS : 0;
+    b.end = sight.at(b.i1) + 1 < b.seq.lk ? sight.at(b.i1) + 1 : b.seq.lk;
+    return true;
+}
+
 // A block's rows.  Returns, for every wave alike, whether some output is not
 // finite and the rows have to be done again with care.
 template <class T, int D, bool CAREFUL>
@@ -147,23 +187,24 @@ __device__ __forceinline__ bool attn_fwd_block(const AttnArgs &a, uint32_t tiles
     typedef typename T::E E;
     typedef typename T::F8 F8;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
-    const int group = a.hq / a.hk;
-    const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk;
-    const AttnItem item = attn_item(blockIdx.x, pairs, tiles, group);
-    if (item.tile < 0) return false;
-    const int32_t n = a.cu ? attn_find(a.cu, static_cast<int32_t>(a.n_seq), a.total_q, item.tile, lane) : item.pair / a.hk;
-    const int hk = item.pair % a.hk, hq = hk * group + item.way;
-    const AttnSeq seq = attn_seq(a, n);
-    const int64_t tile = a.cu ? item.tile - (attn_clamp(a.cu[n], 0, a.total_q) / kAttnRows + n) : item.tile;
-    if (tile < 0 || tile * kAttnRows >= seq.lq) return false;
+    const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
+    AttnItem item = attn_item(blockIdx.x, pairs, tiles, group * a.splits);
+    const int32_t split = item.way / group;
+    item.way %= group;
+    AttnBlock b;
+    if (!attn_block<F::kKeys>(a, item, lane, b)) return false;
+    const AttnSeq &seq = b.seq;
     const AttnSight sight(a, seq);
-    const int32_t i0 = static_cast<int32_t>(tile * kAttnRows);
-    const int32_t i1 = i0 + kAttnRows < seq.lq ? i0 + kAttnRows - 1 : seq.lq - 1;   // last row
-
-    // keys that some row of the block sees, from a whole tile on
-    const int64_t first = static_cast<int64_t>(sight.at(i0)) - sight.back + 1;
-    const int32_t begin = first > 0 ? static_cast<int32_t>(first) / F::kKeys * F::kKeys : 0;
-    const int32_t end = sight.at(i1) + 1 < seq.lk ? sight.at(i1) + 1 : seq.lk;
+    const int32_t i0 = b.i0, i1 = b.i1, hk = b.hk, hq = b.hq;
+    int32_t begin = b.begin, end = b.end;
+    bool alone = true;
+    if (a.splits > 1) {
+        const AttnRun run = attn_run(a, begin < end ? (end - begin + F::kKeys - 1) / F::kKeys : 0, split);
+        if (split >= run.count) return false;
+        alone = run.count == 1;
+        end = begin + run.last * F::kKeys < end ? begin + run.last * F::kKeys : end;
+        begin += run.first * F::kKeys;
+    }
 
     const float c = a.scale * kLog2e;
     typename F::Row w;
@@ -187,15 +228,23 @@ __device__ __forceinline__ bool attn_fwd_block(const AttnArgs &a, uint32_t tiles
         for (int r = 0; r < 16; ++r) x = __builtin_fmaf(w.o[t][r], 0.f, x);
     if (!CAREFUL && __syncthreads_or(x != 0.f)) return true;
     const int32_t i = i0 + 32 * wave + col;
-    // no key seen (or scores of -inf alone): 0, and NaN stays NaN
-    const float sum = half_sum(w.sum), inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (i < seq.lq) {
-        E *o = static_cast<E *>(a.o) + ((seq.q0 + i) * a.hq + hq) * D;
+    const float sum = half_sum(w.sum);
+    if (i >= seq.lq) return false;
+    const int64_t row = (seq.q0 + i) * a.hq + hq;
+    if (alone) {
+        // no key seen (or scores of -inf alone): 0, and NaN stays NaN
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int t = 0; t < F::kParts; ++t) attn_store<T>(o + 32 * t, w.o[t], inv, h);
-        if (a.lse && h == 0)
-            a.lse[(seq.q0 + i) * a.hq + hq] =
-                sum == 0.f ? -__builtin_inff() : (w.ref + __builtin_log2f(sum)) * 0.69314718055994530942f;
+        for (int t = 0; t < F::kParts; ++t) attn_store<T>(static_cast<E *>(a.o) + row * D + 32 * t, w.o[t], inv, h);
+        if (a.lse && h == 0) a.lse[row] = attn_lse(w.ref, sum);
+    } else {
+        const int64_t at = split * a.total_q * a.hq + row;
+#pragma unroll
+        for (int t = 0; t < F::kParts; ++t) attn_store<AttnF32>(a.run_o + at * D + 32 * t, w.o[t], 1.f, h);
+        if (h == 0) {
+            a.run_stat[2 * at] = w.ref;
+            a.run_stat[2 * at + 1] = sum;
+        }
     }
     return false;
 }
@@ -212,17 +261,83 @@ __global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_att
     if (attn_fwd_block<T, D, false>(a, tiles, lds)) attn_fwd_careful<T, D>(attn_args_at(), tiles, &lds);
 }
 
+// Joins a block's runs: 4 channels a thread, 8 rows (d 64: 16) at a time, the
+// rows shared by the blocks along y.
+template <class T, int D>
+__global__ __launch_bounds__(256) void gdr_attn_runs_kernel(AttnArgs a, uint32_t tiles) {
+    typedef typename T::E E;
+    constexpr int kThreads = D / 4;
+    const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
+    AttnBlock b;
+    if (!attn_block<AttnFwd<T, D>::kKeys>(a, attn_item(blockIdx.x, pairs, tiles, group), threadIdx.x & 63, b)) return;
+    constexpr int kKeys = AttnFwd<T, D>::kKeys;
+    const int32_t count = attn_run(a, b.begin < b.end ? (b.end - b.begin + kKeys - 1) / kKeys : 0, 0).count;
+    if (count == 1) return;
+    const int channel = threadIdx.x % kThreads * 4;
+    const int64_t step = a.total_q * a.hq;
+    for (int32_t i = b.i0 + (blockIdx.y * 256 + threadIdx.x) / kThreads; i <= b.i1; i += gridDim.y * 256 / kThreads) {
+        const int64_t row = (b.seq.q0 + i) * a.hq + b.hq;
+        float top = -__builtin_inff();
+#pragma unroll 4
+        for (int32_t s = 0; s < count; ++s) top = fmaxf(top, a.run_stat[2 * (s * step + row)]);
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        float total = 0.f;
+        f32x4 x = zero4();
+#pragma unroll 4
+        for (int32_t s = 0; s < count; ++s) {
+            const float f = fast_exp2(a.run_stat[2 * (s * step + row)] - base);
+            total = __builtin_fmaf(f, a.run_stat[2 * (s * step + row) + 1], total);
+            x += f * *reinterpret_cast<const f32x4 *>(a.run_o + (s * step + row) * D + channel);
+        }
+        x *= total == 0.f ? 0.f : 1.f / total;
+        E *o = static_cast<E *>(a.o) + row * D + channel;
+        if constexpr (T::kBf16) *reinterpret_cast<bf16x4 *>(o) = cvt4(x);
+        else *reinterpret_cast<f32x4 *>(o) = x;
+        if (a.lse && channel == 0) a.lse[row] = attn_lse(top, total);
+    }
+}
+
 template <class T, int D>
 hipError_t run(const AttnArgs &a, hipStream_t stream) {
     const int64_t tiles = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
-    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
-    const int64_t grid = attn_grid(pairs, tiles, a.hq / a.hk);
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
+    const int64_t grid = attn_grid(pairs, tiles, group * a.splits), join = attn_grid(pairs, tiles, group);
     if (grid > 0x7FFFFFFF || tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
     gdr_attn_fwd_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
+    if (a.splits > 1)
+        gdr_attn_runs_kernel<T, D><<<dim3(static_cast<unsigned>(join), D / 8), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
     return hipGetLastError();
 }
 
 }  // namespace
+
+// The runs that cost least by attn_time; a tile of keys as measured on large
+// calls.  Their outputs go through memory at 4 TB/s, the second launch takes 5 us.
+void attn_split(AttnArgs &a) {
+    const int32_t keys = a.bf16 ? 64 : 32;
+    const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{768, 1.95, 0.9} : AttnCost{512, 2.2, 1.35})
+                                 : (a.d == 64 ? AttnCost{256, 2.5, 2.5} : AttnCost{256, 5.0, 5.0});
+    const double seqs = a.n_seq > 0 ? static_cast<double>(a.n_seq) : 1.0;
+    const double lq = a.cu ? a.total_q / seqs : a.seq_q, lk = a.cu ? a.total_k / seqs : a.seq_k;
+    const double blocks = seqs * a.hq * (lq < kAttnRows ? 1.0 : lq / kAttnRows);
+    // keys that a block sees, at most and on average
+    double most = lk, mean = a.causal ? lk - (lq < lk ? lq : lk) / 2 : lk;
+    if (a.window > 0 && a.window + kAttnRows < most) most = a.window + kAttnRows;
+    if (mean > most) mean = most;
+    const double tiles = most / keys + 1;
+    double best = 0;
+    a.splits = 1;
+    a.least = 1;
+    for (int32_t s = 1; s <= 64 && (s == 1 || tiles / s >= 4); s += s < 4 ? 1 : s < 16 ? 2 : 8) {
+        double t = attn_time(cost, blocks * s, (mean / keys + 1) / s, tiles / s);
+        if (s > 1) t += 5 + 8.0 * a.total_q * a.hq * a.d * s / 4e6;
+        if (s == 1 || t < 0.95 * best) {
+            best = t;
+            a.splits = s;
+            a.least = static_cast<int32_t>(tiles / s + 0.999);
+        }
+    }
+}
 
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream) {
     if (a.bf16) return a.d == 64 ? run<AttnBf, 64>(a, stream) : run<AttnBf, 128>(a, stream);

@@ -104,7 +104,7 @@ extern "C" {
 
 int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v, const gdr_tensor *cu_seqlens,
                  const gdr_tensor *cu_seqlens_k, const gdr_tensor *o, const gdr_tensor *lse, int causal, int64_t window,
-                 float scale, hipStream_t stream) {
+                 float scale, void *workspace, int64_t *workspace_bytes, hipStream_t stream) {
     return entry([&]() -> int {
         AttnIn c{q, k, v, cu_seqlens, cu_seqlens_k, causal, window, scale};
         gdr::AttnArgs a;
@@ -120,12 +120,28 @@ int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v, 
         if ((rc = check_overlaps({{"q", c.sq}, {"k", c.sk}, {"v", c.sv}, {"cu_seqlens", c.scu}, {"cu_seqlens_k", c.scuk}},
                                  {{"o", span_of(o, no)}, {"lse", span_of(lse, nl)}})))
             return rc;
+        a.o = o->data;
+        a.lse = lse ? static_cast<float *>(lse->data) : nullptr;
+        gdr::attn_split(a);
+        Carve sizes{nullptr};
+        const auto carve = [&](Carve &w) {
+            const int64_t runs = a.splits > 1 ? a.splits * a.total_q * a.hq : 0;
+            a.run_o = w.take<float>(runs * a.d);
+            a.run_stat = w.take<float>(runs * 2);
+        };
+        carve(sizes);
+        if ((rc = Workspace::check(sizes.used, workspace, workspace_bytes))) return rc == 1 ? ok() : rc;
         if ((rc = check_device())) return rc;
         if ((rc = check_offsets(c, a, stream))) return rc;
         if (a.total_q == 0) return ok();
-        a.o = o->data;
-        a.lse = lse ? static_cast<float *>(lse->data) : nullptr;
-        return launch([&] { return gdr::launch_attn_fwd(a, stream); }, "attention kernel");
+        Workspace ws;
+        void *p;
+        if ((rc = ws.get(sizes.used, workspace, stream, &p))) return rc;
+        Carve parts{static_cast<unsigned char *>(p)};
+        carve(parts);
+        rc = launch([&] { return gdr::launch_attn_fwd(a, stream); }, "attention kernels");
+        const int rr = ws.release();
+        return rc ? rc : rr;
     });
 }
 

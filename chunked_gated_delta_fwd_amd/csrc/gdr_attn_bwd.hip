@@ -427,6 +427,7 @@ __global__ __launch_bounds__(256) void gdr_attn_join_kernel(AttnArgs a, uint32_t
 #pragma unroll
         for (int what = 0; what < 2; ++what) {
             f32x4 sum = zero4();
+#pragma unroll 4
             for (int p = 0; p < a.parts; ++p) sum += *reinterpret_cast<const f32x4 *>(a.part + (2 * p + what) * all + from + x);
             typename T::E *to = static_cast<typename T::E *>(what ? a.dv : a.dk) + from + x;
             if constexpr (T::kBf16) *reinterpret_cast<bf16x4 *>(to) = cvt4(sum);
@@ -446,7 +447,7 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
         gdr_attn_dkv_kernel<T, D><<<dim3(static_cast<unsigned>(grid_k)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
         if (a.part) {
             const int64_t blocks = tiles_k * (a.cu ? 1 : a.n_seq);
-            gdr_attn_join_kernel<T><<<dim3(static_cast<unsigned>(blocks), 8), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
+            gdr_attn_join_kernel<T><<<dim3(static_cast<unsigned>(blocks), 32), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
         }
     }
     return hipGetLastError();
@@ -454,12 +455,32 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// The parts that cost least by attn_time; a step is a tile of queries, as
+// measured on large calls.  Their sums go through memory at 4 TB/s, and joining
+// them takes 5 us more.
 int32_t attn_bwd_parts(const AttnArgs &a) {
-    const int64_t blocks = (a.cu ? 1 : a.n_seq) * a.hk * attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k);
+    const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{512, 1.1, 0.7} : AttnCost{512, 2.2, 1.35})
+                                 : (a.d == 64 ? AttnCost{256, 5.5, 5.5} : AttnCost{256, 11.0, 11.0});
     const int32_t group = a.hq / a.hk;
+    const double seqs = a.n_seq > 0 ? static_cast<double>(a.n_seq) : 1.0;
+    const double lq = a.cu ? a.total_q / seqs : a.seq_q, lk = a.cu ? a.total_k / seqs : a.seq_k;
+    const double blocks = seqs * a.hk * (lk < kAttnRows ? 1.0 : lk / kAttnRows);
+    // queries that see a block's keys, at most and on average
+    double most = lq, mean = a.causal ? lq - (lq < lk ? lq : lk) / 2 : lq;
+    if (a.window > 0 && a.window + kAttnRows < most) most = a.window + kAttnRows;
+    if (mean > most) mean = most;
+    double best = 0;
     int32_t parts = 1;
-    while (parts < group && blocks * parts < 1024) parts *= 2;
-    return parts < group ? parts : group;
+    for (int32_t p = 1; p <= group; p = p < group && 2 * p > group ? group : 2 * p) {
+        const double heads = static_cast<double>(group) / p;
+        double t = attn_time(cost, blocks * p, (mean / 32 + 1) * heads, (most / 32 + 1) * heads);
+        if (p > 1) t += 5 + 16.0 * a.total_k * a.hk * a.d * p / 4e6;
+        if (p == 1 || t < 0.95 * best) {
+            best = t;
+            parts = p;
+        }
+    }
+    return parts;
 }
 
 hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t stream) {

@@ -303,7 +303,7 @@ struct AttnItem {
     int32_t way;          // query head of the group, or part of it
 };
 __host__ __device__ inline int64_t attn_grid(int64_t pairs, int64_t tiles, int64_t ways) {
-    return pairs < 8 && 8 % pairs == 0 ? 8 * ways * ((tiles * pairs + 7) / 8) : pairs * tiles * ways;
+    return pairs < 8 && 8 % pairs == 0 ? 8 * ((tiles * ways * pairs + 7) / 8) : pairs * tiles * ways;
 }
 // All counts are below 2^31, as the grid is.
 __device__ __forceinline__ AttnItem attn_item(uint32_t block, uint32_t pairs, uint32_t tiles, uint32_t ways) {
@@ -315,10 +315,10 @@ __device__ __forceinline__ AttnItem attn_item(uint32_t block, uint32_t pairs, ui
         tile = head % tiles;
         t.pair = head / tiles * 8 + block % 8;
     } else if (8 % pairs == 0) {
-        const uint32_t at = block / 8, x = block % 8;
+        const uint32_t x = block % 8, at = block / 8 * (8 / pairs) + x / pairs;   // the XCDs of a pair in turn
         t.pair = x % pairs;
         t.way = at % ways;
-        tile = at / ways * (8 / pairs) + x / pairs;
+        tile = at / ways;
     } else {
         const uint32_t at = block / pairs;
         t.pair = block % pairs;

@@ -243,8 +243,11 @@ std::tuple<at::Tensor, Opt> attn_fwd(const at::Tensor &q, const at::Tensor &k, c
     at::Tensor o = given_or(o_, q.sizes(), q, q.scalar_type());
     Opt lse = lse_;
     if (!lse && want_lse) lse = empty({q.size(0), q.size(1), q.size(2)}, q, at::kFloat);
-    check(gdr_attn_fwd(Desc(q, c).p(), Desc(k, c).p(), Desc(v, c).p(), Desc(cu, c).p(), Desc(cuk, c).p(), Desc(o, c).p(),
-                       Desc(lse, c).p(), causal, window, scale_or(scale, q), c.stream()));
+    const Desc d[] = {Desc(q, c), Desc(k, c), Desc(v, c), Desc(cu, c), Desc(cuk, c), Desc(o, c), Desc(lse, c)};
+    with_workspace(c, [&](void *ws, int64_t *bytes) {
+        return gdr_attn_fwd(d[0].p(), d[1].p(), d[2].p(), d[3].p(), d[4].p(), d[5].p(), d[6].p(), causal, window,
+                            scale_or(scale, q), ws, bytes, c.stream());
+    });
     return {o, lse};
 }
 

@@ -532,14 +532,16 @@ int gdr_ssm_step(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
  * rounded to bf16 for the product with v, o is rounded once, lse is fp32.  f32
  * inputs: fp32 products throughout.  A k or v that is not finite reaches the
  * queries that see it and no others; a query whose scores are all -inf counts
- * as one that sees no key.  No workspace.  q, k, v rows and o on 16-byte
+ * as one that sees no key.  Where a call has few queries for its keys, the keys
+ * are split in runs; workspace then: 4 (d + 2) bytes a run, query and query
+ * head, else none.  q, k, v rows and o on 16-byte
  * addresses, rows at most 32 MiB apart, at most 2^30 tokens.  Errors as
  * gdr_chunk_fwd, GDR_EINVAL for a negative window or one without causal.
  */
 int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
                  const gdr_tensor *cu_seqlens, const gdr_tensor *cu_seqlens_k, const gdr_tensor *o,
                  const gdr_tensor *lse, int causal, int64_t window, float scale,
-                 hipStream_t stream);
+                 void *workspace, int64_t *workspace_bytes, hipStream_t stream);
 
 /*
  * gdr_attn_bwd - gradients of gdr_attn_fwd, from its o and lse.

@@ -72,14 +72,14 @@ FORWARD = [
 def test_forward_refusals(lib, change, status, text):  # noqa: F811
     d = fwd()
     change(d, Alloc2())
-    got = call(lib, "attn_fwd", list(d.values()), 1, 0, 1.0)
+    got = call(lib, "attn_fwd", list(d.values()), 1, 0, 1.0, None, None)
     assert got[0] == status and text in got[1], got
 
 
 @pytest.mark.parametrize("causal,window,scale,text", [
     (1, -1, 1.0, "window must not"), (0, 4, 1.0, "window needs"), (1, 0, float("nan"), "scale"), (1, 0, float("inf"), "scale")])
 def test_scalars(lib, causal, window, scale, text):  # noqa: F811
-    got = call(lib, "attn_fwd", list(fwd().values()), causal, window, scale)
+    got = call(lib, "attn_fwd", list(fwd().values()), causal, window, scale, None, None)
     assert got[0] == EINVAL and text in got[1], got
     got = call(lib, "attn_bwd", list(bwd().values()), causal, window, scale, None, None)
     assert got[0] == EINVAL and text in got[1], got
@@ -88,7 +88,7 @@ def test_scalars(lib, causal, window, scale, text):  # noqa: F811
 def test_tokens_of_a_call(lib):  # noqa: F811
     A, d = Alloc2(), fwd()
     d.update(q=A(BF, [1, 1 << 30, 1, D]), k=A(BF, [1, (1 << 30) + 1, 1, D]), v=A(BF, [1, (1 << 30) + 1, 1, D]))
-    got = call(lib, "attn_fwd", list(d.values()), 1, 0, 1.0)
+    got = call(lib, "attn_fwd", list(d.values()), 1, 0, 1.0, None, None)
     assert got[0] == ESHAPE and "2^30" in got[1], got
 
 
