@@ -73,8 +73,8 @@ struct AttnFwd {
                 for (int ks = 0; ks < kSteps; ++ks) s[t] = T::mma(Tile::rows(lds.k[buf], l, 32 * t, ks), w.q[ks], s[t]);
             }
             const bool whole = sight.all(lo, hi, j, kKeys);
-            const int32_t d0 = at - j - 4 * h;
             if (!whole) {
+                const int32_t d0 = attn_here(at - j - 4 * h);
 #pragma unroll
                 for (int t = 0; t < kSub; ++t)
 #pragma unroll
@@ -88,7 +88,7 @@ struct AttnFwd {
                 for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
             top = half_max(top) * c;
             if (__builtin_amdgcn_ballot_w64(top > w.ref + kSlack)) {
-                // c >= 0; a row that has seen no key keeps -inf, and a factor of 1 for its zeros
+                // a row that has seen no key keeps -inf, and a factor of 1 for its zeros
                 const float now = fmaxf(top, w.ref), f = now == w.ref ? 1.f : fast_exp2(w.ref - now);
                 w.ref = now;
                 w.sum *= f;
@@ -96,18 +96,15 @@ struct AttnFwd {
                 for (int t = 0; t < kParts; ++t) w.o[t] *= f;
             }
             const float ref = w.ref == -__builtin_inff() ? 0.f : w.ref;
-            const auto exponentials = [&](auto masked) {
+            float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int t = 0; t < kSub; ++t)
+            for (int t = 0; t < kSub; ++t)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float p = fast_exp2(__builtin_fmaf(s[t][r], c, -ref));
-                        s[t][r] = !decltype(masked)::value || sight.sees(d0, 32 * t + 8 * (r / 4) + r % 4) ? p : 0.f;
-                        w.sum += s[t][r];
-                    }
-            };
-            if (whole) exponentials(IntC<0>{});
-            else exponentials(IntC<1>{});
+                for (int r = 0; r < 16; ++r) {   // -inf gives 0: c is above zero
+                    s[t][r] = fast_exp2(__builtin_fmaf(s[t][r], c, -ref));
+                    sums[r % 4] += s[t][r];
+                }
+            w.sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
             // bf16: probabilities are rounded to nearest for the product with the values (relative 2^-9 each, of
             // independent signs); their sum is not
 #pragma unroll
@@ -220,7 +217,7 @@ __device__ __forceinline__ bool attn_fwd_block(const AttnArgs &a, uint32_t tiles
     const E *k = static_cast<const E *>(a.k) + seq.k0 * a.ldk + static_cast<int64_t>(hk) * D;
     const E *v = static_cast<const E *>(a.v) + seq.k0 * a.ldv + static_cast<int64_t>(hk) * D;
     const uint32_t step_k = static_cast<uint32_t>(a.ldk * sizeof(E)), step_v = static_cast<uint32_t>(a.ldv * sizeof(E));
-    F::template walk<CAREFUL>(w, sight, __builtin_fabsf(c), i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    F::template walk<CAREFUL>(w, sight, attn_positive(c), i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
     float x = 0.f;   // 0, or NaN where an output is not finite
 #pragma unroll
     for (int t = 0; t < F::kParts; ++t)

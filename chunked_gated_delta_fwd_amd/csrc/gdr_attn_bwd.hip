@@ -67,16 +67,14 @@ struct AttnDq {
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks) dp = T::mma(Tile::rows(lds.v[buf], l, 32 * u, ks), w.dout[ks], dp);
                 const bool whole = sight.all(lo, hi, ju, 32);
-                const int32_t d0 = at - ju - 4 * h;
-                const auto scores = [&](auto masked) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float p = fast_exp2(__builtin_fmaf(s[r], c, -w.lse)), ds = p * (dp[r] - w.delta);
-                        s[r] = !decltype(masked)::value || sight.sees(d0, 8 * (r / 4) + r % 4) ? ds : 0.f;
-                    }
-                };
-                if (whole) scores(IntC<0>{});
-                else scores(IntC<1>{});
+                for (int r = 0; r < 16; ++r) s[r] = fast_exp2(__builtin_fmaf(s[r], c, -w.lse)) * (dp[r] - w.delta);
+                if (!whole) {
+                    const int32_t d0 = attn_here(at - ju - 4 * h);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (!sight.sees(d0, 8 * (r / 4) + r % 4)) s[r] = 0.f;
+                }
                 // bf16: ds is rounded to nearest for the product with the keys
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
@@ -192,12 +190,12 @@ template <class T, int D>
 struct AttnDkv {
     typedef typename T::E E;
     typedef typename T::F8 F8;
-    static constexpr int kQueries = 32;
+    static constexpr int kQueries = T::kBf16 && D == 64 ? 64 : 32, kSub = kQueries / 32;   // a tile
     typedef AttnTile<T, D, kQueries> Tile;
     static constexpr int kSteps = D / 16, kParts = D / 32;
     typedef AttnTile<T, D, kAttnRows> Values;
     struct Lds {
-        alignas(16) float lse[2][64], delta[2][64];   // a load of a wave each, half of it used
+        alignas(16) float lse[2][64], delta[2][64];   // a load of a wave each
         alignas(16) char q[2][Tile::kBytes];
         alignas(16) char dout[2][Tile::kBytes];
         alignas(16) char v[Values::kBytes];           // the block's values, which registers have no room for
@@ -234,7 +232,7 @@ struct AttnDkv {
                                                        static_cast<int64_t>(i) * from.step_do), from.step_do, rows, lds.dout[b], wave);
             if (wave < 2) {
                 const float *x = (wave == 0 ? from.lse : from.delta) + head * from.total + i;
-                lds_load4(uniform_rsrc(x, 4 * (rows < 32 ? rows : 32)), 4 * lane, lds_address(wave == 0 ? lds.lse[b] : lds.delta[b]));
+                lds_load4(uniform_rsrc(x, 4 * (rows < kQueries ? rows : kQueries)), 4 * lane, lds_address(wave == 0 ? lds.lse[b] : lds.delta[b]));
             }
         };
         load(0, begin, 0);
@@ -250,38 +248,44 @@ struct AttnDkv {
             loads_landed();
             __syncthreads();
             if (nhead < from.heads) load(nhead, next, buf ^ 1);
-            const int32_t last = i + 31 < from.lq ? i + 31 : from.lq - 1;
+            const int32_t last = i + kQueries - 1 < from.lq ? i + kQueries - 1 : from.lq - 1;
             if (lo <= j1 && sight.any(i, last, lo, 32)) {
-                f32x16 p = zero16(), dp = zero16();
+                f32x16 p[kSub], dp[kSub];
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) p = T::mma(Tile::rows(lds.q[buf], l, 0, ks), w.k[ks], p);
+                for (int u = 0; u < kSub; ++u) {
+                    p[u] = dp[u] = zero16();
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) 
-                    dp = T::mma(Tile::rows(lds.dout[buf], l, 0, ks), Tile::rows(lds.v, mine, 0, ks), dp);
+                    for (int ks = 0; ks < kSteps; ++ks) p[u] = T::mma(Tile::rows(lds.q[buf], l, 32 * u, ks), w.k[ks], p[u]);
+#pragma unroll
+                    for (int ks = 0; ks < kSteps; ++ks)
+                        dp[u] = T::mma(Tile::rows(lds.dout[buf], l, 32 * u, ks), Tile::rows(lds.v, mine, 0, ks), dp[u]);
+                }
                 const bool whole = sight.all(i, last, lo, 32);
                 __builtin_amdgcn_sched_barrier(0);   // rows' statistics wait: earlier they cost spilled operands
                 const char *stats = reinterpret_cast<const char *>(lds.lse[buf]) + mine.across;
-                const auto scores = [&](auto masked) {
 #pragma unroll
-                    for (int r4 = 0; r4 < 4; ++r4) {
-                        const f32x4 lse = *reinterpret_cast<const f32x4 *>(stats + 32 * r4);
-                        const f32x4 delta = *reinterpret_cast<const f32x4 *>(stats + 32 * r4 + sizeof(lds.lse));
+                for (int x = 0; x < 4 * kSub; ++x) {
+                    const f32x4 lse = *reinterpret_cast<const f32x4 *>(stats + 32 * x);
+                    const f32x4 delta = *reinterpret_cast<const f32x4 *>(stats + 32 * x + sizeof(lds.lse));
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int r = 4 * r4 + q;
-                            const float e = fast_exp2(__builtin_fmaf(p[r], c, -lse[q])), ds = e * (dp[r] - delta[q]);
-                            const bool seen = !decltype(masked)::value || sight.sees(sight.at(i + 8 * r4 + 4 * h + q), j);
-                            p[r] = seen ? e : 0.f;
-                            dp[r] = seen ? ds : 0.f;
-                        }
+                    for (int q = 0; q < 4; ++q) {
+                        const int u = x / 4, r = 4 * (x % 4) + q;
+                        p[u][r] = fast_exp2(__builtin_fmaf(p[u][r], c, -lse[q]));
+                        dp[u][r] = p[u][r] * (dp[u][r] - delta[q]);
                     }
-                };
-                if (whole) scores(IntC<0>{});
-                else scores(IntC<1>{});
+                }
+                if (!whole) {
+                    const int32_t i4 = attn_here(i + 4 * h);
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (!sight.sees(sight.at(i4 + 32 * u + 8 * (r / 4) + r % 4), j)) p[u][r] = dp[u][r] = 0.f;
+                }
                 // bf16: p and ds are rounded to nearest for the products over the queries
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    const F8 pp = T::part(p, kb), ds = T::part(dp, kb);
+                for (int kb = 0; kb < 2 * kSub; ++kb) {
+                    const F8 pp = T::part(p[kb / 2], kb % 2), ds = T::part(dp[kb / 2], kb % 2);
                     if (!CAREFUL || whole) {
 #pragma unroll
                         for (int t = 0; t < kParts; ++t) {
@@ -459,7 +463,7 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
 // measured on large calls.  Their sums go through memory at 4 TB/s, and joining
 // them takes 5 us more.
 int32_t attn_bwd_parts(const AttnArgs &a) {
-    const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{512, 1.1, 0.7} : AttnCost{512, 2.2, 1.35})
+    const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{512, 1.1, 1.0} : AttnCost{512, 2.2, 1.45})
                                  : (a.d == 64 ? AttnCost{256, 5.5, 5.5} : AttnCost{256, 11.0, 11.0});
     const int32_t group = a.hq / a.hk;
     const double seqs = a.n_seq > 0 ? static_cast<double>(a.n_seq) : 1.0;

@@ -38,6 +38,11 @@ __device__ __forceinline__ float half_sum(float x) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// What scores are multiplied by, in powers of two: one operand of the scores
+// takes a negative factor's sign, and 0 becomes a factor that leaves nothing of
+// a finite score, so that the -inf of a hidden one stays it.
+__device__ __forceinline__ float attn_positive(float c) { return fmaxf(__builtin_fabsf(c), 1e-37f); }
+
 struct AttnBf {
     typedef uint16_t E;
     typedef bf16x8 F8;
@@ -213,7 +218,11 @@ struct AttnTile {
     }
 };
 
-// The same value, which the compiler takes for a new one.
+// The same value, which the compiler takes for a new one: what is made of it stays where it is used.
+__device__ __forceinline__ int32_t attn_here(int32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
 template <class L>
 __device__ __forceinline__ L attn_here(L l) {
     asm volatile("" : "+v"(l.along), "+v"(l.across));
