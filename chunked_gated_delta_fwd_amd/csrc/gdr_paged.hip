@@ -346,8 +346,8 @@ hipError_t launch_page_store(const StoreArgs &a, hipStream_t stream) {
 
 hipError_t launch_page_plan(const PlanArgs &a, hipStream_t stream) {
     const int64_t run = (a.n_seq + 1024) / 1024, blocks = (a.n_seq + run) / run;   // places 0 .. n_seq
-    const int64_t share = a.tokens / (a.n_seq + 1) / 512;
-    const unsigned y = share < 1 ? 1 : share > 32 ? 32 : static_cast<unsigned>(share);
+    const int64_t share = (a.tokens + 2047) / 2048;
+    const unsigned y = share < 1 ? 1 : share > 16 ? 16 : static_cast<unsigned>(share);
     gdr_page_plan_kernel<<<dim3(static_cast<unsigned>(blocks), y), 256, 0, stream>>>(a, run);
     return hipGetLastError();
 }

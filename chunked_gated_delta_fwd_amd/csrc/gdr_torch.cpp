@@ -230,6 +230,9 @@ at::Tensor ssm_step(const at::Tensor &x, const at::Tensor &dt, const at::Tensor 
     return y;
 }
 
+// The calls below make tensors only to fill them: no gradient of theirs is recorded.
+typedef at::AutoDispatchBelowADInplaceOrView Unrecorded;
+
 float scale_or(const std::optional<double> &scale, const at::Tensor &q) {
     const int64_t d = q.size(-1);
     return scale ? static_cast<float>(*scale) : 1.f / std::sqrt(static_cast<float>(d > 0 ? d : 1));
@@ -238,6 +241,7 @@ float scale_or(const std::optional<double> &scale, const at::Tensor &q) {
 std::tuple<at::Tensor, Opt> attn_fwd(const at::Tensor &q, const at::Tensor &k, const at::Tensor &v, const Opt &cu,
                                      const Opt &cuk, bool causal, int64_t window, const std::optional<double> &scale,
                                      bool want_lse, const Opt &o_, const Opt &lse_) {
+    Unrecorded guard;
     want_dims(q, 4, "q");
     Call c(q);
     at::Tensor o = given_or(o_, q.sizes(), q, q.scalar_type());
@@ -256,6 +260,7 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> attn_bwd(const at::Tensor &q, con
                                                         const Opt &cu, const Opt &cuk, bool causal, int64_t window,
                                                         const std::optional<double> &scale, const Opt &dq_, const Opt &dk_,
                                                         const Opt &dv_) {
+    Unrecorded guard;
     want_dims(q, 4, "q");
     Call c(q);
     at::Tensor dq = given_or(dq_, q.sizes(), q, q.scalar_type()), dk = given_or(dk_, k.sizes(), q, k.scalar_type());
@@ -271,6 +276,7 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> attn_bwd(const at::Tensor &q, con
 
 at::Tensor attn_paged_step(const at::Tensor &q, const at::Tensor &kp, const at::Tensor &vp, const at::Tensor &table,
                            const at::Tensor &lens, int64_t window, const std::optional<double> &scale, const Opt &o_) {
+    Unrecorded guard;
     want_dims(q, 3, "q");
     Call c(q);
     at::Tensor o = given_or(o_, q.sizes(), q, q.scalar_type());
@@ -285,6 +291,7 @@ at::Tensor attn_paged_step(const at::Tensor &q, const at::Tensor &kp, const at::
 py::tuple page_plan(const at::Tensor &past, const at::Tensor &fresh, const at::Tensor &pool, const at::Tensor &table,
                     int64_t page, int64_t tokens, const Opt &cu_, const Opt &lens_, const Opt &positions_, const Opt &slots_,
                     const Opt &used_) {
+    Unrecorded guard;
     want_dims(past, 1, "past");
     if (tokens < 0) raise(GDR_EINVAL, "tokens must not be negative");
     if (page < 1 || page > 65536) raise(GDR_ESHAPE, "page: 1 to 65536 tokens are supported, got " + std::to_string(page));
@@ -300,6 +307,7 @@ py::tuple page_plan(const at::Tensor &past, const at::Tensor &fresh, const at::T
 }
 
 void page_store(const at::Tensor &k, const at::Tensor &v, const at::Tensor &slots, const at::Tensor &kp, const at::Tensor &vp) {
+    Unrecorded guard;
     Call c(k);
     check(gdr_page_store(Desc(k, c).p(), Desc(v, c).p(), Desc(slots, c).p(), Desc(kp, c).p(), Desc(vp, c).p(), c.stream()));
 }
