@@ -175,54 +175,65 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(P
     }
 }
 
-// Joins the chunks of a query head: a block takes 32 channels, eight chunks at a time.
-template <class T>
-__global__ __launch_bounds__(256) void gdr_paged_join_kernel(PagedArgs a) {
-    __shared__ float best[4], all[8][32], each[8];
-    const int parts = a.d / 32, x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t out = blockIdx.x / parts, n = out / a.hq;
-    const int channel = static_cast<int>(blockIdx.x % parts) * 32 + x;
+// Joins the chunks of a query head: 4 channels a thread, ROWS chunks at a time.
+// Each row of threads keeps a reference of its own, so that nothing waits for
+// the largest before the outputs are loaded.
+template <class T, int D, int ROWS>
+__global__ __launch_bounds__(ROWS * D / 4) void gdr_paged_join_kernel(PagedArgs a) {
+    constexpr int kThreads = D / 4;
+    __shared__ f32x4 outs[ROWS][kThreads];
+    __shared__ float refs[ROWS], totals[ROWS];
+    const int x = threadIdx.x % kThreads, y = threadIdx.x / kThreads;
+    const int64_t out = blockIdx.x, n = out / a.hq;
     int64_t len = a.lens[n];
     len = len < 0 ? 0 : len > a.width * a.page ? a.width * a.page : len;
     if (a.window > 0 && len > a.window) len = a.window;
-    const int64_t count = len > 0 ? (len + a.chunk - 1) / a.chunk : 1;
+    const int32_t count = len > 0 ? static_cast<int32_t>((len + a.chunk - 1) / a.chunk) : 1;
     const float *stat = a.stat + out * a.splits * 2;
-    float top = -__builtin_inff();
-    for (int64_t s = threadIdx.x; s < count; s += 256) top = fmaxf(top, stat[2 * s]);
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
-    if ((threadIdx.x & 63) == 0) best[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-    if (top == -__builtin_inff()) top = 0.f;
-    float sum = 0.f, total = 0.f;
-    for (int64_t s = y; s < count; s += 8) {
-        const float f = fast_exp2(stat[2 * s] - top);
-        total = __builtin_fmaf(f, stat[2 * s + 1], total);
-        sum = __builtin_fmaf(f, a.part[(out * a.splits + s) * a.d + channel], sum);
+    const float *part = a.part + out * a.splits * D + 4 * x;
+    float top = -__builtin_inff(), total = 0.f;
+    f32x4 sum = zero4();
+#pragma unroll 4
+    for (int32_t s = y; s < count; s += ROWS) {
+        const float ref = stat[2 * s], more = stat[2 * s + 1];
+        const f32x4 o = *reinterpret_cast<const f32x4 *>(part + static_cast<int64_t>(s) * D);
+        const float now = fmaxf(top, ref), base = now == -__builtin_inff() ? 0.f : now;
+        const float f = fast_exp2(top - base), g = fast_exp2(ref - base);
+        top = now;
+        total = __builtin_fmaf(total, f, more * g);
+        sum = sum * f + o * g;
     }
-    all[y][x] = sum;
-    if (x == 0) each[y] = total;
+    outs[y][x] = sum;
+    if (x == 0) {
+        refs[y] = top;
+        totals[y] = total;
+    }
     __syncthreads();
     if (y) return;
-    sum = total = 0.f;
+    for (int i = 1; i < ROWS; ++i) top = fmaxf(top, refs[i]);
+    const float base = top == -__builtin_inff() ? 0.f : top;
+    total = 0.f;
+    sum = zero4();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        sum += all[i][x];
-        total += each[i];
+    for (int i = 0; i < ROWS; ++i) {
+        const float f = fast_exp2(refs[i] - base);
+        total = __builtin_fmaf(totals[i], f, total);
+        sum += outs[i][x] * f;
     }
-    const float o = total == 0.f ? 0.f : sum / total;
-    if constexpr (T::kBf16) static_cast<uint16_t *>(a.o)[out * a.d + channel] = bf16_bits(o);
-    else static_cast<float *>(a.o)[out * a.d + channel] = o;
+    sum *= total == 0.f ? 0.f : 1.f / total;
+    typename T::E *o = static_cast<typename T::E *>(a.o) + out * D + 4 * x;
+    if constexpr (T::kBf16) *reinterpret_cast<bf16x4 *>(o) = cvt4(sum);
+    else *reinterpret_cast<f32x4 *>(o) = sum;
 }
 
 template <class T, int D>
 hipError_t run_step(const PagedArgs &a, hipStream_t stream) {
     const int64_t group = a.hq / a.hk, grid = a.n_seq * a.hk * ((group + 31) / 32) * a.splits;
-    const int64_t join = a.n_seq * a.hq * (a.d / 32);
+    const int64_t join = a.n_seq * a.hq;
     if (grid > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
     gdr_paged_step_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a);
-    if (a.splits > 1) gdr_paged_join_kernel<T><<<dim3(static_cast<unsigned>(join)), 256, 0, stream>>>(a);
+    if (a.splits > 16) gdr_paged_join_kernel<T, D, 32><<<dim3(static_cast<unsigned>(join)), 8 * D, 0, stream>>>(a);
+    else if (a.splits > 1) gdr_paged_join_kernel<T, D, 4><<<dim3(static_cast<unsigned>(join)), D, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -317,19 +328,40 @@ __global__ __launch_bounds__(256) void gdr_page_plan_kernel(PlanArgs a, int64_t 
 
 }  // namespace
 
-// Chunks of a multiple of 128 keys, kLeastChunk at least, of which the sequences
-// at their longest have about 1024 together: two for each block that the chip holds.
-constexpr int64_t kLeastChunk = 512;
+// The chunk (a multiple of 128 keys) that costs least by a model of the launch,
+// in us: a step of 128 keys takes a block 1.25 (64 channels 0.7, f32 7 and 2.9)
+// and the chip holds 512 blocks; the cache is read at 5.1 TB/s where all CUs
+// have a block; a second kernel takes 5.5, 0.02 more a chunk of a sequence, and
+// the traffic of the chunks' outputs.  Measured against 512 and 1024 keys:
+// 64 x 1024 keys, 4 key heads, 30.4 and (one chunk, no second kernel) 23.8 us;
+// 1 x 16384, 2 key heads, 16.9 and 21.9.  At most about 1024 blocks at the
+// longest: more would only split further what fills the chip already.
 void paged_split(PagedArgs &a) {
     int64_t keys = a.width * a.page;
     if (a.window > 0 && keys > a.window) keys = a.window;
     if (keys < 1) keys = 1;
-    const int64_t rows = a.n_seq * a.hk * ((a.hq / a.hk + 31) / 32);
-    int64_t chunk = (rows * keys / 1024 + 127) / 128 * 128;
-    if (chunk < kLeastChunk) chunk = kLeastChunk;
-    if (chunk > 1 << 20) chunk = 1 << 20;
-    a.chunk = static_cast<int32_t>(chunk);
-    a.splits = (keys + chunk - 1) / chunk;
+    const int64_t blocks32 = (a.hq / a.hk + 31) / 32, rows = a.n_seq * a.hk * blocks32;
+    const double step = a.bf16 ? (a.d == 64 ? 0.7 : 1.25) : (a.d == 64 ? 2.9 : 7.0);
+    const double bytes = static_cast<double>(rows / blocks32) * keys * a.d * (a.bf16 ? 4 : 8);
+    int64_t most = (keys + 127) / 128 * 128, least = (rows * keys / 1024 + 127) / 128 * 128;
+    if (most > 1 << 20) most = 1 << 20;
+    if (least < 128) least = 128;
+    double best = 0;
+    a.splits = 0;
+    for (int64_t chunk = most; chunk >= least || a.splits == 0; chunk = (chunk / 2 + 127) / 128 * 128) {
+        const int64_t splits = (keys + chunk - 1) / chunk;
+        const double blocks = static_cast<double>(rows) * splits, rounds = blocks > 512 ? blocks / 512 : 1;
+        double t = 4.3 + chunk / 128 * step * rounds;
+        const double read = bytes / 5.1e6 * (blocks < 256 ? 256 / (blocks > 1 ? blocks : 1) : 1);
+        if (read > t) t = read;
+        if (splits > 1) t += 5.5 + 0.02 * splits + static_cast<double>(a.n_seq) * a.hq * splits * a.d * 8 / 4e6;
+        if (a.splits == 0 || t < 0.97 * best) {
+            best = t;
+            a.chunk = static_cast<int32_t>(chunk);
+            a.splits = splits;
+        }
+        if (chunk == 128) break;
+    }
 }
 
 hipError_t launch_paged_step(const PagedArgs &a, hipStream_t stream) {
