@@ -378,7 +378,7 @@ hipError_t launch_page_store(const StoreArgs &a, hipStream_t stream) {
 
 hipError_t launch_page_plan(const PlanArgs &a, hipStream_t stream) {
     const int64_t run = (a.n_seq + 1024) / 1024, blocks = (a.n_seq + run) / run;   // places 0 .. n_seq
-    const int64_t share = (a.tokens + 2047) / 2048;
+    const int64_t share = (a.tokens + 8191) / 8192;
     const unsigned y = share < 1 ? 1 : share > 16 ? 16 : static_cast<unsigned>(share);
     gdr_page_plan_kernel<<<dim3(static_cast<unsigned>(blocks), y), 256, 0, stream>>>(a, run);
     return hipGetLastError();

@@ -297,9 +297,20 @@ py::tuple page_plan(const at::Tensor &past, const at::Tensor &fresh, const at::T
     if (page < 1 || page > 65536) raise(GDR_ESHAPE, "page: 1 to 65536 tokens are supported, got " + std::to_string(page));
     Call c(past);
     const int64_t n = past.size(0);
-    at::Tensor cu = given_or(cu_, {n + 1}, past, at::kInt), lens = given_or(lens_, {n}, past, at::kInt);
-    at::Tensor positions = given_or(positions_, {1, tokens}, past, at::kInt);
-    at::Tensor slots = given_or(slots_, {1, tokens}, past, at::kInt), used = given_or(used_, {2}, past, at::kInt);
+    // one allocation for what is not given, cut in pieces: a call takes 5.5 us, and 6.7 with five
+    int64_t at = 0;
+    const auto room = [&](const Opt &given, int64_t count) { return given ? 0 : (count + 3) / 4 * 4; };
+    const int64_t all = room(cu_, n + 1) + room(lens_, n) + room(used_, 2) + room(positions_, tokens) + room(slots_, tokens);
+    const at::Tensor whole = all ? empty({all}, past, at::kInt) : at::Tensor();
+    const auto cut = [&](const Opt &given, at::IntArrayRef shape, at::IntArrayRef strides, int64_t count) {
+        if (given) return *given;
+        const at::Tensor t = whole.as_strided(shape, strides, at);
+        at += room(given, count);
+        return t;
+    };
+    const at::Tensor cu = cut(cu_, {n + 1}, {1}, n + 1), lens = cut(lens_, {n}, {1}, n), used = cut(used_, {2}, {1}, 2);
+    const at::Tensor positions = cut(positions_, {1, tokens}, {tokens, 1}, tokens);
+    const at::Tensor slots = cut(slots_, {1, tokens}, {tokens, 1}, tokens);
     check(gdr_page_plan(Desc(past, c).p(), Desc(fresh, c).p(), Desc(pool, c).p(), Desc(table, c).p(), Desc(cu, c).p(),
                         Desc(lens, c).p(), Desc(positions, c).p(), Desc(slots, c).p(), Desc(used, c).p(),
                         static_cast<int32_t>(page), c.stream()));
