@@ -104,13 +104,16 @@ struct AttnF32 {
 // Loads to LDS past the registers: lane l's 16 (4) bytes land at `lds` + 16 l (4 l).
 // Not the builtin: the compiler waits for such loads before every LDS read that
 // follows, and a tile is loaded while another one is read.  A load past the
-// buffer's end stores zeros.
+// buffer's end stores zeros.  The wait states are this code's own affair: a
+// scalar register of the descriptor that a vector instruction wrote (a first
+// lane read, a spilled one read back) may be read by a load five states later,
+// m0 one; the compiler does not see that there is a load in here.
 __device__ __forceinline__ void lds_load16(v4u32 rsrc, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  : : "s"(lds), "v"(off), "s"(rsrc) : "memory");
 }
 __device__ __forceinline__ void lds_load4(v4u32 rsrc, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  : : "s"(lds), "v"(off), "s"(rsrc) : "memory");
 }
 __device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
