@@ -248,14 +248,14 @@ __device__ __forceinline__ bool attn_fwd_block(const AttnArgs &a, uint32_t tiles
 
 // A function of its own: inside the kernel it would cost the other walk registers.
 template <class T, int D>
-__device__ __attribute__((noinline)) void attn_fwd_careful(AttnArgsAt at, uint32_t tiles, typename AttnFwd<T, D>::Lds *lds) {
-    (void)attn_fwd_block<T, D, true>(attn_args(at), tiles, *lds);
+__device__ __attribute__((noinline)) void attn_fwd_careful(AttnArgsAt at, uint32_t tiles, __attribute__((address_space(3))) typename AttnFwd<T, D>::Lds *lds) {
+    (void)attn_fwd_block<T, D, true>(attn_args(attn_scalar(at)), __builtin_amdgcn_readfirstlane(tiles), attn_scalar(lds));
 }
 
 template <class T, int D>
 __global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_attn_fwd_kernel(AttnArgs a, uint32_t tiles) {
     __shared__ typename AttnFwd<T, D>::Lds lds;
-    if (attn_fwd_block<T, D, false>(a, tiles, lds)) attn_fwd_careful<T, D>(attn_args_at(), tiles, &lds);
+    if (attn_fwd_block<T, D, false>(a, tiles, lds)) attn_fwd_careful<T, D>(attn_args_at(), tiles, attn_lds(lds));
 }
 
 // Joins a block's runs: 4 channels a thread, 8 rows (d 64: 16) at a time, the

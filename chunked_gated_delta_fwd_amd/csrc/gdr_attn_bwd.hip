@@ -32,7 +32,8 @@ struct AttnDq {
     };
 
     // CAREFUL as in the forward: a key that is not finite reaches the rows that see it and no other.
-    template <bool CAREFUL>
+    // SUMS: in place of dq, the sum of each row's ds (this lane's half) in delta.
+    template <bool CAREFUL, bool SUMS>
     static __device__ __forceinline__ void walk(Row &w, const AttnSight &sight, float c, int32_t i0, int32_t i1,
                                                 int32_t begin, int32_t end, const E *k, const E *v, uint32_t step_k,
                                                 uint32_t step_v, int32_t lk, Lds &lds, int wave, int lane) {
@@ -41,6 +42,7 @@ struct AttnDq {
         const int32_t lo = i0 + 32 * wave, at = sight.at(lo + col);
 #pragma unroll
         for (int t = 0; t < kParts; ++t) w.dq[t] = zero16();
+        float rest = 0.f;
         const typename Tile::Lane places = Tile::lane_places(lane);
         auto load = [&](int32_t j, int b) {
             Tile::load(fk, reinterpret_cast<const E *>(reinterpret_cast<const char *>(k) + static_cast<int64_t>(j) * step_k),
@@ -75,6 +77,11 @@ struct AttnDq {
                     for (int r = 0; r < 16; ++r)
                         if (!sight.sees(d0, 8 * (r / 4) + r % 4)) s[r] = 0.f;
                 }
+                if constexpr (SUMS) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) rest += s[r];
+                    continue;
+                }
                 // bf16: ds is rounded to nearest for the product with the keys
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
@@ -104,11 +111,23 @@ struct AttnDq {
             tile(IntC<0>{}, j);
             if (j + kKeys < end) tile(IntC<1>{}, j + kKeys);
         }
+        if (SUMS) w.delta = rest;
     }
 };
 
-template <class T, int D, bool CAREFUL>
-__device__ __forceinline__ bool attn_dq_block(const AttnArgs &a, uint32_t tiles, typename AttnDq<T, D>::Lds &lds) {
+// delta cancels against do . v, and made from a bf16 o it carries o's rounding:
+// in dq and dk, relative to that of ds, about n^-1/2 of it where n keys share a
+// row's weight.  A row's ds sum to zero with the delta that belongs to them, so
+// where a block sees at most kFewTiles tiles a walk of its own takes the sum
+// (errors of dq and dk in 2-norm: rows of 2 keys 3.4e-3 without, 2.4e-3 with it,
+// of 30 keys 2.6e-3 and 2.4e-3; one rounding of the result is 1.7e-3).
+constexpr int32_t kFewTiles = 3;
+template <class T, int D>
+__device__ __attribute__((noinline)) float attn_dq_delta(AttnArgsAt at, uint32_t tiles, __attribute__((address_space(3))) typename AttnDq<T, D>::Lds *lds);
+
+template <class T, int D, bool CAREFUL, bool SUMS>
+__device__ __forceinline__ bool attn_dq_block(AttnArgsAt args, const AttnArgs &a, uint32_t tiles,
+                                              typename AttnDq<T, D>::Lds &lds, float &sum) {
     typedef AttnDq<T, D> F;
     typedef typename T::E E;
     typedef typename T::F8 F8;
@@ -128,6 +147,8 @@ __device__ __forceinline__ bool attn_dq_block(const AttnArgs &a, uint32_t tiles,
     const int64_t first = static_cast<int64_t>(sight.at(i0)) - sight.back + 1;
     const int32_t begin = first > 0 ? static_cast<int32_t>(first) / F::kKeys * F::kKeys : 0;
     const int32_t end = sight.at(i1) + 1 < seq.lk ? sight.at(i1) + 1 : seq.lk;
+    const bool few = T::kBf16 && !SUMS && end - begin <= kFewTiles * F::kKeys;
+    if (few) sum = attn_dq_delta<T, D>(args, tiles, attn_lds(lds));
 
     typename F::Row w;
     {
@@ -136,18 +157,18 @@ __device__ __forceinline__ bool attn_dq_block(const AttnArgs &a, uint32_t tiles,
         const E *q = static_cast<const E *>(a.q) + row * a.ldq + head;
         const E *o = static_cast<const E *>(a.o) + row * a.ldo + head;
         const E *dout = static_cast<const E *>(a.dout) + row * a.lddo + head;
-        float sum = 0.f;
+        float dot = 0.f;
 #pragma unroll
         for (int ks = 0; ks < F::kSteps; ++ks) {
             w.q[ks] = T::load(q + 16 * ks);
             w.dout[ks] = T::load(dout + 16 * ks);
             const F8 x = T::load(o + 16 * ks);
 #pragma unroll
-            for (int s = 0; s < 8; ++s) sum = __builtin_fmaf(T::up(w.dout[ks], s), T::up(x, s), sum);
+            for (int s = 0; s < 8; ++s) dot = __builtin_fmaf(T::up(w.dout[ks], s), T::up(x, s), dot);
         }
-        w.delta = half_sum(sum);
+        w.delta = few ? sum : half_sum(dot);
         w.lse = a.lse[row * a.hq + hq] * kLog2e;
-        if (i0 + 32 * wave + col < seq.lq && h == 0) {
+        if (!SUMS && i0 + 32 * wave + col < seq.lq && h == 0) {
             float *stat = a.stat + static_cast<int64_t>(hq) * a.total_q + row;
             stat[0] = w.lse;
             stat[a.hq * a.total_q] = w.delta;
@@ -157,7 +178,14 @@ __device__ __forceinline__ bool attn_dq_block(const AttnArgs &a, uint32_t tiles,
     const E *k = static_cast<const E *>(a.k) + seq.k0 * a.ldk + static_cast<int64_t>(hk) * D;
     const E *v = static_cast<const E *>(a.v) + seq.k0 * a.ldv + static_cast<int64_t>(hk) * D;
     const uint32_t step_k = static_cast<uint32_t>(a.ldk * sizeof(E)), step_v = static_cast<uint32_t>(a.ldv * sizeof(E));
-    F::template walk<CAREFUL>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+    if constexpr (SUMS) {
+        const float before = w.delta;
+        F::template walk<CAREFUL, true>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
+        sum = before + half_sum(w.delta);
+        __syncthreads();   // the tiles are read: other ones may take their place
+        return false;
+    }
+    F::template walk<CAREFUL, false>(w, sight, c, i0, i1, begin, end, k, v, step_k, step_v, seq.lk, lds, wave, lane);
     float x = 0.f;   // 0, or NaN where a gradient is not finite
 #pragma unroll
     for (int t = 0; t < F::kParts; ++t)
@@ -174,14 +202,24 @@ __device__ __forceinline__ bool attn_dq_block(const AttnArgs &a, uint32_t tiles,
 }
 
 template <class T, int D>
-__device__ __attribute__((noinline)) void attn_dq_careful(AttnArgsAt at, uint32_t tiles, typename AttnDq<T, D>::Lds *lds) {
-    (void)attn_dq_block<T, D, true>(attn_args(at), tiles, *lds);
+__device__ __attribute__((noinline)) void attn_dq_careful(AttnArgsAt at, uint32_t tiles, __attribute__((address_space(3))) typename AttnDq<T, D>::Lds *lds) {
+    float sum;
+    at = attn_scalar(at);
+    (void)attn_dq_block<T, D, true, false>(at, attn_args(at), __builtin_amdgcn_readfirstlane(tiles), attn_scalar(lds), sum);
+}
+template <class T, int D>
+__device__ __attribute__((noinline)) float attn_dq_delta(AttnArgsAt at, uint32_t tiles, __attribute__((address_space(3))) typename AttnDq<T, D>::Lds *lds) {
+    float sum;
+    at = attn_scalar(at);
+    (void)attn_dq_block<T, D, false, true>(at, attn_args(at), __builtin_amdgcn_readfirstlane(tiles), attn_scalar(lds), sum);
+    return sum;
 }
 
 template <class T, int D>
 __global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_attn_dq_kernel(AttnArgs a, uint32_t tiles) {
     __shared__ typename AttnDq<T, D>::Lds lds;
-    if (attn_dq_block<T, D, false>(a, tiles, lds)) attn_dq_careful<T, D>(attn_args_at(), tiles, &lds);
+    float sum;
+    if (attn_dq_block<T, D, false, false>(attn_args_at(), a, tiles, lds, sum)) attn_dq_careful<T, D>(attn_args_at(), tiles, attn_lds(lds));
 }
 
 // dk and dv: a block takes 128 key rows of one key head, 32 a wave, and walks
@@ -404,14 +442,14 @@ __device__ __forceinline__ bool attn_dkv_block(const AttnArgs &a, uint32_t tiles
 }
 
 template <class T, int D>
-__device__ __attribute__((noinline)) void attn_dkv_careful(AttnArgsAt at, uint32_t tiles, typename AttnDkv<T, D>::Lds *lds) {
-    (void)attn_dkv_block<T, D, true>(attn_args(at), tiles, *lds);
+__device__ __attribute__((noinline)) void attn_dkv_careful(AttnArgsAt at, uint32_t tiles, __attribute__((address_space(3))) typename AttnDkv<T, D>::Lds *lds) {
+    (void)attn_dkv_block<T, D, true>(attn_args(attn_scalar(at)), __builtin_amdgcn_readfirstlane(tiles), attn_scalar(lds));
 }
 
 template <class T, int D>
 __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(AttnArgs a, uint32_t tiles) {
     __shared__ typename AttnDkv<T, D>::Lds lds;
-    if (attn_dkv_block<T, D, false>(a, tiles, lds)) attn_dkv_careful<T, D>(attn_args_at(), tiles, &lds);
+    if (attn_dkv_block<T, D, false>(a, tiles, lds)) attn_dkv_careful<T, D>(attn_args_at(), tiles, attn_lds(lds));
 }
 
 // Sums the parts of dk and dv in order, for the rows of one tile's sequence.

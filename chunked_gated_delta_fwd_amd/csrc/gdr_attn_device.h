@@ -343,8 +343,26 @@ __device__ __forceinline__ AttnItem attn_item(uint32_t block, uint32_t pairs, ui
 
 // The arguments where the kernel was given them, for functions that are not
 // inlined: a reference to the kernel's own copy would put it on the stack.
+// attn_args_at is for kernels: a function has no such place and takes the pointer.
 typedef __attribute__((address_space(4))) const AttnArgs *AttnArgsAt;
 __device__ __forceinline__ AttnArgsAt attn_args_at() { return (AttnArgsAt)__builtin_amdgcn_kernarg_segment_ptr(); }
+// Functions get their parameters in vector registers: the first lane's make
+// what hangs on them scalar again.
+__device__ __forceinline__ AttnArgsAt attn_scalar(AttnArgsAt at) {
+    const uint64_t p = reinterpret_cast<uint64_t>(at);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32));
+    return reinterpret_cast<AttnArgsAt>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <class L>
+__device__ __forceinline__ __attribute__((address_space(3))) L *attn_lds(L &lds) {
+    return (__attribute__((address_space(3))) L *)&lds;
+}
+template <class L>
+__device__ __forceinline__ L &attn_scalar(__attribute__((address_space(3))) L *lds) {
+    const uint32_t p = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)));
+    return *(L *)reinterpret_cast<__attribute__((address_space(3))) L *>(static_cast<uintptr_t>(p));
+}
 __device__ __forceinline__ AttnArgs attn_args(AttnArgsAt at) {
     AttnArgs a;
     __builtin_memcpy(&a, (const AttnArgs *)at, sizeof(a));
