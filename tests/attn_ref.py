@@ -12,7 +12,8 @@ product: H more.  A sum of n terms adds n U of their absolute values.
   o    (H + E + (n + 16) U) sum p |v| + H |o|
   lse  E + (n + 16) U
   ds   p (E |dp - delta| + (d + 8) U sum |do v| + (H + (d + 8) U) sum |do o|) + (H + 4 U) |ds|
-       (delta is taken from o as it is stored)
+       (delta is taken from o as it is stored.  `few`: from the sum of the row's ds with such a delta, which is off by the
+       sum of their own errors, without the last term, and by (n + 16) U of their absolute sum)
   dq   scale (sum |err ds| |k| + (n + 16) U sum |ds k|) + H |dq|; dk likewise over the queries
   dv   (H + E + (n + 16) U) sum p |do| + H |dv|
 
@@ -88,7 +89,7 @@ def attention(q, k, v, cu=None, cuk=None, causal=True, window=0, scale=None, dty
     return o.reshape(q.shape), lse.reshape(q.shape[:3]), to.reshape(q.shape), tl.reshape(q.shape[:3])
 
 
-def gradient(q, k, v, do, cu=None, cuk=None, causal=True, window=0, scale=None, dtype=torch.float32):
+def gradient(q, k, v, do, cu=None, cuk=None, causal=True, window=0, scale=None, dtype=torch.float32, few=False):
     """((dq, dk, dv), their tolerances) by the formulas; rows outside every sequence are NaN."""
     B, Tq, Hq, d = q.shape
     Hk, H = k.shape[2], half_step(dtype) if dtype != torch.float32 else 0.0
@@ -107,8 +108,12 @@ def gradient(q, k, v, do, cu=None, cuk=None, causal=True, window=0, scale=None, 
             o, _, _, _, p, E = one(qs, ks, vs, seen, scale, H)
             dp, delta = dos @ vs.t(), (dos * o).sum(-1, keepdim=True)
             ds = p * (dp - delta)
-            err = p * (E[:, None] * (dp - delta).abs() + (d + 8) * U * (dos.abs() @ vs.abs().t())
-                       + (H + (d + 8) * U) * (dos * o).abs().sum(-1, keepdim=True)) + (H + 4 * U) * ds.abs()
+            off = E[:, None] * (dp - delta).abs() + (d + 8) * U * (dos.abs() @ vs.abs().t())
+            shift = (H + (d + 8) * U) * (dos * o).abs().sum(-1, keepdim=True)    # of delta
+            if few:
+                worst = (dp - delta).abs() + shift
+                shift = (p * (off + E[:, None] * shift + (n + 16) * U * worst)).sum(-1, keepdim=True)
+            err = p * (off + shift) + (H + 4 * U) * ds.abs()
             got[0][a:b, h] = scale * (ds @ ks)
             tiny = vanishing(n + m, qs, ks, vs, dos) * max(1.0, abs(scale))
             tol[0][a:b, h] = abs(scale) * ((err + (n + 16) * U * ds.abs()) @ ks.abs()) + tiny

@@ -144,6 +144,20 @@ def test_growing_scores():
     run(dev, dbl, None, None, F, causal=False)
 
 
+@pytest.mark.parametrize("lens,window,d", [([2, 3, 9, 30], 0, 64), ([150, 180], 2, 128), ([192], 0, 64), ([500], 40, 128)])
+def test_few_keys_do_not_carry_the_rounding_of_o(lens, window, d):
+    """Where a block sees at most 192 keys, dq and dk carry the rounding of ds and their own, and not o's."""
+    import chunked_gated_delta_fwd_amd as gdr
+    T = sum(lens)
+    dev, dbl = make(1, T, T, 4, 2, d, BF, seed=20)
+    cu = offsets(lens)
+    o, lse = gdr.attn_fwd(dev["q"], dev["k"], dev["v"], ints(cu), window=window)
+    grads = gdr.attn_bwd(dev["q"], dev["k"], dev["v"], o, lse, dev["do"], ints(cu), window=window)
+    rg, tg = ref.gradient(*(dbl[n] for n in ("q", "k", "v", "do")), cu, window=window, dtype=BF, few=True)
+    for name, got, r, t in zip(("dq", "dk", "dv"), grads, rg, tg):
+        check(name, got, r, t)
+
+
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 0), (True, 20)])
 def test_gradient_against_differences(causal, window):
     """<gradient, u> against central differences of the plain forward along u.  The differences are off by h^2 times
