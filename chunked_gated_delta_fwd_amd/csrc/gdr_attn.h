@@ -34,15 +34,23 @@ struct AttnArgs {
 };
 // How long a launch takes, in us, by a model: blocks go through the chip `slots`
 // at a time, and a step of one takes `full` where the CUs are full and `half`
-// where a block has one for itself; the longest block takes its own time.
+// where a block has one for itself.  Blocks of one length go in rounds, uneven
+// ones fill the gaps, and the longest takes its own time.
 struct AttnCost {
     double slots, full, half;
 };
 inline double attn_time(const AttnCost &c, double blocks, double mean_steps, double most_steps) {
     const double rounds = static_cast<double>(static_cast<int64_t>(blocks / c.slots)), rest = blocks - rounds * c.slots;
     const double last = rest > 256 ? c.full : rest > 0.5 ? c.half : 0;
-    const double all = (rounds * c.full + last) * mean_steps, longest = (blocks > 256 ? 0.85 * c.full : c.half) * most_steps;
+    const bool even = rounds < 1 || mean_steps > 0.9 * most_steps;
+    const double all = (even ? rounds * c.full + last : blocks / c.slots * c.full) * mean_steps;
+    const double longest = (blocks > 256 ? 0.85 * c.full : c.half) * most_steps;
     return all > longest ? all : longest;
+}
+// Tiles of kAttnRows rows of all sequences of `rows` rows each, or about so many.
+inline double attn_blocks(bool packed, double sequences, double rows) {
+    if (packed) return sequences * (rows < kAttnRows / 2 ? 1.0 : rows / kAttnRows + 0.5);
+    return sequences * static_cast<double>((static_cast<int64_t>(rows) + kAttnRows - 1) / kAttnRows);
 }
 // Sets splits and least.
 void attn_split(AttnArgs &a);

@@ -309,14 +309,14 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
 }  // namespace
 
 // The runs that cost least by attn_time; a tile of keys as measured on large
-// calls.  Their outputs go through memory at 4 TB/s, the second launch takes 5 us.
+// calls.  Their outputs go through the caches at 6 TB/s, the second launch takes 5 us.
 void attn_split(AttnArgs &a) {
     const int32_t keys = a.bf16 ? 64 : 32;
     const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{768, 1.95, 0.9} : AttnCost{512, 2.2, 1.35})
                                  : (a.d == 64 ? AttnCost{256, 2.5, 2.5} : AttnCost{256, 5.0, 5.0});
     const double seqs = a.n_seq > 0 ? static_cast<double>(a.n_seq) : 1.0;
     const double lq = a.cu ? a.total_q / seqs : a.seq_q, lk = a.cu ? a.total_k / seqs : a.seq_k;
-    const double blocks = seqs * a.hq * (lq < kAttnRows ? 1.0 : lq / kAttnRows);
+    const double blocks = a.hq * attn_blocks(a.cu != nullptr, seqs, lq);
     // keys that a block sees, at most and on average
     double most = lk, mean = a.causal ? lk - (lq < lk ? lq : lk) / 2 : lk;
     if (a.window > 0 && a.window + kAttnRows < most) most = a.window + kAttnRows;
@@ -327,7 +327,7 @@ void attn_split(AttnArgs &a) {
     a.least = 1;
     for (int32_t s = 1; s <= 64 && (s == 1 || tiles / s >= 4); s += s < 4 ? 1 : s < 16 ? 2 : 8) {
         double t = attn_time(cost, blocks * s, (mean / keys + 1) / s, tiles / s);
-        if (s > 1) t += 5 + 8.0 * a.total_q * a.hq * a.d * s / 4e6;
+        if (s > 1) t += 5 + 8.0 * a.total_q * a.hq * a.d * s / 6e6;
         if (s == 1 || t < 0.95 * best) {
             best = t;
             a.splits = s;

@@ -497,18 +497,18 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-// The parts that cost least by attn_time; a step is a tile of queries, as
-// measured on large calls.  Their sums go through memory at 4 TB/s, and joining
-// them takes 5 us more.
+// The parts that cost least by attn_time; a step is 32 queries, as measured on
+// large calls.  Their sums go through the caches at 8 TB/s, and joining them
+// takes 5 us more.
 int32_t attn_bwd_parts(const AttnArgs &a) {
     const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{512, 1.1, 1.0} : AttnCost{512, 2.2, 1.45})
                                  : (a.d == 64 ? AttnCost{256, 5.5, 5.5} : AttnCost{256, 11.0, 11.0});
     const int32_t group = a.hq / a.hk;
     const double seqs = a.n_seq > 0 ? static_cast<double>(a.n_seq) : 1.0;
     const double lq = a.cu ? a.total_q / seqs : a.seq_q, lk = a.cu ? a.total_k / seqs : a.seq_k;
-    const double blocks = seqs * a.hk * (lk < kAttnRows ? 1.0 : lk / kAttnRows);
-    // queries that see a block's keys, at most and on average
-    double most = lq, mean = a.causal ? lq - (lq < lk ? lq : lk) / 2 : lq;
+    const double blocks = a.hk * attn_blocks(a.cu != nullptr, seqs, lk);
+    // queries that see a block's keys, at most and on average; packed sequences have other lengths than the mean
+    double most = a.cu ? 2.5 * lq : lq, mean = a.causal ? lq - (lq < lk ? lq : lk) / 2 : lq;
     if (a.window > 0 && a.window + kAttnRows < most) most = a.window + kAttnRows;
     if (mean > most) mean = most;
     double best = 0;
@@ -516,7 +516,7 @@ int32_t attn_bwd_parts(const AttnArgs &a) {
     for (int32_t p = 1; p <= group; p = p < group && 2 * p > group ? group : 2 * p) {
         const double heads = static_cast<double>(group) / p;
         double t = attn_time(cost, blocks * p, (mean / 32 + 1) * heads, (most / 32 + 1) * heads);
-        if (p > 1) t += 5 + 16.0 * a.total_k * a.hk * a.d * p / 4e6;
+        if (p > 1) t += 5 + 16.0 * a.total_k * a.hk * a.d * p / 8e6;
         if (p == 1 || t < 0.95 * best) {
             best = t;
             parts = p;
