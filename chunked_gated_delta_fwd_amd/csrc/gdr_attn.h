@@ -54,6 +54,9 @@ inline double attn_blocks(bool packed, double sequences, double rows) {
 }
 // Sets splits and least.
 void attn_split(AttnArgs &a);
+// Blocks of the largest launch of a call; more than 2^31 - 1 cannot be launched.
+int64_t attn_fwd_grid(const AttnArgs &a);
+int64_t attn_bwd_grid(const AttnArgs &a);
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream);
 // How many blocks share the query heads of a group for the gradient of keys and values.
 int32_t attn_bwd_parts(const AttnArgs &a);
@@ -77,6 +80,7 @@ struct PagedArgs {
 };
 // Sets chunk and splits.
 void paged_split(PagedArgs &a);
+int64_t paged_grid(const PagedArgs &a);
 hipError_t launch_paged_step(const PagedArgs &a, hipStream_t stream);
 
 struct StoreArgs {
@@ -85,6 +89,7 @@ struct StoreArgs {
     void *kp, *vp;               // [rows] of row_bytes
     int64_t tokens, rows, row_bytes, ldk, ldv;
 };
+int64_t page_store_grid(const StoreArgs &a);
 hipError_t launch_page_store(const StoreArgs &a, hipStream_t stream);
 
 struct PlanArgs {

@@ -298,9 +298,8 @@ template <class T, int D>
 hipError_t run(const AttnArgs &a, hipStream_t stream) {
     const int64_t tiles = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
     const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
-    const int64_t grid = attn_grid(pairs, tiles, group * a.splits), join = attn_grid(pairs, tiles, group);
-    if (grid > 0x7FFFFFFF || tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-    gdr_attn_fwd_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
+    const int64_t join = attn_grid(pairs, tiles, group);
+    gdr_attn_fwd_kernel<T, D><<<dim3(static_cast<unsigned>(attn_fwd_grid(a))), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
     if (a.splits > 1)
         gdr_attn_runs_kernel<T, D><<<dim3(static_cast<unsigned>(join), D / 8), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
     return hipGetLastError();
@@ -334,6 +333,11 @@ void attn_split(AttnArgs &a) {
             a.least = static_cast<int32_t>(tiles / s + 0.999);
         }
     }
+}
+
+int64_t attn_fwd_grid(const AttnArgs &a) {
+    return attn_grid((a.cu ? 1 : a.n_seq) * a.hk, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q),
+                     static_cast<int64_t>(a.hq / a.hk) * a.splits);
 }
 
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream) {

@@ -92,6 +92,11 @@ int plan_attn(AttnIn &c, gdr::AttnArgs &a) {
     return GDR_OK;
 }
 
+int fits(int64_t blocks) {
+    if (blocks > 0x7FFFFFFF) return fail(GDR_ESHAPE, "the call would take %lld blocks, more than 2^31 - 1", (long long)blocks);
+    return GDR_OK;
+}
+
 // Both offsets' contents, with the opt-in check on.
 int check_offsets(const AttnIn &c, const gdr::AttnArgs &a, hipStream_t stream) {
     const int rc = check_cu(c.cu, a.n_seq, c.B * c.Tq, stream);
@@ -123,6 +128,7 @@ int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v, 
         a.o = o->data;
         a.lse = lse ? static_cast<float *>(lse->data) : nullptr;
         gdr::attn_split(a);
+        if ((rc = fits(gdr::attn_fwd_grid(a)))) return rc;
         Carve sizes{nullptr};
         const auto carve = [&](Carve &w) {
             const int64_t runs = a.splits > 1 ? a.splits * a.total_q * a.hq : 0;
@@ -183,6 +189,7 @@ int gdr_attn_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v, 
         a.dk = dk->data;
         a.dv = dv->data;
         a.parts = gdr::attn_bwd_parts(a);
+        if ((rc = fits(gdr::attn_bwd_grid(a)))) return rc;
         Carve sizes{nullptr};
         const auto carve = [&](Carve &w) {
             a.stat = w.take<float>(2 * static_cast<int64_t>(a.hq) * a.total_q);
@@ -267,6 +274,7 @@ int gdr_attn_paged_step(const gdr_tensor *q, const gdr_tensor *k_pages, const gd
         a.magic = static_cast<uint32_t>(((int64_t{1} << shift) + page - 1) / page);
         a.shift = shift;
         gdr::paged_split(a);
+        if ((rc = fits(gdr::paged_grid(a)))) return rc;
         Carve sizes{nullptr};
         const auto carve = [&](Carve &w) {
             const int64_t chunks = a.splits > 1 ? N * hq * a.splits : 0;
@@ -321,7 +329,6 @@ int gdr_page_store(const gdr_tensor *k, const gdr_tensor *v, const gdr_tensor *s
         if ((rc = check_overlaps({{"k", sk}, {"v", sv}, {"slots", span_of(slots, ns)}},
                                  {{"k_pages", span_of(k_pages, nk)}, {"v_pages", span_of(v_pages, nv)}})))
             return rc;
-        if ((rc = check_device())) return rc;
         a.k = k->data;
         a.v = v->data;
         a.slots = static_cast<const int32_t *>(slots->data);
@@ -332,6 +339,8 @@ int gdr_page_store(const gdr_tensor *k, const gdr_tensor *v, const gdr_tensor *s
         a.row_bytes = hk * d * e;
         a.ldk = a.ldk * e;
         a.ldv = a.ldv * e;
+        if ((rc = fits(gdr::page_store_grid(a)))) return rc;
+        if ((rc = check_device())) return rc;
         if (a.tokens == 0 || a.rows == 0) return ok();
         return launch([&] { return gdr::launch_page_store(a, stream); }, "page store kernel");
     });

@@ -483,7 +483,6 @@ hipError_t run(const AttnArgs &a, hipStream_t stream) {
     const int64_t tiles_q = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
     const int64_t tiles_k = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k);
     const int64_t grid_q = attn_grid(pairs, tiles_q, a.hq / a.hk), grid_k = attn_grid(pairs, tiles_k, a.parts);
-    if (grid_q > 0x7FFFFFFF || grid_k > 0x7FFFFFFF || tiles_q > 0x7FFFFFFF || tiles_k > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.total_q > 0) gdr_attn_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid_q)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_q));
     if (a.total_k > 0) {
         gdr_attn_dkv_kernel<T, D><<<dim3(static_cast<unsigned>(grid_k)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
@@ -523,6 +522,13 @@ int32_t attn_bwd_parts(const AttnArgs &a) {
         }
     }
     return parts;
+}
+
+int64_t attn_bwd_grid(const AttnArgs &a) {
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const int64_t q = attn_grid(pairs, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q), a.hq / a.hk);
+    const int64_t k = attn_grid(pairs, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k), a.parts);
+    return q > k ? q : k;
 }
 
 hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t stream) {

@@ -315,7 +315,7 @@ struct AttnItem {
     int32_t way;          // query head of the group, or part of it
 };
 __host__ __device__ inline int64_t attn_grid(int64_t pairs, int64_t tiles, int64_t ways) {
-    return pairs < 8 && 8 % pairs == 0 ? 8 * ((tiles * ways * pairs + 7) / 8) : pairs * tiles * ways;
+    return pairs == 0 ? 0 : pairs < 8 && 8 % pairs == 0 ? 8 * ((tiles * ways * pairs + 7) / 8) : pairs * tiles * ways;
 }
 // All counts are below 2^31, as the grid is.
 __device__ __forceinline__ AttnItem attn_item(uint32_t block, uint32_t pairs, uint32_t tiles, uint32_t ways) {

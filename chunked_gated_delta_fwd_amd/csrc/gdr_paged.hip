@@ -228,10 +228,8 @@ __global__ __launch_bounds__(ROWS * D / 4) void gdr_paged_join_kernel(PagedArgs 
 
 template <class T, int D>
 hipError_t run_step(const PagedArgs &a, hipStream_t stream) {
-    const int64_t group = a.hq / a.hk, grid = a.n_seq * a.hk * ((group + 31) / 32) * a.splits;
     const int64_t join = a.n_seq * a.hq;
-    if (grid > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
-    gdr_paged_step_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), 256, 0, stream>>>(a);
+    gdr_paged_step_kernel<T, D><<<dim3(static_cast<unsigned>(a.n_seq * a.hk * ((a.hq / a.hk + 31) / 32) * a.splits)), 256, 0, stream>>>(a);
     if (a.splits > 16) gdr_paged_join_kernel<T, D, 32><<<dim3(static_cast<unsigned>(join)), 8 * D, 0, stream>>>(a);
     else if (a.splits > 1) gdr_paged_join_kernel<T, D, 4><<<dim3(static_cast<unsigned>(join)), D, 0, stream>>>(a);
     return hipGetLastError();
@@ -364,15 +362,20 @@ void paged_split(PagedArgs &a) {
     }
 }
 
+int64_t paged_grid(const PagedArgs &a) {
+    const int64_t step = a.n_seq * a.hk * ((a.hq / a.hk + 31) / 32) * a.splits, join = a.n_seq * a.hq;
+    return step > join ? step : join;
+}
+
 hipError_t launch_paged_step(const PagedArgs &a, hipStream_t stream) {
     if (a.bf16) return a.d == 64 ? run_step<AttnBf, 64>(a, stream) : run_step<AttnBf, 128>(a, stream);
     return a.d == 64 ? run_step<AttnF32, 64>(a, stream) : run_step<AttnF32, 128>(a, stream);
 }
 
+int64_t page_store_grid(const StoreArgs &a) { return (2 * a.tokens * (a.row_bytes / 16) + 255) / 256; }
+
 hipError_t launch_page_store(const StoreArgs &a, hipStream_t stream) {
-    const int64_t blocks = (2 * a.tokens * (a.row_bytes / 16) + 255) / 256;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    gdr_page_store_kernel<<<dim3(static_cast<unsigned>(blocks)), 256, 0, stream>>>(a);
+    gdr_page_store_kernel<<<dim3(static_cast<unsigned>(page_store_grid(a))), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

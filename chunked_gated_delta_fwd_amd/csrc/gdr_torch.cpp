@@ -293,7 +293,7 @@ py::tuple page_plan(const at::Tensor &past, const at::Tensor &fresh, const at::T
                     const Opt &used_) {
     Unrecorded guard;
     want_dims(past, 1, "past");
-    if (tokens < 0) raise(GDR_EINVAL, "tokens must not be negative");
+    if (tokens < 0 || tokens > int64_t{1} << 30) raise(GDR_EINVAL, "tokens must be between 0 and 2^30, got " + std::to_string(tokens));
     if (page < 1 || page > 65536) raise(GDR_ESHAPE, "page: 1 to 65536 tokens are supported, got " + std::to_string(page));
     Call c(past);
     const int64_t n = past.size(0);
@@ -301,7 +301,7 @@ py::tuple page_plan(const at::Tensor &past, const at::Tensor &fresh, const at::T
     int64_t at = 0;
     const auto room = [&](const Opt &given, int64_t count) { return given ? 0 : (count + 3) / 4 * 4; };
     const int64_t all = room(cu_, n + 1) + room(lens_, n) + room(used_, 2) + room(positions_, tokens) + room(slots_, tokens);
-    const at::Tensor whole = all ? empty({all}, past, at::kInt) : at::Tensor();
+    const at::Tensor whole = empty({all}, past, at::kInt);
     const auto cut = [&](const Opt &given, at::IntArrayRef shape, at::IntArrayRef strides, int64_t count) {
         if (given) return *given;
         const at::Tensor t = whole.as_strided(shape, strides, at);

@@ -92,6 +92,29 @@ def test_tokens_of_a_call(lib):  # noqa: F811
     assert got[0] == ESHAPE and "2^30" in got[1], got
 
 
+@pytest.mark.parametrize("B", [0, 1])
+def test_calls_without_a_token(lib, B):  # noqa: F811
+    """No batch, or rows of no token: nothing is divided by, and only the device check stops the call."""
+    A, size = Alloc2(), ctypes.c_int64(-1)
+    q, k = (A(BF, [B, 0, h, D]) for h in (HQ, HK))
+    got = call(lib, "attn_fwd", [q, k, k, None, None, q, None], 1, 0, 1.0, None, None)
+    assert got[0] == EDEVICE, got
+    lse = A(GDR_F32, [B, 0, HQ])
+    got = call(lib, "attn_bwd", [q, k, k, None, None, q, lse, q, q, k, k], 1, 0, 1.0, None, ctypes.addressof(size))
+    assert got[0] == 0 and size.value == 0, got
+    d = dict(q=A(BF, [0, HQ, D]), kp=A(BF, [0, 16, HK, D]), vp=A(BF, [0, 16, HK, D]), table=A(GDR_I32, [0, 0]),
+             lens=A(GDR_I32, [0]), o=A(BF, [0, HQ, D]))
+    assert call(lib, "attn_paged_step", list(d.values()), 0, 1.0, None, None)[0] == EDEVICE
+
+
+def test_blocks_of_a_call(lib):  # noqa: F811
+    A, n = Alloc2(), 1 << 22
+    d = dict(q=A(BF, [n, 1, 1024, D]), k=A(BF, [n, 1, 1024, D]), v=A(BF, [n, 1, 1024, D]), cu=None, cuk=None,
+             o=A(BF, [n, 1, 1024, D]), lse=None)
+    got = call(lib, "attn_fwd", list(d.values()), 1, 0, 1.0, None, None)
+    assert got[0] == ESHAPE and "blocks" in got[1], got
+
+
 @pytest.mark.parametrize("change,status,text", INPUTS + [
     (lambda d, A: d.update(o=None), EINVAL, "o: descriptor is NULL"),
     (lambda d, A: d.update(lse=None), EINVAL, "lse: descriptor is NULL"),

@@ -81,6 +81,8 @@ def run(dev, dbl, cu, cuk, dtype, scale=None, **kw):
     check("lse", lse.cpu().masked_fill(empty, 0), *held(rl.masked_fill(empty, 0), tl))
     # the gradient from o and lse as the definition gives them, rounded to what the forward stores
     gave = ro.nan_to_num().to(dtype).cuda(), rl.nan_to_num(neginf=-torch.inf).float().cuda()
+    if not dev["q"].is_contiguous():   # o as rows of something wider too
+        gave = torch.cat([gave[0], gave[0]], 2)[:, :, :gave[0].shape[2]], gave[1]
     outs = [torch.full_like(dev[n].contiguous(), 7) for n in ("q", "k", "v")]
     grads = gdr.attn_bwd(dev["q"], dev["k"], dev["v"], *gave, dev["do"], C, CK, scale=scale, dq=outs[0], dk=outs[1],
                          dv=outs[2], **kw)
@@ -98,9 +100,10 @@ def test_packed(lq, lk, hq, hk, d, dtype, causal, window, wide):
     run(dev, dbl, offsets(lq), offsets(lk), dtype, causal=causal, window=window)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("B,Tq,Tk,hq,hk,d,dtype,causal,window", ROWS)
-def test_rows(B, Tq, Tk, hq, hk, d, dtype, causal, window):
-    dev, dbl = make(B, Tq, Tk, hq, hk, d, dtype, seed=2)
+def test_rows(B, Tq, Tk, hq, hk, d, dtype, causal, window, wide):
+    dev, dbl = make(B, Tq, Tk, hq, hk, d, dtype, seed=2, wide=wide)
     run(dev, dbl, None, None, dtype, causal=causal, window=window)
 
 
@@ -315,6 +318,49 @@ def test_graph_on_another_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(bits(a), bits(b)) for a, b in zip(got, want))
         assert all(sound(x).all() for x in eager)
+
+
+def test_calls_on_two_streams():
+    """The library's workspace is handed from one stream's call to the other's in order."""
+    import chunked_gated_delta_fwd_amd as gdr
+    sets = [make(1, 700, 700, 8, 1, 128, BF, seed=s)[0] for s in (21, 22)]
+
+    def call(x):
+        o, lse = gdr.attn_fwd(x["q"], x["k"], x["v"])
+        return [o, lse] + list(gdr.attn_bwd(x["q"], x["k"], x["v"], o, lse, x["do"]))
+
+    want = [call(x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(5):
+        for i, (s, x) in enumerate(zip(streams, sets)):
+            with torch.cuda.stream(s):
+                got[i].append(call(x))
+    torch.cuda.synchronize()
+    for runs, w in zip(got, want):
+        for run_ in runs:
+            assert all(torch.equal(bits(a), bits(b)) for a, b in zip(run_, w))
+
+
+def test_few_queries_over_many_keys():
+    """The keys are split in runs (one of them without a key that a row sees) and joined, NaN and all."""
+    import chunked_gated_delta_fwd_amd as gdr
+    for dtype in (BF, F):
+        for cu, cuk, kw in (([0, 5, 6], [0, 3000, 3900], dict()), (None, None, dict(causal=False)), ([0, 0, 64], [0, 100, 2600], dict(window=900))):
+            Tq, Tk = (cu[-1], cuk[-1]) if cu else (9, 4000)
+            dev, dbl = make(1, Tq, Tk, 4, 2, 64, dtype, seed=23)
+            o, lse = gdr.attn_fwd(dev["q"], dev["k"], dev["v"], ints(cu), ints(cuk), **kw)
+            ro, rl, to, tl = ref.attention(dbl["q"], dbl["k"], dbl["v"], cu, cuk, dtype=dtype, **kw)
+            check("o", o, ro, to)
+            check("lse", lse, rl, tl)
+            v = dev["v"].clone()
+            v[0, Tk - 1, 0, 3] = float("nan")            # seen by the last row alone where causal
+            bad, _ = gdr.attn_fwd(dev["q"], dev["k"], v, ints(cu), ints(cuk), **kw)
+            rows = slice(Tq - 1, Tq) if kw.get("causal", True) else slice(0, Tq)
+            assert not torch.isfinite(bad[0, rows, :2, 3]).any()
+            bad[0, rows, :2, 3] = o[0, rows, :2, 3]
+            check("o beside a NaN", bad, ro, to)
 
 
 def test_rows_far_apart():

@@ -247,6 +247,20 @@ def test_store(B, T, hk, d, page, dtype):
         assert torch.equal(pages.view(torch.int16), w.view(torch.int16))
 
 
+def test_plan_into_given_tensors():
+    import chunked_gated_delta_fwd_amd as gdr
+    want = gdr.page_plan(ints([3, 0]), ints([2, 5]), ints([7, 8, 9]), torch.full((2, 4), 1, dtype=torch.int32, device="cuda"), 4, 7)
+    outs = [torch.full_like(x, 77) for x in want]
+    for given in (dict(zip(("cu_seqlens", "lens", "positions", "slots", "used"), outs)), dict(lens=outs[1], slots=outs[3])):
+        got = gdr.page_plan(ints([3, 0]), ints([2, 5]), ints([7, 8, 9]), torch.full((2, 4), 1, dtype=torch.int32, device="cuda"),
+                            4, 7, **given)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert got[1].data_ptr() == outs[1].data_ptr() and all(x.is_contiguous() for x in got)
+    some = dict(cu_seqlens=outs[0], lens=outs[1], used=outs[4])
+    got = gdr.page_plan(ints([3, 0]), ints([0, 0]), ints([7]), torch.full((2, 4), 1, dtype=torch.int32, device="cuda"), 4, 0, **some)
+    assert got[2].shape == got[3].shape == (1, 0) and got[4].tolist() == [0, 0]
+
+
 def test_refusals():
     import chunked_gated_delta_fwd_amd as gdr
     kp, vp, table = pages_of([40], 16, 2, 64, BF)
@@ -267,6 +281,7 @@ def test_refusals():
             (lambda: gdr.page_plan(L, ints([1]), T[0], T, 16, 4), "block_table overlaps free_pages"),
             (lambda: gdr.page_plan(L, ints([1]), L, T, 0, 4), "page"),
             (lambda: gdr.page_plan(L, ints([1]), L, T, 2 ** 32 + 16, 4), "page"),
-            (lambda: gdr.page_plan(L, ints([1]), L, T, 16, -1), "tokens")):
+            (lambda: gdr.page_plan(L, ints([1]), L, T, 16, -1), "tokens"),
+            (lambda: gdr.page_plan(L, ints([1]), L, T, 16, 2 ** 40), "tokens")):
         with pytest.raises(gdr.GdrError, match=text):
             call()
