@@ -72,6 +72,7 @@ struct AttnFwd {
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks) s[t] = T::mma(Tile::rows(lds.k[buf], l, 32 * t, ks), w.q[ks], s[t]);
             }
+            attn_ahead<T, kSub * kSteps>();
             const bool whole = sight.all(lo, hi, j, kKeys);
             if (!whole) {
                 const int32_t d0 = attn_here(at - j - 4 * h);

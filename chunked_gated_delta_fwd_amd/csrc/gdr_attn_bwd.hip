@@ -68,6 +68,7 @@ struct AttnDq {
                 for (int ks = 0; ks < kSteps; ++ks) s = T::mma(Tile::rows(lds.k[buf], l, 32 * u, ks), w.q[ks], s);
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks) dp = T::mma(Tile::rows(lds.v[buf], l, 32 * u, ks), w.dout[ks], dp);
+                attn_ahead<T, 2 * kSteps>();
                 const bool whole = sight.all(lo, hi, ju, 32);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = fast_exp2(__builtin_fmaf(s[r], c, -w.lse)) * (dp[r] - w.delta);
