@@ -299,7 +299,7 @@ struct AttnDkv {
                     for (int ks = 0; ks < kSteps; ++ks)
                         dp[u] = T::mma(Tile::rows(lds.dout[buf], l, 32 * u, ks), Tile::rows(lds.v, mine, 0, ks), dp[u]);
                 }
-                const bool whole = sight.all(i, last, lo, 32);
+                const bool whole = last == i + kQueries - 1 && sight.all(i, last, lo, 32);
                 __builtin_amdgcn_sched_barrier(0);   // rows' statistics wait: earlier they cost spilled operands
                 const char *stats = reinterpret_cast<const char *>(lds.lse[buf]) + mine.across;
 #pragma unroll
@@ -314,12 +314,15 @@ struct AttnDkv {
                     }
                 }
                 if (!whole) {
-                    const int32_t i4 = attn_here(i + 4 * h);
+                    // rows behind the last are zeros, but a zero times a key that is not finite is not
+                    const int32_t i4 = attn_here(i + 4 * h), rows = from.lq - i4;
 #pragma unroll
                     for (int u = 0; u < kSub; ++u)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (!sight.sees(sight.at(i4 + 32 * u + 8 * (r / 4) + r % 4), j)) p[u][r] = dp[u][r] = 0.f;
+                        for (int r = 0; r < 16; ++r) {
+                            const int x = 32 * u + 8 * (r / 4) + r % 4;
+                            if (x >= rows || !sight.sees(sight.at(i4 + x), j)) p[u][r] = dp[u][r] = 0.f;
+                        }
                 }
                 // bf16: p and ds are rounded to nearest for the products over the queries
 #pragma unroll
@@ -334,7 +337,7 @@ struct AttnDkv {
                     } else {
                         for (int row = 0; row < 16; ++row) {
                             const int slot = (row >> 2 & 1) == h ? (row & 3) + (row >> 1 & 4) : -1;
-                            const bool seen = sight.sees(sight.at(i + 16 * kb + row), j);
+                            const bool seen = i + 16 * kb + row < from.lq && sight.sees(sight.at(i + 16 * kb + row), j);
 #pragma unroll
                             for (int t = 0; t < kParts; ++t) {
                                 const f32x16 x = T::mma(T::only(Tile::across(lds.dout[buf], l, 16 * kb, t), slot),

@@ -251,6 +251,27 @@ def test_values_that_are_not_finite_reach_who_sees_them(dtype, value, window):
                 assert not sound(a[0, r]).all(-1).any(), (name, what)
 
 
+@pytest.mark.parametrize("lq", [1, 33, 130])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_a_key_of_infinity_that_nothing_is_put_on(dtype, d, lq):
+    """Scores of -inf are probabilities of 0, and gradients of 0 for that key, in tiles that the queries end in too: dk and dv
+    are what a score far below the others gives, to the bit."""
+    import chunked_gated_delta_fwd_amd as gdr
+    dev, _ = make(1, lq, 40, 2, 1, d, dtype, seed=17)
+    dev["q"][..., 0] = 1.0
+    got = []
+    for value in (-1e30, -float("inf")):
+        k = dev["k"].clone()
+        k[0, 7, 0, 0] = value
+        o, lse = gdr.attn_fwd(dev["q"], k, dev["v"], causal=False)
+        dq, dk, dv = gdr.attn_bwd(dev["q"], k, dev["v"], o, lse, dev["do"], causal=False)
+        assert all(sound(x).all() for x in (o, lse, dk, dv))
+        assert not dk[0, 7].any() and not dv[0, 7].any()
+        got.append([bits(x) for x in (o, lse, dk, dv)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_offsets_that_break_the_rules_stay_inside():
     """Whatever cu_seqlens holds, nothing outside the tensors is touched (guards around every output keep their bytes)."""
     import chunked_gated_delta_fwd_amd as gdr
