@@ -20,10 +20,12 @@ struct AttnArgs {
     int32_t hq, hk, d, bf16, causal;
     int64_t window;              // keys that a query sees back from its own place, itself included; 0: all
     float scale;
-    // Forward: the keys of a block are split in `splits` runs at most, each of at least `least` tiles, whose
-    // outputs before they are scaled and whose reference and sum are joined by a second kernel.
-    int32_t splits, least;
-    float *run_o, *run_stat;     // [splits][total_q][hq][d], [splits][total_q][hq][2]; splits 1: none
+    // Forward: the keys of the blocks from `whole` (a multiple of 8 team) on are split in `splits` runs at most, each of
+    // at least `least` tiles, whose outputs before they are scaled and whose reference and sum are joined by a second
+    // kernel.  An XCD takes a split of `team` blocks, which share their keys, then the next one.
+    int32_t splits, least, team, run_rows;
+    int64_t whole;
+    float *run_o, *run_stat;     // [blocks from `whole` on][run_rows][d], .. [2]; splits 1: none
     // backward
     const void *dout;            // rows lddo apart
     int64_t lddo;
@@ -52,8 +54,9 @@ inline double attn_blocks(bool packed, double sequences, double rows) {
     if (packed) return sequences * (rows < kAttnRows / 2 ? 1.0 : rows / kAttnRows + 0.5);
     return sequences * static_cast<double>((static_cast<int64_t>(rows) + kAttnRows - 1) / kAttnRows);
 }
-// Sets splits and least.
+// Sets how the keys are split.
 void attn_split(AttnArgs &a);
+int64_t attn_cut_blocks(const AttnArgs &a);   // blocks whose keys are split
 // Blocks of the largest launch of a call; more than 2^31 - 1 cannot be launched.
 int64_t attn_fwd_grid(const AttnArgs &a);
 int64_t attn_bwd_grid(const AttnArgs &a);

@@ -141,6 +141,13 @@ __device__ __forceinline__ float attn_lse(float ref, float sum) {
     return sum == 0.f ? -__builtin_inff() : (ref + __builtin_log2f(sum)) * 0.69314718055994530942f;
 }
 
+// The block that this launched one is a split of: an XCD takes the first split
+// of a team of blocks, then the second, and so on.
+__device__ __forceinline__ uint32_t attn_cut(const AttnArgs &a, uint32_t &split) {
+    const uint32_t at = (blockIdx.x - static_cast<uint32_t>(a.whole)) / 8, runs = a.team * a.splits;
+    split = __builtin_amdgcn_readfirstlane(at % runs / a.team);
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a.whole) + 8 * (at / runs * a.team + at % a.team) + blockIdx.x % 8);
+}
 // The run of key tiles that one of a block's splits walks, of `count` in all.
 struct AttnRun {
     int32_t first, last, count;   // tiles first .. last - 1; count: runs that hold any
@@ -186,19 +193,19 @@ __device__ __forceinline__ bool attn_fwd_block(const AttnArgs &a, uint32_t tiles
     typedef typename T::F8 F8;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
-    AttnItem item = attn_item(blockIdx.x, pairs, tiles, group * a.splits);
-    const int32_t split = item.way / group;
-    item.way %= group;
+    const bool cut = a.splits > 1 && blockIdx.x >= static_cast<uint32_t>(a.whole);
+    uint32_t block = blockIdx.x, split = 0;
+    if (cut) block = attn_cut(a, split);
     AttnBlock b;
-    if (!attn_block<F::kKeys>(a, item, lane, b)) return false;
+    if (!attn_block<F::kKeys>(a, attn_item(block, pairs, tiles, group), lane, b)) return false;
     const AttnSeq &seq = b.seq;
     const AttnSight sight(a, seq);
     const int32_t i0 = b.i0, i1 = b.i1, hk = b.hk, hq = b.hq;
     int32_t begin = b.begin, end = b.end;
     bool alone = true;
-    if (a.splits > 1) {
-        const AttnRun run = attn_run(a, begin < end ? (end - begin + F::kKeys - 1) / F::kKeys : 0, split);
-        if (split >= run.count) return false;
+    if (cut) {
+        const AttnRun run = attn_run(a, begin < end ? (end - begin + F::kKeys - 1) / F::kKeys : 0, static_cast<int32_t>(split));
+        if (static_cast<int32_t>(split) >= run.count) return false;
         alone = run.count == 1;
         end = begin + run.last * F::kKeys < end ? begin + run.last * F::kKeys : end;
         begin += run.first * F::kKeys;
@@ -228,15 +235,15 @@ __device__ __forceinline__ bool attn_fwd_block(const AttnArgs &a, uint32_t tiles
     const int32_t i = i0 + 32 * wave + col;
     const float sum = half_sum(w.sum);
     if (i >= seq.lq) return false;
-    const int64_t row = (seq.q0 + i) * a.hq + hq;
     if (alone) {
+        const int64_t row = (seq.q0 + i) * a.hq + hq;
         // no key seen (or scores of -inf alone): 0, and NaN stays NaN
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int t = 0; t < F::kParts; ++t) attn_store<T>(static_cast<E *>(a.o) + row * D + 32 * t, w.o[t], inv, h);
         if (a.lse && h == 0) a.lse[row] = attn_lse(w.ref, sum);
     } else {
-        const int64_t at = split * a.total_q * a.hq + row;
+        const int64_t at = (blockIdx.x - a.whole) * a.run_rows + i - i0;
 #pragma unroll
         for (int t = 0; t < F::kParts; ++t) attn_store<AttnF32>(a.run_o + at * D + 32 * t, w.o[t], 1.f, h);
         if (h == 0) {
@@ -260,32 +267,36 @@ __global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_att
 }
 
 // Joins a block's runs: 4 channels a thread, 8 rows (d 64: 16) at a time, the
-// rows shared by the blocks along y.
+// rows shared by the launch's blocks along y.
 template <class T, int D>
 __global__ __launch_bounds__(256) void gdr_attn_runs_kernel(AttnArgs a, uint32_t tiles) {
     typedef typename T::E E;
     constexpr int kThreads = D / 4;
     const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
     AttnBlock b;
-    if (!attn_block<AttnFwd<T, D>::kKeys>(a, attn_item(blockIdx.x, pairs, tiles, group), threadIdx.x & 63, b)) return;
+    if (!attn_block<AttnFwd<T, D>::kKeys>(a, attn_item(static_cast<uint32_t>(a.whole) + blockIdx.x, pairs, tiles, group), threadIdx.x & 63, b)) return;
     constexpr int kKeys = AttnFwd<T, D>::kKeys;
     const int32_t count = attn_run(a, b.begin < b.end ? (b.end - b.begin + kKeys - 1) / kKeys : 0, 0).count;
     if (count == 1) return;
     const int channel = threadIdx.x % kThreads * 4;
-    const int64_t step = a.total_q * a.hq;
+    // launched blocks of the runs: attn_cut's inverse
+    const uint32_t place = blockIdx.x / 8;
+    const int64_t slab = (static_cast<int64_t>(place / a.team) * a.splits * a.team + place % a.team) * 8 + blockIdx.x % 8;
+    const int64_t step = 8 * static_cast<int64_t>(a.team) * a.run_rows;
     for (int32_t i = b.i0 + (blockIdx.y * 256 + threadIdx.x) / kThreads; i <= b.i1; i += gridDim.y * 256 / kThreads) {
-        const int64_t row = (b.seq.q0 + i) * a.hq + b.hq;
+        const int64_t row = (b.seq.q0 + i) * a.hq + b.hq, at = slab * a.run_rows + i - b.i0;
+        const float *stat = a.run_stat + 2 * at, *out = a.run_o + at * D + channel;
         float top = -__builtin_inff();
 #pragma unroll 4
-        for (int32_t s = 0; s < count; ++s) top = fmaxf(top, a.run_stat[2 * (s * step + row)]);
+        for (int32_t s = 0; s < count; ++s) top = fmaxf(top, stat[2 * s * step]);
         const float base = top == -__builtin_inff() ? 0.f : top;
         float total = 0.f;
         f32x4 x = zero4();
 #pragma unroll 4
         for (int32_t s = 0; s < count; ++s) {
-            const float f = fast_exp2(a.run_stat[2 * (s * step + row)] - base);
-            total = __builtin_fmaf(f, a.run_stat[2 * (s * step + row) + 1], total);
-            x += f * *reinterpret_cast<const f32x4 *>(a.run_o + (s * step + row) * D + channel);
+            const float f = fast_exp2(stat[2 * s * step] - base);
+            total = __builtin_fmaf(f, stat[2 * s * step + 1], total);
+            x += f * *reinterpret_cast<const f32x4 *>(out + s * step * D);
         }
         x *= total == 0.f ? 0.f : 1.f / total;
         E *o = static_cast<E *>(a.o) + row * D + channel;
@@ -298,18 +309,27 @@ __global__ __launch_bounds__(256) void gdr_attn_runs_kernel(AttnArgs a, uint32_t
 template <class T, int D>
 hipError_t run(const AttnArgs &a, hipStream_t stream) {
     const int64_t tiles = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
-    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
-    const int64_t join = attn_grid(pairs, tiles, group);
     gdr_attn_fwd_kernel<T, D><<<dim3(static_cast<unsigned>(attn_fwd_grid(a))), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
     if (a.splits > 1)
-        gdr_attn_runs_kernel<T, D><<<dim3(static_cast<unsigned>(join), D / 8), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
+        gdr_attn_runs_kernel<T, D><<<dim3(static_cast<unsigned>(attn_cut_blocks(a)), D / 8), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles));
     return hipGetLastError();
 }
 
 }  // namespace
 
-// The runs that cost least by attn_time; a tile of keys as measured on large
-// calls.  Their outputs go through the caches at 6 TB/s, the second launch takes 5 us.
+namespace {
+int64_t all_blocks(const AttnArgs &a) {
+    return attn_grid((a.cu ? 1 : a.n_seq) * a.hk, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q), a.hq / a.hk);
+}
+}  // namespace
+
+// The runs that cost least by attn_time, of all blocks' keys or, where blocks of
+// one length fill the chip some times, of those that are left for a last round;
+// a tile of keys as measured on large calls.  Runs' outputs go through the
+// caches at 6 TB/s, the second launch takes 5 us.  About 512 queries in each of 8
+// sequences, 4000 keys before them, 16 heads on 2, d 128 (about 580 blocks, 512
+// at a time): 222 us with all blocks' keys whole or all split, 188 with the last
+// blocks' split.
 void attn_split(AttnArgs &a) {
     const int32_t keys = a.bf16 ? 64 : 32;
     const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{768, 1.95, 0.9} : AttnCost{512, 2.2, 1.35})
@@ -321,25 +341,39 @@ void attn_split(AttnArgs &a) {
     double most = lk, mean = a.causal ? lk - (lq < lk ? lq : lk) / 2 : lk;
     if (a.window > 0 && a.window + kAttnRows < most) most = a.window + kAttnRows;
     if (mean > most) mean = most;
-    const double tiles = most / keys + 1;
-    double best = 0;
-    a.splits = 1;
-    a.least = 1;
-    for (int32_t s = 1; s <= 64 && (s == 1 || tiles / s >= 4); s += s < 4 ? 1 : s < 16 ? 2 : 8) {
-        double t = attn_time(cost, blocks * s, (mean / keys + 1) / s, tiles / s);
-        if (s > 1) t += 5 + 8.0 * a.total_q * a.hq * a.d * s / 6e6;
-        if (s == 1 || t < 0.95 * best) {
-            best = t;
-            a.splits = s;
-            a.least = static_cast<int32_t>(tiles / s + 0.999);
+    const double tiles = most / keys + 1, steps = mean / keys + 1;
+    const double rounds = mean > 0.9 * most ? static_cast<double>(static_cast<int64_t>(blocks / cost.slots)) : 0;
+    double best = attn_time(cost, blocks, steps, tiles);
+    a.splits = a.least = 1;
+    a.whole = 0;
+    // teams share their keys; where attn_item deals pairs to XCDs, whole ones end at its last block
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk, group = a.hq / a.hk;
+    a.team = static_cast<int32_t>(pairs % 8 == 0 ? group : pairs * group > 8 ? pairs * group / 8 : 1);
+    const int64_t team = 8 * static_cast<int64_t>(a.team);
+    for (int last = 0; last < (rounds > 0 ? 2 : 1); ++last) {
+        const double before = last ? rounds * cost.slots : 0, rest = blocks - before;
+        for (int32_t s = 2; s <= 64 && tiles / s >= 4 && rest > 0.5; s += s < 4 ? 1 : s < 16 ? 2 : 8) {
+            const double t = before / cost.slots * cost.full * steps + attn_time(cost, rest * s, steps / s, tiles / s) + 5 +
+                             8.0 * a.total_q * a.hq * a.d * s * (rest / blocks) / 6e6;
+            if (t < 0.95 * best) {
+                best = t;
+                a.splits = s;
+                a.least = static_cast<int32_t>(tiles / s + 0.999);
+                a.whole = static_cast<int64_t>(all_blocks(a) * (before / blocks)) / team * team;
+            }
         }
     }
+    const int64_t rows = a.cu ? a.total_q : a.seq_q;
+    a.run_rows = static_cast<int32_t>(rows < kAttnRows ? rows : kAttnRows);
 }
 
-int64_t attn_fwd_grid(const AttnArgs &a) {
-    return attn_grid((a.cu ? 1 : a.n_seq) * a.hk, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q),
-                     static_cast<int64_t>(a.hq / a.hk) * a.splits);
+int64_t attn_cut_blocks(const AttnArgs &a) {
+    if (a.splits == 1) return 0;
+    const int64_t team = 8 * static_cast<int64_t>(a.team);
+    return (all_blocks(a) - a.whole + team - 1) / team * team;
 }
+
+int64_t attn_fwd_grid(const AttnArgs &a) { return a.splits == 1 ? all_blocks(a) : a.whole + attn_cut_blocks(a) * a.splits; }
 
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream) {
     if (a.bf16) return a.d == 64 ? run<AttnBf, 64>(a, stream) : run<AttnBf, 128>(a, stream);

@@ -131,7 +131,7 @@ int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v, 
         if ((rc = fits(gdr::attn_fwd_grid(a)))) return rc;
         Carve sizes{nullptr};
         const auto carve = [&](Carve &w) {
-            const int64_t runs = a.splits > 1 ? a.splits * a.total_q * a.hq : 0;
+            const int64_t runs = gdr::attn_cut_blocks(a) * a.splits * a.run_rows;
             a.run_o = w.take<float>(runs * a.d);
             a.run_stat = w.take<float>(runs * 2);
         };

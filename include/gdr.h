@@ -532,9 +532,9 @@ int gdr_ssm_step(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
  * rounded to bf16 for the product with v, o is rounded once, lse is fp32.  f32
  * inputs: fp32 products throughout.  A k or v that is not finite reaches the
  * queries that see it and no others; a query whose scores are all -inf counts
- * as one that sees no key.  Where a call has few queries for its keys, the keys
- * are split in runs; workspace then: 4 (d + 2) bytes a run, query and query
- * head, else none.  q, k, v rows and o on 16-byte
+ * as one that sees no key.  Where a call has few blocks of 128 queries for
+ * the chip, or a few left over, the keys of those are split in runs; workspace
+ * then: 4 (d + 2) bytes a run, query and query head of such a block, else none.  q, k, v rows and o on 16-byte
  * addresses, rows at most 32 MiB apart, at most 2^30 tokens.  Errors as
  * gdr_chunk_fwd, GDR_EINVAL for a negative window or one without causal.
  */

@@ -115,6 +115,22 @@ def test_blocks_of_a_call(lib):  # noqa: F811
     assert got[0] == ESHAPE and "blocks" in got[1], got
 
 
+def test_forward_workspace(lib):  # noqa: F811
+    """None where the blocks of a call fill the chip or their keys are few; for the runs of every block where a few queries
+    stand before many keys; for those of the last ones where 540 blocks of one length come to 512 at a time."""
+    def need(Tq, Tk, hq, hk, d):
+        A, size = Alloc2(), ctypes.c_int64(-1)
+        got = call(lib, "attn_fwd", [A(BF, [1, Tq, hq, d]), A(BF, [1, Tk, hk, d]), A(BF, [1, Tk, hk, d]), None, None,
+                                     A(BF, [1, Tq, hq, d]), None], 0, 0, 1.0, None, ctypes.addressof(size))
+        assert got[0] == 0, got
+        return size.value
+    assert need(T, S, HQ, HK, D) == 0
+    assert need(128 * 64, 8192, 16, 4, 128) == 0                       # 1024 blocks
+    assert need(1, 8192, 16, 4, 128) >= 2 * 4 * (128 + 2) * 16         # two runs at least, of every row
+    last = need(128 * 27, 8192, 20, 5, 128)
+    assert 2 * 28 * 128 * 4 * (128 + 2) <= last < 540 * 128 * 4 * (128 + 2)
+
+
 @pytest.mark.parametrize("change,status,text", INPUTS + [
     (lambda d, A: d.update(o=None), EINVAL, "o: descriptor is NULL"),
     (lambda d, A: d.update(lse=None), EINVAL, "lse: descriptor is NULL"),

@@ -384,6 +384,49 @@ def test_few_queries_over_many_keys():
             check("o beside a NaN", bad, ro, to)
 
 
+LAST = [   # lengths of queries, of keys, hq, hk, d, dtype, causal: some more blocks of one length than the chip holds at once
+    ([3451], [1500], 20, 5, 128, BF, False),
+    ([1111, 1, 2300, 788], [600, 0, 600, 600], 8, 2, 64, F, False),
+    ([2176, 2176], [9000, 9001], 24, 8, 64, BF, True),
+]
+
+
+@pytest.mark.parametrize("lq,lk,hq,hk,d,dtype,causal", LAST)
+def test_keys_of_the_last_blocks_alone_are_split(lq, lk, hq, hk, d, dtype, causal):
+    """Where some blocks are left when the chip was full: on one head of each group (the reference's time), o and lse."""
+    import chunked_gated_delta_fwd_amd as gdr
+    cu, cuk = offsets(lq), offsets(lk)
+    dev, dbl = make(1, cu[-1], cuk[-1], hq, hk, d, dtype, seed=29)
+    dev["v"][0, -1, 0, 3] = dbl["v"][0, -1, 0, 3] = 0.0
+    o, lse = gdr.attn_fwd(dev["q"], dev["k"], dev["v"], ints(cu), ints(cuk), causal=causal)
+    heads = [g * (hq // hk) + g % (hq // hk) for g in range(hk)]
+    for g, h in list(enumerate(heads))[::3]:
+        ro, rl, to, tl = ref.attention(dbl["q"][:, :, h:h + 1], dbl["k"][:, :, g:g + 1], dbl["v"][:, :, g:g + 1], cu, cuk,
+                                       causal=causal, dtype=dtype)
+        check("o", o[:, :, h:h + 1], ro, to)
+        none = rl == -torch.inf                          # a sequence without keys
+        got = lse[:, :, h:h + 1].cpu()
+        assert torch.equal(got == -torch.inf, none)
+        check("lse", got[~none], rl[~none], tl[~none])
+    # every other head: the same rows in a call of its own, whose blocks are split otherwise
+    for h in range(hq):
+        g = h // (hq // hk)
+        alone, _ = gdr.attn_fwd(dev["q"][:, :, h:h + 1].contiguous(), dev["k"][:, :, g:g + 1].contiguous(),
+                                dev["v"][:, :, g:g + 1].contiguous(), ints(cu), ints(cuk), causal=causal)
+        # each within its tolerance of the value, with the largest |v| for the sums of p |v| and of o, and 30 for those of
+        # scale |q k|, whose mean is 15 at most
+        H, U = (2.0 ** -8 if dtype == BF else 0.0), 2.0 ** -24
+        E = 2 * (d + 12) * U * 30 + 8 * U * (1 + 30)
+        assert ((o[:, :, h:h + 1] - alone).float().abs() <= 2 * (2 * H + E + (max(lk) + 20) * U) * 6).all()
+    bad = dev["v"].clone()
+    bad[0, -1, 0, 3] = float("nan")                      # the last sequence's last key: its rows, of the first group's heads
+    got, _ = gdr.attn_fwd(dev["q"], dev["k"], bad, ints(cu), ints(cuk), causal=causal)
+    rows = slice(cu[-1] - 1, cu[-1]) if causal else slice(cu[-2], cu[-1])
+    assert not torch.isfinite(got[0, rows, :hq // hk, 3]).any()
+    got[0, rows, :hq // hk, 3] = o[0, rows, :hq // hk, 3]
+    assert sound(got).all()
+
+
 def test_rows_far_apart():
     """Keys 4 MiB apart: their places pass 2^31 bytes within one sequence."""
     import chunked_gated_delta_fwd_amd as gdr
