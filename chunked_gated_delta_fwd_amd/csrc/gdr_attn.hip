@@ -14,6 +14,12 @@ namespace {
 // query's scores and the maximum and sum cross lanes once a tile, and the
 // result registers are the next product's operand.  The next tile's keys and
 // values load to LDS while this one is worked on.
+//
+// Bound by the matrix unit and the exponentials between its two products, which
+// the second wave of a SIMD fills in part.  2 x 8192 tokens, 32 heads on 4,
+// causal, bf16: d 128 1.00 to 1.05 ms, 1050 to 1100 TFLOP/s of the 1251 of a
+// large matrix product; d 64 920 (twice the exponentials a product).  f32, d 128:
+// 109 of 153.
 template <class T, int D>
 struct AttnFwd {
     typedef typename T::E E;
@@ -266,7 +272,8 @@ __global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_att
     if (attn_fwd_block<T, D, false>(a, tiles, lds)) attn_fwd_careful<T, D>(attn_args_at(), tiles, attn_lds(lds));
 }
 
-// Joins a block's runs: 4 channels a thread, 8 rows (d 64: 16) at a time, the
+// Joins a block's runs, bound by their loads and a launch (8 pieces of 512
+// queries: 8.8 us beside the runs' 197): 4 channels a thread, 8 rows (d 64: 16) at a time, the
 // rows shared by the launch's blocks along y.
 template <class T, int D>
 __global__ __launch_bounds__(256) void gdr_attn_runs_kernel(AttnArgs a, uint32_t tiles) {

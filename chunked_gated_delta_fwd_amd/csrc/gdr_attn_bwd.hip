@@ -8,12 +8,16 @@
 // that holds query rows and walks the keys (dq, delta), one that holds key rows
 // and walks the queries (dk, dv): scores and do . v are made twice, seven
 // products for five, so that every sum stays in registers in a fixed order.
+//
+// 4 x 4096 tokens, 32 heads on 4, d 128, causal, bf16: 1.88 ms a call, the first
+// pass 0.79 (3 products, 1040 TFLOP/s), the second 1.12 (4 products, 990).
 #include "gdr_attn_device.h"
 
 namespace gdr {
 namespace {
 
-// dq: a block takes 128 query rows of one head, 32 a wave, as the forward does.
+// dq: a block takes 128 query rows of one head, 32 a wave, as the forward does,
+// and is bound as it is, with no maximum to keep: 3 products a pair and head.
 template <class T, int D>
 struct AttnDq {
     typedef typename T::E E;
@@ -224,7 +228,10 @@ __global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_att
 }
 
 // dk and dv: a block takes 128 key rows of one key head, 32 a wave, and walks
-// the query rows that see them, head after head of its part of the group.
+// the query rows that see them, head after head of its part of the group.  Keys
+// and both sums fill the registers (256 at d 128), so the block's values lie in
+// LDS and are read again each tile: 4 products a pair and head, bound by them
+// and LDS reads (five operands for four products).
 template <class T, int D>
 struct AttnDkv {
     typedef typename T::E E;
@@ -456,7 +463,9 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(Att
     if (attn_dkv_block<T, D, false>(a, tiles, lds)) attn_dkv_careful<T, D>(attn_args_at(), tiles, attn_lds(lds));
 }
 
-// Sums the parts of dk and dv in order, for the rows of one tile's sequence.
+// Sums the parts of dk and dv in order, for the rows of one tile's sequence;
+// bound by their loads from the caches (16384 keys, 4 heads, two parts of 128
+// channels: 27 us).
 template <class T>
 __global__ __launch_bounds__(256) void gdr_attn_join_kernel(AttnArgs a, uint32_t tiles) {
     const int lane = threadIdx.x & 63;
