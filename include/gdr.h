@@ -553,11 +553,12 @@ int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
  *
  * The probabilities are made again from q, k and lse.  bf16 inputs: they and
  * the scores' gradients are rounded to bf16 for the products over queries and
- * keys; sums are fp32 and each gradient is rounded once.  Whatever is not
- * finite reaches the rows whose sums hold it and no others.  Workspace: 8 bytes
- * a query and query head, and 8 d bytes a key, key head and part where several
- * blocks share a group's heads (small calls; as many parts at most as a group
- * has heads).
+ * keys; sums are fp32 and each gradient is rounded once.  do . o is taken from
+ * o as it is given, for blocks of 128 queries that see 192 keys at most from
+ * the scores' gradients, which sum to zero.  Whatever is not finite reaches the
+ * rows whose sums hold it and no others.  Workspace: 8 bytes a query and query
+ * head, and 8 d bytes a key, key head and part where several blocks share a
+ * group's heads (small calls; as many parts at most as a group has heads).
  */
 int gdr_attn_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
                  const gdr_tensor *cu_seqlens, const gdr_tensor *cu_seqlens_k, const gdr_tensor *o,
