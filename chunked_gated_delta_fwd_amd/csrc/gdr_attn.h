@@ -31,8 +31,11 @@ struct AttnArgs {
     int64_t lddo;
     void *dq, *dk, *dv;          // compact
     float *stat;                 // [2][hq][total_q]: lse in powers of two, and do . o
-    float *part;                 // [parts][2][total_k][hk][d]: sums of dk and dv over a part of a group; NULL: one part
-    int32_t parts;
+    // Where blocks are few, `parts` of them share a key block: its group's heads, and then `runs` the queries of a
+    // head; and runs_q share a query block's keys.
+    float *part;                 // [parts][2][total_k][hk][d]: sums of dk and dv; NULL: one part
+    float *part_q;               // [runs_q][total_q][hq][d]: sums of dq; NULL: one run
+    int32_t parts, runs, runs_q;
 };
 // How long a launch takes, in us, by a model: blocks go through the chip `slots`
 // at a time, and a step of one takes `full` where the CUs are full and `half`
@@ -61,8 +64,8 @@ int64_t attn_cut_blocks(const AttnArgs &a);   // blocks whose keys are split
 int64_t attn_fwd_grid(const AttnArgs &a);
 int64_t attn_bwd_grid(const AttnArgs &a);
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream);
-// How many blocks share the query heads of a group for the gradient of keys and values.
-int32_t attn_bwd_parts(const AttnArgs &a);
+// Sets how blocks are shared.
+void attn_bwd_split(AttnArgs &a);
 hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t stream);
 
 // Keys and values in pages: row r of page p is row p * page + r of [pages * page, hk, d].

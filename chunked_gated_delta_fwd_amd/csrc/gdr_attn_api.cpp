@@ -188,12 +188,13 @@ int gdr_attn_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v, 
         a.dq = dq->data;
         a.dk = dk->data;
         a.dv = dv->data;
-        a.parts = gdr::attn_bwd_parts(a);
+        gdr::attn_bwd_split(a);
         if ((rc = fits(gdr::attn_bwd_grid(a)))) return rc;
         Carve sizes{nullptr};
         const auto carve = [&](Carve &w) {
             a.stat = w.take<float>(2 * static_cast<int64_t>(a.hq) * a.total_q);
             a.part = a.parts > 1 ? w.take<float>(2 * static_cast<int64_t>(a.parts) * a.total_k * a.hk * a.d) : nullptr;
+            a.part_q = a.runs_q > 1 ? w.take<float>(static_cast<int64_t>(a.runs_q) * a.total_q * a.hq * a.d) : nullptr;
         };
         carve(sizes);
         if ((rc = Workspace::check(sizes.used, workspace, workspace_bytes))) return rc == 1 ? ok() : rc;

@@ -127,6 +127,15 @@ struct AttnDq {
 // (errors of dq and dk in 2-norm: rows of 2 keys 3.4e-3 without, 2.4e-3 with it,
 // of 30 keys 2.6e-3 and 2.4e-3; one rounding of the result is 1.7e-3).
 constexpr int32_t kFewTiles = 3;
+
+// The share of begin .. end - 1 that run `part` of `parts` takes, in steps of STEP; it may be empty.
+template <int STEP>
+__device__ __forceinline__ void attn_share(int32_t &begin, int32_t &end, int32_t part, int32_t parts) {
+    const int32_t steps = begin < end ? (end - begin + STEP - 1) / STEP : 0, share = (steps + parts - 1) / parts * STEP;
+    begin += part * share;
+    end = begin + share < end ? begin + share : end;
+}
+
 template <class T, int D>
 __device__ __attribute__((noinline)) float attn_dq_delta(AttnArgsAt at, uint32_t tiles, __attribute__((address_space(3))) typename AttnDq<T, D>::Lds *lds);
 
@@ -139,8 +148,10 @@ __device__ __forceinline__ bool attn_dq_block(AttnArgsAt args, const AttnArgs &a
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, h = lane >> 5;
     const int group = a.hq / a.hk;
     const uint32_t pairs = static_cast<uint32_t>(a.cu ? 1 : a.n_seq) * a.hk;
-    const AttnItem item = attn_item(blockIdx.x, pairs, tiles, group);
+    AttnItem item = attn_item(blockIdx.x, pairs, tiles, group * a.runs_q);
     if (item.tile < 0) return false;
+    const int32_t part = item.way / group;
+    item.way %= group;
     const int32_t n = a.cu ? attn_find(a.cu, static_cast<int32_t>(a.n_seq), a.total_q, item.tile, lane) : item.pair / a.hk;
     const int hk = item.pair % a.hk, hq = hk * group + item.way;
     const AttnSeq seq = attn_seq(a, n);
@@ -150,9 +161,10 @@ __device__ __forceinline__ bool attn_dq_block(AttnArgsAt args, const AttnArgs &a
     const int32_t i0 = static_cast<int32_t>(tile * kAttnRows);
     const int32_t i1 = i0 + kAttnRows < seq.lq ? i0 + kAttnRows - 1 : seq.lq - 1;
     const int64_t first = static_cast<int64_t>(sight.at(i0)) - sight.back + 1;
-    const int32_t begin = first > 0 ? static_cast<int32_t>(first) / F::kKeys * F::kKeys : 0;
-    const int32_t end = sight.at(i1) + 1 < seq.lk ? sight.at(i1) + 1 : seq.lk;
+    int32_t begin = first > 0 ? static_cast<int32_t>(first) / F::kKeys * F::kKeys : 0;
+    int32_t end = sight.at(i1) + 1 < seq.lk ? sight.at(i1) + 1 : seq.lk;
     const bool few = T::kBf16 && !SUMS && end - begin <= kFewTiles * F::kKeys;
+    if (!SUMS && a.runs_q > 1) attn_share<F::kKeys>(begin, end, part, a.runs_q);
     if (few) sum = attn_dq_delta<T, D>(args, tiles, attn_lds(lds));
 
     typename F::Row w;
@@ -173,7 +185,7 @@ __device__ __forceinline__ bool attn_dq_block(AttnArgsAt args, const AttnArgs &a
         }
         w.delta = few ? sum : half_sum(dot);
         w.lse = a.lse[row * a.hq + hq] * kLog2e;
-        if (!SUMS && i0 + 32 * wave + col < seq.lq && h == 0) {
+        if (!SUMS && part == 0 && i0 + 32 * wave + col < seq.lq && h == 0) {
             float *stat = a.stat + static_cast<int64_t>(hq) * a.total_q + row;
             stat[0] = w.lse;
             stat[a.hq * a.total_q] = w.delta;
@@ -199,9 +211,16 @@ __device__ __forceinline__ bool attn_dq_block(AttnArgsAt args, const AttnArgs &a
     if (!CAREFUL && __syncthreads_or(x != 0.f)) return true;
     const int32_t i = i0 + 32 * wave + col;
     if (i < seq.lq) {
-        E *dq = static_cast<E *>(a.dq) + ((seq.q0 + i) * a.hq + hq) * D;
+        const int64_t at = ((seq.q0 + i) * a.hq + hq) * D;
+        if (a.part_q) {
+            float *dq = a.part_q + part * a.total_q * a.hq * D + at;
 #pragma unroll
-        for (int t = 0; t < F::kParts; ++t) attn_store<T>(dq + 32 * t, w.dq[t], a.scale, h);
+            for (int t = 0; t < F::kParts; ++t) attn_store<AttnF32>(dq + 32 * t, w.dq[t], a.scale, h);
+        } else {
+            E *dq = static_cast<E *>(a.dq) + at;
+#pragma unroll
+            for (int t = 0; t < F::kParts; ++t) attn_store<T>(dq + 32 * t, w.dq[t], a.scale, h);
+        }
     }
     return false;
 }
@@ -399,7 +418,8 @@ __device__ __forceinline__ bool attn_dkv_block(const AttnArgs &a, uint32_t tiles
     }
     begin = begin / F::kQueries * F::kQueries;
 
-    const int head0 = group * item.way / a.parts, heads = group * (item.way + 1) / a.parts - head0;
+    const int teams = a.parts / a.runs, team = item.way % teams;
+    const int head0 = group * team / teams, heads = group * (team + 1) / teams - head0;
     const int64_t hq = static_cast<int64_t>(hk) * group + head0;
     typename F::Where from;
     from.q = static_cast<const E *>(a.q) + seq.q0 * a.ldq + hq * D;
@@ -423,7 +443,8 @@ __device__ __forceinline__ bool attn_dkv_block(const AttnArgs &a, uint32_t tiles
         for (int ks = 0; ks < F::kSteps; ++ks) w.k[ks] = T::load(k + 16 * ks);
     }
     const float c = a.scale * kLog2e;
-    const int32_t b = static_cast<int32_t>(begin), e = static_cast<int32_t>(end);
+    int32_t b = static_cast<int32_t>(begin), e = static_cast<int32_t>(end);
+    if (a.runs > 1) attn_share<F::kQueries>(b, e, item.way / teams, a.runs);
     F::template walk<CAREFUL>(w, from, sight, c, j0, j1, b, e, lds, wave, lane);
     float x = 0.f;
 #pragma unroll
@@ -463,28 +484,33 @@ __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_attn_dkv_kernel(Att
     if (attn_dkv_block<T, D, false>(a, tiles, lds)) attn_dkv_careful<T, D>(attn_args_at(), tiles, attn_lds(lds));
 }
 
-// Sums the parts of dk and dv in order, for the rows of one tile's sequence;
-// bound by their loads from the caches (16384 keys, 4 heads, two parts of 128
-// channels: 27 us).
-template <class T>
+// Sums the parts of dk and dv (QUERIES: of dq) in order, for the rows of one
+// tile's sequence; bound by their loads from the caches (16384 keys, 4 heads, two
+// parts of 128 channels: 27 us).
+template <class T, bool QUERIES>
 __global__ __launch_bounds__(256) void gdr_attn_join_kernel(AttnArgs a, uint32_t tiles) {
     const int lane = threadIdx.x & 63;
     const int32_t slot = blockIdx.x % tiles, which = blockIdx.x / tiles;
-    const int32_t *cuk = a.cuk ? a.cuk : a.cu;
-    const int32_t n = a.cu ? attn_find(cuk, static_cast<int32_t>(a.n_seq), a.total_k, slot, lane) : which;
+    const int32_t *cu = QUERIES || !a.cuk ? a.cu : a.cuk;
+    const int64_t total = QUERIES ? a.total_q : a.total_k;
+    const int32_t n = a.cu ? attn_find(cu, static_cast<int32_t>(a.n_seq), total, slot, lane) : which;
     const AttnSeq seq = attn_seq(a, n);
-    const int64_t tile = a.cu ? slot - (attn_clamp(cuk[n], 0, a.total_k) / kAttnRows + n) : slot;
-    if (tile < 0 || tile * kAttnRows >= seq.lk) return;
-    const int64_t row = static_cast<int64_t>(a.hk) * a.d, all = a.total_k * row;
-    const int64_t j0 = tile * kAttnRows, rows = seq.lk - j0 < kAttnRows ? seq.lk - j0 : kAttnRows;
-    const int64_t from = (seq.k0 + j0) * row, count = rows * row;
+    const int32_t length = QUERIES ? seq.lq : seq.lk;
+    const int64_t tile = a.cu ? slot - (attn_clamp(cu[n], 0, total) / kAttnRows + n) : slot;
+    if (tile < 0 || tile * kAttnRows >= length) return;
+    const int64_t row = static_cast<int64_t>(QUERIES ? a.hq : a.hk) * a.d, all = total * row;
+    const int64_t j0 = tile * kAttnRows, rows = length - j0 < kAttnRows ? length - j0 : kAttnRows;
+    const int64_t from = ((QUERIES ? seq.q0 : seq.k0) + j0) * row, count = rows * row;
+    const int32_t parts = QUERIES ? a.runs_q : a.parts;
+    constexpr int kSums = QUERIES ? 1 : 2;
     for (int64_t x = threadIdx.x * 4 + blockIdx.y * 1024; x < count; x += gridDim.y * 1024)
 #pragma unroll
-        for (int what = 0; what < 2; ++what) {
+        for (int what = 0; what < kSums; ++what) {
+            const float *part = (QUERIES ? a.part_q : a.part) + what * all + from + x;
             f32x4 sum = zero4();
 #pragma unroll 4
-            for (int p = 0; p < a.parts; ++p) sum += *reinterpret_cast<const f32x4 *>(a.part + (2 * p + what) * all + from + x);
-            typename T::E *to = static_cast<typename T::E *>(what ? a.dv : a.dk) + from + x;
+            for (int p = 0; p < parts; ++p) sum += *reinterpret_cast<const f32x4 *>(part + p * kSums * all);
+            typename T::E *to = static_cast<typename T::E *>(QUERIES ? a.dq : what ? a.dv : a.dk) + from + x;
             if constexpr (T::kBf16) *reinterpret_cast<bf16x4 *>(to) = cvt4(sum);
             else *reinterpret_cast<f32x4 *>(to) = sum;
         }
@@ -492,54 +518,72 @@ __global__ __launch_bounds__(256) void gdr_attn_join_kernel(AttnArgs a, uint32_t
 
 template <class T, int D>
 hipError_t run(const AttnArgs &a, hipStream_t stream) {
-    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
+    const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk, rows = a.cu ? 1 : a.n_seq;
     const int64_t tiles_q = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q);
     const int64_t tiles_k = attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k);
-    const int64_t grid_q = attn_grid(pairs, tiles_q, a.hq / a.hk), grid_k = attn_grid(pairs, tiles_k, a.parts);
-    if (a.total_q > 0) gdr_attn_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid_q)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_q));
+    const int64_t grid_q = attn_grid(pairs, tiles_q, static_cast<int64_t>(a.hq / a.hk) * a.runs_q), grid_k = attn_grid(pairs, tiles_k, a.parts);
+    if (a.total_q > 0) {
+        gdr_attn_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid_q)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_q));
+        if (a.part_q)
+            gdr_attn_join_kernel<T, true><<<dim3(static_cast<unsigned>(tiles_q * rows), 32), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_q));
+    }
     if (a.total_k > 0) {
         gdr_attn_dkv_kernel<T, D><<<dim3(static_cast<unsigned>(grid_k)), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
-        if (a.part) {
-            const int64_t blocks = tiles_k * (a.cu ? 1 : a.n_seq);
-            gdr_attn_join_kernel<T><<<dim3(static_cast<unsigned>(blocks), 32), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
-        }
+        if (a.part)
+            gdr_attn_join_kernel<T, false><<<dim3(static_cast<unsigned>(tiles_k * rows), 32), 256, 0, stream>>>(a, static_cast<uint32_t>(tiles_k));
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-// The parts that cost least by attn_time; a step is 32 queries, as measured on
-// large calls.  Their sums go through the caches at 8 TB/s, and joining them
-// takes 5 us more.
-int32_t attn_bwd_parts(const AttnArgs &a) {
-    const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{512, 1.1, 1.0} : AttnCost{512, 2.2, 1.45})
+// What costs least by attn_time; a step is 32 queries (dq: a tile of keys), as
+// measured on large calls.  Sums go through the caches at 8 TB/s, and joining
+// them takes 5 us more.  Without and with runs, causal, us a call: bf16, d 128,
+// 2048 tokens, 8 heads on 2, 160 and 102, 4096, 8 on 1, 296 and 197; d 64, 8192, 4
+// on 1, 320 and 171; f32, d 128, 700, 2 on 1, 323 and 110.  They have to promise
+// 15 %: 2048, 32 on 8, 197 and 208.
+void attn_bwd_split(AttnArgs &a) {
+    const AttnCost keys = a.bf16 ? (a.d == 64 ? AttnCost{512, 1.1, 1.0} : AttnCost{512, 2.2, 1.45})
                                  : (a.d == 64 ? AttnCost{256, 5.5, 5.5} : AttnCost{256, 11.0, 11.0});
+    const AttnCost queries = a.bf16 ? (a.d == 64 ? AttnCost{768, 2.6, 1.3} : AttnCost{512, 3.0, 1.9})
+                                    : (a.d == 64 ? AttnCost{256, 3.5, 3.5} : AttnCost{256, 7.0, 7.0});
     const int32_t group = a.hq / a.hk;
     const double seqs = a.n_seq > 0 ? static_cast<double>(a.n_seq) : 1.0;
     const double lq = a.cu ? a.total_q / seqs : a.seq_q, lk = a.cu ? a.total_k / seqs : a.seq_k;
-    const double blocks = a.hk * attn_blocks(a.cu != nullptr, seqs, lk);
-    // queries that see a block's keys, at most and on average; packed sequences have other lengths than the mean
-    double most = a.cu ? 2.5 * lq : lq, mean = a.causal ? lq - (lq < lk ? lq : lk) / 2 : lq;
-    if (a.window > 0 && a.window + kAttnRows < most) most = a.window + kAttnRows;
-    if (mean > most) mean = most;
-    double best = 0;
-    int32_t parts = 1;
-    for (int32_t p = 1; p <= group; p = p < group && 2 * p > group ? group : 2 * p) {
-        const double heads = static_cast<double>(group) / p;
-        double t = attn_time(cost, blocks * p, (mean / 32 + 1) * heads, (most / 32 + 1) * heads);
-        if (p > 1) t += 5 + 16.0 * a.total_k * a.hk * a.d * p / 8e6;
-        if (p == 1 || t < 0.95 * best) {
-            best = t;
-            parts = p;
-        }
-    }
-    return parts;
+    // rows of the other side that a block works on, at most and on average; packed sequences have other lengths
+    // than the mean
+    const auto least = [&](const AttnCost &cost, double blocks, double own, double other, int32_t step, int32_t most_teams,
+                           int32_t &teams, int32_t &runs, double bytes) {
+        double most = a.cu ? 2.5 * other : other, mean = a.causal ? other - (own < other ? own : other) / 2 : other;
+        if (a.window > 0 && a.window + kAttnRows < most) most = a.window + kAttnRows;
+        if (mean > most) mean = most;
+        const double steps = mean / step + 1, longest = most / step + 1;
+        double best = 0;
+        teams = runs = 1;
+        const auto consider = [&](int32_t t, int32_t r) {
+            const double heads = static_cast<double>(most_teams) / t / r;
+            double time = attn_time(cost, blocks * t * r, steps * heads, longest * heads);
+            if (t * r > 1) time += 5 + bytes * t * r / 8e6;
+            if (t * r == 1 || time < (r > 1 ? 0.85 : 0.95) * best) {
+                best = time;
+                teams = t;
+                runs = r;
+            }
+        };
+        for (int32_t t = 1; t <= most_teams; t = t < most_teams && 2 * t > most_teams ? most_teams : 2 * t) consider(t, 1);
+        for (int32_t r = 2; r <= 16 && longest / r >= 4; r += r < 4 ? 1 : 4) consider(most_teams, r);
+    };
+    int32_t teams, one;
+    least(keys, a.hk * attn_blocks(a.cu != nullptr, seqs, lk), lk, lq, 32, group, teams, a.runs, 16.0 * a.total_k * a.hk * a.d);
+    a.parts = teams * a.runs;
+    least(queries, a.hq * attn_blocks(a.cu != nullptr, seqs, lq), lq, lk, a.bf16 ? 64 : 32, 1, one, a.runs_q,
+          8.0 * a.total_q * a.hq * a.d);
 }
 
 int64_t attn_bwd_grid(const AttnArgs &a) {
     const int64_t pairs = (a.cu ? 1 : a.n_seq) * a.hk;
-    const int64_t q = attn_grid(pairs, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q), a.hq / a.hk);
+    const int64_t q = attn_grid(pairs, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_q, a.total_q), static_cast<int64_t>(a.hq / a.hk) * a.runs_q);
     const int64_t k = attn_grid(pairs, attn_tiles(a.cu != nullptr, a.n_seq, a.seq_k, a.total_k), a.parts);
     return q > k ? q : k;
 }

@@ -557,8 +557,9 @@ int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
  * o as it is given, for blocks of 128 queries that see 192 keys at most from
  * the scores' gradients, which sum to zero.  Whatever is not finite reaches the
  * rows whose sums hold it and no others.  Workspace: 8 bytes a query and query
- * head, and 8 d bytes a key, key head and part where several blocks share a
- * group's heads (small calls; as many parts at most as a group has heads).
+ * head, and where blocks are few: 8 d bytes a key, key head and block that
+ * shares it (the group's heads, then runs of the queries), 4 d bytes a query,
+ * query head and run of its keys.
  */
 int gdr_attn_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
                  const gdr_tensor *cu_seqlens, const gdr_tensor *cu_seqlens_k, const gdr_tensor *o,

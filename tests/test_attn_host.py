@@ -173,6 +173,19 @@ def test_backward_workspace(lib):  # noqa: F811
     assert call(lib, "attn_bwd", list(d.values()), 1, 0, 1.0, None, ctypes.addressof(size))[0] == 0 and size.value == 0
 
 
+def test_backward_workspace_of_few_blocks(lib):  # noqa: F811
+    """8 bytes a query and head where the blocks fill the chip; sums of shared blocks beside them where they are few."""
+    def need(B, Tn, hq, hk, d):
+        A, size = Alloc2(), ctypes.c_int64(-1)
+        q, k = [A(GDR_F32, [B, Tn, hq, d]) for _ in range(4)], [A(GDR_F32, [B, Tn, hk, d]) for _ in range(4)]
+        got = call(lib, "attn_bwd", [q[0], k[0], k[1], None, None, q[1], A(GDR_F32, [B, Tn, hq]), q[2], q[3], k[2], k[3]], 1, 0, 1.0,
+                   None, ctypes.addressof(size))
+        assert got[0] == 0, got
+        return size.value
+    assert need(64, 512, 4, 4, 64) == 8 * 64 * 512 * 4               # 1024 blocks
+    assert need(1, 900, 2, 1, 128) >= 8 * 900 * 2 + 2 * 8 * 128 * 900 * 2 + 2 * 4 * 128 * 900 * 2
+
+
 def step(P=9, page=16, M=5):
     A = Alloc()
     return dict(q=A(BF, [N, HQ, D]), kp=A(BF, [P, page, HK, D]), vp=A(BF, [P, page, HK, D]), table=A(GDR_I32, [N, M]),

@@ -427,6 +427,34 @@ def test_keys_of_the_last_blocks_alone_are_split(lq, lk, hq, hk, d, dtype, causa
     assert sound(got).all()
 
 
+@pytest.mark.parametrize("lq,lk,hq,hk,d,dtype,causal,window", [
+    ([900], None, 2, 1, 128, F, True, 0),
+    ([1300], None, 3, 3, 64, F, True, 300),
+    ([700, 0, 1200], None, 4, 2, 64, BF, True, 0),
+    ([1500], None, 2, 1, 128, BF, False, 0),
+    ([200, 900], [1900, 900], 2, 2, 128, BF, True, 0),
+    ([1025], [70], 2, 1, 64, BF, False, 0),             # many queries over few keys
+])
+def test_gradients_of_few_blocks(lq, lk, hq, hk, d, dtype, causal, window):
+    """Runs of a block's queries, or of its keys, in blocks of their own, joined in order; behind the last sequence nothing is
+    written."""
+    import chunked_gated_delta_fwd_amd as gdr
+    cu, cuk = offsets(lq), offsets(lk)
+    Tq, Tk = cu[-1] + 9, (cuk or cu)[-1] + 9
+    dev, dbl = make(1, Tq, Tk, hq, hk, d, dtype, seed=31)
+    kw = dict(causal=causal, window=window)
+    o, lse = gdr.attn_fwd(dev["q"], dev["k"], dev["v"], ints(cu), ints(cuk), **kw)
+    full = [torch.full_like(dev[n], 7.0) for n in "qkv"]
+    got = gdr.attn_bwd(dev["q"], dev["k"], dev["v"], o, lse, dev["do"], ints(cu), ints(cuk), dq=full[0], dk=full[1], dv=full[2], **kw)
+    rg, tg = ref.gradient(*(dbl[n] for n in ("q", "k", "v", "do")), cu, cuk, dtype=dtype, **kw)
+    for name, a, r, t, end in zip(("dq", "dk", "dv"), got, rg, tg, (cu[-1], (cuk or cu)[-1], (cuk or cu)[-1])):
+        check(name, a[:, :end], r[:, :end], t[:, :end])
+        assert (a[:, end:] == 7.0).all()
+    again = gdr.attn_bwd(dev["q"], dev["k"], dev["v"], o, lse, dev["do"], ints(cu), ints(cuk), **kw)
+    assert all(torch.equal(bits(a[:, :end]), bits(b[:, :end])) for a, b, end in
+               zip(got, again, (cu[-1], (cuk or cu)[-1], (cuk or cu)[-1])))
+
+
 def test_rows_far_apart():
     """Keys 4 MiB apart: their places pass 2^31 bytes within one sequence."""
     import chunked_gated_delta_fwd_amd as gdr
