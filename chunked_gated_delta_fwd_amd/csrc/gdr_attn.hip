@@ -273,7 +273,7 @@ __global__ __launch_bounds__(256, T::kBf16 ? (D == 64 ? 3 : 2) : 1) void gdr_att
 }
 
 // Joins a block's runs, bound by their loads and a launch (8 pieces of 512
-// queries: 8.8 us beside the runs' 197): 4 channels a thread, 8 rows (d 64: 16) at a time, the
+// queries: 9 us beside the runs' 200): 4 channels a thread, 8 rows (d 64: 16) at a time, the
 // rows shared by the launch's blocks along y.
 template <class T, int D>
 __global__ __launch_bounds__(256) void gdr_attn_runs_kernel(AttnArgs a, uint32_t tiles) {

@@ -341,6 +341,30 @@ def test_graph_on_another_stream():
         assert all(sound(x).all() for x in eager)
 
 
+def test_two_graphs_that_share_memory():
+    """Calls whose blocks are shared and joined, captured in two graphs of one memory pool and replayed in turn: neither reads
+    what the other left."""
+    import chunked_gated_delta_fwd_amd as gdr
+    sets = [make(1, tq, tk, 2, 1, d, BF, seed=41)[0] for tq, tk, d in ((600, 600, 128), (40, 3000, 64))]
+
+    def call(x):
+        o, lse = gdr.attn_fwd(x["q"], x["k"], x["v"])
+        return [o, lse] + list(gdr.attn_bwd(x["q"], x["k"], x["v"], o, lse, x["do"]))
+
+    want = [[x.clone() for x in call(x)] for x in sets]
+    torch.cuda.synchronize()
+    pool, graphs, got = torch.cuda.graph_pool_handle(), [], []
+    for x in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], pool=pool):
+            got.append(call(x))
+    for _ in range(3):
+        for graph, a, b in zip(graphs, got, want):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(bits(y), bits(z)) for y, z in zip(a, b))
+
+
 def test_calls_on_two_streams():
     """The library's workspace is handed from one stream's call to the other's in order."""
     import chunked_gated_delta_fwd_amd as gdr
