@@ -174,8 +174,8 @@ def prepare(case, seed):
     if case["op"] == "store":
         t, hk, d, page = case["tokens"], case["hk"], case["d"], case["page"]
         pages = -(-t // page) + 3
-        s["slots"] = shuffled(pages * page)[None, :t].clone()
-        s["slots"][:, :case["dropped"]] = -1
+        s["slots"] = shuffled(pages * page)[:t].clone()
+        s["slots"][:case["dropped"]] = -1
         s["k"], s["v"] = randn(1, t, hk, d, dtype=dt), randn(1, t, hk, d, dtype=dt)
         s["kp"], s["vp"] = randn(pages, page, hk, d, dtype=dt), randn(pages, page, hk, d, dtype=dt)
         return s
@@ -331,12 +331,12 @@ def _plain_plan(s):
     slots = torch.where(which >= 0, which * page + position % page, -1)
     cu = torch.cat([ends.new_zeros(1), ends])
     used = torch.stack([ends[-1], need.sum()])
-    return table, tuple(x.int() for x in (cu, past + new, position[None], slots[None], used))
+    return table, tuple(x.int() for x in (cu, past + new, position, slots, used))
 
 
 def _plain_store(s):
-    keep = s["slots"][0] >= 0
-    at = s["slots"][0][keep].long()
+    keep = s["slots"] >= 0
+    at = s["slots"][keep].long()
     for pages, x in (("kp", "k"), ("vp", "v")):
         s[pages].flatten(0, 1)[at] = s[x][0][keep]
     return s["kp"], s["vp"]
@@ -389,9 +389,9 @@ def exact(case, seed):
         got = []
         for pages, x in (("kp", "k"), ("vp", "v")):
             flat = s[pages].double().flatten(0, 1)
-            for slot, row in zip(s["slots"][0].tolist()[:case["dropped"]], s[x][0].double()[:case["dropped"]]):
+            for slot, row in zip(s["slots"].tolist()[:case["dropped"]], s[x][0].double()[:case["dropped"]]):
                 assert slot < 0
-            at = s["slots"][0, case["dropped"]:].long()[:, None, None].expand(-1, case["hk"], case["d"])
+            at = s["slots"][case["dropped"]:].long()[:, None, None].expand(-1, case["hk"], case["d"])
             got.append(flat.scatter(0, at, s[x][0, case["dropped"]:].double()).reshape(s[pages].shape))
         return tuple(got)
     return _exact_token(s, case) if case["op"] == "token" else _exact_attn(s, case)
