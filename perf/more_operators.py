@@ -225,8 +225,9 @@ def _own(s):
     if case["op"] == "token":
         return gdr.attn_paged_step(s["q"], s["kp"], s["vp"], s["table"], s["lens"], window=case["window"])
     if case["op"] == "plan":
-        return s["table"], gdr.page_plan(s["past"], s["new"], s["free"], s["table"], case["page"], s["tokens"])
-    gdr.page_store(s["k"], s["v"], s["slots"], s["kp"], s["vp"])
+        cu, lens, positions, slots, used = gdr.page_plan(s["past"], s["new"], s["free"], s["table"], case["page"], s["tokens"])
+        return s["table"], (cu, lens, positions[0], slots[0], used)
+    gdr.page_store(s["k"], s["v"], s["slots"][None], s["kp"], s["vp"])
     return s["kp"], s["vp"]
 
 
