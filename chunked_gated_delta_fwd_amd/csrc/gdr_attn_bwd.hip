@@ -185,7 +185,10 @@ __device__ __forceinline__ bool attn_dq_block(AttnArgsAt args, const AttnArgs &a
             for (int s = 0; s < 8; ++s) dot = __builtin_fmaf(T::up(w.dout[ks], s), T::up(x, s), dot);
         }
         w.delta = few ? sum : half_sum(dot);
-        w.lse = a.lse[row * a.hq + hq] * kLog2e;
+        // a row that sees no key, or whose scores are all -inf: +inf makes its probabilities 0, where -inf would take
+        // -inf from -inf
+        const float lse = a.lse[row * a.hq + hq];
+        w.lse = lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
         if (!SUMS && part == 0 && i0 + 32 * wave + col < seq.lq && h == 0) {
             float *stat = a.stat + static_cast<int64_t>(hq) * a.total_q + row;
             stat[0] = w.lse;
