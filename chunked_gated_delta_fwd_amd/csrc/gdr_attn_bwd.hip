@@ -124,10 +124,10 @@ struct AttnDq {
 // delta cancels against do . v, and made from a bf16 o it carries o's rounding:
 // in dq and dk, relative to that of ds, about n^-1/2 of it where n keys share a
 // row's weight.  A row's ds sum to zero with the delta that belongs to them, so
-// where a block sees at most kFewTiles tiles a walk of its own takes the sum
+// where a block's rows see at most kFewKeys keys a walk of its own takes the sum
 // (errors of dq and dk in 2-norm: rows of 2 keys 3.4e-3 without, 2.4e-3 with it,
 // of 30 keys 2.6e-3 and 2.4e-3; one rounding of the result is 1.7e-3).
-constexpr int32_t kFewTiles = 3;
+constexpr int32_t kFewKeys = 192;
 
 // The share of begin .. end - 1 that run `part` of `parts` takes, in steps of STEP; it may be empty.
 template <int STEP>
@@ -161,10 +161,11 @@ __device__ __forceinline__ bool attn_dq_block(AttnArgsAt args, const AttnArgs &a
     const AttnSight sight(a, seq);
     const int32_t i0 = static_cast<int32_t>(tile * kAttnRows);
     const int32_t i1 = i0 + kAttnRows < seq.lq ? i0 + kAttnRows - 1 : seq.lq - 1;
-    const int64_t first = static_cast<int64_t>(sight.at(i0)) - sight.back + 1;
-    int32_t begin = first > 0 ? static_cast<int32_t>(first) / F::kKeys * F::kKeys : 0;
+    const int64_t back = static_cast<int64_t>(sight.at(i0)) - sight.back + 1;
+    const int32_t first = back > 0 ? static_cast<int32_t>(back) : 0;
+    int32_t begin = first / F::kKeys * F::kKeys;
     int32_t end = sight.at(i1) + 1 < seq.lk ? sight.at(i1) + 1 : seq.lk;
-    const bool few = T::kBf16 && !SUMS && end - begin <= kFewTiles * F::kKeys;
+    const bool few = T::kBf16 && !SUMS && end - first <= kFewKeys;
     if (!SUMS && a.runs_q > 1) attn_share<F::kKeys>(begin, end, part, a.runs_q);
     if (few) sum = attn_dq_delta<T, D>(args, tiles, attn_lds(lds));
 
