@@ -60,7 +60,7 @@ inline double attn_blocks(bool packed, double sequences, double rows) {
 // Sets how the keys are split.
 void attn_split(AttnArgs &a);
 int64_t attn_cut_blocks(const AttnArgs &a);   // blocks whose keys are split
-// Blocks of the largest launch of a call; more than 2^31 - 1 cannot be launched.
+// Blocks (of 256 threads) of the largest launch of a call; more than 2^24 - 1 cannot be launched.
 int64_t attn_fwd_grid(const AttnArgs &a);
 int64_t attn_bwd_grid(const AttnArgs &a);
 hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t stream);

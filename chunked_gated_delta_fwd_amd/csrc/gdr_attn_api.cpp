@@ -92,8 +92,10 @@ int plan_attn(AttnIn &c, gdr::AttnArgs &a) {
     return GDR_OK;
 }
 
+// A launch holds fewer than 2^32 threads along x.
 int fits(int64_t blocks) {
-    if (blocks > 0x7FFFFFFF) return fail(GDR_ESHAPE, "the call would take %lld blocks, more than 2^31 - 1", (long long)blocks);
+    if (blocks >= 1 << 24)
+        return fail(GDR_ESHAPE, "the call would take %lld blocks of 256 threads, more than the 2^24 - 1 of a launch", (long long)blocks);
     return GDR_OK;
 }
 

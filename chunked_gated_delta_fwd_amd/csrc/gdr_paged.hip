@@ -369,8 +369,9 @@ void paged_split(PagedArgs &a) {
 }
 
 int64_t paged_grid(const PagedArgs &a) {
-    const int64_t step = a.n_seq * a.hk * ((a.hq / a.hk + 31) / 32) * a.splits, join = a.n_seq * a.hq;
-    return step > join ? step : join;
+    const int64_t step = a.n_seq * a.hk * ((a.hq / a.hk + 31) / 32) * a.splits, join = a.splits > 1 ? a.n_seq * a.hq : 0;
+    const int64_t threads = a.splits > 16 ? 8 * a.d : a.d;   // of a block that joins
+    return step > (join * threads + 255) / 256 ? step : (join * threads + 255) / 256;
 }
 
 hipError_t launch_paged_step(const PagedArgs &a, hipStream_t stream) {

@@ -507,7 +507,10 @@ int gdr_ssm_step(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
 /* ------------------------------------------------------------------------
  * Softmax attention and the paged key-value cache it decodes from, for the
  * layers of a stack that are not recurrent.  Rows, workspaces and the order of
- * sums as for the operators above.
+ * sums as for the operators above.  A launch holds 2^24 - 1 blocks: a call that
+ * would take more (a block for 128 queries of a sequence and query head, for a
+ * sequence and key head of a single token, for 4 KiB that are stored) ends in
+ * GDR_ESHAPE.
  * ------------------------------------------------------------------------ */
 
 /*
