@@ -107,15 +107,21 @@ struct AttnF32 {
 // buffer's end stores zeros.  The wait states are this code's own affair: a
 // scalar register of the descriptor that a vector instruction wrote (a first
 // lane read, a spilled one read back) may be read by a load five states later,
-// m0 one; the compiler does not see that there is a load in here.
+// m0 one; the compiler does not see that there is a load in here.  m0 is named
+// as written, so that none of the compiler's own uses is carried across; that
+// it may not be preserved, which the warning for reserved registers says, is
+// what is meant.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_load16(v4u32 rsrc, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 : : "s"(lds), "v"(off), "s"(rsrc) : "memory");
+                 : : "s"(lds), "v"(off), "s"(rsrc) : "m0", "memory");
 }
 __device__ __forceinline__ void lds_load4(v4u32 rsrc, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 : : "s"(lds), "v"(off), "s"(rsrc) : "memory");
+                 : : "s"(lds), "v"(off), "s"(rsrc) : "m0", "memory");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ v4u32 uniform_rsrc(const void *base, uint32_t bytes) {
