@@ -62,6 +62,16 @@ struct AttnBf {
         for (int i = 0; i < 8; ++i) r[i] = (__bf16)x[8 * kb + i];
         return r;
     }
+    // registers 8 kb .. as the sum of two parts: cut to bf16, and what is left, rounded, 2^-15 of it away at most.  Both are
+    // above zero where it is (2^-120 at least, or as much again of something smaller), so that an infinite factor stays one.
+    static __device__ __forceinline__ void parts(const f32x16 &x, int kb, F8 &high, F8 &low) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = x[8 * kb + i], z = __uint_as_float(__float_as_uint(y) & 0xFFFF0000u);
+            high[i] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(__float_as_uint(y) >> 16));
+            low[i] = (__bf16)fmaxf(y - z, fminf(z, 0x1p-120f));
+        }
+    }
     static __device__ __forceinline__ F8 only(F8 x, int i) {   // element i, zeros elsewhere (i at run time)
         F8 r;
 #pragma unroll

@@ -582,7 +582,8 @@ int gdr_attn_bwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
  *   o            [N, Hq, d] out, rounded once; zeros for a sequence without keys
  *   window       0, or the number of last keys that are seen
  *
- * Arithmetic as gdr_attn_fwd.  The keys of a sequence are split in chunks where
+ * Arithmetic as gdr_attn_fwd, but for bf16 probabilities, which are kept to
+ * 2^-15 of them.  The keys of a sequence are split in chunks where
  * that pays for the second kernel that joins them; workspace: 4 (d + 2) Hq bytes
  * a sequence and chunk of the longest one that the table holds (of about 1024
  * blocks in a call, one for each chunk and key head), none for one chunk.
