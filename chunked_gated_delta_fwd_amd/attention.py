@@ -42,11 +42,12 @@ def page_plan(past, new, free_pages, block_table, page, tokens, cu_seqlens=None,
     block_table int32 ``[N, M]`` is updated in place with pages from free_pages.
     Returns ``(cu_seqlens, lens, positions, slots, used)``: offsets ``[N+1]``,
     past + new ``[N]``, place in the request and row in the pages ``[1, tokens]``
-    (-1: no page), and ``[2]`` the tokens and pages taken."""
+    (-1: no page; given ones may be ``[tokens]``), and ``[2]`` the tokens and pages
+    taken."""
     return _t.page_plan(past, new, free_pages, block_table, page, tokens, cu_seqlens, lens, positions, slots, used)
 
 
 def page_store(k, v, slots, k_pages, v_pages):
-    """Copies k and v ``[B, T, Hk, d]`` to the rows ``slots`` (int32 ``[B, T]``)
-    of k_pages and v_pages ``[P, page, Hk, d]``; a negative slot stores nothing."""
+    """Copies k and v ``[B, T, Hk, d]`` to the rows ``slots`` (int32 ``[B, T]``
+    or ``[B * T]``) of k_pages and v_pages ``[P, page, Hk, d]``; a negative slot stores nothing."""
     _t.page_store(k, v, slots, k_pages, v_pages)

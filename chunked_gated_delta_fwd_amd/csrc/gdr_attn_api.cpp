@@ -99,6 +99,9 @@ int fits(int64_t blocks) {
     return GDR_OK;
 }
 
+// Dimensions of a tensor with a number a token: [tokens], or rows of a batch.
+int token_dims(const gdr_tensor *t) { return t && t->ndim == 1 ? 1 : 2; }
+
 // Both offsets' contents, with the opt-in check on.
 int check_offsets(const AttnIn &c, const gdr::AttnArgs &a, hipStream_t stream) {
     const int rc = check_cu(c.cu, a.n_seq, c.B * c.Tq, stream);
@@ -310,7 +313,7 @@ int gdr_page_store(const gdr_tensor *k, const gdr_tensor *v, const gdr_tensor *s
         if (!k) return fail(GDR_EINVAL, "k: descriptor is NULL");
         if (!is_float(k)) return fail(GDR_EDTYPE, "k: dtype must be bf16 or f32, got %s", dtype_name(k->dtype));
         if ((rc = check_rows(k, "k", 4, 2, 16, &a.ldk, &sk)) || (rc = check_rows(v, "v", 4, 2, 16, &a.ldv, &sv)) ||
-            (rc = check_tensor(slots, "slots", 2, &ns, 4)) || (rc = check_tensor(k_pages, "k_pages", 4, &nk, 16)) ||
+            (rc = check_tensor(slots, "slots", token_dims(slots), &ns, 4)) || (rc = check_tensor(k_pages, "k_pages", 4, &nk, 16)) ||
             (rc = check_tensor(v_pages, "v_pages", 4, &nv, 16)))
             return rc;
         if ((rc = want_dtype(v, "v", k->dtype)) || (rc = want_dtype(slots, "slots", GDR_I32)) ||
@@ -325,7 +328,8 @@ int gdr_page_store(const gdr_tensor *k, const gdr_tensor *v, const gdr_tensor *s
                         (long long)d);
         if (page < 1 || page > 65536) return fail(GDR_ESHAPE, "k_pages: pages of 1 to 65536 tokens are supported, got %lld", (long long)page);
         if (P > 0x7FFFFFFF / page) return fail(GDR_ESHAPE, "k_pages: more than 2^31 - 1 tokens in all pages");
-        if ((rc = want_shape(v, "v", {B, T, hk, d}, "k's shape")) || (rc = want_shape(slots, "slots", {B, T}, "[B, T]")) ||
+        if ((rc = want_shape(v, "v", {B, T, hk, d}, "k's shape")) ||
+            (rc = slots->ndim == 1 ? want_shape(slots, "slots", {B * T}, "[B * T]") : want_shape(slots, "slots", {B, T}, "[B, T]")) ||
             (rc = want_shape(k_pages, "k_pages", {P, page, hk, d}, "[pages, page, Hk, d] with k's Hk and d")) ||
             (rc = want_shape(v_pages, "v_pages", {P, page, hk, d}, "k_pages' shape")))
             return rc;
@@ -363,22 +367,24 @@ int gdr_page_plan(const gdr_tensor *past, const gdr_tensor *fresh, const gdr_ten
             Span span;
         } args[] = {{past, "past", 1, {}},         {fresh, "new", 1, {}},   {free_pages, "free_pages", 1, {}},
                     {block_table, "block_table", 2, {}}, {cu_seqlens, "cu_seqlens", 1, {}}, {lens, "lens", 1, {}},
-                    {positions, "positions", 2, {}}, {slots, "slots", 2, {}}, {used, "used", 1, {}}};
+                    {positions, "positions", token_dims(positions), {}}, {slots, "slots", token_dims(slots), {}}, {used, "used", 1, {}}};
         int rc;
         for (Arg &x : args) {
             int64_t n;
             if ((rc = check_tensor(x.t, x.name, x.ndim, &n, 4)) || (rc = want_dtype(x.t, x.name, GDR_I32))) return rc;
             x.span = span_of(x.t, n);
         }
-        const int64_t N = past->shape[0], M = block_table->shape[1], T = positions->shape[1];
+        const int64_t N = past->shape[0], M = block_table->shape[1], T = positions->shape[positions->ndim - 1];
         if (N > kMostRows) return fail(GDR_ESHAPE, "past: at most 2^30 sequences are supported");
         if (T > kMostRows) return fail(GDR_ESHAPE, "positions: at most 2^30 tokens are supported");
         if (page < 1 || page > 65536) return fail(GDR_ESHAPE, "page: 1 to 65536 tokens are supported, got %d", page);
         if (M > kMostRows / page) return fail(GDR_ESHAPE, "block_table: more than 2^30 tokens a sequence");
         if ((rc = want_shape(fresh, "new", {N}, "[N]")) || (rc = want_shape(block_table, "block_table", {N, M}, "[N, pages of a sequence]")) ||
             (rc = want_shape(cu_seqlens, "cu_seqlens", {N + 1}, "[N + 1]")) || (rc = want_shape(lens, "lens", {N}, "[N]")) ||
-            (rc = want_shape(positions, "positions", {1, T}, "[1, tokens]")) ||
-            (rc = want_shape(slots, "slots", {1, T}, "positions' shape")) || (rc = want_shape(used, "used", {2}, "[2]")))
+            (rc = positions->ndim == 1 ? GDR_OK : want_shape(positions, "positions", {1, T}, "[1, tokens]")) ||
+            (rc = slots->ndim == 1 ? want_shape(slots, "slots", {T}, "[tokens] of positions")
+                                   : want_shape(slots, "slots", {1, T}, "[1, tokens] of positions")) ||
+            (rc = want_shape(used, "used", {2}, "[2]")))
             return rc;
         if ((rc = check_overlaps({{"past", args[0].span}, {"new", args[1].span}, {"free_pages", args[2].span}},
                                  {{"block_table", args[3].span}, {"cu_seqlens", args[4].span}, {"lens", args[5].span},

@@ -605,8 +605,8 @@ int gdr_attn_paged_step(const gdr_tensor *q, const gdr_tensor *k_pages, const gd
  *                request, or -1 where none is left; the others are kept
  *   cu_seqlens   [N+1] int32 out: sums of fresh, at most T
  *   lens         [N] int32 out: past + fresh
- *   positions    [1, T] int32 out: each new token's place in its request
- *   slots        [1, T] int32 out: its row in the pages, page * page size +
+ *   positions    [1, T] or [T] int32 out: each new token's place in its request
+ *   slots        [1, T] or [T] int32 out: its row in the pages, page * page size +
  *                place in the page; -1 without a page
  *   used         [2] int32 out: all fresh tokens and all pages wanted, whether
  *                or not T, F and M held them
@@ -622,7 +622,7 @@ int gdr_page_plan(const gdr_tensor *past, const gdr_tensor *fresh, const gdr_ten
  * gdr_page_store - copies the keys and values of tokens into their slots.
  *
  *   k, v     [B, T, Hk, d] rows, bf16 or f32, Hk * d a multiple of 16 bytes
- *   slots    [B, T] int32 rows of the pages; a slot outside 0 .. P * page - 1
+ *   slots    [B, T] or [B * T] int32 rows of the pages; a slot outside 0 .. P * page - 1
  *            stores nothing.  A slot that is named twice gets pieces of both.
  *   k_pages, v_pages  [P, page, Hk, d] out, dtype of k; other rows are kept
  *
