@@ -18,8 +18,9 @@ namespace {
 // Bound by the matrix unit and the exponentials between its two products, which
 // the second wave of a SIMD fills in part.  2 x 8192 tokens, 32 heads on 4,
 // causal, bf16: d 128 1.00 to 1.05 ms, 1050 to 1100 TFLOP/s of the 1251 of a
-// large matrix product; d 64 920 (twice the exponentials a product).  f32, d 128:
-// 109 of 153.
+// large matrix product; d 64 860 (twice the exponentials a product).  f32, 2 x
+// 4096, 16 heads on 4: d 128 116 of 153, d 64 105: one wave a SIMD, whose
+// exponentials nothing overlaps.
 template <class T, int D>
 struct AttnFwd {
     typedef typename T::E E;
@@ -112,7 +113,7 @@ struct AttnFwd {
                     sums[r % 4] += s[t][r];
                 }
             w.sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-            // bf16: probabilities are rounded to nearest for the product with the values (relative 2^-9 each, of
+            // bf16: probabilities are rounded to nearest for the product with the values (2^-8 of each at most, of
             // independent signs); their sum is not
 #pragma unroll
             for (int kb = 0; kb < 2 * kSub; ++kb) {
@@ -337,6 +338,8 @@ int64_t all_blocks(const AttnArgs &a) {
 // sequences, 4000 keys before them, 16 heads on 2, d 128 (about 580 blocks, 512
 // at a time): 222 us with all blocks' keys whole or all split, 188 with the last
 // blocks' split.
+// Packed sequences are taken to be alike: 64 queries over 32768 keys are split by
+// themselves (78 us) and walked whole beside 63 sequences of 500 keys (590).
 void attn_split(AttnArgs &a) {
     const int32_t keys = a.bf16 ? 64 : 32;
     const AttnCost cost = a.bf16 ? (a.d == 64 ? AttnCost{768, 1.95, 0.9} : AttnCost{512, 2.2, 1.35})

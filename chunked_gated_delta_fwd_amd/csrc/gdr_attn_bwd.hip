@@ -9,9 +9,9 @@
 // and walks the queries (dk, dv): scores and do . v are made twice, seven
 // products for five, so that every sum stays in registers in a fixed order.
 //
-// 4 x 4096 tokens, 32 heads on 4, d 128, causal, bf16: 1.88 ms a call, the first
-// pass 0.79 to 0.82 (3 products, 1010 to 1040 TFLOP/s), the second 1.12 to 1.14
-// (4 products, 970 to 990).
+// 4 x 4096 tokens, 32 heads on 4, d 128, causal, bf16: 1.83 to 1.92 ms a call. In
+// a traced run of 1.94: the first pass 0.80 (3 products, 1030 TFLOP/s), the second
+// 1.11 (4 products, 990), the join of dk and dv of a group's halves 0.027.
 #include "gdr_attn_device.h"
 
 namespace gdr {

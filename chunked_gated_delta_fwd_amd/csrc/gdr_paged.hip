@@ -13,8 +13,8 @@ namespace {
 // wave's own that are read transposed.  The next tile's loads start once this
 // one's keys are multiplied and its values are in LDS.  The waves' sums are
 // joined in LDS, the blocks' by a second kernel.  Bound by HBM: 64 sequences of
-// 4096 to 8192 keys, 32 heads on 4, d 128: 170 us, 4.7 TB/s (a large copy: 5.1);
-// one of 131072, 16 heads on 2: 22.9 us, 5.9 TB/s, and 4.4 for the join.
+// 4096 to 8192 keys, 32 heads on 4, d 128: 167 us, 4.8 TB/s (a large copy: 5.1);
+// one of 131072, 16 heads on 2: 29.2 us, 4.6 TB/s, and 4.6 for the join.
 template <class T, int D>
 __global__ __launch_bounds__(256, T::kBf16 ? 2 : 1) void gdr_paged_step_kernel(PagedArgs a) {
     typedef typename T::E E;
@@ -248,8 +248,8 @@ hipError_t run_step(const PagedArgs &a, hipStream_t stream) {
 
 // --- store ------------------------------------------------------------------------------
 
-// 16 bytes a thread.  Bound by HBM: 16384 tokens of 8 heads of 128, bf16, 20.8 us
-// (6.4 TB/s: pages just written stay in the caches); a few tokens by the launch.
+// 16 bytes a thread.  Bound by HBM: 16384 tokens of 8 heads of 128, bf16, 26.1 us
+// (5.1 TB/s, as a large copy); a few tokens by the launch.
 __global__ __launch_bounds__(256) void gdr_page_store_kernel(StoreArgs a) {
     const int64_t pieces = a.row_bytes / 16, count = 2 * a.tokens * pieces;
     const int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
@@ -284,8 +284,8 @@ __device__ __forceinline__ int32_t plan_int(int64_t x) { return x > 0x7FFFFFFF ?
 // stands for the totals).  The tokens and pages before its run are sums over the
 // lengths, which every block makes for itself, N values from the caches, so that
 // one launch does.  Blocks along y share a sequence's tokens.  Bound by latency:
-// 5.2 us for 256 requests, 12 of them prompts of up to 4096 tokens; 3.5 for 8
-// tokens, where a call's host time is 5.5.
+// 5.5 us for 256 requests, 12 of them prompts of up to 4096 tokens; 3.6 for 8
+// tokens, where a call's host time is 5.1.
 __global__ __launch_bounds__(256) void gdr_page_plan_kernel(PlanArgs a, int64_t run) {
     __shared__ int64_t sums[2][4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -348,7 +348,9 @@ __global__ __launch_bounds__(256) void gdr_page_plan_kernel(PlanArgs a, int64_t 
 // the traffic of the chunks' outputs.  Measured against 512 and 1024 keys:
 // 64 x 1024 keys, 4 key heads, 30.4 and (one chunk, no second kernel) 23.8 us;
 // 1 x 16384, 2 key heads, 16.9 and 21.9.  At most about 1024 blocks at the
-// longest: more would only split further what fills the chip already.
+// longest: more would only split further what fills the chip already.  All
+// sequences are taken to be as long as the table holds: one of 131072 keys
+// beside 63 of 1000 in such a table is one chunk, 1910 us for 78 us of bytes.
 void paged_split(PagedArgs &a) {
     int64_t keys = a.width * a.page;
     if (a.window > 0 && keys > a.window) keys = a.window;

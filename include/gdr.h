@@ -535,11 +535,13 @@ int gdr_ssm_step(const gdr_tensor *x, const gdr_tensor *dt, const gdr_tensor *A,
  * rounded to bf16 for the product with v, o is rounded once, lse is fp32.  f32
  * inputs: fp32 products throughout.  A k or v that is not finite reaches the
  * queries that see it and no others; a query whose scores are all -inf counts
- * as one that sees no key.  Where a call has few blocks of 128 queries for
- * the chip, or a few left over, the keys of those are split in runs; workspace
- * then: 4 (d + 2) bytes a run, query and query head of such a block, else none.  q, k, v rows and o on 16-byte
- * addresses, rows at most 32 MiB apart, at most 2^30 tokens.  Errors as
- * gdr_chunk_fwd, GDR_EINVAL for a negative window or one without causal.
+ * as one that sees no key.  The largest score of a query, where it is finite,
+ * has to stay below 2^29 in size.  Where a call has few blocks of 128 queries
+ * for the chip, or a few left over, the keys of those are split in runs;
+ * workspace then: 4 (d + 2) bytes a run, query and query head of such a block,
+ * else none.  q, k, v rows and o on 16-byte addresses, rows at most 32 MiB
+ * apart, at most 2^30 tokens.  Errors as gdr_chunk_fwd, GDR_EINVAL for a negative
+ * window or one without causal.
  */
 int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
                  const gdr_tensor *cu_seqlens, const gdr_tensor *cu_seqlens_k, const gdr_tensor *o,
@@ -554,12 +556,15 @@ int gdr_attn_fwd(const gdr_tensor *q, const gdr_tensor *k, const gdr_tensor *v,
  *           key head's query heads; dtype of q.  Rows of tokens outside every
  *           segment are not written.
  *
- * The probabilities are made again from q, k and lse.  bf16 inputs: they and
- * the scores' gradients are rounded to bf16 for the products over queries and
- * keys; sums are fp32 and each gradient is rounded once.  do . o is taken from
- * o as it is given, for blocks of 128 queries that see 192 keys at most from
- * the scores' gradients, which sum to zero.  Whatever is not finite reaches the
- * rows whose sums hold it and no others.  Workspace: 8 bytes a query and query
+ * The probabilities are made again from q, k and lse, whose fp32 leaves them
+ * within 2^-22 |lse| or so of themselves: nothing means anything from an |lse| of
+ * 2^20 on.  bf16 inputs: they and the scores' gradients are rounded to bf16 for
+ * the products over queries and keys; sums are fp32 and each gradient is rounded
+ * once.  do . o is taken from o as it is given, for blocks of 128 queries that
+ * see 192 keys at most from the scores' gradients, which sum to zero.  A query
+ * that sees no key, or whose scores are all -inf, has probabilities of 0: it puts
+ * nothing on dk and dv, and its dq is 0 where the keys that it sees are finite.
+ * Whatever is not finite reaches the rows whose sums hold it and no others.  Workspace: 8 bytes a query and query
  * head, and where blocks are few: 8 d bytes a key, key head and block that
  * shares it (the group's heads, then runs of the queries), 4 d bytes a query,
  * query head and run of its keys.

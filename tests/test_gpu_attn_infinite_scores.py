@@ -82,3 +82,29 @@ def test_a_first_row_that_sees_a_key_of_infinity_alone(T, d, dtype):
     o2, lse2, (_, dk2, dv2) = gradients(x, None)
     for a, b in ((o[:, 1:], o2[:, 1:]), (lse[:, 1:], lse2[:, 1:]), (dk, dk2), (dv, dv2)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_scores_of_2_to_the_28(dtype, sign):
+    """Exact and all alike, so that o is the mean of the values that are seen, by the forward and by one token over pages.
+    Tolerance: sums of n terms, (n + 16) 2^-24 of the mean |v| for the sums and the quotient, half a step of bf16 for each
+    probability and for o; lse is rounded to fp32 twice (2^-23 of it)."""
+    import chunked_gated_delta_fwd_amd as gdr
+    n, d = 300, 64
+    g = torch.Generator().manual_seed(53)
+    q, k = torch.zeros(1, n, 2, d), torch.zeros(1, n, 1, d)
+    q[..., 0], k[..., 0] = 2.0 ** 17, sign * 2.0 ** 14
+    v = torch.randn(1, n, 1, d, generator=g).to(dtype)
+    q, k = q.to(dtype).cuda(), k.to(dtype).cuda()
+    o, lse = gdr.attn_fwd(q, k, v.cuda())
+    count = torch.arange(1, n + 1).double()[None, :, None, None]
+    mean, size = (x.double().cumsum(1) / count for x in (v, v.abs()))
+    H = 2.0 ** -8 if dtype == BF else 0.0
+    tol = (H + (n + 16) * 2.0 ** -24) * size + H * mean.abs()
+    assert ((o.double().cpu() - mean).abs() <= tol).all()
+    assert (lse.double().cpu() - (sign * 2.0 ** 28 + count[..., 0].log())).abs().max() <= 2.0 ** -23 * 2.0 ** 28
+    kp, vp = (torch.zeros(3, 100, 1, d, dtype=dtype, device="cuda") for _ in range(2))
+    gdr.page_store(k, v.cuda(), torch.arange(n, device="cuda").int(), kp, vp)
+    got = gdr.attn_paged_step(q[:, -1], kp, vp, ints([[0, 1, 2]]), ints([n]))
+    assert ((got.double().cpu() - mean[:, -1]).abs() <= tol[:, -1]).all()
